@@ -1,6 +1,7 @@
 /*
  * nsgb300 -- shape-batched quintic Newton-Schulz for GB300 (sm_103a), with the
- * shard -> home pack and home -> shard unpack around it.
+ * shard -> home pack and home -> shard unpack around it, and operators of the
+ * training step whose gradients it orthogonalises.
  *
  * C ABI of libnsgb300.so. Every function returns an int status (NS_OK = 0 or
  * a negative NS_ERR_* code), never throws and never aborts the process.
@@ -302,6 +303,148 @@ int ns_check_status(ns_plan_t* plan, void* stream);
 int ns_orthogonalize_batched_fixed_ws(ns_plan_t* plan, const void* const* in, void* const* out, int n,
                                       void* stream);
 
+/* ------------------------------------------------ training-step operators
+ * No counterpart on the pages: what a training step needs next to the
+ * optimiser, around the matrices it orthogonalises -- the routing of tokens
+ * to the experts of a mixture-of-experts layer, the norms and the rotation of
+ * a fused QKV projection's queries and keys, and a distillation loss -- each
+ * with its gradient.
+ *
+ * Common to all: device buffers are the caller's; strides are in elements and
+ * the last dimension is contiguous; element types are NS_DT_*; sums, norms and
+ * softmax statistics are in fp32 and a result is rounded to its type once;
+ * results do not depend on the launch (no atomics on floating values). Buffers
+ * of one call must not overlap unless its text says so. A zero count (tokens,
+ * heads, rows) is valid and does what the formulas say. Workspaces are scratch
+ * (no contents kept between calls), 256-byte aligned. Work is asynchronous on
+ * `stream`; after a first call on a device every call may be captured into a
+ * CUDA graph. An index that points outside its buffer is refused on the
+ * device: the access is skipped and ns_check_status reports
+ * NS_ERR_DEVICE_CHECK. Arguments are checked on the host: NS_ERR_ARG for null
+ * pointers and values outside their domain, NS_ERR_SHAPE for sizes or strides
+ * that do not fit each other, NS_ERR_UNSUPPORTED past a stated limit,
+ * NS_ERR_WORKSPACE as elsewhere. */
+
+/* Element types. */
+enum {
+  NS_DT_BF16 = 0,
+  NS_DT_FP16 = 1,
+  NS_DT_FP32 = 2
+};
+
+/* Rows that hold any routing of tokens x k slots to `experts` experts when
+ * every expert's segment is padded to a multiple of `align` rows and keeps at
+ * most `capacity` slots (0: all). Host only. */
+int ns_moe_rows(int64_t tokens, int k, int experts, int align, int64_t capacity, int64_t* rows_out);
+
+/* Bytes of device workspace of ns_moe_sort (may be 0). Host only. */
+int ns_moe_sort_workspace_bytes(int64_t tokens, int k, int experts, uint64_t* bytes);
+
+/* Tokens sorted by expert. expert_ids[t * k + j] (int32 or int64: id_bytes 4
+ * or 8) is token t's j-th choice; a negative one goes nowhere, one >= experts
+ * is refused and goes nowhere. The sort is stable: within an expert, slots
+ * s = t * k + j keep their order, and those past `capacity` (0: no limit) are
+ * dropped. counts[e] = slots kept by expert e; offsets[e] = first row of its
+ * segment, offsets[experts] = rows in use (segments padded to multiples of
+ * align); row_of_slot[s] = row of slot s or -1; slot_of_row[r] = slot of row r
+ * or -1, for all `rows` rows (rows >= ns_moe_rows, NS_ERR_SHAPE otherwise).
+ * 1 <= k <= 32, 1 <= experts <= 1024, tokens * k < 2^31 - 4096. */
+int ns_moe_sort(const void* expert_ids, int id_bytes, int64_t tokens, int k, int experts, int align,
+                int64_t capacity, int64_t rows, int32_t* row_of_slot, int32_t* slot_of_row, int32_t* counts,
+                int32_t* offsets, void* workspace, uint64_t workspace_bytes, void* stream);
+
+/* out[r] = x[slot_of_row[r] / k], and 0 for every row without a slot, so that
+ * a product over padded segments sees no stale values. x is [tokens][dim],
+ * out [rows][dim]; row_of_slot and slot_of_row as ns_moe_sort wrote them. */
+int ns_moe_dispatch(const void* x, int64_t x_stride, int dtype, int64_t tokens, int k, int64_t dim,
+                    const int32_t* row_of_slot, const int32_t* slot_of_row, int64_t rows, void* out,
+                    int64_t out_stride, void* stream);
+
+/* Gradient of ns_moe_dispatch: grad_x[t] = sum over token t's kept slots of
+ * grad_rows[row] (0 if it has none). */
+int ns_moe_dispatch_grad(const void* grad_rows, int64_t rows_stride, int dtype, int64_t tokens, int k, int64_t dim,
+                         const int32_t* row_of_slot, int64_t rows, void* grad_x, int64_t grad_x_stride,
+                         void* stream);
+
+/* y[t] = sum over token t's kept slots of weights[t * k + j] * expert_rows[row]
+ * (0 if it has none). weights fp32 [tokens][k], NULL = 1; the weight of a
+ * dropped slot is not used, whatever it holds. */
+int ns_moe_combine(const void* expert_rows, int64_t rows_stride, int dtype, int64_t tokens, int k, int64_t dim,
+                   const int32_t* row_of_slot, const float* weights, int64_t rows, void* y, int64_t y_stride,
+                   void* stream);
+
+/* Gradient of ns_moe_combine: grad_rows[row] = weight * grad_y[t] (0 for every
+ * row without a slot), grad_weights[t * k + j] = <grad_y[t], expert_rows[row]>
+ * (0 for a dropped slot). grad_rows may be expert_rows itself, with the same
+ * stride. */
+int ns_moe_combine_grad(const void* grad_y, int64_t grad_y_stride, const void* expert_rows, int64_t rows_stride,
+                        int dtype, int64_t tokens, int k, int64_t dim, const int32_t* row_of_slot,
+                        const int32_t* slot_of_row, const float* weights, int64_t rows, void* grad_rows,
+                        int64_t grad_rows_stride, float* grad_weights, void* stream);
+
+/* Norms of queries and keys for each head with the position rotation:
+ * y = R_pos (x / sqrt(mean(x^2) + eps) * weight) for every head x of head_dim
+ * values. q is [tokens][q_heads][head_dim] and k [tokens][k_heads][head_dim]
+ * (for instance column ranges of one fused projection); strides[8] holds the
+ * (token, head) strides of q, k, q_out, k_out in that order. q_weight and
+ * k_weight (NULL = 1) have head_dim values of weight_dtype (dtype or fp32).
+ * The rotation acts on the first rot_dim (even, 0 = none) values: pairs
+ * (i, i + rot_dim / 2), or (2i, 2i + 1) if interleaved = 1, turned by the
+ * angle whose cosine and sine are table[pos][i] and
+ * table[pos][rot_dim / 2 + i] (fp32 [table_rows][rot_dim]). positions[t] is
+ * int32 or int64 (position_bytes 4 or 8), NULL = t; a token whose position is
+ * outside the table is refused (its outputs are not written). head_dim <= 1024.
+ * q_out may be q and k_out may be k, with the same strides. */
+int ns_qk_norm_rope(const void* q, const void* k, void* q_out, void* k_out, const int64_t* strides, int dtype,
+                    int64_t tokens, int q_heads, int k_heads, int head_dim, int rot_dim, int interleaved,
+                    const void* q_weight, const void* k_weight, int weight_dtype, float eps, const float* table,
+                    int64_t table_rows, const void* positions, int position_bytes, void* stream);
+
+/* Bytes of device workspace of ns_qk_norm_rope_grad (needed only with a
+ * weight gradient). Host only. */
+int ns_qk_norm_rope_grad_workspace_bytes(int head_dim, uint64_t* bytes);
+
+/* Gradient of ns_qk_norm_rope: from grad_q_out, grad_k_out and the forward's
+ * q and k, grad_q and grad_k, and the weights' gradients (fp32 [head_dim], sums
+ * over tokens and heads; NULL = not wanted). strides[12] holds the (token,
+ * head) strides of q, k, grad_q, grad_k, grad_q_out, grad_k_out. grad_q may be
+ * grad_q_out or q, and grad_k likewise, with the same strides. */
+int ns_qk_norm_rope_grad(const void* grad_q_out, const void* grad_k_out, const void* q, const void* k, void* grad_q,
+                         void* grad_k, const int64_t* strides, int dtype, int64_t tokens, int q_heads, int k_heads,
+                         int head_dim, int rot_dim, int interleaved, const void* q_weight, const void* k_weight,
+                         int weight_dtype, float* grad_q_weight, float* grad_k_weight, float eps,
+                         const float* table, int64_t table_rows, const void* positions, int position_bytes,
+                         void* workspace, uint64_t workspace_bytes, void* stream);
+
+/* Distillation from a teacher's top logits. For token t with student logits s
+ * (vocab values), the teacher's `top` values z at entries i (teacher_values and
+ * teacher_ids, contiguous [tokens][top]; ids int32 or int64):
+ *   p_j  = exp(z_j / temperature - Z), Z = teacher_lse[t] (the teacher's
+ *          log-sum-exp of z / temperature over its whole vocabulary) or, if
+ *          teacher_lse is NULL, the log-sum-exp over the entries given
+ *   lse  = log-sum-exp of s / temperature
+ *   loss = weights[t] * sum_j p_j (log p_j - s[i_j] / temperature + lse)
+ * and, unless grad_logits is NULL,
+ *   grad_logits[v] = weights[t] / temperature *
+ *                    (sum_j p_j * exp(s[v] / temperature - lse) - sum of the p_j with i_j = v).
+ * weights NULL = 1. Entries with a negative id (padding) or a value of -inf
+ * are left out; an id >= vocab is refused and left out. A token whose weight is
+ * 0 or that has no entry left gets loss 0, lse 0 and a zero gradient, and its
+ * logits are not read. grad_logits may be logits itself, with the same stride.
+ * top <= 1024. A finite logit is needed in every row that is read; a row of
+ * -inf gives NaN. */
+int ns_distill_loss(const void* logits, int64_t logits_stride, int dtype, int64_t tokens, int64_t vocab,
+                    const void* teacher_values, int teacher_dtype, const void* teacher_ids, int id_bytes, int top,
+                    const float* weights, const float* teacher_lse, float temperature, float* loss, float* lse,
+                    void* grad_logits, int64_t grad_stride, void* stream);
+
+/* The gradient alone, from the lse that ns_distill_loss wrote for the same
+ * logits: for a backward pass that comes later, with other weights. */
+int ns_distill_grad(const void* logits, int64_t logits_stride, int dtype, int64_t tokens, int64_t vocab,
+                    const void* teacher_values, int teacher_dtype, const void* teacher_ids, int id_bytes, int top,
+                    const float* weights, const float* teacher_lse, float temperature, const float* lse,
+                    void* grad_logits, int64_t grad_stride, void* stream);
+
 /* ---------------------------------------------------------- test support
  * No counterpart on the pages: hooks with which tests drive the library's
  * device-side error paths without faulting or hanging the GPU. */
@@ -376,6 +519,10 @@ int ns_profile_enable(int enable);
  * (may be NULL) the summed event time per kind since the last reset; reset
  * != 0 clears both afterwards. */
 int ns_profile_read(int reset, int64_t* launches, double* gpu_ms);
+
+/* The same for the training-step operators, launches[3] and gpu_ms[3]:
+ * 0 = sort, dispatch and combine, 1 = norms and rotation, 2 = distillation. */
+int ns_profile_read_training(int reset, int64_t* launches, double* gpu_ms);
 
 #ifdef __cplusplus
 }

@@ -7,7 +7,9 @@ of the hot path runs in the library's CUDA kernels; if the library is missing
 the import fails.
 
 Buffers are torch CUDA tensors (or raw device addresses as ints); streams
-default to torch's current stream.
+default to torch's current stream. The operators of the training step
+(``ns_moe_*``, ``ns_qk_norm_rope*``, ``ns_distill_*``) take torch tensors and
+are in ``training.py``.
 """
 
 from __future__ import annotations
@@ -16,10 +18,24 @@ import ctypes
 
 from ._lib import (NS_BF16, NS_ERR_ARG, NS_ERR_CUDA, NS_ERR_DEVICE_CHECK, NS_ERR_HOME,  # noqa: F401
                    NS_ERR_NOT_DIVISIBLE, NS_ERR_SHAPE, NS_ERR_TIMEOUT, NS_ERR_UNSUPPORTED,
-                   NS_ERR_WORKSPACE, NS_FP32_GRAM, NS_FP32_GRAM_SPACE, NS_FP32_AUTO, NS_LAYOUT_FLAT, NS_LAYOUT_ROW_SHARD, NS_LAYOUT_TWO_STAGE, NS_OK,
+                   NS_ERR_WORKSPACE, NS_DT_BF16, NS_DT_FP16, NS_DT_FP32, NS_FP32_GRAM, NS_FP32_GRAM_SPACE, NS_FP32_AUTO, NS_LAYOUT_FLAT, NS_LAYOUT_ROW_SHARD, NS_LAYOUT_TWO_STAGE, NS_OK,
                    LIB_PATH, NsError, check, header_symbols, i32_array, i64_array, lib, ptr_array)
 
 A_COEF, B_COEF, C_COEF = 3.4445, -4.7750, 2.0315
+
+# The training-step operators (training.py) take torch tensors; they are
+# imported when one is first used, so that the rest needs no torch.
+_TRAINING = ("ns_moe_rows", "ns_moe_sort_workspace_bytes", "ns_moe_sort", "ns_moe_dispatch", "ns_moe_dispatch_grad",
+             "ns_moe_combine", "ns_moe_combine_grad", "ns_qk_norm_rope", "ns_qk_norm_rope_grad_workspace_bytes",
+             "ns_qk_norm_rope_grad", "ns_distill_loss", "ns_distill_grad", "ns_profile_read_training")
+
+
+def __getattr__(name):
+    if name not in _TRAINING:
+        raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+    from . import training
+    globals().update({n: getattr(training, n) for n in _TRAINING})
+    return globals()[name]
 
 
 def _addr(x) -> int:

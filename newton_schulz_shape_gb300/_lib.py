@@ -32,6 +32,9 @@ NS_FP32_AUTO = 3
 NS_LAYOUT_ROW_SHARD = 0
 NS_LAYOUT_FLAT = 1
 NS_LAYOUT_TWO_STAGE = 2
+NS_DT_BF16 = 0
+NS_DT_FP16 = 1
+NS_DT_FP32 = 2
 
 _i32p = ctypes.POINTER(ctypes.c_int32)
 _i64p = ctypes.POINTER(ctypes.c_int64)
@@ -39,6 +42,8 @@ _u8p = ctypes.POINTER(ctypes.c_uint8)
 _u64p = ctypes.POINTER(ctypes.c_uint64)
 _vpp = ctypes.POINTER(ctypes.c_void_p)
 _planp = ctypes.c_void_p
+# short names for the long argument lists of the training-step operators
+_ptr, _int, _i64, _f32 = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_float
 
 _SIGS = {
     "ns_cost": (ctypes.c_int, [_i64p, ctypes.c_int, ctypes.c_int, _i64p]),
@@ -80,6 +85,26 @@ _SIGS = {
     "ns_set_gemm_cluster": (ctypes.c_int, [ctypes.c_int]),
     "ns_set_small_path": (ctypes.c_int, [ctypes.c_int]),
     "ns_set_symmetric_store": (ctypes.c_int, [ctypes.c_int]),
+    "ns_moe_rows": (_int, [_i64, _int, _int, _int, _i64, _i64p]),
+    "ns_moe_sort_workspace_bytes": (_int, [_i64, _int, _int, _u64p]),
+    "ns_moe_sort": (_int, [_ptr, _int, _i64, _int, _int, _int, _i64, _i64, _ptr, _ptr, _ptr, _ptr, _ptr,
+                           ctypes.c_uint64, _ptr]),
+    "ns_moe_dispatch": (_int, [_ptr, _i64, _int, _i64, _int, _i64, _ptr, _ptr, _i64, _ptr, _i64, _ptr]),
+    "ns_moe_dispatch_grad": (_int, [_ptr, _i64, _int, _i64, _int, _i64, _ptr, _i64, _ptr, _i64, _ptr]),
+    "ns_moe_combine": (_int, [_ptr, _i64, _int, _i64, _int, _i64, _ptr, _ptr, _i64, _ptr, _i64, _ptr]),
+    "ns_moe_combine_grad": (_int, [_ptr, _i64, _ptr, _i64, _int, _i64, _int, _i64, _ptr, _ptr, _ptr, _i64, _ptr,
+                                   _i64, _ptr, _ptr]),
+    "ns_qk_norm_rope": (_int, [_ptr, _ptr, _ptr, _ptr, _i64p, _int, _i64, _int, _int, _int, _int, _int, _ptr, _ptr,
+                               _int, _f32, _ptr, _i64, _ptr, _int, _ptr]),
+    "ns_qk_norm_rope_grad_workspace_bytes": (_int, [_int, _u64p]),
+    "ns_qk_norm_rope_grad": (_int, [_ptr, _ptr, _ptr, _ptr, _ptr, _ptr, _i64p, _int, _i64, _int, _int, _int, _int,
+                                    _int, _ptr, _ptr, _int, _ptr, _ptr, _f32, _ptr, _i64, _ptr, _int, _ptr,
+                                    ctypes.c_uint64, _ptr]),
+    "ns_distill_loss": (_int, [_ptr, _i64, _int, _i64, _i64, _ptr, _int, _ptr, _int, _int, _ptr, _ptr, _f32, _ptr,
+                               _ptr, _ptr, _i64, _ptr]),
+    "ns_distill_grad": (_int, [_ptr, _i64, _int, _i64, _i64, _ptr, _int, _ptr, _int, _int, _ptr, _ptr, _f32, _ptr,
+                               _ptr, _i64, _ptr]),
+    "ns_profile_read_training": (_int, [_int, _i64p, ctypes.POINTER(ctypes.c_double)]),
     "ns_profile_read": (ctypes.c_int, [ctypes.c_int, _i64p, ctypes.POINTER(ctypes.c_double)]),
 }
 

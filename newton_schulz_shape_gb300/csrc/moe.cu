@@ -1,0 +1,593 @@
+// Tokens sorted by expert and back: the routing between a mixture-of-experts
+// layer's tokens and its experts' rows, forward and backward.
+//
+// Slot s = t * k + j is token t's j-th choice. With e_s its expert,
+//   rank_s   = number of slots s' < s with e_s' = e_s
+//   kept     : 0 <= e_s < E and rank_s < capacity
+//   row_s    = offset[e_s] + rank_s, offset the exclusive sum of the kept
+//              counts, each rounded up to a multiple of `align`
+// and then
+//   dispatch       xs[row_s]  = x[t]             (0 in rows without a slot)
+//   its gradient   dx[t]      = sum_j dxs[row(t, j)]
+//   combine        y[t]       = sum_j w[t, j] ys[row(t, j)]
+//   its gradient   dys[row_s] = w_s dy[t], dw[t, j] = <dy[t], ys[row(t, j)]>
+// Sums are in fp32 in the order of j, so results do not depend on the launch.
+#include <algorithm>
+#include <climits>
+
+#include "elem.cuh"
+#include "launch.cuh"
+#include "orchestrate.h"
+#include "ptx.cuh"
+#include "status.h"
+
+namespace nsk {
+namespace {
+
+constexpr int MAX_EXPERTS = 1024;
+constexpr int MAX_K = 32;
+constexpr int SORT_THREADS = 512;
+constexpr int SORT_WARPS = SORT_THREADS / 32;
+constexpr int SORT_MAX_BLOCKS = 256;
+constexpr int ROW_THREADS = 256;
+
+struct SortParams {
+  const void* ids;
+  int id_bytes;
+  int slots, experts, align, capacity, rows;
+  int chunk;   // slots per block, a multiple of SORT_THREADS
+  int blocks;
+  int* row_of_slot;
+  int* slot_of_row;
+  int* counts;
+  int* offsets;
+  int* block_counts;  // [blocks][experts]
+  unsigned int* status;
+};
+
+// Expert of a slot; -1 for a slot that goes nowhere (a negative id, or one
+// past the last expert, which is refused).
+__device__ __forceinline__ int slot_expert(const SortParams& p, int s, bool* refused) {
+  const long long e = load_index(p.ids, p.id_bytes, s);
+  if (e >= p.experts) *refused = true;
+  return e >= 0 && e < p.experts ? static_cast<int>(e) : -1;
+}
+
+// Counts of one chunk's experts.
+__global__ void __launch_bounds__(SORT_THREADS) ns_moe_count_kernel(const __grid_constant__ SortParams p) {
+  extern __shared__ int sm[];
+  for (int e = threadIdx.x; e < p.experts; e += SORT_THREADS) sm[e] = 0;
+  nsptx::griddep_wait();
+  nsptx::griddep_launch_dependents();
+  __syncthreads();
+  const int s0 = blockIdx.x * p.chunk, s1 = min(p.slots, s0 + p.chunk);
+  bool refused = false;
+  for (int s = s0 + threadIdx.x; s < s1; s += SORT_THREADS) {
+    const int e = slot_expert(p, s, &refused);
+    if (e >= 0) atomicAdd(&sm[e], 1);
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < p.experts; e += SORT_THREADS) p.block_counts[blockIdx.x * p.experts + e] = sm[e];
+}
+
+// Places one chunk's slots. Warp w owns a contiguous part of the chunk; the
+// rank of a slot is (slots of its expert in earlier chunks) + (in earlier
+// warps) + (in earlier rounds of this warp) + (in lower lanes).
+__global__ void __launch_bounds__(SORT_THREADS) ns_moe_place_kernel(const __grid_constant__ SortParams p) {
+  extern __shared__ int sm[];
+  const int E = p.experts, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int* next = sm;                       // [warps][E]: count, then the next rank
+  int* before = sm + SORT_WARPS * E;    // [E]: slots in earlier chunks
+  int* total = before + E;              // [E]
+  int* offset = total + E;              // [E + 1]
+  for (int i = threadIdx.x; i < (SORT_WARPS + 2) * E; i += SORT_THREADS) sm[i] = 0;
+  nsptx::griddep_wait();
+  nsptx::griddep_launch_dependents();
+  __syncthreads();
+
+  const int per_warp = p.chunk / SORT_WARPS;
+  const int w0 = min(p.slots, static_cast<int>(blockIdx.x) * p.chunk + warp * per_warp);
+  const int w1 = min(p.slots, w0 + per_warp);
+  bool refused = false;
+  for (int s = w0 + lane; s < w1; s += 32) {
+    const int e = slot_expert(p, s, &refused);
+    if (e >= 0) atomicAdd(&next[warp * E + e], 1);
+  }
+  if (refused) atomicOr(p.status, NS_DEV_BAD_INDEX);
+  if (p.blocks > 1) {
+    for (int i = threadIdx.x; i < p.blocks * E; i += SORT_THREADS) {
+      const int b = i / E, e = i - b * E, c = p.block_counts[i];
+      if (c) {
+        atomicAdd(&total[e], c);
+        if (b < static_cast<int>(blockIdx.x)) atomicAdd(&before[e], c);
+      }
+    }
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < E; e += SORT_THREADS) {
+    int run = before[e];
+    for (int w = 0; w < SORT_WARPS; ++w) {
+      const int c = next[w * E + e];
+      next[w * E + e] = run;
+      run += c;
+    }
+    if (p.blocks == 1) total[e] = run;
+  }
+  __syncthreads();
+  if (warp == 0) {
+    // exclusive sum of the padded kept counts, a run of experts per lane
+    const int per = (E + 31) / 32, e0 = min(E, lane * per), e1 = min(E, e0 + per);
+    int mine = 0;
+    for (int e = e0; e < e1; ++e) mine += (min(total[e], p.capacity) + p.align - 1) / p.align * p.align;
+    int upto = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += v;
+    }
+    int run = upto - mine;
+    for (int e = e0; e < e1; ++e) {
+      offset[e] = run;
+      run += (min(total[e], p.capacity) + p.align - 1) / p.align * p.align;
+    }
+    if (lane == 31) offset[E] = run;
+  }
+  __syncthreads();
+
+  if (blockIdx.x == 0) {
+    for (int e = threadIdx.x; e < E; e += SORT_THREADS) p.counts[e] = min(total[e], p.capacity);
+    for (int e = threadIdx.x; e <= E; e += SORT_THREADS) p.offsets[e] = offset[e];
+  }
+  for (int i = w0; i < w1; i += 32) {
+    const int s = i + lane;
+    const int e = s < w1 ? slot_expert(p, s, &refused) : -1;
+    const unsigned peers = __match_any_sync(0xffffffffu, e);
+    if (e >= 0) {
+      const int lower = __popc(peers & ((1u << lane) - 1));
+      const int rank = next[warp * E + e] + lower;
+      int row = -1;
+      if (rank < p.capacity) {
+        row = offset[e] + rank;
+        p.slot_of_row[row] = s;
+      }
+      p.row_of_slot[s] = row;
+    } else if (s < w1) {
+      p.row_of_slot[s] = -1;
+    }
+    __syncwarp();
+    if (e >= 0 && (peers >> lane) == 1u) next[warp * E + e] += __popc(peers);  // the highest lane of its peers
+    __syncwarp();
+  }
+  // rows without a slot: the ends of the segments, and what follows the last
+  for (int e = blockIdx.x; e < E; e += p.blocks)
+    for (int r = offset[e] + min(total[e], p.capacity) + threadIdx.x; r < offset[e + 1]; r += SORT_THREADS)
+      p.slot_of_row[r] = -1;
+  for (int r = offset[E] + blockIdx.x * SORT_THREADS + threadIdx.x; r < p.rows; r += p.blocks * SORT_THREADS)
+    p.slot_of_row[r] = -1;
+}
+
+// --------------------------------------------------------- rows of tokens
+struct RowParams {
+  const void* src;          // dispatch: x; dispatch gradient, combine: rows; combine gradient: dy
+  const void* rows_in;      // combine gradient: ys
+  void* dst;
+  long long src_ld, rows_ld, dst_ld;  // elements between rows
+  const int* row_of_slot;
+  const int* slot_of_row;
+  const float* weights;     // null: 1
+  float* grad_weights;
+  long long tokens, rows, dim;
+  int k;
+  int parts;                // warps that share one token
+  long long token_warps;    // warps before the ones that clear rows without a slot
+  unsigned int* status;
+};
+
+// Row of token t's slot `lane`, -1 where there is none; a row outside the
+// buffer is refused.
+__device__ __forceinline__ int lane_row(const RowParams& p, long long t, int lane) {
+  int r = -1;
+  if (lane < p.k) r = p.row_of_slot[t * p.k + lane];
+  if (r >= p.rows) {
+    atomicOr(p.status, NS_DEV_BAD_INDEX);
+    r = -1;
+  }
+  return r;
+}
+
+// Clears those of 32 rows that hold no slot.
+template <typename T, int V>
+__device__ __forceinline__ void clear_rows(const RowParams& p, long long group, int lane) {
+  const long long r = group * 32 + lane;
+  unsigned todo = __ballot_sync(0xffffffffu, r < p.rows && p.slot_of_row[r] < 0);
+  while (todo) {
+    const int i = __ffs(todo) - 1;
+    todo &= todo - 1;
+    T* row = static_cast<T*>(p.dst) + (group * 32 + i) * p.dst_ld;
+    for (long long c = lane * V; c < p.dim; c += 32 * V) store_vec<T, V>(row + c, zero_vec<T, V>());
+  }
+}
+
+// dispatch: a warp holds up to 32 * V * U elements of a token's row and stores
+// them to each of its rows, so x is read once.
+template <typename T, int V, int U>
+__global__ void __launch_bounds__(ROW_THREADS) ns_moe_dispatch_kernel(const __grid_constant__ RowParams p) {
+  nsptx::griddep_wait();
+  nsptx::griddep_launch_dependents();
+  const int lane = threadIdx.x & 31;
+  const long long w = static_cast<long long>(blockIdx.x) * (ROW_THREADS / 32) + (threadIdx.x >> 5);
+  if (w >= p.token_warps) {
+    clear_rows<T, V>(p, w - p.token_warps, lane);
+    return;
+  }
+  const long long t = w / p.parts;
+  const long long c0 = (w - t * p.parts) * (32 * V * U) + lane * V;
+  const T* src = static_cast<const T*>(p.src) + t * p.src_ld;
+  const int mine = lane_row(p, t, lane);
+  Vec<T, V> x[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+    if (c0 + u * 32 * V < p.dim) x[u] = load_vec<T, V>(src + c0 + u * 32 * V);
+  for (int j = 0; j < p.k; ++j) {
+    const int r = __shfl_sync(0xffffffffu, mine, j);
+    if (r < 0) continue;
+    T* dst = static_cast<T*>(p.dst) + r * p.dst_ld;
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (c0 + u * 32 * V < p.dim) store_vec<T, V>(dst + c0 + u * 32 * V, x[u]);
+  }
+}
+
+// combine and the gradient of dispatch: a warp sums 32 * V * U elements of a
+// token's rows.
+template <typename T, int V, int U>
+__global__ void __launch_bounds__(ROW_THREADS) ns_moe_gather_kernel(const __grid_constant__ RowParams p) {
+  nsptx::griddep_wait();
+  nsptx::griddep_launch_dependents();
+  const int lane = threadIdx.x & 31;
+  const long long w = static_cast<long long>(blockIdx.x) * (ROW_THREADS / 32) + (threadIdx.x >> 5);
+  if (w >= p.token_warps) return;
+  const long long t = w / p.parts;
+  const long long c0 = (w - t * p.parts) * (32 * V * U) + lane * V;
+  const int mine = lane_row(p, t, lane);
+  const float my_weight = p.weights && lane < p.k ? p.weights[t * p.k + lane] : 1.0f;
+  float acc[U][V];
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+#pragma unroll
+    for (int i = 0; i < V; ++i) acc[u][i] = 0.0f;
+#pragma unroll 4
+  for (int j = 0; j < p.k; ++j) {
+    const int r = __shfl_sync(0xffffffffu, mine, j);
+    const float wt = __shfl_sync(0xffffffffu, my_weight, j);
+    if (r < 0) continue;
+    const T* src = static_cast<const T*>(p.src) + r * p.src_ld;
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (c0 + u * 32 * V < p.dim) {
+        const Vec<T, V> x = load_vec<T, V>(src + c0 + u * 32 * V);
+#pragma unroll
+        for (int i = 0; i < V; ++i) acc[u][i] = fmaf(wt, to_float(x.v[i]), acc[u][i]);
+      }
+  }
+  T* dst = static_cast<T*>(p.dst) + t * p.dst_ld;
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+    if (c0 + u * 32 * V < p.dim) {
+      Vec<T, V> y;
+#pragma unroll
+      for (int i = 0; i < V; ++i) y.v[i] = from_float<T>(acc[u][i]);
+      store_vec<T, V>(dst + c0 + u * 32 * V, y);
+    }
+}
+
+// combine's gradient: `parts` warps of one block share a token; each walks its
+// pieces of the row, writes w dy and sums dy ys, slot j's sum in lane j.
+template <typename T, int V, int U>
+__global__ void __launch_bounds__(ROW_THREADS) ns_moe_combine_grad_kernel(const __grid_constant__ RowParams p) {
+  __shared__ float part_sum[ROW_THREADS / 32][MAX_K];
+  nsptx::griddep_wait();
+  nsptx::griddep_launch_dependents();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const long long w = static_cast<long long>(blockIdx.x) * (ROW_THREADS / 32) + warp;
+  const bool on = w < p.token_warps;
+  const long long t = w / p.parts;
+  const int part = static_cast<int>(w - t * p.parts);
+  float sum = 0.0f;
+  if (on) {
+    const T* dy = static_cast<const T*>(p.src) + t * p.src_ld;
+    const int mine = lane_row(p, t, lane);
+    const float my_weight = lane < p.k ? p.weights[t * p.k + lane] : 0.0f;
+    for (long long c0 = part * (32 * V * U) + lane * V; c0 - lane * V < p.dim; c0 += p.parts * (32 * V * U)) {
+      float g[U][V];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        Vec<T, V> x = zero_vec<T, V>();
+        if (c0 + u * 32 * V < p.dim) x = load_vec<T, V>(dy + c0 + u * 32 * V);
+#pragma unroll
+        for (int i = 0; i < V; ++i) g[u][i] = to_float(x.v[i]);
+      }
+      for (int j = 0; j < p.k; ++j) {
+        const int r = __shfl_sync(0xffffffffu, mine, j);
+        const float wt = __shfl_sync(0xffffffffu, my_weight, j);
+        if (r < 0) continue;
+        const T* ys = static_cast<const T*>(p.rows_in) + r * p.rows_ld;
+        T* out = static_cast<T*>(p.dst) + r * p.dst_ld;
+        Vec<T, V> y[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          if (c0 + u * 32 * V < p.dim) y[u] = load_vec<T, V>(ys + c0 + u * 32 * V);
+        float dot = 0.0f;
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          if (c0 + u * 32 * V < p.dim) {
+            Vec<T, V> o;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+              dot = fmaf(g[u][i], to_float(y[u].v[i]), dot);
+              o.v[i] = from_float<T>(wt * g[u][i]);
+            }
+            store_vec<T, V>(out + c0 + u * 32 * V, o);
+          }
+        dot = warp_sum(dot);
+        if (lane == j) sum += dot;
+      }
+    }
+    if (p.parts == 1 && lane < p.k) p.grad_weights[t * p.k + lane] = sum;
+  } else {
+    clear_rows<T, V>(p, w - p.token_warps, lane);
+  }
+  if (p.parts == 1) return;
+  part_sum[warp][lane] = sum;
+  __syncthreads();
+  if (on && part == 0 && lane < p.k) {
+    for (int q = 1; q < p.parts; ++q) sum += part_sum[warp + q][lane];
+    p.grad_weights[t * p.k + lane] = sum;
+  }
+}
+
+}  // namespace
+}  // namespace nsk
+
+using namespace nsorch;
+
+namespace {
+
+int elem_bytes(int dtype) { return dtype == NS_DT_FP32 ? 4 : 2; }
+bool dtype_ok(int dtype) { return dtype == NS_DT_BF16 || dtype == NS_DT_FP16 || dtype == NS_DT_FP32; }
+bool aligned16(const void* p, long long ld, int bytes) {
+  return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && ld * bytes % 16 == 0;
+}
+
+// Slots per block and blocks of a sort.
+void sort_split(long long slots, int* chunk, int* blocks) {
+  long long c = (slots + nsk::SORT_MAX_BLOCKS - 1) / nsk::SORT_MAX_BLOCKS;
+  c = std::max<long long>(c, 2048);
+  c = (c + nsk::SORT_THREADS - 1) / nsk::SORT_THREADS * nsk::SORT_THREADS;
+  *chunk = static_cast<int>(c);
+  *blocks = static_cast<int>(std::max<long long>(1, (slots + c - 1) / c));
+}
+
+int sort_args(int64_t tokens, int k, int experts) {
+  if (tokens < 0 || k < 1 || experts < 1) return NS_ERR_ARG;
+  if (k > nsk::MAX_K || experts > nsk::MAX_EXPERTS) return NS_ERR_UNSUPPORTED;
+  if (tokens > (INT_MAX - 4096) / k) return NS_ERR_SHAPE;
+  return NS_OK;
+}
+
+// Checks shared by the four row operators.
+int row_args(int dtype, int64_t tokens, int k, int64_t dim, int64_t rows) {
+  if (!dtype_ok(dtype) || tokens < 0 || k < 1 || dim < 0 || rows < 0) return NS_ERR_ARG;
+  if (k > nsk::MAX_K) return NS_ERR_UNSUPPORTED;
+  if (tokens > (INT_MAX - 4096) / k || rows > INT_MAX) return NS_ERR_SHAPE;
+  return NS_OK;
+}
+
+enum RowOp { DISPATCH, GATHER, COMBINE_GRAD };
+
+template <typename T, int V, int U>
+cudaError_t launch_rows(RowOp op, nsk::RowParams& p, cudaStream_t st) {
+  using namespace nsk;
+  const int warps = ROW_THREADS / 32;
+  const long long pieces = (p.dim + 32 * V * U - 1) / (32 * V * U);
+  if (op == COMBINE_GRAD) {
+    // a token's warps sit in one block; few tokens are shared by more warps
+    p.parts = 1;
+    while (p.parts < warps && p.parts < pieces && p.tokens * p.parts < 152 * 16) p.parts *= 2;
+  } else {
+    p.parts = static_cast<int>(pieces);
+  }
+  p.token_warps = p.tokens * p.parts;
+  const long long all = p.token_warps + (op == GATHER ? 0 : (p.rows + 31) / 32);
+  const long long blocks = (all + warps - 1) / warps;
+  if (blocks > INT_MAX) return cudaErrorInvalidValue;
+  const dim3 grid(static_cast<unsigned>(blocks)), block(ROW_THREADS);
+  if (op == DISPATCH) return launch_pdl(ns_moe_dispatch_kernel<T, V, U>, grid, block, 0, st, p);
+  if (op == GATHER) return launch_pdl(ns_moe_gather_kernel<T, V, U>, grid, block, 0, st, p);
+  return launch_pdl(ns_moe_combine_grad_kernel<T, V, U>, grid, block, 0, st, p);
+}
+
+template <typename T>
+cudaError_t launch_rows_of(RowOp op, bool wide, nsk::RowParams& p, cudaStream_t st) {
+  constexpr int V = 16 / sizeof(T);
+  if (op == GATHER) return wide ? launch_rows<T, V, 2>(op, p, st) : launch_rows<T, 1, 8>(op, p, st);
+  return wide ? launch_rows<T, V, 8>(op, p, st) : launch_rows<T, 1, 8>(op, p, st);
+}
+
+int run_rows(RowOp op, int dtype, nsk::RowParams& p, bool wide, void* stream) {
+  int dev, nsm;
+  const int rc = device_setup(&dev, &p.status, &nsm);
+  if (rc != NS_OK) return rc;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = counted(K_MOE, st, [&] {
+    if (dtype == NS_DT_BF16) return launch_rows_of<__nv_bfloat16>(op, wide, p, st);
+    if (dtype == NS_DT_FP16) return launch_rows_of<__half>(op, wide, p, st);
+    return launch_rows_of<float>(op, wide, p, st);
+  });
+  return e == cudaSuccess ? NS_OK : NS_ERR_CUDA;
+}
+
+}  // namespace
+
+extern "C" {
+
+int ns_moe_rows(int64_t tokens, int k, int experts, int align, int64_t capacity, int64_t* rows_out) {
+  if (!rows_out || align < 1 || capacity < 0) return NS_ERR_ARG;
+  const int rc = sort_args(tokens, k, experts);
+  if (rc != NS_OK) return rc;
+  const int64_t slots = tokens * k;
+  int64_t rows = slots + std::min<int64_t>(experts, slots) * (align - 1);
+  if (capacity > 0) {
+    const int64_t cap = std::min(capacity, slots);
+    rows = std::min(rows, experts * ((cap + align - 1) / align * align));
+  }
+  if (rows > INT_MAX) return NS_ERR_SHAPE;
+  *rows_out = rows;
+  return NS_OK;
+}
+
+int ns_moe_sort_workspace_bytes(int64_t tokens, int k, int experts, uint64_t* bytes) {
+  if (!bytes) return NS_ERR_ARG;
+  const int rc = sort_args(tokens, k, experts);
+  if (rc != NS_OK) return rc;
+  int chunk, blocks;
+  sort_split(tokens * k, &chunk, &blocks);
+  *bytes = blocks > 1 ? static_cast<uint64_t>(blocks) * experts * sizeof(int) : 0;
+  return NS_OK;
+}
+
+int ns_moe_sort(const void* expert_ids, int id_bytes, int64_t tokens, int k, int experts, int align,
+                int64_t capacity, int64_t rows, int32_t* row_of_slot, int32_t* slot_of_row, int32_t* counts,
+                int32_t* offsets, void* workspace, uint64_t workspace_bytes, void* stream) {
+  int64_t need_rows = 0;
+  int rc = ns_moe_rows(tokens, k, experts, align, capacity, &need_rows);
+  if (rc != NS_OK) return rc;
+  if (id_bytes != 4 && id_bytes != 8) return NS_ERR_ARG;
+  if (rows < need_rows || rows > INT_MAX) return NS_ERR_SHAPE;
+  if (!counts || !offsets || (tokens > 0 && (!expert_ids || !row_of_slot)) || (rows > 0 && !slot_of_row))
+    return NS_ERR_ARG;
+  nsk::SortParams p = {};
+  p.ids = expert_ids;
+  p.id_bytes = id_bytes;
+  p.slots = static_cast<int>(tokens * k);
+  p.experts = experts;
+  p.align = align;
+  p.capacity = capacity > 0 && capacity < INT_MAX ? static_cast<int>(capacity) : INT_MAX;
+  p.rows = static_cast<int>(rows);
+  sort_split(p.slots, &p.chunk, &p.blocks);
+  const uint64_t need = p.blocks > 1 ? static_cast<uint64_t>(p.blocks) * experts * sizeof(int) : 0;
+  if (need && (!workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255)))
+    return NS_ERR_WORKSPACE;
+  p.row_of_slot = row_of_slot;
+  p.slot_of_row = slot_of_row;
+  p.counts = counts;
+  p.offsets = offsets;
+  p.block_counts = static_cast<int*>(workspace);
+  int dev, nsm;
+  rc = device_setup(&dev, &p.status, &nsm);
+  if (rc != NS_OK) return rc;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (p.blocks > 1) {
+    const cudaError_t e = counted(K_MOE, st, [&] {
+      return nsk::launch_pdl(nsk::ns_moe_count_kernel, dim3(p.blocks), dim3(nsk::SORT_THREADS),
+                             experts * sizeof(int), st, p);
+    });
+    if (e != cudaSuccess) return NS_ERR_CUDA;
+  }
+  const size_t smem = (static_cast<size_t>(nsk::SORT_WARPS + 3) * experts + 1) * sizeof(int);
+  if (smem > 48 * 1024 && cudaFuncSetAttribute(nsk::ns_moe_place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               static_cast<int>(smem)) != cudaSuccess)
+    return NS_ERR_CUDA;
+  const cudaError_t e = counted(K_MOE, st, [&] {
+    return nsk::launch_pdl(nsk::ns_moe_place_kernel, dim3(p.blocks), dim3(nsk::SORT_THREADS), smem, st, p);
+  });
+  return e == cudaSuccess ? NS_OK : NS_ERR_CUDA;
+}
+
+int ns_moe_dispatch(const void* x, int64_t x_stride, int dtype, int64_t tokens, int k, int64_t dim,
+                    const int32_t* row_of_slot, const int32_t* slot_of_row, int64_t rows, void* out,
+                    int64_t out_stride, void* stream) {
+  const int rc = row_args(dtype, tokens, k, dim, rows);
+  if (rc != NS_OK) return rc;
+  if (x_stride < dim || out_stride < dim) return NS_ERR_SHAPE;
+  if (rows == 0 || dim == 0) return NS_OK;
+  if (!out || !slot_of_row || (tokens > 0 && (!x || !row_of_slot))) return NS_ERR_ARG;
+  nsk::RowParams p = {};
+  p.src = x;
+  p.src_ld = x_stride;
+  p.dst = out;
+  p.dst_ld = out_stride;
+  p.row_of_slot = row_of_slot;
+  p.slot_of_row = slot_of_row;
+  p.tokens = tokens;
+  p.rows = rows;
+  p.dim = dim;
+  p.k = k;
+  const int b = elem_bytes(dtype);
+  const bool wide = dim * b % 16 == 0 && aligned16(x, x_stride, b) && aligned16(out, out_stride, b);
+  return run_rows(DISPATCH, dtype, p, wide, stream);
+}
+
+int ns_moe_combine(const void* expert_rows, int64_t rows_stride, int dtype, int64_t tokens, int k, int64_t dim,
+                   const int32_t* row_of_slot, const float* weights, int64_t rows, void* y, int64_t y_stride,
+                   void* stream) {
+  const int rc = row_args(dtype, tokens, k, dim, rows);
+  if (rc != NS_OK) return rc;
+  if (rows_stride < dim || y_stride < dim) return NS_ERR_SHAPE;
+  if (tokens == 0 || dim == 0) return NS_OK;
+  if (!y || !row_of_slot || (rows > 0 && !expert_rows)) return NS_ERR_ARG;
+  nsk::RowParams p = {};
+  p.src = expert_rows;
+  p.src_ld = rows_stride;
+  p.dst = y;
+  p.dst_ld = y_stride;
+  p.row_of_slot = row_of_slot;
+  p.weights = weights;
+  p.tokens = tokens;
+  p.rows = rows;
+  p.dim = dim;
+  p.k = k;
+  const int b = elem_bytes(dtype);
+  const bool wide = dim * b % 16 == 0 && aligned16(expert_rows, rows_stride, b) && aligned16(y, y_stride, b);
+  return run_rows(GATHER, dtype, p, wide, stream);
+}
+
+int ns_moe_dispatch_grad(const void* grad_rows, int64_t rows_stride, int dtype, int64_t tokens, int k, int64_t dim,
+                         const int32_t* row_of_slot, int64_t rows, void* grad_x, int64_t grad_x_stride,
+                         void* stream) {
+  return ns_moe_combine(grad_rows, rows_stride, dtype, tokens, k, dim, row_of_slot, nullptr, rows, grad_x,
+                        grad_x_stride, stream);
+}
+
+int ns_moe_combine_grad(const void* grad_y, int64_t grad_y_stride, const void* expert_rows, int64_t rows_stride,
+                        int dtype, int64_t tokens, int k, int64_t dim, const int32_t* row_of_slot,
+                        const int32_t* slot_of_row, const float* weights, int64_t rows, void* grad_rows,
+                        int64_t grad_rows_stride, float* grad_weights, void* stream) {
+  const int rc = row_args(dtype, tokens, k, dim, rows);
+  if (rc != NS_OK) return rc;
+  if (grad_y_stride < dim || rows_stride < dim || grad_rows_stride < dim) return NS_ERR_SHAPE;
+  if (tokens == 0 && rows == 0) return NS_OK;
+  if (tokens > 0 && (!row_of_slot || !weights || !grad_weights || (dim > 0 && !grad_y))) return NS_ERR_ARG;
+  if (rows > 0 && (!slot_of_row || (dim > 0 && (!expert_rows || !grad_rows)))) return NS_ERR_ARG;
+  nsk::RowParams p = {};
+  p.src = grad_y;
+  p.src_ld = grad_y_stride;
+  p.rows_in = expert_rows;
+  p.rows_ld = rows_stride;
+  p.dst = grad_rows;
+  p.dst_ld = grad_rows_stride;
+  p.row_of_slot = row_of_slot;
+  p.slot_of_row = slot_of_row;
+  p.weights = weights;
+  p.grad_weights = grad_weights;
+  p.tokens = tokens;
+  p.rows = rows;
+  p.dim = dim;
+  p.k = k;
+  const int b = elem_bytes(dtype);
+  const bool wide = dim * b % 16 == 0 && aligned16(grad_y, grad_y_stride, b) &&
+                    aligned16(expert_rows, rows_stride, b) && aligned16(grad_rows, grad_rows_stride, b);
+  return run_rows(COMBINE_GRAD, dtype, p, wide, stream);
+}
+
+}  // extern "C"

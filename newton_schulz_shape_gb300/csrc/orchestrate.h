@@ -47,8 +47,10 @@ int make_map(CUtensorMap* m, void* base, uint64_t inner, uint64_t outer, uint64_
 int make_epi_map(CUtensorMap* m, void* base, uint64_t inner, uint64_t outer, uint64_t count);
 
 // Launch kinds of ns_profile_read.
-constexpr int kKinds = 7;
-enum { K_GRAM = 0, K_A2B = 1, K_BX = 2, K_PRO = 3, K_PACK = 4, K_BX_FINAL = 5, K_SMALL = 6 };
+// ns_profile_read reports the first kNsKinds, ns_profile_read_training the rest.
+constexpr int kNsKinds = 7, kKinds = 10;
+enum { K_GRAM = 0, K_A2B = 1, K_BX = 2, K_PRO = 3, K_PACK = 4, K_BX_FINAL = 5, K_SMALL = 6,
+       K_MOE = 7, K_QK = 8, K_DISTILL = 9 };
 // Count a launch of `kind`; when timing is on, hand out two events for it.
 bool prof_begin(int kind, cudaEvent_t* a, cudaEvent_t* b);
 // Queue the bracketing events of a timed launch for ns_profile_read.

@@ -74,6 +74,36 @@ void prof_end(int kind, cudaEvent_t a, cudaEvent_t b) {
   g_pending.push_back({a, b, kind});
 }
 
+namespace {
+
+// Settle the timed launches, then report (and on reset clear) the kinds
+// [first, last).
+int profile_read(int first, int last, int reset, int64_t* launches, double* gpu_ms) {
+  std::lock_guard<std::mutex> lk(g_prof_mu);
+  int rc = NS_OK;
+  for (const PendingTiming& t : g_pending) {
+    float ms = 0.0f;
+    if (cudaEventSynchronize(t.b) != cudaSuccess || cudaEventElapsedTime(&ms, t.a, t.b) != cudaSuccess)
+      rc = NS_ERR_CUDA;
+    else
+      g_ms[t.kind] += ms;
+    g_free_events.push_back(t.a);
+    g_free_events.push_back(t.b);
+  }
+  g_pending.clear();
+  for (int k = first; k < last; ++k) {
+    if (launches) launches[k - first] = g_launches[k];
+    if (gpu_ms) gpu_ms[k - first] = g_ms[k];
+    if (reset) {
+      g_launches[k] = 0;
+      g_ms[k] = 0.0;
+    }
+  }
+  return rc;
+}
+
+}  // namespace
+
 unsigned long long take_gemm_stall() { return g_stall_next.exchange(0); }
 
 bool small_path_enabled() { return g_small_path.load() != 0; }
@@ -198,27 +228,11 @@ int ns_profile_enable(int enable) {
 }
 
 int ns_profile_read(int reset, int64_t* launches, double* gpu_ms) {
-  std::lock_guard<std::mutex> lk(g_prof_mu);
-  int rc = NS_OK;
-  for (const PendingTiming& t : g_pending) {
-    float ms = 0.0f;
-    if (cudaEventSynchronize(t.b) != cudaSuccess || cudaEventElapsedTime(&ms, t.a, t.b) != cudaSuccess)
-      rc = NS_ERR_CUDA;
-    else
-      g_ms[t.kind] += ms;
-    g_free_events.push_back(t.a);
-    g_free_events.push_back(t.b);
-  }
-  g_pending.clear();
-  for (int k = 0; k < kKinds; ++k) {
-    if (launches) launches[k] = g_launches[k];
-    if (gpu_ms) gpu_ms[k] = g_ms[k];
-    if (reset) {
-      g_launches[k] = 0;
-      g_ms[k] = 0.0;
-    }
-  }
-  return rc;
+  return profile_read(0, kNsKinds, reset, launches, gpu_ms);
+}
+
+int ns_profile_read_training(int reset, int64_t* launches, double* gpu_ms) {
+  return profile_read(kNsKinds, kKinds, reset, launches, gpu_ms);
 }
 
 }  // extern "C"
