@@ -28,6 +28,7 @@ namespace {
 constexpr int DISTILL_THREADS = 512;
 constexpr int DISTILL_WARPS = DISTILL_THREADS / 32;
 constexpr int DISTILL_MAX_TOP = 1024;
+constexpr int DISTILL_MAX_CLUSTER = 8;  // the portable limit
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 
 struct DistillParams {
@@ -45,6 +46,9 @@ struct DistillParams {
   float inv_tau;
   float* loss;          // null: the log-sum-exp is given
   float* lse;
+  int places;           // of the hash table of the teacher's ids
+  int cluster;          // blocks that share a token
+  int slice_words;      // most words of 16 bytes of a block
   unsigned int* status;
 };
 
@@ -75,16 +79,360 @@ __device__ __forceinline__ long long head_of(const T* p, long long n) {
   return h < n ? h : n;
 }
 
-// One block takes one token: the teacher's entries into shared memory, one
-// pass over the logits for the log-sum-exp, and one for the gradient.
+// Places of the hash table of `top` ids: a power of two, twice the ids or more.
+__host__ __device__ inline int table_size(int top) {
+  int n = 4;
+  while (n < 2 * top) n *= 2;
+  return n;
+}
+
+// The teacher's entries of a token, in shared memory.
+struct Teacher {
+  float* p;    // [top] probability
+  float* s;    // [top] the student's logit at the entry
+  int* id;     // [top] the entry, -1 if left out
+  int* table;  // hash table of the ids; bit 31 marks one that is named more than once
+  float* sums; // [2] sum of the probabilities, sum of p (log p - s / tau)
+  int* any;    // whether an entry is left
+  __device__ __forceinline__ Teacher(void* at, int top, int places)
+      : p(static_cast<float*>(at)), s(p + top), id(reinterpret_cast<int*>(s + top)), table(id + top),
+        sums(reinterpret_cast<float*>(table + places)), any(reinterpret_cast<int*>(sums + 2)) {}
+};
+size_t teacher_bytes(int top) { return sizeof(float) * (3 * static_cast<size_t>(top) + table_size(top) + 4); }
+
+constexpr int NO_ID = 0x7fffffff;  // an empty place; ids are below it
+
+__device__ __forceinline__ int table_place(int id, int mask) {
+  return static_cast<int>(static_cast<unsigned>(id) * 2654435761u >> 16) & mask;
+}
+
+// Loads the entries with `n` threads, 4 at a time each so that their latencies
+// overlap; whether this thread left any in.
 template <typename T>
-__global__ void __launch_bounds__(DISTILL_THREADS) ns_distill_kernel(const __grid_constant__ DistillParams p) {
+__device__ __forceinline__ bool load_teacher(const DistillParams& p, const Teacher& te, long long t, const T* row,
+                                             float weight, int first, int n) {
+  constexpr int B = 4;
+  bool refused = false, some = false;
+  for (int j0 = first; j0 < p.top; j0 += B * n) {
+    long long id[B];
+    float z[B], s[B];
+#pragma unroll
+    for (int b = 0; b < B; ++b) {
+      const int j = j0 + b * n;
+      const long long i = t * p.top + j;
+      id[b] = -1;
+      z[b] = -INFINITY;
+      if (j < p.top && weight != 0.0f) {
+        id[b] = load_index(p.ids, p.id_bytes, i);
+        z[b] = p.teacher_dtype == NS_DT_FP32   ? static_cast<const float*>(p.teacher)[i]
+               : p.teacher_dtype == NS_DT_BF16 ? to_float(static_cast<const __nv_bfloat16*>(p.teacher)[i])
+                                               : to_float(static_cast<const __half*>(p.teacher)[i]);
+      }
+    }
+#pragma unroll
+    for (int b = 0; b < B; ++b) {
+      refused |= id[b] >= p.vocab;
+      // NaN stays in: it shows in the outputs
+      if (id[b] < 0 || id[b] >= p.vocab || z[b] == -INFINITY) id[b] = -1;
+      some |= id[b] >= 0;
+      s[b] = id[b] >= 0 ? to_float(row[id[b]]) : 0.0f;
+    }
+#pragma unroll
+    for (int b = 0; b < B; ++b) {
+      const int j = j0 + b * n;
+      if (j < p.top) {
+        te.id[j] = static_cast<int>(id[b]);
+        te.p[j] = id[b] >= 0 ? z[b] : -INFINITY;
+        te.s[j] = s[b];
+      }
+    }
+  }
+  if (refused) atomicOr(p.status, NS_DEV_BAD_INDEX);
+  return some;
+}
+
+// Enters the ids in the hash table, by one warp.
+__device__ __forceinline__ void mark_repeated(const Teacher& te, int top, int mask, int lane) {
+  for (int i = lane; i <= mask; i += 32) te.table[i] = NO_ID;
+  __syncwarp();
+  for (int j = lane; j < top; j += 32) {
+    const int id = te.id[j];
+    if (id < 0) continue;
+    for (int h = table_place(id, mask);; h = (h + 1) & mask) {  // ends: at least half of the places stay empty
+      const int old = atomicCAS(&te.table[h], NO_ID, id);
+      if (old == NO_ID) break;
+      if ((old & 0x7fffffff) == id) {
+        atomicOr(&te.table[h], 0x80000000);
+        break;
+      }
+    }
+  }
+}
+
+// Probabilities and their sums, by one warp; visible to the block after its
+// next barrier.
+__device__ __forceinline__ void teacher_probabilities(const DistillParams& p, const Teacher& te, long long t, int lane) {
+  // log-sum-exp of the entries left, relative to their maximum so that values
+  // near the type's lowest stay finite, unless the teacher's own is given
+  float z0 = 0.0f, zlog;
+  if (p.teacher_lse) {
+    zlog = p.teacher_lse[t];
+  } else {
+    z0 = -INFINITY;
+    for (int j = lane; j < p.top; j += 32) z0 = fmaxf(z0, te.p[j]);
+    z0 = warp_max(z0);
+    float sum = 0.0f;
+    for (int j = lane; j < p.top; j += 32) sum += te.id[j] >= 0 ? expf((te.p[j] - z0) * p.inv_tau) : 0.0f;
+    zlog = logf(warp_sum(sum));
+  }
+  float mass = 0.0f, part = 0.0f;
+  for (int j = lane; j < p.top; j += 32) {
+    const float logp = (te.p[j] - z0) * p.inv_tau - zlog;
+    const float pr = te.id[j] >= 0 ? expf(logp) : 0.0f;
+    if (pr != 0.0f) part += pr * (logp - te.s[j] * p.inv_tau);
+    mass += pr;
+    te.p[j] = pr;
+  }
+  mass = warp_sum(mass);
+  part = warp_sum(part);
+  if (lane == 0) {
+    te.sums[0] = mass;
+    te.sums[1] = part;
+  }
+}
+
+// The elements of a row that a block writes: its words, and for one block those
+// before and after all words.
+struct Slice {
+  long long first, last;     // this block's words
+  long long body, body_end;  // all blocks' words
+  bool edges;
+  __device__ __forceinline__ bool has(long long v) const {
+    return (v >= first && v < last) || (edges && (v < body || v >= body_end));
+  }
+};
+
+// Gradient of the teacher's entries in the slice, each with every probability
+// that names it; once the rest of the slice is written.
+template <typename T>
+__device__ __forceinline__ void write_entries(const DistillParams& p, const Teacher& te, const Slice& slice, T* grad,
+                                              float c, float lse2, float scale, int start, int n) {
+  const int mask = p.places - 1;
+  for (int j = start; j < p.top; j += n) {
+    const int id = te.id[j];
+    if (id < 0 || !slice.has(id)) continue;
+    int h = table_place(id, mask);
+    while ((te.table[h] & 0x7fffffff) != id) h = (h + 1) & mask;
+    float sum = te.p[j];
+    if (te.table[h] < 0) {
+      sum = 0.0f;
+      for (int i = 0; i < p.top; ++i) sum += te.id[i] == id ? te.p[i] : 0.0f;
+    }
+    grad[id] = from_float<T>(scale * te.sums[0] * exp2_fast(fmaf(te.s[j], c, -lse2)) - scale * sum);
+  }
+}
+
+// The maximum and sum of a warp's threads, in all of them.
+__device__ __forceinline__ Online join_warp(Online o) {
+  // one rescaling to the warp's maximum, then plain sums
+  const float m = warp_max(o.m);
+  o.s = m == -INFINITY ? o.s : o.s * exp2_fast(o.m - m);
+  o.m = m;
+  o.s = warp_sum(o.s);
+  return o;
+}
+
+// log2 of the sum over all parts of a token, in every lane.
+template <int WARPS>
+__device__ __forceinline__ float join_parts(const float2* parts, int C, int lane) {
+  Online o;
+  for (int i = lane; i < C * WARPS; i += 32) o.join(parts[i].x, parts[i].y);
+  o = join_warp(o);
+  return o.m + log2f(o.s);
+}
+
+// A cluster of blocks takes one token. NT threads of a block copy its logits to
+// shared memory, each the words that it will use itself, and use them twice
+// there, for the log-sum-exp and for the gradient, so that each is read once;
+// one more warp sees to the teacher's entries meanwhile. Every warp writes its
+// maximum and sum to all blocks of the cluster through distributed shared
+// memory, so that one barrier joins them. The copies of a block are all in
+// flight at once, and the blocks that share an SM overlap their phases: with
+// slices of 64 KB there are three of them.
+// Bound by memory: 4096 rows of 131072 bf16, loss and gradient, 362 us, 5.9 TB/s
+// (0.89 of the measured copy). Two passes of one block a row took 564 us (the
+// second read came from L2, but the phases of a row did not overlap), slices
+// kept in registers 453 us (two blocks an SM at 56 registers).
+template <typename T, int NT>
+__global__ void __launch_bounds__(NT + 32) ns_distill_kernel(const __grid_constant__ DistillParams p) {
+  constexpr int V = 16 / sizeof(T), WARPS = NT / 32, B = 4;  // B words at a time
+  extern __shared__ uint4 slice_smem[];
+  const Teacher te(slice_smem + p.slice_words, p.top, p.places);
+  __shared__ float2 parts[DISTILL_MAX_CLUSTER * WARPS];
+  nsptx::griddep_wait();
+  nsptx::griddep_launch_dependents();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int C = p.cluster, rank = C > 1 ? static_cast<int>(nsptx::cluster_ctarank()) : 0;
+  const bool joins = C > 1 && p.loss;  // blocks that write each other's shared memory: all have to run by then
+  if (joins) nsptx::cluster_arrive_relaxed();
+  const long long t = blockIdx.x / C;
+  const T* row = static_cast<const T*>(p.logits) + t * p.logits_ld;
+  T* grad = static_cast<T*>(p.grad) + t * p.grad_ld;
+  const float weight = p.weights ? p.weights[t] : 1.0f;
+  const float c = p.inv_tau * LOG2E;  // logits to powers of two
+  const int vocab = static_cast<int>(p.vocab);
+  const int head = static_cast<int>(head_of(row, p.vocab)), words = (vocab - head) / V, tail = head + words * V;
+  const int per = (words + C - 1) / C, w0 = min(words, rank * per), n = min(words, w0 + per) - w0;
+  const int edge = tid < head ? tid : tail + tid - head;  // the elements around the words, rank 0's
+  const bool has_edge = rank == 0 && edge < vocab && (tid < head || edge >= tail);
+
+  if (warp == WARPS) {
+    const bool some = load_teacher(p, te, t, row, weight, lane, 32);
+    const int any = __any_sync(0xffffffffu, some);
+    __syncwarp();
+    if (any) {
+      teacher_probabilities(p, te, t, lane);
+      if (p.grad) mark_repeated(te, p.top, p.places - 1, lane);
+    }
+    if (lane == 0) *te.any = any;
+    if (joins) {
+      nsptx::cluster_wait();
+      nsptx::cluster_sync_all();
+    } else {
+      __syncthreads();
+    }
+    if (!any) {
+      if (p.loss && rank == 0 && lane == 0) {
+        p.loss[t] = 0.0f;
+        p.lse[t] = 0.0f;
+      }
+      return;
+    }
+    float lse2;
+    if (p.loss) {
+      lse2 = join_parts<WARPS>(parts, C, lane);
+      if (rank == 0 && lane == 0) {
+        p.loss[t] = weight * (te.sums[1] + te.sums[0] * (lse2 * LN2));
+        p.lse[t] = lse2 * LN2;
+      }
+    } else {
+      lse2 = p.lse[t] * LOG2E;
+    }
+    if (!p.grad) return;
+    __syncthreads();  // the plain part of the gradient is written
+    const int first = head + w0 * V;
+    const Slice slice = {first, first + n * V, head, tail, rank == 0};
+    write_entries<T>(p, te, slice, grad, c, lse2, weight * p.inv_tau, lane, 32);
+    return;
+  }
+
+  float ex = -INFINITY;
+  const T* body = row + head + static_cast<long long>(w0) * V;
+  uint4* mine = slice_smem + tid;
+  const int rounds = (n + NT - 1) / NT, quarter = (rounds + 4 * B - 1) / (4 * B) * B;  // words a thread; in a copy group
+  if (weight != 0.0f) {
+    for (int g = 0; g < 4; ++g) {
+      for (int u = g * quarter; u < min(rounds, (g + 1) * quarter); ++u)
+        if (u * NT + tid < n) nsptx::cp_async16(mine + u * NT, body + (u * NT + tid) * V);
+      nsptx::cp_async_commit();
+    }
+    if (has_edge) ex = to_float(row[edge]);
+  }
+  auto word = [&](int u) {
+    return u * NT + tid < n ? *reinterpret_cast<const Vec<T, V>*>(mine + u * NT) : fill_vec<T, V>(-INFINITY);
+  };
+  const float2 c2 = make_float2(c, c);
+  float lse2 = 0.0f;
+  if (p.loss) {
+    Online o;
+    if (weight != 0.0f) {
+      o.m = ex * c;
+      o.s = o.m == -INFINITY ? 0.0f : exp2_fast(o.m - o.m);
+      for (int g = 0; g < 4; ++g) {
+        if (g == 0) nsptx::cp_async_wait<3>();
+        if (g == 1) nsptx::cp_async_wait<2>();
+        if (g == 2) nsptx::cp_async_wait<1>();
+        if (g == 3) nsptx::cp_async_wait<0>();
+        for (int u = g * quarter; u < min(rounds, (g + 1) * quarter); u += B) {
+          Vec<T, V> x[B];
+#pragma unroll
+          for (int i = 0; i < B; ++i) x[i] = word(u + i);
+          const float m = max_of(max_vec(max_vec(x[0], x[1]), max_vec(x[2], x[3]))) * c;
+          const float top = fmaxf(o.m, m), base = top == -INFINITY ? 0.0f : top;
+          const float2 b2 = make_float2(-base, -base);
+          float2 sum = make_float2(o.s * exp2_fast(o.m - base), 0.0f);
+#pragma unroll
+          for (int i = 0; i < B; ++i)
+#pragma unroll
+            for (int k = 0; k < V; k += 2) {
+              const float2 a = fma2(make_float2(get(x[i], k), get(x[i], k + 1)), c2, b2);
+              sum = add2(sum, make_float2(exp2_fast(a.x), exp2_fast(a.y)));
+            }
+          o.m = top;
+          o.s = sum.x + sum.y;
+        }
+      }
+    }
+    o = join_warp(o);
+    if (joins) nsptx::cluster_wait();
+    if (C == 1) {
+      if (lane == 0) parts[warp] = make_float2(o.m, o.s);
+    } else if (lane < C) {
+      const uint32_t to = nsptx::map_to_rank(&parts[rank * WARPS + warp], lane);
+      asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(to), "f"(o.m), "f"(o.s) : "memory");
+    }
+    if (joins)
+      nsptx::cluster_sync_all();
+    else
+      __syncthreads();
+    lse2 = join_parts<WARPS>(parts, C, lane);
+  } else {
+    nsptx::cp_async_wait<0>();
+    __syncthreads();
+    lse2 = p.lse[t] * LOG2E;
+  }
+  if (!p.grad) return;
+
+  const bool same = ((reinterpret_cast<uintptr_t>(row) ^ reinterpret_cast<uintptr_t>(grad)) & 15) == 0;
+  T* out = grad + head + static_cast<long long>(w0) * V + tid * V;
+  const bool any = *te.any;  // if no entry is left: zeros, whatever the logits hold
+  const float mass = any ? weight * p.inv_tau * te.sums[0] : 0.0f;
+  const float2 b2 = make_float2(-lse2, -lse2), m2 = make_float2(mass, mass);
+  for (int u = 0; u < rounds; u += B) {
+    Vec<T, V> x[B];
+#pragma unroll
+    for (int i = 0; i < B; ++i) x[i] = word(u + i);
+#pragma unroll
+    for (int i = 0; i < B; ++i) {
+      if ((u + i) * NT + tid >= n) break;
+      float y[V];
+#pragma unroll
+      for (int k = 0; k < V; k += 2) {
+        const float2 a = fma2(make_float2(get(x[i], k), get(x[i], k + 1)), c2, b2);
+        const float2 b = mul2(m2, make_float2(exp2_fast(a.x), exp2_fast(a.y)));
+        y[k] = any ? b.x : 0.0f;
+        y[k + 1] = any ? b.y : 0.0f;
+      }
+      if (same) {
+        store_once(out + (u + i) * NT * V, pack<T, V>(y));
+      } else {
+#pragma unroll
+        for (int k = 0; k < V; ++k) out[(u + i) * NT * V + k] = from_float<T>(y[k]);
+      }
+    }
+  }
+  if (has_edge) grad[edge] = from_float<T>(any ? mass * exp2_fast(fmaf(ex, c, -lse2)) : 0.0f);
+  if (any) __syncthreads();
+}
+
+// Rows too long for the registers of a cluster: one block takes one token in
+// two passes over its logits.
+template <typename T>
+__global__ void __launch_bounds__(DISTILL_THREADS) ns_distill_long_kernel(const __grid_constant__ DistillParams p) {
   constexpr int V = 16 / sizeof(T);
-  __shared__ float tp[DISTILL_MAX_TOP];      // p_j
-  __shared__ float ts[DISTILL_MAX_TOP];      // the student's logit at the entry
-  __shared__ int ti[DISTILL_MAX_TOP];        // the entry, -1 if left out
-  __shared__ float red_m[DISTILL_WARPS], red_s[DISTILL_WARPS];
-  __shared__ float sh_mass, sh_lse2;
+  extern __shared__ uint4 slice_smem[];
+  const Teacher te(slice_smem, p.top, p.places);
+  __shared__ float2 parts[DISTILL_WARPS];
   nsptx::griddep_wait();
   nsptx::griddep_launch_dependents();
   const long long t = blockIdx.x;
@@ -92,105 +440,49 @@ __global__ void __launch_bounds__(DISTILL_THREADS) ns_distill_kernel(const __gri
   const T* row = static_cast<const T*>(p.logits) + t * p.logits_ld;
   T* grad = static_cast<T*>(p.grad) + t * p.grad_ld;
   const float weight = p.weights ? p.weights[t] : 1.0f;
-  const float c = p.inv_tau * LOG2E;  // logits to powers of two
-
-  // teacher: values times c, then probabilities
-  float zmax = -INFINITY;
-  bool refused = false;
-  for (int j = tid; j < p.top; j += DISTILL_THREADS) {
-    const long long i = t * p.top + j, id = load_index(p.ids, p.id_bytes, i);
-    float z = -INFINITY;
-    if (id >= p.vocab) refused = true;
-    if (id >= 0 && id < p.vocab && weight != 0.0f)
-      z = p.teacher_dtype == NS_DT_FP32   ? static_cast<const float*>(p.teacher)[i]
-          : p.teacher_dtype == NS_DT_BF16 ? to_float(static_cast<const __nv_bfloat16*>(p.teacher)[i])
-                                          : to_float(static_cast<const __half*>(p.teacher)[i]);
-    const bool in = !(z == -INFINITY);
-    ti[j] = in ? static_cast<int>(id) : -1;
-    tp[j] = z;
-    if (in) ts[j] = to_float(row[id]);
-    zmax = z != z ? z : fmaxf(zmax, z);
-  }
-  if (refused) atomicOr(p.status, NS_DEV_BAD_INDEX);
-  const int any = __syncthreads_or(zmax != -INFINITY);
-  if (!any) {
-    // nothing to learn from: zeros, without a look at the logits
+  const float c = p.inv_tau * LOG2E;
+  if (!__syncthreads_or(load_teacher(p, te, t, row, weight, tid, DISTILL_THREADS))) {
     if (p.loss && tid == 0) {
       p.loss[t] = 0.0f;
       p.lse[t] = 0.0f;
     }
     if (p.grad) {
       const long long head = head_of(grad, p.vocab), words = (p.vocab - head) / V;
-      for (long long i = tid; i < head; i += DISTILL_THREADS) grad[i] = from_float<T>(0.0f);
-      for (long long i = tid; i < words; i += DISTILL_THREADS)
-        store_vec<T, V>(grad + head + i * V, zero_vec<T, V>());
-      for (long long i = head + words * V + tid; i < p.vocab; i += DISTILL_THREADS) grad[i] = from_float<T>(0.0f);
+      for (long long i = tid; i < words; i += DISTILL_THREADS) store_once(grad + head + i * V, zero_vec<T, V>());
+      for (long long i = tid; i < p.vocab - words * V; i += DISTILL_THREADS)
+        grad[i < head ? i : words * V + i] = from_float<T>(0.0f);
     }
     return;
   }
   if (warp == 0) {
-    // log-sum-exp of the entries left, unless the teacher's own is given
-    // (relative to their maximum, so that values near the type's lowest stay finite)
-    float z0 = 0.0f, zlog;
-    if (p.teacher_lse) {
-      zlog = p.teacher_lse[t];
-    } else {
-      z0 = -INFINITY;
-      for (int j = lane; j < p.top; j += 32) z0 = fmaxf(z0, tp[j]);
-      z0 = warp_max(z0);
-      float sum = 0.0f;
-      for (int j = lane; j < p.top; j += 32) sum += ti[j] >= 0 ? expf((tp[j] - z0) * p.inv_tau) : 0.0f;
-      zlog = logf(warp_sum(sum));
-    }
-    float mass = 0.0f, part = 0.0f;
-    for (int j = lane; j < p.top; j += 32) {
-      const float logp = (tp[j] - z0) * p.inv_tau - zlog;
-      const float pr = ti[j] >= 0 ? expf(logp) : 0.0f;
-      if (pr != 0.0f) part += pr * (logp - ts[j] * p.inv_tau);
-      mass += pr;
-      tp[j] = pr;
-    }
-    mass = warp_sum(mass);
-    part = warp_sum(part);
-    if (lane == 0) {
-      sh_mass = mass;
-      sh_lse2 = part;  // kept here until the log-sum-exp is known
-    }
+    teacher_probabilities(p, te, t, lane);
+    mark_repeated(te, p.top, p.places - 1, lane);
   }
 
-  const long long head = head_of(row, p.vocab), words = (p.vocab - head) / V, tail = head + words * V;
+  const long long head = head_of(row, p.vocab), words = (p.vocab - head) / V, edges = p.vocab - words * V;
   float lse2;
   if (p.loss) {
     Online o;
     for (long long i = tid; i < words; i += DISTILL_THREADS) {
       const Vec<T, V> x = load_vec<T, V>(row + head + i * V);
-      float v[V], m = -INFINITY, s = 0.0f;
+      float m = -INFINITY, s = 0.0f;
 #pragma unroll
-      for (int k = 0; k < V; ++k) {
-        v[k] = to_float(x.v[k]) * c;
-        m = fmaxf(m, v[k]);
-      }
+      for (int k = 0; k < V; ++k) m = fmaxf(m, get(x, k) * c);
       const float base = m == -INFINITY ? 0.0f : m;
 #pragma unroll
-      for (int k = 0; k < V; ++k) s += exp2_fast(v[k] - base);
+      for (int k = 0; k < V; ++k) s += exp2_fast(fmaf(get(x, k), c, -base));
       o.join(m, s);
     }
-    for (long long i = tid; i < head + (p.vocab - tail); i += DISTILL_THREADS) {
-      const float v = to_float(row[i < head ? i : tail + i - head]) * c;
+    for (long long i = tid; i < edges; i += DISTILL_THREADS) {
+      const float v = to_float(row[i < head ? i : words * V + i]) * c;
       o.join(v, v == -INFINITY ? 0.0f : exp2_fast(v - v));
     }
-#pragma unroll
-    for (int k = 16; k; k >>= 1) o.join(__shfl_xor_sync(0xffffffffu, o.m, k), __shfl_xor_sync(0xffffffffu, o.s, k));
-    if (lane == 0) {
-      red_m[warp] = o.m;
-      red_s[warp] = o.s;
-    }
+    o = join_warp(o);
+    if (lane == 0) parts[warp] = make_float2(o.m, o.s);
     __syncthreads();
-    Online all;
-    for (int k = 0; k < DISTILL_WARPS; ++k) all.join(red_m[k], red_s[k]);
-    lse2 = all.m + log2f(all.s);
+    lse2 = join_parts<DISTILL_WARPS>(parts, 1, lane);
     if (tid == 0) {
-      p.loss[t] = weight * (sh_lse2 + sh_mass * (lse2 * LN2));
+      p.loss[t] = weight * (te.sums[1] + te.sums[0] * (lse2 * LN2));
       p.lse[t] = lse2 * LN2;
     }
   } else {
@@ -199,17 +491,17 @@ __global__ void __launch_bounds__(DISTILL_THREADS) ns_distill_kernel(const __gri
   }
   if (!p.grad) return;
 
-  const float scale = weight * p.inv_tau, mass = scale * sh_mass;
-  const bool same = ((reinterpret_cast<uintptr_t>(row) ^ reinterpret_cast<uintptr_t>(grad)) & 15) == 0;
-  if (same) {
+  const float scale = weight * p.inv_tau, mass = scale * te.sums[0];
+  if (((reinterpret_cast<uintptr_t>(row) ^ reinterpret_cast<uintptr_t>(grad)) & 15) == 0) {
     for (long long i = tid; i < words; i += DISTILL_THREADS) {
-      Vec<T, V> x = load_vec<T, V>(row + head + i * V);
+      const Vec<T, V> x = load_vec<T, V>(row + head + i * V);
+      float y[V];
 #pragma unroll
-      for (int k = 0; k < V; ++k) x.v[k] = from_float<T>(mass * exp2_fast(fmaf(to_float(x.v[k]), c, -lse2)));
-      store_vec<T, V>(grad + head + i * V, x);
+      for (int k = 0; k < V; ++k) y[k] = mass * exp2_fast(fmaf(get(x, k), c, -lse2));
+      store_vec<T, V>(grad + head + i * V, pack<T, V>(y));
     }
-    for (long long i = tid; i < head + (p.vocab - tail); i += DISTILL_THREADS) {
-      const long long v = i < head ? i : tail + i - head;
+    for (long long i = tid; i < edges; i += DISTILL_THREADS) {
+      const long long v = i < head ? i : words * V + i;
       grad[v] = from_float<T>(mass * exp2_fast(fmaf(to_float(row[v]), c, -lse2)));
     }
   } else {
@@ -217,14 +509,40 @@ __global__ void __launch_bounds__(DISTILL_THREADS) ns_distill_kernel(const __gri
       grad[v] = from_float<T>(mass * exp2_fast(fmaf(to_float(row[v]), c, -lse2)));
   }
   __syncthreads();
-  // the teacher's entries, each with all probabilities that name it
-  for (int j = tid; j < p.top; j += DISTILL_THREADS) {
-    const int id = ti[j];
-    if (id < 0) continue;
-    float sum = 0.0f;
-    for (int i = 0; i < p.top; ++i) sum += ti[i] == id ? tp[i] : 0.0f;
-    grad[id] = from_float<T>(mass * exp2_fast(fmaf(ts[j], c, -lse2)) - scale * sum);
+  const Slice slice = {0, p.vocab, 0, p.vocab, false};
+  write_entries<T>(p, te, slice, grad, c, lse2, scale, tid, DISTILL_THREADS);
+}
+
+constexpr int DISTILL_MAX_SMEM = 200 * 1024;
+
+template <typename T, int NT>
+cudaError_t launch_slices(const DistillParams& p, long long tokens, size_t smem, cudaStream_t st) {
+  if (smem > 48 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(ns_distill_kernel<T, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               DISTILL_MAX_SMEM);
+    if (e != cudaSuccess) return e;
   }
+  return launch_pdl_cluster(ns_distill_kernel<T, NT>, dim3(static_cast<unsigned>(tokens * p.cluster)), dim3(NT + 32),
+                            smem, p.cluster, st, p);
+}
+
+template <typename T>
+cudaError_t launch_distill(DistillParams& p, long long tokens, int nsm, cudaStream_t st) {
+  constexpr int V = 16 / sizeof(T);
+  const long long words = (p.vocab + V - 1) / V;
+  const int nt = words <= 128 * 8 ? 128 : 256;
+  int C = 1;
+  while (C < DISTILL_MAX_CLUSTER && (words + C - 1) / C > 4096) C *= 2;
+  // few rows: split further, down to a word a thread
+  while (C < DISTILL_MAX_CLUSTER && tokens * C < nsm && words / C > nt) C *= 2;
+  p.cluster = C;
+  p.slice_words = static_cast<int>((words + C - 1) / C);
+  p.places = table_size(p.top);
+  const size_t smem = 16 * static_cast<size_t>(p.slice_words) + teacher_bytes(p.top);
+  if (smem > DISTILL_MAX_SMEM || tokens * C > INT_MAX)
+    return launch_pdl(ns_distill_long_kernel<T>, dim3(static_cast<unsigned>(tokens)), dim3(DISTILL_THREADS),
+                      teacher_bytes(p.top), st, p);
+  return nt == 128 ? launch_slices<T, 128>(p, tokens, smem, st) : launch_slices<T, 256>(p, tokens, smem, st);
 }
 
 }  // namespace
@@ -268,11 +586,10 @@ int run_distill(const void* logits, int64_t logits_stride, int dtype, int64_t to
   const int rc = device_setup(&dev, &p.status, &nsm);
   if (rc != NS_OK) return rc;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const dim3 grid(static_cast<unsigned>(tokens)), block(nsk::DISTILL_THREADS);
   const cudaError_t e = counted(K_DISTILL, st, [&] {
-    if (dtype == NS_DT_BF16) return nsk::launch_pdl(nsk::ns_distill_kernel<__nv_bfloat16>, grid, block, 0, st, p);
-    if (dtype == NS_DT_FP16) return nsk::launch_pdl(nsk::ns_distill_kernel<__half>, grid, block, 0, st, p);
-    return nsk::launch_pdl(nsk::ns_distill_kernel<float>, grid, block, 0, st, p);
+    if (dtype == NS_DT_BF16) return nsk::launch_distill<__nv_bfloat16>(p, tokens, nsm, st);
+    if (dtype == NS_DT_FP16) return nsk::launch_distill<__half>(p, tokens, nsm, st);
+    return nsk::launch_distill<float>(p, tokens, nsm, st);
   });
   return e == cudaSuccess ? NS_OK : NS_ERR_CUDA;
 }

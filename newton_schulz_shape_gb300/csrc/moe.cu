@@ -267,18 +267,13 @@ __global__ void __launch_bounds__(ROW_THREADS) ns_moe_gather_kernel(const __grid
       if (c0 + u * 32 * V < p.dim) {
         const Vec<T, V> x = load_vec<T, V>(src + c0 + u * 32 * V);
 #pragma unroll
-        for (int i = 0; i < V; ++i) acc[u][i] = fmaf(wt, to_float(x.v[i]), acc[u][i]);
+        for (int i = 0; i < V; ++i) acc[u][i] = fmaf(wt, get(x, i), acc[u][i]);
       }
   }
   T* dst = static_cast<T*>(p.dst) + t * p.dst_ld;
 #pragma unroll
   for (int u = 0; u < U; ++u)
-    if (c0 + u * 32 * V < p.dim) {
-      Vec<T, V> y;
-#pragma unroll
-      for (int i = 0; i < V; ++i) y.v[i] = from_float<T>(acc[u][i]);
-      store_vec<T, V>(dst + c0 + u * 32 * V, y);
-    }
+    if (c0 + u * 32 * V < p.dim) store_vec<T, V>(dst + c0 + u * 32 * V, pack<T, V>(acc[u]));
 }
 
 // combine's gradient: `parts` warps of one block share a token; each walks its
@@ -305,7 +300,7 @@ __global__ void __launch_bounds__(ROW_THREADS) ns_moe_combine_grad_kernel(const 
         Vec<T, V> x = zero_vec<T, V>();
         if (c0 + u * 32 * V < p.dim) x = load_vec<T, V>(dy + c0 + u * 32 * V);
 #pragma unroll
-        for (int i = 0; i < V; ++i) g[u][i] = to_float(x.v[i]);
+        for (int i = 0; i < V; ++i) g[u][i] = get(x, i);
       }
       for (int j = 0; j < p.k; ++j) {
         const int r = __shfl_sync(0xffffffffu, mine, j);
@@ -321,13 +316,13 @@ __global__ void __launch_bounds__(ROW_THREADS) ns_moe_combine_grad_kernel(const 
 #pragma unroll
         for (int u = 0; u < U; ++u)
           if (c0 + u * 32 * V < p.dim) {
-            Vec<T, V> o;
+            float o[V];
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-              dot = fmaf(g[u][i], to_float(y[u].v[i]), dot);
-              o.v[i] = from_float<T>(wt * g[u][i]);
+              dot = fmaf(g[u][i], get(y[u], i), dot);
+              o[i] = wt * g[u][i];
             }
-            store_vec<T, V>(out + c0 + u * 32 * V, o);
+            store_vec<T, V>(out + c0 + u * 32 * V, pack<T, V>(o));
           }
         dot = warp_sum(dot);
         if (lane == j) sum += dot;

@@ -92,6 +92,19 @@ __device__ __forceinline__ bool mbar_wait_drain(uint64_t* bar, uint32_t parity, 
   return true;
 }
 
+// ------------------------------------------------- per-thread asynchronous copy
+// 16 bytes global -> shared, seen by the issuing thread after it waited for
+// the copy's group (commit closes a group; wait<N> leaves at most the N most
+// recent groups pending).
+__device__ __forceinline__ void cp_async16(void* smem_dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(smem_dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 // ------------------------------------------- programmatic dependent launch
 // Kernels are launched with programmatic stream serialization: a kernel may
 // start (and do its set-up) while its predecessor in the stream still runs.
@@ -183,6 +196,14 @@ __device__ __forceinline__ uint32_t cluster_count_x() {
   uint32_t r;
   asm volatile("mov.u32 %0, %%nclusterid.x;" : "=r"(r));
   return r;
+}
+// The barrier below in two halves, without ordering of memory: after the wait,
+// every CTA of the cluster has started (its shared memory may be written).
+__device__ __forceinline__ void cluster_arrive_relaxed() {
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 // Whole-cluster barrier (every thread of every CTA, warps converged).
 __device__ __forceinline__ void cluster_sync_all() {

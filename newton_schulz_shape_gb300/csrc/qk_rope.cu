@@ -134,8 +134,8 @@ __device__ __forceinline__ void load_angles(const QkParams& p, const Lane<T>& l,
     const Vec<float, V / 2> a = load_vec<float, V / 2>(cr), b = load_vec<float, V / 2>(sr);
 #pragma unroll
     for (int i = 0; i < V / 2; ++i) {
-      c[i] = a.v[i];
-      s[i] = b.v[i];
+      c[i] = get(a, i);
+      s[i] = get(b, i);
     }
   } else {
 #pragma unroll
@@ -143,8 +143,8 @@ __device__ __forceinline__ void load_angles(const QkParams& p, const Lane<T>& l,
       const Vec<float, 4> a = load_vec<float, 4>(cr + i), b = load_vec<float, 4>(sr + i);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        c[i + j] = a.v[j];
-        s[i + j] = b.v[j];
+        c[i + j] = get(a, j);
+        s[i + j] = get(b, j);
       }
     }
   }
@@ -213,18 +213,18 @@ __global__ void __launch_bounds__(QK_THREADS) ns_qk_kernel(const __grid_constant
     float xf[V], sum = 0.0f;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      xf[i] = to_float(x[u].v[i]);
+      xf[i] = get(x[u], i);
       sum = fmaf(xf[i], xf[i], sum);
     }
     sum = group_sum<G>(sum);
     const float r = rsqrtf(sum / p.dim + p.eps);
-    Vec<T, V> y;
+    float y[V];
     if (p.interleaved && l.rotated) {
 #pragma unroll
       for (int i = 0; i < V; i += 2) {
         const float a = xf[i] * r * g[i], b = xf[i + 1] * r * g[i + 1];
-        y.v[i] = from_float<T>(a * c[i / 2] - b * s[i / 2]);
-        y.v[i + 1] = from_float<T>(b * c[i / 2] + a * s[i / 2]);
+        y[i] = a * c[i / 2] - b * s[i / 2];
+        y[i + 1] = b * c[i / 2] + a * s[i / 2];
       }
     }
     const Vec<T, V> other = from_partner<T>(x[u], l.partner);
@@ -232,12 +232,12 @@ __global__ void __launch_bounds__(QK_THREADS) ns_qk_kernel(const __grid_constant
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         const float a = xf[i] * r * g[i];
-        const float b = to_float(other.v[i]) * r * gp[i];
-        y.v[i] = from_float<T>(l.rotated ? a * c[i] + l.sign * (b * s[i]) : a);
+        const float b = get(other, i) * r * gp[i];
+        y[i] = l.rotated ? a * c[i] + l.sign * (b * s[i]) : a;
       }
     }
     if (live && l.on && (row || !p.rot_dim))
-      store_vec<T, V>(static_cast<T*>(side.out) + at.t * side.out_token + at.h * side.out_head + l.d0, y);
+      store_vec<T, V>(static_cast<T*>(side.out) + at.t * side.out_token + at.h * side.out_head + l.d0, pack<T, V>(y));
     at.step(32 / G, side.heads);
   }
 }
@@ -296,8 +296,8 @@ __global__ void __launch_bounds__(QK_THREADS) ns_qk_grad_kernel(const __grid_con
         float xf[V], t[V], sum = 0.0f, dot = 0.0f;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-          xf[i] = to_float(x[u].v[i]);
-          t[i] = to_float(dy[u].v[i]);
+          xf[i] = get(x[u], i);
+          t[i] = get(dy[u], i);
         }
         if (l.rotated) {
           if (p.interleaved) {
@@ -309,7 +309,7 @@ __global__ void __launch_bounds__(QK_THREADS) ns_qk_grad_kernel(const __grid_con
             }
           } else {
 #pragma unroll
-            for (int i = 0; i < V; ++i) t[i] = t[i] * c[i] - l.sign * (to_float(other.v[i]) * s[i]);
+            for (int i = 0; i < V; ++i) t[i] = t[i] * c[i] - l.sign * (get(other, i) * s[i]);
           }
         }
 #pragma unroll
@@ -322,13 +322,14 @@ __global__ void __launch_bounds__(QK_THREADS) ns_qk_grad_kernel(const __grid_con
         const float r = rsqrtf(sum / p.dim + p.eps);
         const float m = r * r * (dot / p.dim);
         if (live && l.on) {
-          Vec<T, V> dx;
+          float dx[V];
 #pragma unroll
           for (int i = 0; i < V; ++i) {
             dg[i] = fmaf(t[i], xf[i] * r, dg[i]);
-            dx.v[i] = from_float<T>(r * (t[i] * g[i] - xf[i] * m));
+            dx[i] = r * (t[i] * g[i] - xf[i] * m);
           }
-          store_vec<T, V>(static_cast<T*>(side.out) + at.t * side.out_token + at.h * side.out_head + l.d0, dx);
+          store_vec<T, V>(static_cast<T*>(side.out) + at.t * side.out_token + at.h * side.out_head + l.d0,
+                          pack<T, V>(dx));
         }
         at.step(32 / G, side.heads);
       }
