@@ -28,6 +28,7 @@ constexpr int MAX_EXPERTS = 1024;
 constexpr int MAX_K = 32;
 constexpr int SORT_THREADS = 512;
 constexpr int SORT_WARPS = SORT_THREADS / 32;
+constexpr int SORT_HELD = 4;  // rounds of 32 slots that a warp keeps in registers
 constexpr int SORT_MAX_BLOCKS = 256;
 constexpr int ROW_THREADS = 256;
 
@@ -70,11 +71,15 @@ __global__ void __launch_bounds__(SORT_THREADS) ns_moe_count_kernel(const __grid
   for (int e = threadIdx.x; e < p.experts; e += SORT_THREADS) p.block_counts[blockIdx.x * p.experts + e] = sm[e];
 }
 
-// Places one chunk's slots. Warp w owns a contiguous part of the chunk; the
-// rank of a slot is (slots of its expert in earlier chunks) + (in earlier
-// warps) + (in earlier rounds of this warp) + (in lower lanes).
+// Places one chunk's slots. Warp w owns a contiguous part of the chunk, 32
+// slots a round; the rank of a slot is (slots of its expert in earlier chunks)
+// + (in earlier warps) + (in earlier rounds of this warp) + (in lower lanes).
+// HELD: the warp's slots fit SORT_HELD rounds, whose experts and ranks stay in
+// registers; else they are read and ranked once more when they are placed.
+template <bool HELD>
 __global__ void __launch_bounds__(SORT_THREADS) ns_moe_place_kernel(const __grid_constant__ SortParams p) {
   extern __shared__ int sm[];
+  __shared__ int warp_rows[SORT_WARPS];
   const int E = p.experts, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int* next = sm;                       // [warps][E]: count, then the next rank
   int* before = sm + SORT_WARPS * E;    // [E]: slots in earlier chunks
@@ -83,86 +88,125 @@ __global__ void __launch_bounds__(SORT_THREADS) ns_moe_place_kernel(const __grid
   for (int i = threadIdx.x; i < (SORT_WARPS + 2) * E; i += SORT_THREADS) sm[i] = 0;
   nsptx::griddep_wait();
   nsptx::griddep_launch_dependents();
-  __syncthreads();
 
   const int per_warp = p.chunk / SORT_WARPS;
   const int w0 = min(p.slots, static_cast<int>(blockIdx.x) * p.chunk + warp * per_warp);
   const int w1 = min(p.slots, w0 + per_warp);
   bool refused = false;
-  for (int s = w0 + lane; s < w1; s += 32) {
-    const int e = slot_expert(p, s, &refused);
-    if (e >= 0) atomicAdd(&next[warp * E + e], 1);
+  int held[SORT_HELD], rank[SORT_HELD];
+  if (HELD) {
+#pragma unroll
+    for (int i = 0; i < SORT_HELD; ++i) held[i] = w0 + i * 32 + lane < w1 ? slot_expert(p, w0 + i * 32 + lane, &refused) : -1;
+  }
+  __syncthreads();
+  // rank of a slot among this warp's of its expert so far, counted on top of
+  // what `next` holds
+  auto take = [&](int e) {
+    const unsigned peers = __match_any_sync(0xffffffffu, e);
+    int r = 0;
+    if (e >= 0) r = next[warp * E + e] + __popc(peers & ((1u << lane) - 1));
+    __syncwarp();
+    if (e >= 0 && (peers >> lane) == 1u) next[warp * E + e] = r + 1;  // the highest lane of its peers
+    __syncwarp();
+    return r;
+  };
+  if (HELD) {
+#pragma unroll
+    for (int i = 0; i < SORT_HELD; ++i)
+      if (w0 + i * 32 < w1) rank[i] = take(held[i]);
+  } else {
+    for (int s = w0 + lane; s < w1; s += 32) {
+      const int e = slot_expert(p, s, &refused);
+      if (e >= 0) atomicAdd(&next[warp * E + e], 1);
+    }
   }
   if (refused) atomicOr(p.status, NS_DEV_BAD_INDEX);
   if (p.blocks > 1) {
-    for (int i = threadIdx.x; i < p.blocks * E; i += SORT_THREADS) {
-      const int b = i / E, e = i - b * E, c = p.block_counts[i];
+    const int n = p.blocks * E, earlier = static_cast<int>(blockIdx.x) * E;
+#pragma unroll 4
+    for (int i = threadIdx.x; i < n; i += SORT_THREADS) {
+      const int c = p.block_counts[i], e = i % E;
       if (c) {
         atomicAdd(&total[e], c);
-        if (b < static_cast<int>(blockIdx.x)) atomicAdd(&before[e], c);
+        if (i < earlier) atomicAdd(&before[e], c);
       }
     }
   }
   __syncthreads();
-  for (int e = threadIdx.x; e < E; e += SORT_THREADS) {
-    int run = before[e];
-    for (int w = 0; w < SORT_WARPS; ++w) {
-      const int c = next[w * E + e];
-      next[w * E + e] = run;
-      run += c;
+  // per expert: the warps' first ranks, and the rows of its segment; then the
+  // exclusive sum of those, SORT_THREADS experts at a time
+  int rows_before = 0;
+  for (int e0 = 0; e0 < E; e0 += SORT_THREADS) {
+    const int e = e0 + threadIdx.x;
+    int rows = 0;
+    if (e < E) {
+      int run = before[e];
+#pragma unroll
+      for (int w = 0; w < SORT_WARPS; ++w) {
+        const int c = next[w * E + e];
+        next[w * E + e] = run;
+        run += c;
+      }
+      if (p.blocks == 1) total[e] = run;
+      const unsigned kept = min(total[e], p.capacity), align = p.align;
+      rows = static_cast<int>(align == 1 ? kept : (kept + align - 1) / align * align);
     }
-    if (p.blocks == 1) total[e] = run;
-  }
-  __syncthreads();
-  if (warp == 0) {
-    // exclusive sum of the padded kept counts, a run of experts per lane
-    const int per = (E + 31) / 32, e0 = min(E, lane * per), e1 = min(E, e0 + per);
-    int mine = 0;
-    for (int e = e0; e < e1; ++e) mine += (min(total[e], p.capacity) + p.align - 1) / p.align * p.align;
-    int upto = mine;
+    int upto = rows;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int v = __shfl_up_sync(0xffffffffu, upto, o);
       if (lane >= o) upto += v;
     }
-    int run = upto - mine;
-    for (int e = e0; e < e1; ++e) {
-      offset[e] = run;
-      run += (min(total[e], p.capacity) + p.align - 1) / p.align * p.align;
+    if (lane == 31) warp_rows[warp] = upto;
+    __syncthreads();
+    int start = rows_before + upto - rows;
+#pragma unroll
+    for (int w = 0; w < SORT_WARPS; ++w) {
+      const int v = warp_rows[w];
+      if (w < warp) start += v;
+      rows_before += v;
     }
-    if (lane == 31) offset[E] = run;
-  }
-  __syncthreads();
-
-  if (blockIdx.x == 0) {
-    for (int e = threadIdx.x; e < E; e += SORT_THREADS) p.counts[e] = min(total[e], p.capacity);
-    for (int e = threadIdx.x; e <= E; e += SORT_THREADS) p.offsets[e] = offset[e];
-  }
-  for (int i = w0; i < w1; i += 32) {
-    const int s = i + lane;
-    const int e = s < w1 ? slot_expert(p, s, &refused) : -1;
-    const unsigned peers = __match_any_sync(0xffffffffu, e);
-    if (e >= 0) {
-      const int lower = __popc(peers & ((1u << lane) - 1));
-      const int rank = next[warp * E + e] + lower;
-      int row = -1;
-      if (rank < p.capacity) {
-        row = offset[e] + rank;
-        p.slot_of_row[row] = s;
+    if (e < E) {
+      offset[e] = start;
+      if (blockIdx.x == 0) {
+        p.counts[e] = min(total[e], p.capacity);
+        p.offsets[e] = start;
       }
-      p.row_of_slot[s] = row;
-    } else if (s < w1) {
-      p.row_of_slot[s] = -1;
     }
-    __syncwarp();
-    if (e >= 0 && (peers >> lane) == 1u) next[warp * E + e] += __popc(peers);  // the highest lane of its peers
-    __syncwarp();
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) {
+    offset[E] = rows_before;
+    if (blockIdx.x == 0) p.offsets[E] = rows_before;
+  }
+
+  auto place = [&](int s, int e, int r) {
+    int row = -1;
+    if (e >= 0 && r < p.capacity) {
+      row = offset[e] + r;
+      p.slot_of_row[row] = s;
+    }
+    p.row_of_slot[s] = row;
+  };
+  if (HELD) {
+#pragma unroll
+    for (int i = 0; i < SORT_HELD; ++i) {
+      const int s = w0 + i * 32 + lane;
+      if (s < w1) place(s, held[i], held[i] >= 0 ? next[warp * E + held[i]] + rank[i] : 0);
+    }
+  } else {
+    for (int i = w0; i < w1; i += 32) {
+      const int s = i + lane;
+      const int e = s < w1 ? slot_expert(p, s, &refused) : -1;
+      const int r = take(e);
+      if (s < w1) place(s, e, r);
+    }
   }
   // rows without a slot: the ends of the segments, and what follows the last
-  for (int e = blockIdx.x; e < E; e += p.blocks)
-    for (int r = offset[e] + min(total[e], p.capacity) + threadIdx.x; r < offset[e + 1]; r += SORT_THREADS)
-      p.slot_of_row[r] = -1;
-  for (int r = offset[E] + blockIdx.x * SORT_THREADS + threadIdx.x; r < p.rows; r += p.blocks * SORT_THREADS)
+  __syncthreads();
+  for (int e = blockIdx.x * SORT_WARPS + warp; e < E; e += p.blocks * SORT_WARPS)
+    for (int r = offset[e] + min(total[e], p.capacity) + lane; r < offset[e + 1]; r += 32) p.slot_of_row[r] = -1;
+  for (int r = rows_before + blockIdx.x * SORT_THREADS + threadIdx.x; r < p.rows; r += p.blocks * SORT_THREADS)
     p.slot_of_row[r] = -1;
 }
 
@@ -354,11 +398,12 @@ bool aligned16(const void* p, long long ld, int bytes) {
   return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && ld * bytes % 16 == 0;
 }
 
-// Slots per block and blocks of a sort.
+// Slots per block and blocks of a sort: one block up to what its warps hold in
+// registers, then as many blocks of that size, then larger blocks.
 void sort_split(long long slots, int* chunk, int* blocks) {
-  long long c = (slots + nsk::SORT_MAX_BLOCKS - 1) / nsk::SORT_MAX_BLOCKS;
-  c = std::max<long long>(c, 2048);
-  c = (c + nsk::SORT_THREADS - 1) / nsk::SORT_THREADS * nsk::SORT_THREADS;
+  constexpr int held = nsk::SORT_THREADS * nsk::SORT_HELD;
+  long long c = slots <= held ? slots : std::max<long long>(held, (slots + nsk::SORT_MAX_BLOCKS - 1) / nsk::SORT_MAX_BLOCKS);
+  c = std::max<long long>(1, (c + nsk::SORT_THREADS - 1) / nsk::SORT_THREADS) * nsk::SORT_THREADS;
   *chunk = static_cast<int>(c);
   *blocks = static_cast<int>(std::max<long long>(1, (slots + c - 1) / c));
 }
@@ -490,11 +535,13 @@ int ns_moe_sort(const void* expert_ids, int id_bytes, int64_t tokens, int k, int
     if (e != cudaSuccess) return NS_ERR_CUDA;
   }
   const size_t smem = (static_cast<size_t>(nsk::SORT_WARPS + 3) * experts + 1) * sizeof(int);
-  if (smem > 48 * 1024 && cudaFuncSetAttribute(nsk::ns_moe_place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               static_cast<int>(smem)) != cudaSuccess)
+  void (*const place)(nsk::SortParams) = p.chunk <= nsk::SORT_THREADS * nsk::SORT_HELD ? nsk::ns_moe_place_kernel<true>
+                                                                                      : nsk::ns_moe_place_kernel<false>;
+  if (smem > 48 * 1024 &&
+      cudaFuncSetAttribute(place, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
     return NS_ERR_CUDA;
   const cudaError_t e = counted(K_MOE, st, [&] {
-    return nsk::launch_pdl(nsk::ns_moe_place_kernel, dim3(p.blocks), dim3(nsk::SORT_THREADS), smem, st, p);
+    return nsk::launch_pdl(place, dim3(p.blocks), dim3(nsk::SORT_THREADS), smem, st, p);
   });
   return e == cudaSuccess ? NS_OK : NS_ERR_CUDA;
 }
