@@ -393,7 +393,8 @@ int ns_moe_combine_grad(const void* grad_y, int64_t grad_y_stride, const void* e
  * angle whose cosine and sine are table[pos][i] and
  * table[pos][rot_dim / 2 + i] (fp32 [table_rows][rot_dim]). positions[t] is
  * int32 or int64 (position_bytes 4 or 8), NULL = t; a token whose position is
- * outside the table is refused (its outputs are not written). head_dim <= 1024.
+ * outside the table is refused (its outputs are not written). head_dim <= 1024,
+ * tokens * (q_heads + k_heads) < 2^30.
  * q_out may be q and k_out may be k, with the same strides. */
 int ns_qk_norm_rope(const void* q, const void* k, void* q_out, void* k_out, const int64_t* strides, int dtype,
                     int64_t tokens, int q_heads, int k_heads, int head_dim, int rot_dim, int interleaved,

@@ -22,8 +22,10 @@
 namespace nsk {
 namespace {
 
-constexpr int QK_THREADS = 256;
+constexpr int QK_THREADS = 128;
 constexpr int QK_WARPS = QK_THREADS / 32;
+constexpr int QK_BLOCKS = 5, QK_GRAD_BLOCKS = 4;  // that share an SM
+constexpr int QK_AHEAD = 3;  // rounds whose words are on their way
 constexpr int QK_ANY_THREADS = 128;
 constexpr int QK_MAX_DIM = 1024;
 constexpr int QK_MAX_BLOCKS = 1024;  // blocks of a gradient launch, each with its own sums of dg
@@ -35,7 +37,19 @@ struct QkSide {
   const void* weight; // null: 1
   long long x_token, x_head, dy_token, dy_head, out_token, out_head;  // strides in elements
   int heads;
+  // what a step adds to each address, in bytes: x, dy, out
+  long long within[3], between[3], wrap[3];
 };
+
+// A pair (token, head) of one side, in token order; steps go by a number of
+// pairs split into tokens and heads.
+struct Place {
+  int t, h;
+};
+__host__ __device__ __forceinline__ Place place_of(int pair, int heads) {
+  const int t = pair / heads;
+  return {t, pair - t * heads};
+}
 
 struct QkParams {
   QkSide side[2];     // queries, keys
@@ -46,7 +60,9 @@ struct QkParams {
   long long table_rows;
   const void* positions;  // null: the token's index
   int position_bytes;
-  long long q_warps;  // forward: warps on the queries, the rest are on the keys
+  int chunk;          // rounds of 32 / G heads that a warp takes at a time
+  int chunks[2];      // of the queries and of the keys
+  Place within[2], between[2];  // steps of a warp from round to round: in a chunk, to its next chunk
   float* partial;     // gradient: [blocks][2][dim]
   unsigned int* status;
 };
@@ -74,281 +90,334 @@ __device__ __forceinline__ float group_sum(float x) {
   return x;
 }
 
-// What a lane knows of its 16 bytes of every head: V values from d0 on.
+// A lane holds two words of 16 bytes of every head, a and b. Where the pairs
+// (i, i + rot_dim / 2) are rotated, b lies rot_dim / 2 values after a, so that
+// both values of each pair are in the lane and the two words share their
+// angles; a head then takes dim / V / 2 lanes (8 for 128 bf16 values).
 template <typename T>
 struct Lane {
   static constexpr int V = 16 / sizeof(T);
-  int d0;
-  bool on;       // inside the head
-  bool rotated;  // inside the rotated part
-  int partner;   // lane that holds the other values of the pairs (i, i + rot_dim / 2)
-  int angle;     // first angle of the lane's values
-  float sign;    // of the partner's sine term, forward
+  int a, b;            // first values of the words
+  bool on_a, on_b;     // inside the head
+  bool turn_a, turn_b; // rotated
 };
 
 template <typename T, int G>
 __device__ __forceinline__ Lane<T> lane_of(const QkParams& p, int lane) {
   constexpr int V = Lane<T>::V;
   Lane<T> l;
-  const int chunk = lane % G, half = p.rot_dim / 2;
-  l.d0 = chunk * V;
-  l.on = l.d0 < p.dim;
-  l.rotated = l.d0 < p.rot_dim;
-  const bool first = l.d0 < half;
-  l.partner = l.rotated && !p.interleaved ? lane + (first ? half / V : -(half / V)) : lane;
-  l.angle = p.interleaved ? l.d0 / 2 : (first ? l.d0 : l.d0 - half);
-  l.sign = first ? -1.0f : 1.0f;
+  const int i = lane % G, words = p.dim / V, turned = p.rot_dim / V;
+  if (p.interleaved) {
+    const int a = i, b = i + (words + 1) / 2;
+    l.on_a = a < (words + 1) / 2;
+    l.on_b = l.on_a && b < words;
+    l.turn_a = l.on_a && a < turned;
+    l.turn_b = l.on_b && b < turned;
+    l.a = a * V;
+    l.b = b * V;
+  } else if (i < turned / 2) {
+    l.on_a = l.on_b = l.turn_a = l.turn_b = true;
+    l.a = i * V;
+    l.b = l.a + p.rot_dim / 2;
+  } else {
+    const int rest = words - turned, a = i - turned / 2, b = a + (rest + 1) / 2;
+    l.on_a = a < (rest + 1) / 2;
+    l.on_b = l.on_a && b < rest;
+    l.turn_a = l.turn_b = false;
+    l.a = (turned + a) * V;
+    l.b = (turned + b) * V;
+  }
   return l;
 }
 
+// The two words as pairs of fp32 values.
 template <typename T>
-__device__ __forceinline__ Vec<T, Lane<T>::V> from_partner(const Vec<T, Lane<T>::V>& x, int lane) {
-  Vec<T, Lane<T>::V> y;
-  const uint4 a = *reinterpret_cast<const uint4*>(&x);
-  uint4 b;
-  b.x = __shfl_sync(0xffffffffu, a.x, lane);
-  b.y = __shfl_sync(0xffffffffu, a.y, lane);
-  b.z = __shfl_sync(0xffffffffu, a.z, lane);
-  b.w = __shfl_sync(0xffffffffu, a.w, lane);
-  *reinterpret_cast<uint4*>(&y) = b;
-  return y;
+struct Two {
+  static constexpr int N = Lane<T>::V / 2;
+  float2 a[N], b[N];
+};
+
+template <typename T>
+__device__ __forceinline__ Two<T> unpack(const uint4* from) {
+  constexpr int V = Lane<T>::V;
+  const Vec<T, V> a = *reinterpret_cast<const Vec<T, V>*>(from), b = *reinterpret_cast<const Vec<T, V>*>(from + 32);
+  Two<T> x;
+#pragma unroll
+  for (int i = 0; i < V / 2; ++i) {
+    x.a[i] = make_float2(get(a, 2 * i), get(a, 2 * i + 1));
+    x.b[i] = make_float2(get(b, 2 * i), get(b, 2 * i + 1));
+  }
+  return x;
 }
 
-// The lane's cosines and sines of one table row: V of each, or V / 2 when the
-// pairs are interleaved.
 template <typename T>
-__device__ __forceinline__ void load_angles(const QkParams& p, const Lane<T>& l, const float* row,
-                                            float (&c)[Lane<T>::V], float (&s)[Lane<T>::V]) {
+__device__ __forceinline__ void store_words(char* a, int to_b, const Lane<T>& l, const Two<T>& y) {
   constexpr int V = Lane<T>::V;
-  if (!row || !l.rotated) {
+  float fa[V], fb[V];
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      c[i] = 1.0f;
-      s[i] = 0.0f;
-    }
-    return;
+  for (int i = 0; i < V / 2; ++i) {
+    fa[2 * i] = y.a[i].x;
+    fa[2 * i + 1] = y.a[i].y;
+    fb[2 * i] = y.b[i].x;
+    fb[2 * i + 1] = y.b[i].y;
   }
-  const float* cr = row + l.angle;
-  const float* sr = cr + p.rot_dim / 2;
-  if (p.interleaved) {
-    const Vec<float, V / 2> a = load_vec<float, V / 2>(cr), b = load_vec<float, V / 2>(sr);
+  if (l.on_a) store_vec<T, V>(reinterpret_cast<T*>(a), pack<T, V>(fa));
+  if (l.on_b) store_vec<T, V>(reinterpret_cast<T*>(a + to_b), pack<T, V>(fb));
+}
+
+// Cosines and sines of the lane's V pairs at one table row: the pairs of both
+// words, or (interleaved) those of word a and then those of word b.
+template <typename T>
+struct Angles {
+  float2 c[Two<T>::N], s[Two<T>::N];
+};
+
+template <typename T>
+__device__ __forceinline__ void load_angles(const QkParams& p, const Lane<T>& l, const float* row, Angles<T>& g) {
+  constexpr int N = Two<T>::N;
+  const int half = p.rot_dim / 2;
+  const int a = p.interleaved ? l.a / 2 : l.a, b = p.interleaved ? l.b / 2 : l.a + N;
 #pragma unroll
-    for (int i = 0; i < V / 2; ++i) {
-      c[i] = get(a, i);
-      s[i] = get(b, i);
+  for (int i = 0; i < N / 2; ++i) {
+    if (l.turn_a) {
+      g.c[i] = *reinterpret_cast<const float2*>(row + a + 2 * i);
+      g.s[i] = *reinterpret_cast<const float2*>(row + half + a + 2 * i);
     }
-  } else {
+    if (l.turn_b) {
+      g.c[N / 2 + i] = *reinterpret_cast<const float2*>(row + b + 2 * i);
+      g.s[N / 2 + i] = *reinterpret_cast<const float2*>(row + half + b + 2 * i);
+    }
+  }
+}
+
+// Rotates the lane's pairs, forward (sign 1) or back (sign -1).
+template <typename T>
+__device__ __forceinline__ void turn(const QkParams& p, const Lane<T>& l, const Angles<T>& g, Two<T>& x, float sign) {
+  constexpr int N = Two<T>::N;
+  if (p.interleaved) {
+    // pair i of a word: cosine and sine i of the word's N
+    auto one = [&](float2& v, float c, float s) { v = make_float2(v.x * c - v.y * s, v.y * c + v.x * s); };
 #pragma unroll
-    for (int i = 0; i < V; i += 4) {
-      const Vec<float, 4> a = load_vec<float, 4>(cr + i), b = load_vec<float, 4>(sr + i);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        c[i + j] = get(a, j);
-        s[i + j] = get(b, j);
+    for (int i = 0; i < N; i += 2) {
+      const int k = i / 2;
+      if (l.turn_a) {
+        one(x.a[i], g.c[k].x, sign * g.s[k].x);
+        one(x.a[i + 1], g.c[k].y, sign * g.s[k].y);
+      }
+      if (l.turn_b) {
+        one(x.b[i], g.c[N / 2 + k].x, sign * g.s[N / 2 + k].x);
+        one(x.b[i + 1], g.c[N / 2 + k].y, sign * g.s[N / 2 + k].y);
       }
     }
+  } else if (l.turn_a) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float2 a = x.a[i], b = x.b[i], minus = mul2(g.s[i], make_float2(-1.0f, -1.0f));
+      x.a[i] = fma2(a, g.c[i], mul2(b, sign > 0 ? minus : g.s[i]));
+      x.b[i] = fma2(b, g.c[i], mul2(a, sign > 0 ? g.s[i] : minus));
+    }
   }
 }
 
-// Position in the pairs (token, head) of one side, in token order.
-struct Place {
-  long long t;
-  int h;
-  __device__ __forceinline__ Place(long long pair, int heads) : t(pair / heads), h(static_cast<int>(pair - t * heads)) {}
-  __device__ __forceinline__ void step(int n, int heads) {
-    h += n;
-    while (h >= heads) {
+// The weights of one of the lane's words.
+template <typename T>
+__device__ __forceinline__ void weights_of(const QkParams& p, const void* w, int first, bool on, float2 (&g)[Two<T>::N]) {
+  constexpr int V = Lane<T>::V, N = Two<T>::N;
+  if (!w || !on) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) g[i] = make_float2(1.0f, 1.0f);
+  } else if (p.weight_fp32) {
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+      const float4 f = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(w) + first + 2 * i));
+      g[i] = make_float2(f.x, f.y);
+      g[i + 1] = make_float2(f.z, f.w);
+    }
+  } else {
+    Vec<T, V> x;
+    *reinterpret_cast<uint4*>(&x) = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(w) + first));
+#pragma unroll
+    for (int i = 0; i < N; ++i) g[i] = make_float2(get(x, 2 * i), get(x, 2 * i + 1));
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ Two<T> lane_weights(const QkParams& p, const QkSide& side, const Lane<T>& l) {
+  Two<T> g;
+  weights_of<T>(p, side.weight, l.a, l.on_a, g.a);
+  weights_of<T>(p, side.weight, l.b, l.on_b, g.b);
+  return g;
+}
+
+// The heads that a lane's group goes through: p.chunk rounds in a row, then
+// those of the warp's next chunk.
+struct Walk {
+  int t, h, left;
+  bool wrapped;  // the last step went past the token's last head
+  __device__ __forceinline__ explicit Walk(const Place& at) : t(at.t), h(at.h), left(0), wrapped(false) {}
+  // One step; whether it went to the next chunk.
+  __device__ __forceinline__ bool step(const QkParams& p, int which, int heads) {
+    const bool jump = --left == 0;
+    if (jump) left = p.chunk;
+    t += jump ? p.between[which].t : p.within[which].t;
+    h += jump ? p.between[which].h : p.within[which].h;
+    wrapped = h >= heads;
+    if (wrapped) {
       h -= heads;
       ++t;
     }
+    return jump;
   }
 };
 
-// Forward: G lanes hold one head, 16 bytes each; a warp takes U rounds of
-// 32 / G consecutive heads.
-template <typename T, int G, int U>
-__global__ void __launch_bounds__(QK_THREADS) ns_qk_kernel(const __grid_constant__ QkParams p) {
-  constexpr int V = Lane<T>::V;
-  nsptx::griddep_wait();
-  nsptx::griddep_launch_dependents();
-  const int lane = threadIdx.x & 31;
-  long long w = static_cast<long long>(blockIdx.x) * QK_WARPS + (threadIdx.x >> 5);
-  const int which = w < p.q_warps ? 0 : 1;
-  if (which) w -= p.q_warps;
-  const QkSide& side = p.side[which];
-  const long long pairs = p.tokens * side.heads;
-  const long long first = w * (U * (32 / G)) + lane / G;
-  if (w * (U * (32 / G)) >= pairs) return;
-  const Lane<T> l = lane_of<T, G>(p, lane);
-
-  Vec<T, V> x[U];
-  {
-    Place at(first, side.heads);
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      x[u] = zero_vec<T, V>();
-      if (l.on && first + u * (32 / G) < pairs)
-        x[u] = load_vec<T, V>(static_cast<const T*>(side.x) + at.t * side.x_token + at.h * side.x_head + l.d0);
-      at.step(32 / G, side.heads);
-    }
-  }
-  float g[V], gp[V];  // the lane's weights and its partner's
-#pragma unroll
-  for (int i = 0; i < V; ++i) {
-    g[i] = l.on ? weight_at<T>(p, side.weight, l.d0 + i) : 0.0f;
-    gp[i] = __shfl_sync(0xffffffffu, g[i], l.partner);
-  }
-  Place at(first, side.heads);
-  long long angles_of = -1;
-  const float* row = nullptr;
-  float c[V], s[V];
-#pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const bool live = first + u * (32 / G) < pairs;
-    if (live && p.rot_dim && at.t != angles_of) {
-      row = table_row(p, at.t);
-      load_angles<T>(p, l, row, c, s);
-      angles_of = at.t;
-    }
-    float xf[V], sum = 0.0f;
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      xf[i] = get(x[u], i);
-      sum = fmaf(xf[i], xf[i], sum);
-    }
-    sum = group_sum<G>(sum);
-    const float r = rsqrtf(sum / p.dim + p.eps);
-    float y[V];
-    if (p.interleaved && l.rotated) {
-#pragma unroll
-      for (int i = 0; i < V; i += 2) {
-        const float a = xf[i] * r * g[i], b = xf[i + 1] * r * g[i + 1];
-        y[i] = a * c[i / 2] - b * s[i / 2];
-        y[i + 1] = b * c[i / 2] + a * s[i / 2];
-      }
-    }
-    const Vec<T, V> other = from_partner<T>(x[u], l.partner);
-    if (!p.interleaved || !l.rotated) {
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const float a = xf[i] * r * g[i];
-        const float b = get(other, i) * r * gp[i];
-        y[i] = l.rotated ? a * c[i] + l.sign * (b * s[i]) : a;
-      }
-    }
-    if (live && l.on && (row || !p.rot_dim))
-      store_vec<T, V>(static_cast<T*>(side.out) + at.t * side.out_token + at.h * side.out_head + l.d0, pack<T, V>(y));
-    at.step(32 / G, side.heads);
-  }
-}
-
-// Gradient: the same lanes, in a grid that stays on the card; a lane keeps the
-// sums of its V columns of dg, which a block joins in a fixed order.
-template <typename T, int G, int U>
-__global__ void __launch_bounds__(QK_THREADS) ns_qk_grad_kernel(const __grid_constant__ QkParams p) {
-  constexpr int V = Lane<T>::V;
-  __shared__ float joined[QK_WARPS][G * V];
+// The norm, its rotation and (GRAD) its gradient: G lanes hold one head, a warp
+// 32 / G consecutive heads a round. The warps of a grid that fits the card deal
+// the queries and then the keys among them, p.chunk rounds at a time, so that
+// together they walk through memory in order; a warp copies the words of its
+// next QK_AHEAD rounds to shared memory while it computes one. For the gradient
+// a lane keeps the sums of its columns of dg, which a block joins in a fixed
+// order.
+template <typename T, int G, bool GRAD>
+__global__ void __launch_bounds__(QK_THREADS, GRAD ? QK_GRAD_BLOCKS : QK_BLOCKS) ns_qk_kernel(const __grid_constant__ QkParams p) {
+  constexpr int V = Lane<T>::V, N = Two<T>::N, H = 32 / G, STAGES = QK_AHEAD + 1, STAGE = GRAD ? 128 : 64;
+  extern __shared__ uint4 ring_smem[];
   nsptx::griddep_wait();
   nsptx::griddep_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  uint4* ring = ring_smem + warp * (STAGES * STAGE) + lane;
   const Lane<T> l = lane_of<T, G>(p, lane);
+  const float inv_dim = 1.0f / p.dim;
+  // words outside the head are zero and stay so
+  for (int i = 0; i < STAGES * STAGE; i += 64) {
+    if (!l.on_a) ring[i] = make_uint4(0, 0, 0, 0);
+    if (!l.on_b) ring[i + 32] = make_uint4(0, 0, 0, 0);
+  }
+  const int warps = gridDim.x * QK_WARPS, me = blockIdx.x * QK_WARPS + warp;
+  int chunk = me;  // this warp's next, in those of the queries and then of the keys
   for (int which = 0; which < 2; ++which) {
     const QkSide& side = p.side[which];
-    const long long pairs = p.tokens * side.heads;
-    float g[V], dg[V];
+    const int first = chunk - (which ? p.chunks[0] : 0), todo = p.chunks[which] - first;
+    const int mine = todo > 0 ? (todo + warps - 1) / warps : 0, n = mine * p.chunk;
+    chunk += mine * warps;
+    Two<T> dg;
+    if (GRAD) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      g[i] = l.on ? weight_at<T>(p, side.weight, l.d0 + i) : 0.0f;
-      dg[i] = 0.0f;
+      for (int i = 0; i < N; ++i) dg.a[i] = dg.b[i] = make_float2(0.0f, 0.0f);
     }
-    const long long stride = static_cast<long long>(gridDim.x) * QK_WARPS * (U * (32 / G));
-    for (long long base = (static_cast<long long>(blockIdx.x) * QK_WARPS + warp) * (U * (32 / G)); base < pairs;
-         base += stride) {
-      const long long first = base + lane / G;
-      Vec<T, V> x[U], dy[U];
-      {
-        Place at(first, side.heads);
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          x[u] = zero_vec<T, V>();
-          dy[u] = zero_vec<T, V>();
-          if (l.on && first + u * (32 / G) < pairs) {
-            x[u] = load_vec<T, V>(static_cast<const T*>(side.x) + at.t * side.x_token + at.h * side.x_head + l.d0);
-            dy[u] = load_vec<T, V>(static_cast<const T*>(side.dy) + at.t * side.dy_token + at.h * side.dy_head + l.d0);
-          }
-          at.step(32 / G, side.heads);
+    if (n > 0) {
+      const Two<T> g = lane_weights<T>(p, side, l);
+      const Place start = place_of(first * p.chunk * H + lane / G, side.heads);
+      Walk ahead(start), at(start);  // of the copies, and of the rounds
+      const char* x_at = static_cast<const char*>(side.x) + sizeof(T) * (start.t * side.x_token + start.h * side.x_head + l.a);
+      const char* dy_at = static_cast<const char*>(side.dy) + sizeof(T) * (start.t * side.dy_token + start.h * side.dy_head + l.a);
+      char* out_at = static_cast<char*>(side.out) + sizeof(T) * (start.t * side.out_token + start.h * side.out_head + l.a);
+      const int to_b = static_cast<int>(sizeof(T)) * (l.b - l.a);
+      ahead.left = at.left = p.chunk;
+      int fill = 0, take = 0;
+      auto copy = [&](bool more) {
+        if (more && ahead.t < p.tokens) {
+          if (l.on_a) nsptx::cp_async16(ring + fill, x_at);
+          if (l.on_b) nsptx::cp_async16(ring + fill + 32, x_at + to_b);
+          if (GRAD && l.on_a) nsptx::cp_async16(ring + fill + 64, dy_at);
+          if (GRAD && l.on_b) nsptx::cp_async16(ring + fill + 96, dy_at + to_b);
         }
-      }
-      Place at(first, side.heads);
-      long long angles_of = -1;
+        nsptx::cp_async_commit();
+        const bool jump = ahead.step(p, which, side.heads), wrap = ahead.wrapped;
+        x_at += (jump ? side.between[0] : side.within[0]) + (wrap ? side.wrap[0] : 0);
+        if (GRAD) dy_at += (jump ? side.between[1] : side.within[1]) + (wrap ? side.wrap[1] : 0);
+        fill = fill + STAGE == STAGES * STAGE ? 0 : fill + STAGE;
+      };
+      for (int r = 0; r < QK_AHEAD; ++r) copy(r < n);
+      int angles_of = -1;
       const float* row = nullptr;
-      float c[V], s[V];
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        bool live = first + u * (32 / G) < pairs;
-        if (live && p.rot_dim && at.t != angles_of) {
+      Angles<T> angles;
+      for (int r = 0; r < n; ++r) {
+        copy(r + QK_AHEAD < n);
+        nsptx::cp_async_wait<QK_AHEAD>();
+        bool live = at.t < p.tokens;  // of a whole group of lanes; the others' values go nowhere
+        const Two<T> xf = unpack<T>(ring + take);
+        Two<T> u;
+        if (GRAD) u = unpack<T>(ring + take + 64);
+        take = take + STAGE == STAGES * STAGE ? 0 : take + STAGE;
+        if (p.rot_dim && live && at.t != angles_of) {
           row = table_row(p, at.t);
-          load_angles<T>(p, l, row, c, s);
+          if (row) load_angles<T>(p, l, row, angles);
           angles_of = at.t;
         }
         if (p.rot_dim && !row) live = false;
-        const Vec<T, V> other = from_partner<T>(dy[u], l.partner);
-        float xf[V], t[V], sum = 0.0f, dot = 0.0f;
+        float2 s2 = make_float2(0.0f, 0.0f);
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-          xf[i] = get(x[u], i);
-          t[i] = get(dy[u], i);
+        for (int i = 0; i < N; ++i) {
+          s2 = fma2(xf.a[i], xf.a[i], s2);
+          s2 = fma2(xf.b[i], xf.b[i], s2);
         }
-        if (l.rotated) {
-          if (p.interleaved) {
+        const float r_norm = rsqrtf(fmaf(group_sum<G>(s2.x + s2.y), inv_dim, p.eps));
+        const float2 r2 = make_float2(r_norm, r_norm);
+        if (!GRAD) {
 #pragma unroll
-            for (int i = 0; i < V; i += 2) {
-              const float a = t[i], b = t[i + 1];
-              t[i] = a * c[i / 2] + b * s[i / 2];
-              t[i + 1] = b * c[i / 2] - a * s[i / 2];
+          for (int i = 0; i < N; ++i) {
+            u.a[i] = mul2(xf.a[i], mul2(g.a[i], r2));
+            u.b[i] = mul2(xf.b[i], mul2(g.b[i], r2));
+          }
+          turn<T>(p, l, angles, u, 1.0f);
+        } else {
+          turn<T>(p, l, angles, u, -1.0f);
+          if (live) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+              dg.a[i] = fma2(u.a[i], mul2(xf.a[i], r2), dg.a[i]);
+              dg.b[i] = fma2(u.b[i], mul2(xf.b[i], r2), dg.b[i]);
             }
-          } else {
+          }
+          float2 d2 = make_float2(0.0f, 0.0f);
 #pragma unroll
-            for (int i = 0; i < V; ++i) t[i] = t[i] * c[i] - l.sign * (get(other, i) * s[i]);
+          for (int i = 0; i < N; ++i) {
+            u.a[i] = mul2(u.a[i], g.a[i]);
+            u.b[i] = mul2(u.b[i], g.b[i]);
+            d2 = fma2(u.a[i], xf.a[i], d2);
+            d2 = fma2(u.b[i], xf.b[i], d2);
+          }
+          const float m = -r_norm * r_norm * r_norm * (group_sum<G>(d2.x + d2.y) * inv_dim);
+          const float2 m2 = make_float2(m, m);
+#pragma unroll
+          for (int i = 0; i < N; ++i) {
+            u.a[i] = fma2(u.a[i], r2, mul2(xf.a[i], m2));
+            u.b[i] = fma2(u.b[i], r2, mul2(xf.b[i], m2));
           }
         }
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-          sum = fmaf(xf[i], xf[i], sum);
-          dot = fmaf(t[i] * g[i], xf[i], dot);
-        }
-        sum = group_sum<G>(sum);
-        dot = group_sum<G>(dot);
-        const float r = rsqrtf(sum / p.dim + p.eps);
-        const float m = r * r * (dot / p.dim);
-        if (live && l.on) {
-          float dx[V];
-#pragma unroll
-          for (int i = 0; i < V; ++i) {
-            dg[i] = fmaf(t[i], xf[i] * r, dg[i]);
-            dx[i] = r * (t[i] * g[i] - xf[i] * m);
-          }
-          store_vec<T, V>(static_cast<T*>(side.out) + at.t * side.out_token + at.h * side.out_head + l.d0,
-                          pack<T, V>(dx));
-        }
-        at.step(32 / G, side.heads);
+        if (live) store_words<T>(out_at, to_b, l, u);
+        const bool jump = at.step(p, which, side.heads);
+        out_at += (jump ? side.between[2] : side.within[2]) + (at.wrapped ? side.wrap[2] : 0);
       }
+      nsptx::cp_async_wait<0>();
     }
-    if (!p.partial) continue;
+    if (GRAD && p.partial) {
+      float(*joined)[2 * G * V] = reinterpret_cast<float(*)[2 * G * V]>(ring_smem);  // the rings are done with
+      __syncthreads();
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
+      for (int i = 0; i < N; ++i) {
+        float* d = reinterpret_cast<float*>(&dg.a[i]);
+        float* e = reinterpret_cast<float*>(&dg.b[i]);
 #pragma unroll
-      for (int o = G; o < 32; o <<= 1) dg[i] += __shfl_xor_sync(0xffffffffu, dg[i], o);
-      if (lane < G) joined[warp][lane * V + i] = dg[i];
+        for (int k = 0; k < 2; ++k) {
+#pragma unroll
+          for (int o = G; o < 32; o <<= 1) {
+            d[k] += __shfl_xor_sync(0xffffffffu, d[k], o);
+            e[k] += __shfl_xor_sync(0xffffffffu, e[k], o);
+          }
+          if (lane < G && l.on_a) joined[warp][l.a + 2 * i + k] = d[k];
+          if (lane < G && l.on_b) joined[warp][l.b + 2 * i + k] = e[k];
+        }
+      }
+      __syncthreads();
+      for (int d = threadIdx.x; d < p.dim; d += QK_THREADS) {
+        float sum = 0.0f;
+#pragma unroll
+        for (int k = 0; k < QK_WARPS; ++k) sum += joined[k][d];
+        p.partial[(static_cast<long long>(blockIdx.x) * 2 + which) * p.dim + d] = sum;
+      }
+      __syncthreads();
     }
-    __syncthreads();
-    for (int d = threadIdx.x; d < p.dim; d += QK_THREADS) {
-      float sum = 0.0f;
-#pragma unroll
-      for (int k = 0; k < QK_WARPS; ++k) sum += joined[k][d];
-      p.partial[(static_cast<long long>(blockIdx.x) * 2 + which) * p.dim + d] = sum;
-    }
-    __syncthreads();
   }
 }
 
@@ -371,7 +440,7 @@ __global__ void __launch_bounds__(QK_ANY_THREADS) ns_qk_any_kernel(const __grid_
       for (int d = lane; d < D; d += 32) dg[d] = 0.0f;
     for (long long pair = static_cast<long long>(blockIdx.x) * WARPS + warp; pair < pairs;
          pair += static_cast<long long>(gridDim.x) * WARPS) {
-      const Place at(pair, side.heads);
+      const Place at = place_of(static_cast<int>(pair), side.heads);
       const float* row = p.rot_dim ? table_row(p, at.t) : nullptr;
       if (p.rot_dim && !row) continue;
       const T* x = static_cast<const T*>(side.x) + at.t * side.x_token + at.h * side.x_head;
@@ -465,24 +534,40 @@ __global__ void __launch_bounds__(256) ns_qk_sum_kernel(const __grid_constant__ 
 
 template <typename T, int G>
 cudaError_t launch_lanes(bool grad, QkParams& p, int nsm, int* blocks, cudaStream_t st) {
-  constexpr int U = 4, PER = U * (32 / G);
-  const long long qw = (p.tokens * p.side[0].heads + PER - 1) / PER, kw = (p.tokens * p.side[1].heads + PER - 1) / PER;
-  if (grad) {
-    const long long want = (std::max(qw, kw) + QK_WARPS - 1) / QK_WARPS;
-    *blocks = static_cast<int>(std::max<long long>(1, std::min<long long>(want, std::min(nsm * 4, QK_MAX_BLOCKS))));
-    return launch_pdl(ns_qk_grad_kernel<T, G, 2>, dim3(*blocks), dim3(QK_THREADS), 0, st, p);
+  constexpr int H = 32 / G;
+  const int most = std::min(nsm * (grad ? QK_GRAD_BLOCKS : QK_BLOCKS), QK_MAX_BLOCKS);
+  // up to 8 rounds a chunk (a token's angles serve them all: 16384 tokens of 32/8 heads take 131, 107, 97
+  // and 93 us backward with 1, 2, 4 and 8), but 4 chunks a warp, so that the warps end together
+  const int rounds = static_cast<int>((p.tokens * (p.side[0].heads + p.side[1].heads) + H - 1) / H);
+  p.chunk = std::min(8, std::max(1, rounds / (most * QK_WARPS * 4)));
+  for (int i = 0; i < 2; ++i)
+    p.chunks[i] = static_cast<int>((p.tokens * p.side[i].heads + H * p.chunk - 1) / (H * p.chunk));
+  *blocks = std::min((p.chunks[0] + p.chunks[1] + QK_WARPS - 1) / QK_WARPS, most);
+  for (int i = 0; i < 2; ++i) {
+    if (!p.side[i].heads) continue;
+    p.within[i] = place_of(H, p.side[i].heads);
+    p.between[i] = place_of(H + (*blocks * QK_WARPS - 1) * p.chunk * H, p.side[i].heads);
+    QkSide& s = p.side[i];
+    const long long token[3] = {s.x_token, s.dy_token, s.out_token}, head[3] = {s.x_head, s.dy_head, s.out_head};
+    for (int k = 0; k < 3; ++k) {
+      s.within[k] = static_cast<long long>(sizeof(T)) * (p.within[i].t * token[k] + p.within[i].h * head[k]);
+      s.between[k] = static_cast<long long>(sizeof(T)) * (p.between[i].t * token[k] + p.between[i].h * head[k]);
+      s.wrap[k] = static_cast<long long>(sizeof(T)) * (token[k] - s.heads * head[k]);
+    }
   }
-  p.q_warps = qw;
-  const long long n = (qw + kw + QK_WARPS - 1) / QK_WARPS;
-  if (n > INT_MAX) return cudaErrorInvalidValue;
-  return launch_pdl(ns_qk_kernel<T, G, U>, dim3(static_cast<unsigned>(n)), dim3(QK_THREADS), 0, st, p);
+  const size_t smem = sizeof(uint4) * QK_WARPS * (QK_AHEAD + 1) * (grad ? 128 : 64);
+  if (!grad) return launch_pdl(ns_qk_kernel<T, G, false>, dim3(*blocks), dim3(QK_THREADS), smem, st, p);
+  const cudaError_t e = cudaFuncSetAttribute(ns_qk_kernel<T, G, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             static_cast<int>(smem));
+  if (e != cudaSuccess) return e;
+  return launch_pdl(ns_qk_kernel<T, G, true>, dim3(*blocks), dim3(QK_THREADS), smem, st, p);
 }
 
 template <typename T>
 cudaError_t launch_qk(bool grad, bool lanes, QkParams& p, int nsm, int* blocks, cudaStream_t st) {
   constexpr int V = Lane<T>::V;
   if (lanes) {
-    const int need = p.dim / V;
+    const int need = (p.dim / V + 1) / 2;
     if (need <= 4) return launch_lanes<T, 4>(grad, p, nsm, blocks, st);
     if (need <= 8) return launch_lanes<T, 8>(grad, p, nsm, blocks, st);
     if (need <= 16) return launch_lanes<T, 16>(grad, p, nsm, blocks, st);
@@ -523,7 +608,8 @@ int run_qk(bool grad, const void* const* x, const void* const* dy, void* const* 
   if (rot_dim > 0 && !table) return NS_ERR_ARG;
   if (positions && position_bytes != 4 && position_bytes != 8) return NS_ERR_ARG;
   const int most = std::max(heads[0], heads[1]);
-  if (most > 0 && tokens > INT64_MAX / 4 / most / head_dim) return NS_ERR_SHAPE;
+  const int64_t both = static_cast<int64_t>(heads[0]) + heads[1];
+  if (both > 0 && tokens > INT_MAX / 2 / both) return NS_ERR_SHAPE;
   const bool sums = grad && (grad_weight[0] || grad_weight[1]);
   for (int i = 0; i < 2; ++i) {
     if (tokens == 0 || heads[i] == 0) continue;
@@ -535,7 +621,7 @@ int run_qk(bool grad, const void* const* x, const void* const* dy, void* const* 
   if ((tokens == 0 || most == 0) && !sums) return NS_OK;
   nsk::QkParams p = {};
   const int b = dtype == NS_DT_FP32 ? 4 : 2, V = 16 / b;
-  bool lanes = head_dim % V == 0 && head_dim / V <= 32 && rot_dim % (interleaved ? V : 2 * V) == 0 &&
+  bool lanes = head_dim % V == 0 && head_dim / V <= 64 && rot_dim % (interleaved ? V : 2 * V) == 0 &&
                (reinterpret_cast<uintptr_t>(table) & 15) == 0;
   // strides: (token, head) of x, of out and, for the gradient, of dy; queries then keys of each
   for (int i = 0; i < 2; ++i) {
@@ -554,7 +640,7 @@ int run_qk(bool grad, const void* const* x, const void* const* dy, void* const* 
       s.dy_head = strides[9 + 2 * i];
     }
     if (heads[i] == 0) continue;
-    lanes = lanes && words_ok(s.x, s.x_token, s.x_head, b) && words_ok(s.out, s.out_token, s.out_head, b) &&
+    lanes = lanes && (reinterpret_cast<uintptr_t>(s.weight) & 15) == 0 && words_ok(s.x, s.x_token, s.x_head, b) && words_ok(s.out, s.out_token, s.out_head, b) &&
             (!grad || words_ok(s.dy, s.dy_token, s.dy_head, b));
   }
   p.tokens = tokens;
