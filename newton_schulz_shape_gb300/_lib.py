@@ -94,10 +94,10 @@ _SIGS = {
     "ns_moe_combine": (_int, [_ptr, _i64, _int, _i64, _int, _i64, _ptr, _ptr, _i64, _ptr, _i64, _ptr]),
     "ns_moe_combine_grad": (_int, [_ptr, _i64, _ptr, _i64, _int, _i64, _int, _i64, _ptr, _ptr, _ptr, _i64, _ptr,
                                    _i64, _ptr, _ptr]),
-    "ns_qk_norm_rope": (_int, [_ptr, _ptr, _ptr, _ptr, _i64p, _int, _i64, _int, _int, _int, _int, _int, _ptr, _ptr,
+    "ns_qk_norm_rope": (_int, [_ptr, _ptr, _ptr, _ptr, _ptr, _int, _i64, _int, _int, _int, _int, _int, _ptr, _ptr,
                                _int, _f32, _ptr, _i64, _ptr, _int, _ptr]),
     "ns_qk_norm_rope_grad_workspace_bytes": (_int, [_int, _u64p]),
-    "ns_qk_norm_rope_grad": (_int, [_ptr, _ptr, _ptr, _ptr, _ptr, _ptr, _i64p, _int, _i64, _int, _int, _int, _int,
+    "ns_qk_norm_rope_grad": (_int, [_ptr, _ptr, _ptr, _ptr, _ptr, _ptr, _ptr, _int, _i64, _int, _int, _int, _int,
                                     _int, _ptr, _ptr, _int, _ptr, _ptr, _f32, _ptr, _i64, _ptr, _int, _ptr,
                                     ctypes.c_uint64, _ptr]),
     "ns_distill_loss": (_int, [_ptr, _i64, _int, _i64, _i64, _ptr, _int, _ptr, _int, _int, _ptr, _ptr, _f32, _ptr,

@@ -30,7 +30,8 @@ constexpr int SORT_THREADS = 512;
 constexpr int SORT_WARPS = SORT_THREADS / 32;
 constexpr int SORT_HELD = 4;  // rounds of 32 slots that a warp keeps in registers
 constexpr int SORT_MAX_BLOCKS = 256;
-constexpr int ROW_THREADS = 256;
+constexpr int ROW_THREADS = 128;
+constexpr int CLEAR_ROWS = 4;
 
 struct SortParams {
   const void* ids;
@@ -239,15 +240,17 @@ __device__ __forceinline__ int lane_row(const RowParams& p, long long t, int lan
   return r;
 }
 
-// Clears those of 32 rows that hold no slot.
+// Clears those of CLEAR_ROWS rows that hold no slot. Few rows a warp: they come
+// in runs (the ends of segments), and a warp with 32 of them to clear would end
+// long after the others.
 template <typename T, int V>
 __device__ __forceinline__ void clear_rows(const RowParams& p, long long group, int lane) {
-  const long long r = group * 32 + lane;
-  unsigned todo = __ballot_sync(0xffffffffu, r < p.rows && p.slot_of_row[r] < 0);
+  const long long r = group * CLEAR_ROWS + lane;
+  unsigned todo = __ballot_sync(0xffffffffu, lane < CLEAR_ROWS && r < p.rows && p.slot_of_row[r] < 0);
   while (todo) {
     const int i = __ffs(todo) - 1;
     todo &= todo - 1;
-    T* row = static_cast<T*>(p.dst) + (group * 32 + i) * p.dst_ld;
+    T* row = static_cast<T*>(p.dst) + (group * CLEAR_ROWS + i) * p.dst_ld;
     for (long long c = lane * V; c < p.dim; c += 32 * V) store_vec<T, V>(row + c, zero_vec<T, V>());
   }
 }
@@ -438,7 +441,7 @@ cudaError_t launch_rows(RowOp op, nsk::RowParams& p, cudaStream_t st) {
     p.parts = static_cast<int>(pieces);
   }
   p.token_warps = p.tokens * p.parts;
-  const long long all = p.token_warps + (op == GATHER ? 0 : (p.rows + 31) / 32);
+  const long long all = p.token_warps + (op == GATHER ? 0 : (p.rows + CLEAR_ROWS - 1) / CLEAR_ROWS);
   const long long blocks = (all + warps - 1) / warps;
   if (blocks > INT_MAX) return cudaErrorInvalidValue;
   const dim3 grid(static_cast<unsigned>(blocks)), block(ROW_THREADS);
@@ -451,7 +454,7 @@ template <typename T>
 cudaError_t launch_rows_of(RowOp op, bool wide, nsk::RowParams& p, cudaStream_t st) {
   constexpr int V = 16 / sizeof(T);
   if (op == GATHER) return wide ? launch_rows<T, V, 2>(op, p, st) : launch_rows<T, 1, 8>(op, p, st);
-  return wide ? launch_rows<T, V, 8>(op, p, st) : launch_rows<T, 1, 8>(op, p, st);
+  return wide ? launch_rows<T, V, 4>(op, p, st) : launch_rows<T, 1, 8>(op, p, st);
 }
 
 int run_rows(RowOp op, int dtype, nsk::RowParams& p, bool wide, void* stream) {

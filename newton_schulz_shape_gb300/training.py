@@ -12,6 +12,7 @@ to torch's current stream.
 from __future__ import annotations
 
 import ctypes
+import struct
 
 import torch
 
@@ -21,23 +22,29 @@ _DTYPES = {torch.bfloat16: NS_DT_BF16, torch.float16: NS_DT_FP16, torch.float32:
 _INDEX_BYTES = {torch.int32: 4, torch.int64: 8}
 
 
+# The calls below are written for few attribute reads and calls: at the sizes
+# of a decoding step the host's part is most of a call.
+_raw_stream, _device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+
+
 def _stream(stream) -> int:
     if stream is None:
-        # the handle alone: building a torch.cuda.Stream object costs 3.5 us of a small call
-        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+        # the handle alone: building a torch.cuda.Stream object costs 3.5 us
+        return _raw_stream(_device())
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
 def _bad(name, t, want):
-    got = f"{t.dtype} {tuple(t.shape)} on {t.device}" if isinstance(t, torch.Tensor) else type(t).__name__
+    got = f"{t.dtype} {tuple(t.shape)} strides {t.stride()} on {t.device}" if isinstance(t, torch.Tensor) else type(t).__name__
     raise ValueError(f"{name}: {want}, got {got}")
 
 
 def _rows2d(name, t, dtype, rows=None, cols=None):
     """Address and row stride of a [rows, cols] tensor with contiguous rows."""
-    if not t.is_cuda or t.dtype != dtype or t.dim() != 2:
+    shape = t.shape
+    if not t.is_cuda or t.dtype is not dtype or len(shape) != 2:
         _bad(name, t, f"a GPU matrix of {dtype}")
-    n, d = t.shape
+    n, d = shape
     if (rows is not None and n != rows) or (cols is not None and d != cols):
         _bad(name, t, f"shape ({rows}, {cols})")
     ld, inner = t.stride()
@@ -50,15 +57,16 @@ def _whole(name, t, dtype, numel):
     """Address of a contiguous tensor of `numel` values; None passes as NULL."""
     if t is None:
         return 0
-    if not t.is_cuda or t.dtype != dtype or t.numel() != numel or not t.is_contiguous():
+    if not t.is_cuda or t.dtype is not dtype or t.numel() != numel or not t.is_contiguous():
         _bad(name, t, f"{numel} contiguous GPU values of {dtype}")
     return t.data_ptr()
 
 
 def _indices(name, t, numel):
-    if not t.is_cuda or t.dtype not in _INDEX_BYTES or t.numel() != numel or not t.is_contiguous():
+    size = _INDEX_BYTES.get(t.dtype)
+    if size is None or not t.is_cuda or t.numel() != numel or not t.is_contiguous():
         _bad(name, t, f"{numel} contiguous GPU indices (int32 or int64)")
-    return t.data_ptr(), _INDEX_BYTES[t.dtype]
+    return t.data_ptr(), size
 
 
 def _scratch(t):
@@ -66,7 +74,7 @@ def _scratch(t):
         return 0, 0
     if not t.is_cuda or not t.is_contiguous():
         _bad("workspace", t, "a contiguous GPU tensor")
-    return t.data_ptr(), t.numel() * t.element_size()
+    return t.data_ptr(), t.nbytes
 
 
 def _dtype(name, t):
@@ -165,26 +173,35 @@ def ns_moe_combine_grad(grad_y, expert_rows, weights, row_of_slot, slot_of_row, 
 
 
 # ------------------------------------------------------- queries and keys
-def _heads(name, t, like=None):
-    """(address, token stride, head stride) of a [tokens, heads, dim] tensor."""
-    if not t.is_cuda or t.dim() != 3:
-        _bad(name, t, "a GPU tensor [tokens, heads, dim]")
-    if like is not None and (t.dtype != like.dtype or t.shape != like.shape):
-        _bad(name, t, f"{like.dtype} {tuple(like.shape)}")
+_pack8, _pack12 = struct.Struct("8q").pack, struct.Struct("12q").pack
+
+
+def _check_heads(names, tensors, q, k):
+    """Say what is wrong with queries, keys or what has their shapes."""
+    for name, t, like in zip(names, tensors, (q, k) * 3):
+        if not t.is_cuda or t.dim() != 3:
+            _bad(name, t, "a GPU tensor [tokens, heads, dim]")
+        if t.dtype is not q.dtype:
+            _bad(name, t, f"{q.dtype}, as q")
+        if t.shape != like.shape:
+            _bad(name, t, f"shape {tuple(like.shape)}")
+    if k.shape[0] != q.shape[0] or k.shape[2] != q.shape[2]:
+        _bad("k", k, f"({q.shape[0]}, heads, {q.shape[2]})")
+
+
+def _heads(name, t, dim):
+    """(token stride, head stride) of a [tokens, heads, dim] tensor."""
     token, head, inner = t.stride()
-    if inner != 1 and t.shape[2] > 1:
+    if inner != 1 and dim > 1:
         _bad(name, t, "contiguous heads")
-    return t.data_ptr(), token, head
+    return token, head
 
 
-def _qk_common(q, k, q_weight, k_weight, table, positions):
-    tokens, q_heads, dim = q.shape
-    if k.dim() != 3 or k.shape[0] != tokens or k.shape[2] != dim or k.dtype != q.dtype:
-        _bad("k", k, f"{q.dtype} ({tokens}, heads, {dim})")
-    first = q_weight if q_weight is not None else k_weight
-    wt = first.dtype if first is not None else q.dtype
-    if wt != q.dtype and wt != torch.float32:
-        _bad("q_weight", first, f"{q.dtype} or float32")
+def _qk_common(q, dim, tokens, q_weight, k_weight, table, positions):
+    wt = q_weight.dtype if q_weight is not None else k_weight.dtype if k_weight is not None else q.dtype
+    if wt is not q.dtype and wt is not torch.float32:
+        _bad("q_weight" if q_weight is not None else "k_weight", q_weight if q_weight is not None else k_weight,
+             f"{q.dtype} or float32")
     qw, kw = _whole("q_weight", q_weight, wt, dim), _whole("k_weight", k_weight, wt, dim)
     tp, table_rows, rot = 0, 0, 0
     if table is not None:
@@ -193,7 +210,7 @@ def _qk_common(q, k, q_weight, k_weight, table, positions):
         table_rows, rot = table.shape
         tp = _whole("table", table, torch.float32, table_rows * rot)
     pp, pb = (0, 4) if positions is None else _indices("positions", positions, tokens)
-    return (_dtype("q", q), tokens, q_heads, k.shape[1], dim, rot), (qw, kw, _DTYPES[wt]), (tp, table_rows, pp, pb)
+    return qw, kw, _DTYPES[wt] if wt in _DTYPES else _dtype("q", q), tp, table_rows, rot, pp, pb
 
 
 def ns_qk_norm_rope(q, k, q_out, k_out, q_weight=None, k_weight=None, table=None, positions=None, eps: float = 1e-6,
@@ -201,14 +218,19 @@ def ns_qk_norm_rope(q, k, q_out, k_out, q_weight=None, k_weight=None, table=None
     """Root-mean-square norm of every head of q and k [tokens, heads, dim], then
     the rotation by table [positions, rot_dim] (cosines, then sines) at
     positions [tokens] (None: 0, 1, ...). Tokens and heads may be strided."""
-    qp, qt, qh = _heads("q", q)
-    kp, kt, kh = _heads("k", k)
-    qo, qot, qoh = _heads("q_out", q_out, q)
-    ko, kot, koh = _heads("k_out", k_out, k)
-    sizes, weights, rotation = _qk_common(q, k, q_weight, k_weight, table, positions)
-    strides = (ctypes.c_int64 * 8)(qt, qh, kt, kh, qot, qoh, kot, koh)
-    check(lib.ns_qk_norm_rope(qp, kp, qo, ko, strides, *sizes, 1 if interleaved else 0, *weights, eps, *rotation,
-                              _stream(stream)), "ns_qk_norm_rope")
+    dtype, shape, k_shape = q.dtype, q.shape, k.shape
+    if not (q.is_cuda and k.is_cuda and q_out.is_cuda and k_out.is_cuda and len(shape) == 3 and len(k_shape) == 3
+            and k.dtype is dtype and q_out.dtype is dtype and k_out.dtype is dtype and q_out.shape == shape
+            and k_out.shape == k_shape and k_shape[0] == shape[0] and k_shape[2] == shape[2]):
+        _check_heads(("q", "k", "q_out", "k_out"), (q, k, q_out, k_out), q, k)
+    tokens, heads, dim = shape
+    qw, kw, wt, tp, table_rows, rot, pp, pb = _qk_common(q, dim, tokens, q_weight, k_weight, table, positions)
+    strides = _pack8(*_heads("q", q, dim), *_heads("k", k, dim), *_heads("q_out", q_out, dim), *_heads("k_out", k_out, dim))
+    rc = lib.ns_qk_norm_rope(q.data_ptr(), k.data_ptr(), q_out.data_ptr(), k_out.data_ptr(), strides, _dtype("q", q), tokens,
+                             heads, k_shape[1], dim, rot, 1 if interleaved else 0, qw, kw, wt, eps, tp, table_rows, pp,
+                             pb, _stream(stream))
+    if rc:
+        check(rc, "ns_qk_norm_rope")
 
 
 def ns_qk_norm_rope_grad_workspace_bytes(head_dim: int) -> int:
@@ -222,35 +244,40 @@ def ns_qk_norm_rope_grad(grad_q_out, grad_k_out, q, k, grad_q, grad_k, q_weight=
                          eps: float = 1e-6, interleaved: bool = False, stream=None) -> None:
     """Gradient of ns_qk_norm_rope: grad_q, grad_k and, where given, the fp32
     weight gradients [dim] (these need the workspace)."""
-    qp, qt, qh = _heads("q", q)
-    kp, kt, kh = _heads("k", k)
-    dq, dqt, dqh = _heads("grad_q", grad_q, q)
-    dk, dkt, dkh = _heads("grad_k", grad_k, k)
-    gq, gqt, gqh = _heads("grad_q_out", grad_q_out, q)
-    gk, gkt, gkh = _heads("grad_k_out", grad_k_out, k)
-    sizes, weights, rotation = _qk_common(q, k, q_weight, k_weight, table, positions)
-    strides = (ctypes.c_int64 * 12)(qt, qh, kt, kh, dqt, dqh, dkt, dkh, gqt, gqh, gkt, gkh)
-    dim = q.shape[2]
+    _check_heads(("q", "k", "grad_q", "grad_k", "grad_q_out", "grad_k_out"),
+                 (q, k, grad_q, grad_k, grad_q_out, grad_k_out), q, k)
+    tokens, heads, dim = q.shape
+    qw, kw, wt, tp, table_rows, rot, pp, pb = _qk_common(q, dim, tokens, q_weight, k_weight, table, positions)
+    strides = _pack12(*_heads("q", q, dim), *_heads("k", k, dim), *_heads("grad_q", grad_q, dim),
+                      *_heads("grad_k", grad_k, dim), *_heads("grad_q_out", grad_q_out, dim),
+                      *_heads("grad_k_out", grad_k_out, dim))
     ws, ws_bytes = _scratch(workspace)
-    check(lib.ns_qk_norm_rope_grad(gq, gk, qp, kp, dq, dk, strides, *sizes, 1 if interleaved else 0, *weights,
+    check(lib.ns_qk_norm_rope_grad(grad_q_out.data_ptr(), grad_k_out.data_ptr(), q.data_ptr(), k.data_ptr(),
+                                   grad_q.data_ptr(), grad_k.data_ptr(), strides, _dtype("q", q), tokens, heads,
+                                   k.shape[1], dim, rot, 1 if interleaved else 0, qw, kw, wt,
                                    _whole("grad_q_weight", grad_q_weight, torch.float32, dim),
-                                   _whole("grad_k_weight", grad_k_weight, torch.float32, dim), eps, *rotation, ws,
-                                   ws_bytes, _stream(stream)), "ns_qk_norm_rope_grad")
+                                   _whole("grad_k_weight", grad_k_weight, torch.float32, dim), eps, tp, table_rows, pp,
+                                   pb, ws, ws_bytes, _stream(stream)), "ns_qk_norm_rope_grad")
 
 
 # ------------------------------------------------------------ distillation
-def _distill_args(logits, teacher_values, teacher_ids, weights, teacher_lse, temperature):
-    lp, ld = _rows2d("logits", logits, logits.dtype)
+def _distill_args(logits, teacher_values, teacher_ids, weights, teacher_lse, temperature, grad_logits):
+    """The common arguments, up to the temperature, and the gradient's address and stride."""
+    dtype = logits.dtype
+    lp, ld = _rows2d("logits", logits, dtype)
     tokens, vocab = logits.shape
-    if teacher_values.dim() != 2 or teacher_ids.shape != teacher_values.shape:
+    shape = teacher_values.shape
+    if len(shape) != 2 or teacher_ids.shape != shape:
         _bad("teacher_ids", teacher_ids, f"the shape of teacher_values, ({tokens}, top)")
-    top = teacher_values.shape[1]
-    ids, id_bytes = _indices("teacher_ids", teacher_ids, tokens * top)
-    return (lp, ld, _dtype("logits", logits), tokens, vocab,
-            _whole("teacher_values", teacher_values, teacher_values.dtype, tokens * top),
-            _dtype("teacher_values", teacher_values), ids, id_bytes, top,
-            _whole("weights", weights, torch.float32, tokens),
-            _whole("teacher_lse", teacher_lse, torch.float32, tokens), temperature)
+    top = shape[1]
+    n = tokens * top
+    ids, id_bytes = _indices("teacher_ids", teacher_ids, n)
+    t_dtype = teacher_values.dtype
+    values = _whole("teacher_values", teacher_values, t_dtype, n)
+    grad = (0, 0) if grad_logits is None else _rows2d("grad_logits", grad_logits, dtype, tokens, vocab)
+    return (lp, ld, _dtype("logits", logits), tokens, vocab, values, _dtype("teacher_values", teacher_values), ids,
+            id_bytes, top, 0 if weights is None else _whole("weights", weights, torch.float32, tokens),
+            0 if teacher_lse is None else _whole("teacher_lse", teacher_lse, torch.float32, tokens), temperature), grad
 
 
 def ns_distill_loss(logits, teacher_values, teacher_ids, loss, lse, grad_logits=None, weights=None, teacher_lse=None,
@@ -258,21 +285,21 @@ def ns_distill_loss(logits, teacher_values, teacher_ids, loss, lse, grad_logits=
     """Divergence of the student's softmax from the teacher's top entries:
     loss and lse fp32 [tokens] and, if grad_logits is given, the gradient in the
     logits [tokens, vocab] in the same pass. grad_logits may be logits itself."""
-    args = _distill_args(logits, teacher_values, teacher_ids, weights, teacher_lse, temperature)
-    tokens, vocab = logits.shape
-    gp, g_ld = (0, 0) if grad_logits is None else _rows2d("grad_logits", grad_logits, logits.dtype, tokens, vocab)
-    check(lib.ns_distill_loss(*args, _whole("loss", loss, torch.float32, tokens),
-                              _whole("lse", lse, torch.float32, tokens), gp, g_ld, _stream(stream)), "ns_distill_loss")
+    args, (gp, g_ld) = _distill_args(logits, teacher_values, teacher_ids, weights, teacher_lse, temperature, grad_logits)
+    tokens = args[3]
+    rc = lib.ns_distill_loss(*args, _whole("loss", loss, torch.float32, tokens),
+                             _whole("lse", lse, torch.float32, tokens), gp, g_ld, _stream(stream))
+    if rc:
+        check(rc, "ns_distill_loss")
 
 
 def ns_distill_grad(logits, teacher_values, teacher_ids, lse, grad_logits, weights=None, teacher_lse=None,
                     temperature: float = 1.0, stream=None) -> None:
     """The gradient alone, from the lse that ns_distill_loss wrote."""
-    args = _distill_args(logits, teacher_values, teacher_ids, weights, teacher_lse, temperature)
-    tokens, vocab = logits.shape
-    gp, g_ld = _rows2d("grad_logits", grad_logits, logits.dtype, tokens, vocab)
-    check(lib.ns_distill_grad(*args, _whole("lse", lse, torch.float32, tokens), gp, g_ld, _stream(stream)),
-          "ns_distill_grad")
+    args, (gp, g_ld) = _distill_args(logits, teacher_values, teacher_ids, weights, teacher_lse, temperature, grad_logits)
+    rc = lib.ns_distill_grad(*args, _whole("lse", lse, torch.float32, args[3]), gp, g_ld, _stream(stream))
+    if rc:
+        check(rc, "ns_distill_grad")
 
 
 TRAINING_KERNEL_KINDS = ("moe", "qk_norm_rope", "distill")
