@@ -355,7 +355,8 @@ int ns_moe_sort(const void* expert_ids, int id_bytes, int64_t tokens, int k, int
 
 /* out[r] = x[slot_of_row[r] / k], and 0 for every row without a slot, so that
  * a product over padded segments sees no stale values. x is [tokens][dim],
- * out [rows][dim]; row_of_slot and slot_of_row as ns_moe_sort wrote them. */
+ * out [rows][dim], dim < 2^29; row_of_slot and slot_of_row as ns_moe_sort wrote
+ * them. */
 int ns_moe_dispatch(const void* x, int64_t x_stride, int dtype, int64_t tokens, int k, int64_t dim,
                     const int32_t* row_of_slot, const int32_t* slot_of_row, int64_t rows, void* out,
                     int64_t out_stride, void* stream);

@@ -14,6 +14,8 @@
 // Sums are in fp32 in the order of j, so results do not depend on the launch.
 #include <algorithm>
 #include <climits>
+#include <initializer_list>
+#include <utility>
 
 #include "elem.cuh"
 #include "launch.cuh"
@@ -30,8 +32,12 @@ constexpr int SORT_THREADS = 512;
 constexpr int SORT_WARPS = SORT_THREADS / 32;
 constexpr int SORT_HELD = 4;  // rounds of 32 slots that a warp keeps in registers
 constexpr int SORT_MAX_BLOCKS = 256;
+constexpr int SORT_ONE_BLOCK = 3584;  // 600 x 6 slots: 9.0 us in one block, 9.6 in two launches; 680 x 6: 10.3 and 9.5
 constexpr int ROW_THREADS = 128;
 constexpr int CLEAR_ROWS = 4;
+
+// Counts of a block, a whole number of 16-byte words.
+__host__ __device__ inline int count_stride(int experts) { return (experts + 3) / 4 * 4; }
 
 struct SortParams {
   const void* ids;
@@ -43,7 +49,7 @@ struct SortParams {
   int* slot_of_row;
   int* counts;
   int* offsets;
-  int* block_counts;  // [blocks][experts]
+  int* block_counts;  // [blocks][count_stride]
   unsigned int* status;
 };
 
@@ -69,7 +75,9 @@ __global__ void __launch_bounds__(SORT_THREADS) ns_moe_count_kernel(const __grid
     if (e >= 0) atomicAdd(&sm[e], 1);
   }
   __syncthreads();
-  for (int e = threadIdx.x; e < p.experts; e += SORT_THREADS) p.block_counts[blockIdx.x * p.experts + e] = sm[e];
+  const int stride = count_stride(p.experts);
+  for (int e = threadIdx.x; e < stride; e += SORT_THREADS)
+    p.block_counts[blockIdx.x * stride + e] = e < p.experts ? sm[e] : 0;
 }
 
 // Places one chunk's slots. Warp w owns a contiguous part of the chunk, 32
@@ -123,14 +131,27 @@ __global__ void __launch_bounds__(SORT_THREADS) ns_moe_place_kernel(const __grid
   }
   if (refused) atomicOr(p.status, NS_DEV_BAD_INDEX);
   if (p.blocks > 1) {
-    const int n = p.blocks * E, earlier = static_cast<int>(blockIdx.x) * E;
-#pragma unroll 4
-    for (int i = threadIdx.x; i < n; i += SORT_THREADS) {
-      const int c = p.block_counts[i], e = i % E;
-      if (c) {
-        atomicAdd(&total[e], c);
-        if (i < earlier) atomicAdd(&before[e], c);
+    // four experts a thread; the threads that share them split the blocks
+    const int lanes = count_stride(E) / 4, group = threadIdx.x / lanes, groups = SORT_THREADS / lanes;
+    const int e = (threadIdx.x - group * lanes) * 4;
+    int all[4] = {0, 0, 0, 0}, early[4] = {0, 0, 0, 0};
+    if (group < groups) {
+#pragma unroll 8
+      for (int b = group; b < p.blocks; b += groups) {
+        const int4 c = *reinterpret_cast<const int4*>(p.block_counts + b * count_stride(E) + e);
+        const int v[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          all[i] += v[i];
+          if (b < static_cast<int>(blockIdx.x)) early[i] += v[i];
+        }
       }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (e + i < E) {
+          atomicAdd(&total[e + i], all[i]);
+          atomicAdd(&before[e + i], early[i]);
+        }
     }
   }
   __syncthreads();
@@ -397,15 +418,28 @@ namespace {
 
 int elem_bytes(int dtype) { return dtype == NS_DT_FP32 ? 4 : 2; }
 bool dtype_ok(int dtype) { return dtype == NS_DT_BF16 || dtype == NS_DT_FP16 || dtype == NS_DT_FP32; }
-bool aligned16(const void* p, long long ld, int bytes) {
-  return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && ld * bytes % 16 == 0;
+// Whether rows at p, `ld` elements apart, and their width are whole words.
+bool in_words(const void* p, long long ld, long long dim, int elem, int word) {
+  return reinterpret_cast<uintptr_t>(p) % word == 0 && ld * elem % word == 0 && dim * elem % word == 0;
+}
+// The widest word that all rows are made of: 16 bytes, 4, or an element.
+int common_word(int elem, long long dim, std::initializer_list<std::pair<const void*, long long>> rows) {
+  for (int word : {16, 4}) {
+    bool all = true;
+    for (const auto& r : rows) all = all && in_words(r.first, r.second, dim, elem, word);
+    if (all) return word;
+  }
+  return elem;
 }
 
-// Slots per block and blocks of a sort: one block up to what its warps hold in
-// registers, then as many blocks of that size, then larger blocks.
+// Slots per block and blocks of a sort. One block up to SORT_ONE_BLOCK slots
+// (more blocks need the counts first, a second launch); then blocks of what
+// their warps hold in registers, then larger blocks.
 void sort_split(long long slots, int* chunk, int* blocks) {
   constexpr int held = nsk::SORT_THREADS * nsk::SORT_HELD;
-  long long c = slots <= held ? slots : std::max<long long>(held, (slots + nsk::SORT_MAX_BLOCKS - 1) / nsk::SORT_MAX_BLOCKS);
+  long long c = slots;
+  if (slots > nsk::SORT_ONE_BLOCK)
+    c = std::max<long long>(held, (slots + nsk::SORT_MAX_BLOCKS - 1) / nsk::SORT_MAX_BLOCKS);
   c = std::max<long long>(1, (c + nsk::SORT_THREADS - 1) / nsk::SORT_THREADS) * nsk::SORT_THREADS;
   *chunk = static_cast<int>(c);
   *blocks = static_cast<int>(std::max<long long>(1, (slots + c - 1) / c));
@@ -422,21 +456,21 @@ int sort_args(int64_t tokens, int k, int experts) {
 int row_args(int dtype, int64_t tokens, int k, int64_t dim, int64_t rows) {
   if (!dtype_ok(dtype) || tokens < 0 || k < 1 || dim < 0 || rows < 0) return NS_ERR_ARG;
   if (k > nsk::MAX_K) return NS_ERR_UNSUPPORTED;
-  if (tokens > (INT_MAX - 4096) / k || rows > INT_MAX) return NS_ERR_SHAPE;
+  if (tokens > (INT_MAX - 4096) / k || rows > INT_MAX || dim > INT_MAX / 4) return NS_ERR_SHAPE;
   return NS_OK;
 }
 
 enum RowOp { DISPATCH, GATHER, COMBINE_GRAD };
 
 template <typename T, int V, int U>
-cudaError_t launch_rows(RowOp op, nsk::RowParams& p, cudaStream_t st) {
+cudaError_t launch_rows(RowOp op, nsk::RowParams& p, int nsm, cudaStream_t st) {
   using namespace nsk;
   const int warps = ROW_THREADS / 32;
   const long long pieces = (p.dim + 32 * V * U - 1) / (32 * V * U);
   if (op == COMBINE_GRAD) {
     // a token's warps sit in one block; few tokens are shared by more warps
     p.parts = 1;
-    while (p.parts < warps && p.parts < pieces && p.tokens * p.parts < 152 * 16) p.parts *= 2;
+    while (p.parts < warps && p.parts < pieces && p.tokens * p.parts < nsm * 16) p.parts *= 2;
   } else {
     p.parts = static_cast<int>(pieces);
   }
@@ -450,22 +484,27 @@ cudaError_t launch_rows(RowOp op, nsk::RowParams& p, cudaStream_t st) {
   return launch_pdl(ns_moe_combine_grad_kernel<T, V, U>, grid, block, 0, st, p);
 }
 
+// Words of 16 bytes where rows allow it, else of 4 (16-bit rows of an even
+// width), else single elements: 8192 x 6 bf16 rows of 2048, 2046 and 2047 sum
+// at 5.9, 4.2 and 3.6 TB/s.
 template <typename T>
-cudaError_t launch_rows_of(RowOp op, bool wide, nsk::RowParams& p, cudaStream_t st) {
+cudaError_t launch_rows_of(RowOp op, int word, nsk::RowParams& p, int nsm, cudaStream_t st) {
   constexpr int V = 16 / sizeof(T);
-  if (op == GATHER) return wide ? launch_rows<T, V, 2>(op, p, st) : launch_rows<T, 1, 8>(op, p, st);
-  return wide ? launch_rows<T, V, 4>(op, p, st) : launch_rows<T, 1, 8>(op, p, st);
+  if (word == 16) return op == GATHER ? launch_rows<T, V, 2>(op, p, nsm, st) : launch_rows<T, V, 4>(op, p, nsm, st);
+  if constexpr (sizeof(T) == 2)
+    if (word == 4) return launch_rows<T, 2, 8>(op, p, nsm, st);
+  return launch_rows<T, 1, 8>(op, p, nsm, st);
 }
 
-int run_rows(RowOp op, int dtype, nsk::RowParams& p, bool wide, void* stream) {
+int run_rows(RowOp op, int dtype, nsk::RowParams& p, int word, void* stream) {
   int dev, nsm;
   const int rc = device_setup(&dev, &p.status, &nsm);
   if (rc != NS_OK) return rc;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const cudaError_t e = counted(K_MOE, st, [&] {
-    if (dtype == NS_DT_BF16) return launch_rows_of<__nv_bfloat16>(op, wide, p, st);
-    if (dtype == NS_DT_FP16) return launch_rows_of<__half>(op, wide, p, st);
-    return launch_rows_of<float>(op, wide, p, st);
+    if (dtype == NS_DT_BF16) return launch_rows_of<__nv_bfloat16>(op, word, p, nsm, st);
+    if (dtype == NS_DT_FP16) return launch_rows_of<__half>(op, word, p, nsm, st);
+    return launch_rows_of<float>(op, word, p, nsm, st);
   });
   return e == cudaSuccess ? NS_OK : NS_ERR_CUDA;
 }
@@ -495,7 +534,7 @@ int ns_moe_sort_workspace_bytes(int64_t tokens, int k, int experts, uint64_t* by
   if (rc != NS_OK) return rc;
   int chunk, blocks;
   sort_split(tokens * k, &chunk, &blocks);
-  *bytes = blocks > 1 ? static_cast<uint64_t>(blocks) * experts * sizeof(int) : 0;
+  *bytes = blocks > 1 ? static_cast<uint64_t>(blocks) * nsk::count_stride(experts) * sizeof(int) : 0;
   return NS_OK;
 }
 
@@ -518,7 +557,7 @@ int ns_moe_sort(const void* expert_ids, int id_bytes, int64_t tokens, int k, int
   p.capacity = capacity > 0 && capacity < INT_MAX ? static_cast<int>(capacity) : INT_MAX;
   p.rows = static_cast<int>(rows);
   sort_split(p.slots, &p.chunk, &p.blocks);
-  const uint64_t need = p.blocks > 1 ? static_cast<uint64_t>(p.blocks) * experts * sizeof(int) : 0;
+  const uint64_t need = p.blocks > 1 ? static_cast<uint64_t>(p.blocks) * nsk::count_stride(experts) * sizeof(int) : 0;
   if (need && (!workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255)))
     return NS_ERR_WORKSPACE;
   p.row_of_slot = row_of_slot;
@@ -569,8 +608,7 @@ int ns_moe_dispatch(const void* x, int64_t x_stride, int dtype, int64_t tokens, 
   p.dim = dim;
   p.k = k;
   const int b = elem_bytes(dtype);
-  const bool wide = dim * b % 16 == 0 && aligned16(x, x_stride, b) && aligned16(out, out_stride, b);
-  return run_rows(DISPATCH, dtype, p, wide, stream);
+  return run_rows(DISPATCH, dtype, p, common_word(b, dim, {{x, x_stride}, {out, out_stride}}), stream);
 }
 
 int ns_moe_combine(const void* expert_rows, int64_t rows_stride, int dtype, int64_t tokens, int k, int64_t dim,
@@ -593,8 +631,7 @@ int ns_moe_combine(const void* expert_rows, int64_t rows_stride, int dtype, int6
   p.dim = dim;
   p.k = k;
   const int b = elem_bytes(dtype);
-  const bool wide = dim * b % 16 == 0 && aligned16(expert_rows, rows_stride, b) && aligned16(y, y_stride, b);
-  return run_rows(GATHER, dtype, p, wide, stream);
+  return run_rows(GATHER, dtype, p, common_word(b, dim, {{expert_rows, rows_stride}, {y, y_stride}}), stream);
 }
 
 int ns_moe_dispatch_grad(const void* grad_rows, int64_t rows_stride, int dtype, int64_t tokens, int k, int64_t dim,
@@ -630,9 +667,8 @@ int ns_moe_combine_grad(const void* grad_y, int64_t grad_y_stride, const void* e
   p.dim = dim;
   p.k = k;
   const int b = elem_bytes(dtype);
-  const bool wide = dim * b % 16 == 0 && aligned16(grad_y, grad_y_stride, b) &&
-                    aligned16(expert_rows, rows_stride, b) && aligned16(grad_rows, grad_rows_stride, b);
-  return run_rows(COMBINE_GRAD, dtype, p, wide, stream);
+  const int word = common_word(b, dim, {{grad_y, grad_y_stride}, {expert_rows, rows_stride}, {grad_rows, grad_rows_stride}});
+  return run_rows(COMBINE_GRAD, dtype, p, word, stream);
 }
 
 }  // extern "C"
