@@ -1,4 +1,5 @@
-"""Build libnsgb300.so in-tree with nvcc for sm_103a.
+"""Build libnsgb300.so in-tree with nvcc for sm_103a, and the Python binding of
+its training-step operators (_training.so) against the installed torch.
 
 Each translation unit compiles in parallel into ``_build/``; the shared
 library lands next to this file. Rebuilds only when a source or header is
@@ -8,9 +9,11 @@ newer than the library. No cmake, one -gencode.
 from __future__ import annotations
 
 import concurrent.futures as cf
+import importlib.util
 import os
 import shutil
 import subprocess
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -18,6 +21,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libnsgb300.so")
+BINDING = os.path.join(PKG, "_training.so")
 SOURCES = ["planner.cpp", "api.cu", "runtime.cu", "route.cu", "ns_bf16.cu", "ns_fp32.cu", "pipeline.cu",
            "gemm.cu", "gemm2sm.cu", "gemm32.cu", "prologue.cu", "pack.cu", "small.cu", "noalloc.cu",
            "moe.cu", "qk_rope.cu", "distill.cu"]
@@ -38,11 +42,43 @@ def _deps() -> list:
     return files
 
 
+def _torch_dir():
+    """Where torch is installed, without importing it; None if it is not."""
+    spec = importlib.util.find_spec("torch")
+    return os.path.dirname(spec.origin) if spec and spec.origin else None
+
+
 def _stale() -> bool:
-    if not os.path.exists(LIB):
+    made = [LIB] + ([BINDING] if _torch_dir() else [])
+    if not all(os.path.exists(f) for f in made):
         return True
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(f) for f in made)
     return any(os.path.getmtime(f) > t for f in _deps())
+
+
+def _run(cmd, what) -> str:
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{what} failed:\n{r.stdout}\n{r.stderr}")
+    return r.stdout + r.stderr
+
+
+def _compile_binding(nvcc: str) -> str:
+    """binding.cpp alone is host code on torch's headers."""
+    torch_dir, obj = _torch_dir(), os.path.join(BUILD, "binding.o")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc))), "include")
+    inc = [os.path.join(torch_dir, "include"), os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
+           sysconfig.get_paths()["include"], cuda]
+    _run(["g++", "-std=c++17", "-O2", "-fPIC", "-fvisibility=hidden", "-I", INCLUDE] + [x for d in inc for x in ("-isystem", d)]
+         + ["-c", os.path.join(CSRC, "binding.cpp"), "-o", obj], "g++ on binding.cpp")
+    return obj
+
+
+def _link_binding(obj: str) -> None:
+    tmp = BINDING + ".tmp"
+    _run(["g++", "-shared", obj, "-o", tmp, "-L", PKG, "-l:libnsgb300.so", "-Wl,-rpath,$ORIGIN",
+          "-L", os.path.join(_torch_dir(), "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"], "link of _training.so")
+    os.replace(tmp, BINDING)
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
@@ -58,12 +94,10 @@ def build(force: bool = False, verbose: bool = False) -> str:
         cmd = [nvcc] + common + ["-c", os.path.join(CSRC, src), "-o", obj]
         if src.endswith(".cu"):
             cmd += ["-Xptxas", "-v"] if verbose else []
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode != 0:
-            raise RuntimeError(f"nvcc failed on {src}:\n{r.stdout}\n{r.stderr}")
-        return obj, r.stdout + r.stderr
+        return obj, _run(cmd, f"nvcc on {src}")
 
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        binding = ex.submit(_compile_binding, nvcc) if _torch_dir() else None
         results = list(ex.map(compile_one, SOURCES))
     if verbose:
         for _, log in results:
@@ -71,10 +105,10 @@ def build(force: bool = False, verbose: bool = False) -> str:
                 print(log)
     tmp = LIB + ".tmp"
     cmd = [nvcc, "-shared"] + ARCH + ["-o", tmp] + [o for o, _ in results]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    _run(cmd, "link")
     os.replace(tmp, LIB)
+    if binding:
+        _link_binding(binding.result())
     return LIB
 
 
