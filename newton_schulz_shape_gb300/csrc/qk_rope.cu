@@ -60,7 +60,8 @@ struct QkParams {
   long long table_rows;
   const void* positions;  // null: the token's index
   int position_bytes;
-  int chunk;          // rounds of 32 / G heads that a warp takes at a time
+  int lanes;          // of a head's group
+  int chunk;          // rounds of 32 / lanes heads that a warp takes at a time
   int chunks[2];      // of the queries and of the keys
   Place within[2], between[2];  // steps of a warp from round to round: in a chunk, to its next chunk
   float* partial;     // gradient: [blocks][2][dim]
@@ -83,11 +84,21 @@ __device__ __forceinline__ float weight_at(const QkParams& p, const void* w, int
   return p.weight_fp32 ? static_cast<const float*>(w)[d] : to_float(static_cast<const T*>(w)[d]);
 }
 
+// Sum over the lanes of a group, in all of them. G lanes, a power of two, or
+// (G = 0) n, this one the i-th of them.
 template <int G>
-__device__ __forceinline__ float group_sum(float x) {
+__device__ __forceinline__ float group_sum(float x, int n, int i) {
+  if constexpr (G > 0) {
 #pragma unroll
-  for (int o = G / 2; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-  return x;
+    for (int o = G / 2; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    return x;
+  } else {
+    for (int o = 1; o < n; o <<= 1) {
+      const float y = __shfl_down_sync(0xffffffffu, x, o);
+      if (i + o < n) x += y;
+    }
+    return __shfl_sync(0xffffffffu, x, (threadIdx.x & 31) - i);
+  }
 }
 
 // A lane holds two words of 16 bytes of every head, a and b. Where the pairs
@@ -102,11 +113,12 @@ struct Lane {
   bool turn_a, turn_b; // rotated
 };
 
-template <typename T, int G>
-__device__ __forceinline__ Lane<T> lane_of(const QkParams& p, int lane) {
+// Lane i of a head's group.
+template <typename T>
+__device__ __forceinline__ Lane<T> lane_of(const QkParams& p, int i) {
   constexpr int V = Lane<T>::V;
   Lane<T> l;
-  const int i = lane % G, words = p.dim / V, turned = p.rot_dim / V;
+  const int words = p.dim / V, turned = p.rot_dim / V;
   if (p.interleaved) {
     const int a = i, b = i + (words + 1) / 2;
     l.on_a = a < (words + 1) / 2;
@@ -270,8 +282,8 @@ struct Walk {
   }
 };
 
-// The norm, its rotation and (GRAD) its gradient: G lanes hold one head, a warp
-// 32 / G consecutive heads a round. The warps of a grid that fits the card deal
+// The norm, its rotation and (GRAD) its gradient: G (or, 0, p.lanes) lanes hold
+// one head, a warp as many consecutive heads a round as fit 32 lanes. The warps of a grid that fits the card deal
 // the queries and then the keys among them, p.chunk rounds at a time, so that
 // together they walk through memory in order; a warp copies the words of its
 // next QK_AHEAD rounds to shared memory while it computes one. For the gradient
@@ -279,13 +291,14 @@ struct Walk {
 // order.
 template <typename T, int G, bool GRAD>
 __global__ void __launch_bounds__(QK_THREADS, GRAD ? QK_GRAD_BLOCKS : QK_BLOCKS) ns_qk_kernel(const __grid_constant__ QkParams p) {
-  constexpr int V = Lane<T>::V, N = Two<T>::N, H = 32 / G, STAGES = QK_AHEAD + 1, STAGE = GRAD ? 128 : 64;
+  constexpr int N = Two<T>::N, STAGES = QK_AHEAD + 1, STAGE = GRAD ? 128 : 64;
   extern __shared__ uint4 ring_smem[];
   nsptx::griddep_wait();
   nsptx::griddep_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   uint4* ring = ring_smem + warp * (STAGES * STAGE) + lane;
-  const Lane<T> l = lane_of<T, G>(p, lane);
+  const int group_size = G ? G : p.lanes, H = 32 / group_size, group = lane / group_size, i_lane = lane - group * group_size;
+  const Lane<T> l = lane_of<T>(p, i_lane);
   const float inv_dim = 1.0f / p.dim;
   // words outside the head are zero and stay so
   for (int i = 0; i < STAGES * STAGE; i += 64) {
@@ -306,12 +319,13 @@ __global__ void __launch_bounds__(QK_THREADS, GRAD ? QK_GRAD_BLOCKS : QK_BLOCKS)
     }
     if (n > 0) {
       const Two<T> g = lane_weights<T>(p, side, l);
-      const Place start = place_of(first * p.chunk * H + lane / G, side.heads);
+      const Place start = place_of(first * p.chunk * H + min(group, H - 1), side.heads);
       Walk ahead(start), at(start);  // of the copies, and of the rounds
       const char* x_at = static_cast<const char*>(side.x) + sizeof(T) * (start.t * side.x_token + start.h * side.x_head + l.a);
       const char* dy_at = static_cast<const char*>(side.dy) + sizeof(T) * (start.t * side.dy_token + start.h * side.dy_head + l.a);
       char* out_at = static_cast<char*>(side.out) + sizeof(T) * (start.t * side.out_token + start.h * side.out_head + l.a);
       const int to_b = static_cast<int>(sizeof(T)) * (l.b - l.a);
+      if (group >= H) ahead.t = at.t = static_cast<int>(p.tokens);  // a lane left over takes no head
       ahead.left = at.left = p.chunk;
       int fill = 0, take = 0;
       auto copy = [&](bool more) {
@@ -351,7 +365,7 @@ __global__ void __launch_bounds__(QK_THREADS, GRAD ? QK_GRAD_BLOCKS : QK_BLOCKS)
           s2 = fma2(xf.a[i], xf.a[i], s2);
           s2 = fma2(xf.b[i], xf.b[i], s2);
         }
-        const float r_norm = rsqrtf(fmaf(group_sum<G>(s2.x + s2.y), inv_dim, p.eps));
+        const float r_norm = rsqrtf(fmaf(group_sum<G>(s2.x + s2.y, group_size, i_lane), inv_dim, p.eps));
         const float2 r2 = make_float2(r_norm, r_norm);
         if (!GRAD) {
 #pragma unroll
@@ -377,7 +391,7 @@ __global__ void __launch_bounds__(QK_THREADS, GRAD ? QK_GRAD_BLOCKS : QK_BLOCKS)
             d2 = fma2(u.a[i], xf.a[i], d2);
             d2 = fma2(u.b[i], xf.b[i], d2);
           }
-          const float m = -r_norm * r_norm * r_norm * (group_sum<G>(d2.x + d2.y) * inv_dim);
+          const float m = -r_norm * r_norm * r_norm * (group_sum<G>(d2.x + d2.y, group_size, i_lane) * inv_dim);
           const float2 m2 = make_float2(m, m);
 #pragma unroll
           for (int i = 0; i < N; ++i) {
@@ -392,28 +406,23 @@ __global__ void __launch_bounds__(QK_THREADS, GRAD ? QK_GRAD_BLOCKS : QK_BLOCKS)
       nsptx::cp_async_wait<0>();
     }
     if (GRAD && p.partial) {
-      float(*joined)[2 * G * V] = reinterpret_cast<float(*)[2 * G * V]>(ring_smem);  // the rings are done with
+      float* joined = reinterpret_cast<float*>(ring_smem);  // [warps][dim]; the rings are done with
       __syncthreads();
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        float* d = reinterpret_cast<float*>(&dg.a[i]);
-        float* e = reinterpret_cast<float*>(&dg.b[i]);
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-#pragma unroll
-          for (int o = G; o < 32; o <<= 1) {
-            d[k] += __shfl_xor_sync(0xffffffffu, d[k], o);
-            e[k] += __shfl_xor_sync(0xffffffffu, e[k], o);
-          }
-          if (lane < G && l.on_a) joined[warp][l.a + 2 * i + k] = d[k];
-          if (lane < G && l.on_b) joined[warp][l.b + 2 * i + k] = e[k];
+        for (int k = 0; k < 4; ++k) {
+          const float mine = k < 2 ? (k ? dg.a[i].y : dg.a[i].x) : (k & 1 ? dg.b[i].y : dg.b[i].x);
+          float sum = 0.0f;
+          for (int h = 0; h < H; ++h) sum += __shfl_sync(0xffffffffu, mine, h * group_size + i_lane);
+          if (group == 0 && (k < 2 ? l.on_a : l.on_b)) joined[warp * p.dim + (k < 2 ? l.a : l.b) + 2 * i + (k & 1)] = sum;
         }
       }
       __syncthreads();
       for (int d = threadIdx.x; d < p.dim; d += QK_THREADS) {
         float sum = 0.0f;
 #pragma unroll
-        for (int k = 0; k < QK_WARPS; ++k) sum += joined[k][d];
+        for (int k = 0; k < QK_WARPS; ++k) sum += joined[k * p.dim + d];
         p.partial[(static_cast<long long>(blockIdx.x) * 2 + which) * p.dim + d] = sum;
       }
       __syncthreads();
@@ -534,7 +543,7 @@ __global__ void __launch_bounds__(256) ns_qk_sum_kernel(const __grid_constant__ 
 
 template <typename T, int G>
 cudaError_t launch_lanes(bool grad, QkParams& p, int nsm, int* blocks, cudaStream_t st) {
-  constexpr int H = 32 / G;
+  const int H = 32 / p.lanes;
   const int most = std::min(nsm * (grad ? QK_GRAD_BLOCKS : QK_BLOCKS), QK_MAX_BLOCKS);
   // up to 8 rounds a chunk (a token's angles serve them all: 16384 tokens of 32/8 heads take 131, 107, 97
   // and 93 us backward with 1, 2, 4 and 8), but 4 chunks a warp, so that the warps end together
@@ -567,11 +576,10 @@ template <typename T>
 cudaError_t launch_qk(bool grad, bool lanes, QkParams& p, int nsm, int* blocks, cudaStream_t st) {
   constexpr int V = Lane<T>::V;
   if (lanes) {
-    const int need = (p.dim / V + 1) / 2;
-    if (need <= 4) return launch_lanes<T, 4>(grad, p, nsm, blocks, st);
-    if (need <= 8) return launch_lanes<T, 8>(grad, p, nsm, blocks, st);
-    if (need <= 16) return launch_lanes<T, 16>(grad, p, nsm, blocks, st);
-    return launch_lanes<T, 32>(grad, p, nsm, blocks, st);
+    p.lanes = (p.dim / V + 1) / 2;
+    if (p.lanes == 8) return launch_lanes<T, 8>(grad, p, nsm, blocks, st);
+    if (p.lanes == 16) return launch_lanes<T, 16>(grad, p, nsm, blocks, st);
+    return launch_lanes<T, 0>(grad, p, nsm, blocks, st);
   }
   constexpr int WARPS = QK_ANY_THREADS / 32;
   const long long pairs = p.tokens * std::max(p.side[0].heads, p.side[1].heads);
