@@ -113,13 +113,14 @@ struct Lane {
   bool turn_a, turn_b; // rotated
 };
 
-// Lane i of a head's group.
-template <typename T>
+// Lane i of a head's group. SPREAD: the pairs are not made of whole words, so
+// the words are taken in order.
+template <typename T, bool SPREAD>
 __device__ __forceinline__ Lane<T> lane_of(const QkParams& p, int i) {
   constexpr int V = Lane<T>::V;
   Lane<T> l;
   const int words = p.dim / V, turned = p.rot_dim / V;
-  if (p.interleaved) {
+  if (SPREAD || p.interleaved) {
     const int a = i, b = i + (words + 1) / 2;
     l.on_a = a < (words + 1) / 2;
     l.on_b = l.on_a && b < words;
@@ -231,6 +232,38 @@ __device__ __forceinline__ void turn(const QkParams& p, const Lane<T>& l, const 
   }
 }
 
+// The same for pairs that are not made of whole words: the other value of a
+// pair comes from its lane through `scratch` (the warp's, 2 V values a lane).
+// `first`: the group's first lane.
+template <typename T>
+__device__ __forceinline__ void turn_spread(const QkParams& p, const Lane<T>& l, const float* row, Two<T>& x, float sign,
+                                            float* scratch, int lane, int first) {
+  constexpr int V = Lane<T>::V, N = Two<T>::N;
+  const int half = p.rot_dim / 2, words_a = (p.dim / V + 1) / 2;
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    reinterpret_cast<float2*>(scratch + lane * V)[i] = x.a[i];
+    reinterpret_cast<float2*>(scratch + (32 + lane) * V)[i] = x.b[i];
+  }
+  __syncwarp();
+  auto one = [&](float v, int d) {
+    if (!row || d >= p.rot_dim) return v;
+    const bool second = p.interleaved ? d & 1 : d >= half;
+    const int o = p.interleaved ? d ^ 1 : (second ? d - half : d + half);
+    const int angle = p.interleaved ? d >> 1 : (second ? d - half : d);
+    const int word = o / V, b = word >= words_a;
+    const float other = scratch[(32 * b + first + word - b * words_a) * V + o % V];
+    const float s = second ? sign * row[half + angle] : -sign * row[half + angle];
+    return v * row[angle] + other * s;
+  };
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    if (l.on_a) x.a[i] = make_float2(one(x.a[i].x, l.a + 2 * i), one(x.a[i].y, l.a + 2 * i + 1));
+    if (l.on_b) x.b[i] = make_float2(one(x.b[i].x, l.b + 2 * i), one(x.b[i].y, l.b + 2 * i + 1));
+  }
+}
+
 // The weights of one of the lane's words.
 template <typename T>
 __device__ __forceinline__ void weights_of(const QkParams& p, const void* w, int first, bool on, float2 (&g)[Two<T>::N]) {
@@ -283,13 +316,13 @@ struct Walk {
 };
 
 // The norm, its rotation and (GRAD) its gradient: G (or, 0, p.lanes) lanes hold
-// one head, a warp as many consecutive heads a round as fit 32 lanes. The warps of a grid that fits the card deal
-// the queries and then the keys among them, p.chunk rounds at a time, so that
-// together they walk through memory in order; a warp copies the words of its
-// next QK_AHEAD rounds to shared memory while it computes one. For the gradient
-// a lane keeps the sums of its columns of dg, which a block joins in a fixed
-// order.
-template <typename T, int G, bool GRAD>
+// one head, a warp as many consecutive heads a round as fit 32 lanes. The warps
+// of a grid that fits the card deal the queries and then the keys among them,
+// p.chunk rounds at a time, so that together they walk through memory in order;
+// a warp copies the words of its next QK_AHEAD rounds to shared memory while it
+// computes one. For the gradient a lane keeps the sums of its columns of dg,
+// which a block joins in a fixed order. SPREAD: see turn_spread.
+template <typename T, int G, bool GRAD, bool SPREAD>
 __global__ void __launch_bounds__(QK_THREADS, GRAD ? QK_GRAD_BLOCKS : QK_BLOCKS) ns_qk_kernel(const __grid_constant__ QkParams p) {
   constexpr int N = Two<T>::N, STAGES = QK_AHEAD + 1, STAGE = GRAD ? 128 : 64;
   extern __shared__ uint4 ring_smem[];
@@ -298,7 +331,8 @@ __global__ void __launch_bounds__(QK_THREADS, GRAD ? QK_GRAD_BLOCKS : QK_BLOCKS)
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   uint4* ring = ring_smem + warp * (STAGES * STAGE) + lane;
   const int group_size = G ? G : p.lanes, H = 32 / group_size, group = lane / group_size, i_lane = lane - group * group_size;
-  const Lane<T> l = lane_of<T>(p, i_lane);
+  const Lane<T> l = lane_of<T, SPREAD>(p, i_lane);
+  float* scratch = reinterpret_cast<float*>(ring_smem + QK_WARPS * STAGES * STAGE) + warp * 64 * Lane<T>::V;
   const float inv_dim = 1.0f / p.dim;
   // words outside the head are zero and stay so
   for (int i = 0; i < STAGES * STAGE; i += 64) {
@@ -355,7 +389,7 @@ __global__ void __launch_bounds__(QK_THREADS, GRAD ? QK_GRAD_BLOCKS : QK_BLOCKS)
         take = take + STAGE == STAGES * STAGE ? 0 : take + STAGE;
         if (p.rot_dim && live && at.t != angles_of) {
           row = table_row(p, at.t);
-          if (row) load_angles<T>(p, l, row, angles);
+          if (row && !SPREAD) load_angles<T>(p, l, row, angles);
           angles_of = at.t;
         }
         if (p.rot_dim && !row) live = false;
@@ -373,9 +407,15 @@ __global__ void __launch_bounds__(QK_THREADS, GRAD ? QK_GRAD_BLOCKS : QK_BLOCKS)
             u.a[i] = mul2(xf.a[i], mul2(g.a[i], r2));
             u.b[i] = mul2(xf.b[i], mul2(g.b[i], r2));
           }
-          turn<T>(p, l, angles, u, 1.0f);
+          if (SPREAD)
+            turn_spread<T>(p, l, row, u, 1.0f, scratch, lane, lane - i_lane);
+          else
+            turn<T>(p, l, angles, u, 1.0f);
         } else {
-          turn<T>(p, l, angles, u, -1.0f);
+          if (SPREAD)
+            turn_spread<T>(p, l, row, u, -1.0f, scratch, lane, lane - i_lane);
+          else
+            turn<T>(p, l, angles, u, -1.0f);
           if (live) {
 #pragma unroll
             for (int i = 0; i < N; ++i) {
@@ -541,7 +581,7 @@ __global__ void __launch_bounds__(256) ns_qk_sum_kernel(const __grid_constant__ 
   if (out) out[col >= p.dim ? col - p.dim : col] = sum;
 }
 
-template <typename T, int G>
+template <typename T, int G, bool SPREAD = false>
 cudaError_t launch_lanes(bool grad, QkParams& p, int nsm, int* blocks, cudaStream_t st) {
   const int H = 32 / p.lanes;
   const int most = std::min(nsm * (grad ? QK_GRAD_BLOCKS : QK_BLOCKS), QK_MAX_BLOCKS);
@@ -564,12 +604,13 @@ cudaError_t launch_lanes(bool grad, QkParams& p, int nsm, int* blocks, cudaStrea
       s.wrap[k] = static_cast<long long>(sizeof(T)) * (token[k] - s.heads * head[k]);
     }
   }
-  const size_t smem = sizeof(uint4) * QK_WARPS * (QK_AHEAD + 1) * (grad ? 128 : 64);
-  if (!grad) return launch_pdl(ns_qk_kernel<T, G, false>, dim3(*blocks), dim3(QK_THREADS), smem, st, p);
-  const cudaError_t e = cudaFuncSetAttribute(ns_qk_kernel<T, G, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  const size_t smem = sizeof(uint4) * QK_WARPS * (QK_AHEAD + 1) * (grad ? 128 : 64) +
+                      (SPREAD ? sizeof(float) * QK_WARPS * 64 * Lane<T>::V : 0);
+  if (!grad) return launch_pdl(ns_qk_kernel<T, G, false, SPREAD>, dim3(*blocks), dim3(QK_THREADS), smem, st, p);
+  const cudaError_t e = cudaFuncSetAttribute(ns_qk_kernel<T, G, true, SPREAD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              static_cast<int>(smem));
   if (e != cudaSuccess) return e;
-  return launch_pdl(ns_qk_kernel<T, G, true>, dim3(*blocks), dim3(QK_THREADS), smem, st, p);
+  return launch_pdl(ns_qk_kernel<T, G, true, SPREAD>, dim3(*blocks), dim3(QK_THREADS), smem, st, p);
 }
 
 template <typename T>
@@ -577,6 +618,7 @@ cudaError_t launch_qk(bool grad, bool lanes, QkParams& p, int nsm, int* blocks, 
   constexpr int V = Lane<T>::V;
   if (lanes) {
     p.lanes = (p.dim / V + 1) / 2;
+    if (p.rot_dim % (p.interleaved ? V : 2 * V)) return launch_lanes<T, 0, true>(grad, p, nsm, blocks, st);
     if (p.lanes == 8) return launch_lanes<T, 8>(grad, p, nsm, blocks, st);
     if (p.lanes == 16) return launch_lanes<T, 16>(grad, p, nsm, blocks, st);
     return launch_lanes<T, 0>(grad, p, nsm, blocks, st);
@@ -629,8 +671,7 @@ int run_qk(bool grad, const void* const* x, const void* const* dy, void* const* 
   if ((tokens == 0 || most == 0) && !sums) return NS_OK;
   nsk::QkParams p = {};
   const int b = dtype == NS_DT_FP32 ? 4 : 2, V = 16 / b;
-  bool lanes = head_dim % V == 0 && head_dim / V <= 64 && rot_dim % (interleaved ? V : 2 * V) == 0 &&
-               (reinterpret_cast<uintptr_t>(table) & 15) == 0;
+  bool lanes = head_dim % V == 0 && head_dim / V <= 64 && (reinterpret_cast<uintptr_t>(table) & 15) == 0;
   // strides: (token, head) of x, of out and, for the gradient, of dy; queries then keys of each
   for (int i = 0; i < 2; ++i) {
     nsk::QkSide& s = p.side[i];
