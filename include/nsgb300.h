@@ -348,7 +348,8 @@ int ns_moe_sort_workspace_bytes(int64_t tokens, int k, int experts, uint64_t* by
  * segment, offsets[experts] = rows in use (segments padded to multiples of
  * align); row_of_slot[s] = row of slot s or -1; slot_of_row[r] = slot of row r
  * or -1, for all `rows` rows (rows >= ns_moe_rows, NS_ERR_SHAPE otherwise).
- * 1 <= k <= 32, 1 <= experts <= 1024, tokens * k < 2^31 - 4096. */
+ * 1 <= k <= 32, 1 <= experts <= 1024; tokens * k and rows at most 2^30, here and
+ * below. */
 int ns_moe_sort(const void* expert_ids, int id_bytes, int64_t tokens, int k, int experts, int align,
                 int64_t capacity, int64_t rows, int32_t* row_of_slot, int32_t* slot_of_row, int32_t* counts,
                 int32_t* offsets, void* workspace, uint64_t workspace_bytes, void* stream);

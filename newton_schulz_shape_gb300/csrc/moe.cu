@@ -28,6 +28,7 @@ namespace {
 
 constexpr int MAX_EXPERTS = 1024;
 constexpr int MAX_K = 32;
+constexpr long long MAX_SLOTS = 1 << 30;  // and rows: indexes and their steps fit an int
 constexpr int SORT_THREADS = 512;
 constexpr int SORT_WARPS = SORT_THREADS / 32;
 constexpr int SORT_HELD = 4;  // rounds of 32 slots that a warp keeps in registers
@@ -448,7 +449,7 @@ void sort_split(long long slots, int* chunk, int* blocks) {
 int sort_args(int64_t tokens, int k, int experts) {
   if (tokens < 0 || k < 1 || experts < 1) return NS_ERR_ARG;
   if (k > nsk::MAX_K || experts > nsk::MAX_EXPERTS) return NS_ERR_UNSUPPORTED;
-  if (tokens > (INT_MAX - 4096) / k) return NS_ERR_SHAPE;
+  if (tokens > nsk::MAX_SLOTS / k) return NS_ERR_SHAPE;
   return NS_OK;
 }
 
@@ -456,7 +457,7 @@ int sort_args(int64_t tokens, int k, int experts) {
 int row_args(int dtype, int64_t tokens, int k, int64_t dim, int64_t rows) {
   if (!dtype_ok(dtype) || tokens < 0 || k < 1 || dim < 0 || rows < 0) return NS_ERR_ARG;
   if (k > nsk::MAX_K) return NS_ERR_UNSUPPORTED;
-  if (tokens > (INT_MAX - 4096) / k || rows > INT_MAX || dim > INT_MAX / 4) return NS_ERR_SHAPE;
+  if (tokens > nsk::MAX_SLOTS / k || rows > nsk::MAX_SLOTS || dim > INT_MAX / 4) return NS_ERR_SHAPE;
   return NS_OK;
 }
 
@@ -523,7 +524,7 @@ int ns_moe_rows(int64_t tokens, int k, int experts, int align, int64_t capacity,
     const int64_t cap = std::min(capacity, slots);
     rows = std::min(rows, experts * ((cap + align - 1) / align * align));
   }
-  if (rows > INT_MAX) return NS_ERR_SHAPE;
+  if (rows > nsk::MAX_SLOTS) return NS_ERR_SHAPE;
   *rows_out = rows;
   return NS_OK;
 }
@@ -545,7 +546,7 @@ int ns_moe_sort(const void* expert_ids, int id_bytes, int64_t tokens, int k, int
   int rc = ns_moe_rows(tokens, k, experts, align, capacity, &need_rows);
   if (rc != NS_OK) return rc;
   if (id_bytes != 4 && id_bytes != 8) return NS_ERR_ARG;
-  if (rows < need_rows || rows > INT_MAX) return NS_ERR_SHAPE;
+  if (rows < need_rows || rows > nsk::MAX_SLOTS) return NS_ERR_SHAPE;
   if (!counts || !offsets || (tokens > 0 && (!expert_ids || !row_of_slot)) || (rows > 0 && !slot_of_row))
     return NS_ERR_ARG;
   nsk::SortParams p = {};

@@ -359,11 +359,11 @@ __global__ void __launch_bounds__(QK_THREADS, GRAD ? QK_GRAD_BLOCKS : QK_BLOCKS)
       const char* dy_at = static_cast<const char*>(side.dy) + sizeof(T) * (start.t * side.dy_token + start.h * side.dy_head + l.a);
       char* out_at = static_cast<char*>(side.out) + sizeof(T) * (start.t * side.out_token + start.h * side.out_head + l.a);
       const int to_b = static_cast<int>(sizeof(T)) * (l.b - l.a);
-      if (group >= H) ahead.t = at.t = static_cast<int>(p.tokens);  // a lane left over takes no head
+      const bool takes = group < H;  // a lane left over takes no head
       ahead.left = at.left = p.chunk;
       int fill = 0, take = 0;
       auto copy = [&](bool more) {
-        if (more && ahead.t < p.tokens) {
+        if (more && takes && ahead.t < p.tokens) {
           if (l.on_a) nsptx::cp_async16(ring + fill, x_at);
           if (l.on_b) nsptx::cp_async16(ring + fill + 32, x_at + to_b);
           if (GRAD && l.on_a) nsptx::cp_async16(ring + fill + 64, dy_at);
@@ -382,7 +382,7 @@ __global__ void __launch_bounds__(QK_THREADS, GRAD ? QK_GRAD_BLOCKS : QK_BLOCKS)
       for (int r = 0; r < n; ++r) {
         copy(r + QK_AHEAD < n);
         nsptx::cp_async_wait<QK_AHEAD>();
-        bool live = at.t < p.tokens;  // of a whole group of lanes; the others' values go nowhere
+        bool live = takes && at.t < p.tokens;  // of a whole group of lanes; the others' values go nowhere
         const Two<T> xf = unpack<T>(ring + take);
         Two<T> u;
         if (GRAD) u = unpack<T>(ring + take + 64);

@@ -1,0 +1,206 @@
+"""The training-step operators at the edges of their domains: nothing to do,
+odd rotations, rows too long for shared memory, many teacher entries, calls on
+the same buffers in a row. Against the float64 oracle; tolerances as in
+test_gpu_training_ops.py (u = 2^-24, U half the output type's eps)."""
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import training as ot
+
+pytestmark = pytest.mark.gpu
+nsg = pytest.importorskip("newton_schulz_shape_gb300")
+
+DEV = "cuda"
+u = 2.0 ** -24
+
+
+def f64(t):
+    return t.double().cpu().numpy()
+
+
+def gen(seed):
+    return torch.Generator(device=DEV).manual_seed(seed)
+
+
+def randn(g, *shape, dtype=torch.float32):
+    return torch.randn(*shape, generator=g, device=DEV).to(dtype)
+
+
+def empty(*shape, dtype=torch.float32):
+    return torch.full(shape, 5, dtype=dtype, device=DEV)
+
+
+def ok():
+    assert nsg.ns_check_status() == nsg.NS_OK
+
+
+def test_nothing_to_do():
+    i32 = torch.int32
+    row, slot, counts, off = empty(0, 2, dtype=i32), empty(0, dtype=i32), empty(3, dtype=i32), empty(4, dtype=i32)
+    nsg.ns_moe_sort(torch.empty(0, 2, dtype=torch.int64, device=DEV), 3, row, slot, counts, off, None)
+    assert counts.tolist() == [0, 0, 0] and off.tolist() == [0, 0, 0, 0]
+    nsg.ns_moe_dispatch(empty(0, 8), row, slot, empty(0, 8))
+    nsg.ns_moe_dispatch_grad(empty(0, 8), row, empty(0, 8))
+    nsg.ns_moe_combine(empty(0, 8), empty(0, 2), row, empty(0, 8))
+    nsg.ns_moe_combine_grad(empty(0, 8), empty(0, 8), empty(0, 2), row, slot, empty(0, 8), empty(0, 2))
+    # tokens, but no rows: everything was dropped
+    none = torch.full((3, 2), -1, dtype=i32, device=DEV)
+    y, dw = empty(3, 8), empty(3, 2)
+    nsg.ns_moe_combine(empty(0, 8), empty(3, 2), none, y)
+    nsg.ns_moe_combine_grad(empty(3, 8), empty(0, 8), empty(3, 2), none, slot, empty(0, 8), dw)
+    assert not y.any() and not dw.any()
+    # rows, but no tokens: all of them are padding
+    rows = empty(5, 8)
+    nsg.ns_moe_dispatch(empty(0, 8), row, torch.full((5,), -1, dtype=i32, device=DEV), rows)
+    assert not rows.any()
+    e, dqw = empty(0, 2, 8), empty(8)
+    ws = torch.empty(nsg.ns_qk_norm_rope_grad_workspace_bytes(8), dtype=torch.uint8, device=DEV)
+    nsg.ns_qk_norm_rope(e, e, e, e)
+    nsg.ns_qk_norm_rope_grad(e, e, e, e, e, e, grad_q_weight=dqw, workspace=ws)
+    assert not dqw.any()
+    nsg.ns_distill_loss(empty(0, 9), empty(0, 2), torch.empty(0, 2, dtype=torch.int64, device=DEV), empty(0), empty(0))
+    ok()
+
+
+ROTATIONS = [  # dim, rot, interleaved
+    (128, 34, False), (128, 34, True), (72, 72, False), (72, 36, False), (72, 38, True), (40, 40, False), (8, 2, False),
+    (8, 6, True), (16, 14, False), (112, 112, False), (112, 50, True), (24, 24, False), (192, 130, False), (256, 250, True),
+    (512, 510, False), (160, 160, False), (64, 2, True),
+]
+
+
+@pytest.mark.parametrize("D,rot,interleaved", ROTATIONS)
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+@pytest.mark.parametrize("T,H,K", [(37, 5, 2), (300, 3, 3)])
+def test_rotations_of_any_even_width(D, rot, interleaved, dtype, T, H, K):
+    g = gen(D + rot)
+    q, k, gq, gk = randn(g, T, H, D, dtype=dtype), randn(g, T, K, D, dtype=dtype), randn(g, T, H, D, dtype=dtype), randn(g, T, K, D, dtype=dtype)
+    qw, kw = randn(g, D, dtype=dtype), randn(g, D, dtype=dtype)
+    angle = torch.rand(T + 9, rot // 2, generator=g, device=DEV, dtype=torch.float64) * 6
+    table = torch.cat([angle.cos(), angle.sin()], 1).float()
+    pos = torch.randint(0, T + 9, (T,), generator=g, device=DEV)
+    qo, ko, dq, dk = (torch.full_like(t, float("nan")) for t in (q, k, q, k))
+    dqw, dkw = empty(D), empty(D)
+    ws = torch.empty(nsg.ns_qk_norm_rope_grad_workspace_bytes(D), dtype=torch.uint8, device=DEV)
+    nsg.ns_qk_norm_rope(q, k, qo, ko, qw, kw, table, pos, interleaved=interleaved)
+    nsg.ns_qk_norm_rope_grad(gq, gk, q, k, dq, dk, qw, kw, dqw, dkw, table, pos, ws, interleaved=interleaved)
+    ok()
+    U, tiny, c = torch.finfo(dtype).eps / 2, float(torch.finfo(dtype).tiny) * float(torch.finfo(dtype).eps), (D + 16) * u
+    at = (f64(table), pos.cpu().numpy(), rot, 1e-6, interleaved)
+    R = np.abs(ot._rotation(at[0], at[1], rot, D, interleaved))
+    for x, y, dy, dx, w, dw in ((q, qo, gq, dq, qw, dqw), (k, ko, gk, dk, kw, dkw)):
+        xv, dyv, wv = f64(x), f64(dy), f64(w)
+        r = 1 / np.sqrt((xv * xv).mean(-1, keepdims=True) + 1e-6)
+        want, bound = ot.norm_rope(xv, wv, *at), c * np.einsum("tab,thb->tha", R, np.abs(xv * r * wv))
+        assert (np.abs(f64(y) - want) <= bound + U * (np.abs(want) + bound) + tiny).all()
+        want, want_w = ot.norm_rope_grad(dyv, xv, wv, *at)
+        ua = np.einsum("tab,tha->thb", R, np.abs(dyv))
+        h = ua * np.abs(wv)
+        bound = 2 * c * (r * h + np.abs(xv) * r ** 3 * (h * np.abs(xv)).mean(-1, keepdims=True))
+        assert (np.abs(f64(dx) - want) <= bound + U * (np.abs(want) + bound) + tiny).all()
+        assert (np.abs(f64(dw) - want_w) <= ((T * x.shape[1] + 2) * u + c) * (ua * np.abs(xv) * r).sum((0, 1)) + u).all()
+
+
+@pytest.mark.parametrize("dtype,V", [(torch.bfloat16, 900001), (torch.float32, 450000)])
+def test_rows_too_long_for_a_cluster(dtype, V):
+    g = gen(V)
+    T, K = 3, 9
+    logits = randn(g, T, V, dtype=dtype)
+    ids, values = torch.randint(0, V, (T, K), generator=g, device=DEV), randn(g, T, K)
+    ids[0, 1], ids[1] = ids[0, 0], -1
+    loss, lse, grad, later = empty(T), empty(T), empty(T, V, dtype=dtype), empty(T, V, dtype=dtype)
+    nsg.ns_distill_loss(logits, values, ids, loss, lse, grad_logits=grad, temperature=0.8)
+    nsg.ns_distill_grad(logits, values, ids, lse, later, temperature=0.8)
+    ok()
+    want_loss, want_lse, want = ot.distill(f64(logits), f64(values), ids.cpu().numpy(), None, None, 0.8)
+    e = (V / 128 + 64) * u
+    assert np.abs(f64(lse) - want_lse).max() <= e * 20 and np.abs(f64(loss) - want_loss).max() <= e * 40
+    U = torch.finfo(dtype).eps / 2
+    for got in (grad, later):
+        assert (np.abs(f64(got) - want) <= U * np.abs(want) + 4 * e * (np.abs(want) + 1e-3)).all()
+
+
+def test_the_most_teacher_entries_with_every_one_repeated():
+    g = gen(3)
+    T, V, K = 5, 2000, 1024
+    logits, values = randn(g, T, V), randn(g, T, K)
+    ids = torch.randint(0, 300, (T, K), generator=g, device=DEV, dtype=torch.int32)
+    ids[4] = 7                                             # one entry, 1024 times
+    loss, lse, grad = empty(T), empty(T), empty(T, V)
+    for _ in range(2):                                     # the second call finds the first one's outputs
+        nsg.ns_distill_loss(logits, values, ids, loss, lse, grad_logits=grad)
+    ok()
+    want_loss, want_lse, want = ot.distill(f64(logits), f64(values), ids.cpu().numpy())
+    assert np.abs(f64(loss) - want_loss).max() <= 1100 * u * 16
+    assert np.abs(f64(grad) - want).max() <= 1100 * u
+
+
+def test_other_weights_later():
+    g = gen(4)
+    T, V, K = 6, 3001, 8
+    logits, values, ids = randn(g, T, V), randn(g, T, K), torch.randint(0, V, (T, K), generator=g, device=DEV)
+    w = torch.tensor([1.0, -2.0, 0.0, 3.0, 0.5, 0.0], device=DEV)
+    loss, lse, grad = empty(T), empty(T), empty(T, V)
+    nsg.ns_distill_loss(logits, values, ids, loss, lse)     # weights 1
+    nsg.ns_distill_grad(logits, values, ids, lse, grad, weights=w)
+    ok()
+    want = ot.distill(f64(logits), f64(values), ids.cpu().numpy(), f64(w))[2]
+    assert np.abs(f64(grad) - want).max() <= 64 * u * 3
+    assert not grad[2].any() and not grad[5].any()
+
+
+def test_infinite_weights_and_rows_stay_where_they_are():
+    # an infinity in one expert row or weight reaches only the tokens that use it
+    row = torch.tensor([[0, 1], [2, 3], [-1, 4]], dtype=torch.int32, device=DEV)
+    slot = torch.tensor([0, 1, 2, 3, 5], dtype=torch.int32, device=DEV)
+    ys, w = torch.ones(5, 16, device=DEV), torch.ones(3, 2, device=DEV)
+    ys[0, 3], w[1, 0] = float("inf"), float("inf")
+    y = empty(3, 16)
+    nsg.ns_moe_combine(ys, w, row, y)
+    assert y[0, 3].isinf() and (y[0, 4:] == 2).all() and y[1].isinf().all() and (y[2] == 1).all()
+    grad_rows, dw = empty(5, 16), empty(3, 2)
+    nsg.ns_moe_combine_grad(torch.ones(3, 16, device=DEV), ys, w, row, slot, grad_rows, dw)
+    ok()
+    assert dw[0, 0].isinf() and dw[0, 1] == 16 and dw[2].tolist() == [0, 16]
+    assert grad_rows[2].isinf().all() and (grad_rows[[0, 1, 3, 4]] == 1).all()
+
+
+def test_launch_counts():
+    nsg.ns_profile_read_training(reset=True)
+    x = torch.ones(4, 2, 64, device=DEV)
+    nsg.ns_qk_norm_rope(x, x, torch.empty_like(x), torch.empty_like(x))
+    launches, _ = nsg.ns_profile_read_training(reset=True)
+    assert launches == {"moe": 0, "qk_norm_rope": 1, "distill": 0}
+
+
+def test_binding_arguments():
+    x = torch.ones(4, 2, 64, device=DEV)
+    with pytest.raises(TypeError, match="k_out"):
+        nsg.ns_qk_norm_rope(x, x, x)
+    with pytest.raises(TypeError, match="unexpected"):
+        nsg.ns_qk_norm_rope(x, x, x, x, epsilon=1.0)
+    with pytest.raises(TypeError, match="multiple"):
+        nsg.ns_qk_norm_rope(x, x, x, x, q=x)
+    with pytest.raises(ValueError, match="k_out"):
+        nsg.ns_qk_norm_rope(x, x, x, x[:, :1])
+    with pytest.raises(ValueError, match="q:.*contiguous heads"):
+        nsg.ns_qk_norm_rope(x[..., ::2], x, x, x)
+    with pytest.raises(ValueError, match="q_weight"):
+        nsg.ns_qk_norm_rope(x, x, x, x, torch.ones(64, dtype=torch.float64, device=DEV))
+    with pytest.raises(ValueError, match="positions"):
+        nsg.ns_qk_norm_rope(x, x, x, x, table=torch.ones(4, 2, device=DEV), positions=torch.zeros(3, dtype=torch.int64, device=DEV))
+    with pytest.raises(ValueError, match="logits"):
+        nsg.ns_distill_loss(x[0].t(), x[0], x[0], x, x)
+    with pytest.raises(ValueError, match="weights"):
+        nsg.ns_moe_combine(torch.ones(4, 8, device=DEV), torch.ones(2, 2, device=DEV).half(),
+                           torch.zeros(2, 2, dtype=torch.int32, device=DEV), torch.ones(2, 8, device=DEV))
+    with pytest.raises(nsg.NsError) as e:
+        nsg.ns_qk_norm_rope(x, x, x, x, eps=-1.0)
+    assert e.value.code == nsg.NS_ERR_ARG
+    s = torch.cuda.Stream()
+    for stream in (s, s.cuda_stream, None):
+        nsg.ns_qk_norm_rope(x, x, torch.empty_like(x), torch.empty_like(x), stream=stream)
+    torch.cuda.synchronize()
+    ok()
