@@ -308,8 +308,8 @@ __global__ void __launch_bounds__(ROW_THREADS) ns_moe_dispatch_kernel(const __gr
 }
 
 // combine and the gradient of dispatch: a warp sums 32 * V * U elements of a
-// token's rows.
-template <typename T, int V, int U>
+// token's rows, with those of J rows on their way at once.
+template <typename T, int V, int U, int J>
 __global__ void __launch_bounds__(ROW_THREADS) ns_moe_gather_kernel(const __grid_constant__ RowParams p) {
   nsptx::griddep_wait();
   nsptx::griddep_launch_dependents();
@@ -325,19 +325,27 @@ __global__ void __launch_bounds__(ROW_THREADS) ns_moe_gather_kernel(const __grid
   for (int u = 0; u < U; ++u)
 #pragma unroll
     for (int i = 0; i < V; ++i) acc[u][i] = 0.0f;
-#pragma unroll 4
-  for (int j = 0; j < p.k; ++j) {
-    const int r = __shfl_sync(0xffffffffu, mine, j);
-    const float wt = __shfl_sync(0xffffffffu, my_weight, j);
-    if (r < 0) continue;
-    const T* src = static_cast<const T*>(p.src) + r * p.src_ld;
+  for (int j0 = 0; j0 < p.k; j0 += J) {
+    Vec<T, V> x[J][U];
+    float wt[J];
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (c0 + u * 32 * V < p.dim) {
-        const Vec<T, V> x = load_vec<T, V>(src + c0 + u * 32 * V);
+    for (int j = 0; j < J; ++j) {
+      const int r = j0 + j < MAX_K ? __shfl_sync(0xffffffffu, mine, j0 + j) : -1;  // -1 past the last slot too
+      wt[j] = __shfl_sync(0xffffffffu, my_weight, j0 + j);
+      if (r < 0) wt[j] = 0.0f;
+      const T* src = static_cast<const T*>(p.src) + (r < 0 ? 0 : r) * p.src_ld;
 #pragma unroll
-        for (int i = 0; i < V; ++i) acc[u][i] = fmaf(wt, get(x, i), acc[u][i]);
+      for (int u = 0; u < U; ++u) {
+        x[j][u] = zero_vec<T, V>();
+        if (r >= 0 && c0 + u * 32 * V < p.dim) x[j][u] = load_vec<T, V>(src + c0 + u * 32 * V);
       }
+    }
+#pragma unroll
+    for (int j = 0; j < J; ++j)
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int i = 0; i < V; ++i) acc[u][i] = fmaf(wt[j], get(x[j][u], i), acc[u][i]);
   }
   T* dst = static_cast<T*>(p.dst) + t * p.dst_ld;
 #pragma unroll
@@ -346,8 +354,9 @@ __global__ void __launch_bounds__(ROW_THREADS) ns_moe_gather_kernel(const __grid
 }
 
 // combine's gradient: `parts` warps of one block share a token; each walks its
-// pieces of the row, writes w dy and sums dy ys, slot j's sum in lane j.
-template <typename T, int V, int U>
+// pieces of the row, writes w dy and sums dy ys, slot j's sum in lane j, with
+// the pieces of J rows on their way at once.
+template <typename T, int V, int U, int J>
 __global__ void __launch_bounds__(ROW_THREADS) ns_moe_combine_grad_kernel(const __grid_constant__ RowParams p) {
   __shared__ float part_sum[ROW_THREADS / 32][MAX_K];
   nsptx::griddep_wait();
@@ -371,30 +380,37 @@ __global__ void __launch_bounds__(ROW_THREADS) ns_moe_combine_grad_kernel(const 
 #pragma unroll
         for (int i = 0; i < V; ++i) g[u][i] = get(x, i);
       }
-      for (int j = 0; j < p.k; ++j) {
-        const int r = __shfl_sync(0xffffffffu, mine, j);
-        const float wt = __shfl_sync(0xffffffffu, my_weight, j);
-        if (r < 0) continue;
-        const T* ys = static_cast<const T*>(p.rows_in) + r * p.rows_ld;
-        T* out = static_cast<T*>(p.dst) + r * p.dst_ld;
-        Vec<T, V> y[U];
+      for (int j0 = 0; j0 < p.k; j0 += J) {
+        int r[J];
+        Vec<T, V> y[J][U];
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-          if (c0 + u * 32 * V < p.dim) y[u] = load_vec<T, V>(ys + c0 + u * 32 * V);
-        float dot = 0.0f;
+        for (int j = 0; j < J; ++j) {
+          r[j] = j0 + j < MAX_K ? __shfl_sync(0xffffffffu, mine, j0 + j) : -1;  // -1 past the last slot too
+          const T* ys = static_cast<const T*>(p.rows_in) + (r[j] < 0 ? 0 : r[j]) * p.rows_ld;
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-          if (c0 + u * 32 * V < p.dim) {
-            float o[V];
+          for (int u = 0; u < U; ++u)
+            if (r[j] >= 0 && c0 + u * 32 * V < p.dim) y[j][u] = load_vec<T, V>(ys + c0 + u * 32 * V);
+        }
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-              dot = fmaf(g[u][i], get(y[u], i), dot);
-              o[i] = wt * g[u][i];
+        for (int j = 0; j < J; ++j) {
+          if (r[j] < 0) continue;
+          const float wt = __shfl_sync(0xffffffffu, my_weight, j0 + j);
+          T* out = static_cast<T*>(p.dst) + r[j] * p.dst_ld;
+          float dot = 0.0f;
+#pragma unroll
+          for (int u = 0; u < U; ++u)
+            if (c0 + u * 32 * V < p.dim) {
+              float o[V];
+#pragma unroll
+              for (int i = 0; i < V; ++i) {
+                dot = fmaf(g[u][i], get(y[j][u], i), dot);
+                o[i] = wt * g[u][i];
+              }
+              store_vec<T, V>(out + c0 + u * 32 * V, pack<T, V>(o));
             }
-            store_vec<T, V>(out + c0 + u * 32 * V, pack<T, V>(o));
-          }
-        dot = warp_sum(dot);
-        if (lane == j) sum += dot;
+          dot = warp_sum(dot);
+          if (lane == j0 + j) sum += dot;
+        }
       }
     }
     if (p.parts == 1 && lane < p.k) p.grad_weights[t * p.k + lane] = sum;
@@ -463,12 +479,13 @@ int row_args(int dtype, int64_t tokens, int k, int64_t dim, int64_t rows) {
 
 enum RowOp { DISPATCH, GATHER, COMBINE_GRAD };
 
-template <typename T, int V, int U>
-cudaError_t launch_rows(RowOp op, nsk::RowParams& p, int nsm, cudaStream_t st) {
+// J: rows on their way at once, see the kernels.
+template <RowOp OP, typename T, int V, int U, int J>
+cudaError_t launch_rows(nsk::RowParams& p, int nsm, cudaStream_t st) {
   using namespace nsk;
   const int warps = ROW_THREADS / 32;
   const long long pieces = (p.dim + 32 * V * U - 1) / (32 * V * U);
-  if (op == COMBINE_GRAD) {
+  if (OP == COMBINE_GRAD) {
     // a token's warps sit in one block; few tokens are shared by more warps
     p.parts = 1;
     while (p.parts < warps && p.parts < pieces && p.tokens * p.parts < nsm * 16) p.parts *= 2;
@@ -476,37 +493,42 @@ cudaError_t launch_rows(RowOp op, nsk::RowParams& p, int nsm, cudaStream_t st) {
     p.parts = static_cast<int>(pieces);
   }
   p.token_warps = p.tokens * p.parts;
-  const long long all = p.token_warps + (op == GATHER ? 0 : (p.rows + CLEAR_ROWS - 1) / CLEAR_ROWS);
+  const long long all = p.token_warps + (OP == GATHER ? 0 : (p.rows + CLEAR_ROWS - 1) / CLEAR_ROWS);
   const long long blocks = (all + warps - 1) / warps;
   if (blocks > INT_MAX) return cudaErrorInvalidValue;
   const dim3 grid(static_cast<unsigned>(blocks)), block(ROW_THREADS);
-  if (op == DISPATCH) return launch_pdl(ns_moe_dispatch_kernel<T, V, U>, grid, block, 0, st, p);
-  if (op == GATHER) return launch_pdl(ns_moe_gather_kernel<T, V, U>, grid, block, 0, st, p);
-  return launch_pdl(ns_moe_combine_grad_kernel<T, V, U>, grid, block, 0, st, p);
+  if constexpr (OP == DISPATCH) return launch_pdl(ns_moe_dispatch_kernel<T, V, U>, grid, block, 0, st, p);
+  if constexpr (OP == GATHER) return launch_pdl(ns_moe_gather_kernel<T, V, U, J>, grid, block, 0, st, p);
+  if constexpr (OP == COMBINE_GRAD) return launch_pdl(ns_moe_combine_grad_kernel<T, V, U, J>, grid, block, 0, st, p);
 }
 
 // Words of 16 bytes where rows allow it, else of 4 (16-bit rows of an even
-// width), else single elements: 8192 x 6 bf16 rows of 2048, 2046 and 2047 sum
-// at 5.9, 4.2 and 3.6 TB/s.
-template <typename T>
-cudaError_t launch_rows_of(RowOp op, int word, nsk::RowParams& p, int nsm, cudaStream_t st) {
-  constexpr int V = 16 / sizeof(T);
-  if (word == 16) return op == GATHER ? launch_rows<T, V, 2>(op, p, nsm, st) : launch_rows<T, V, 4>(op, p, nsm, st);
+// width), else single elements: 8192 x 6 bf16 rows of 2048, 2046 and 2047 are
+// summed in 39.7, 40.6 and 56.2 us (5.9, 5.8 and 4.2 TB/s), backward in 68, 77
+// and 106 us.
+template <RowOp OP, typename T>
+cudaError_t launch_words(int word, nsk::RowParams& p, int nsm, cudaStream_t st) {
+  if (word == 16) return launch_rows<OP, T, 16 / sizeof(T), OP == GATHER ? 2 : 4, 3>(p, nsm, st);
+  constexpr int J = OP == GATHER ? 3 : 2;
   if constexpr (sizeof(T) == 2)
-    if (word == 4) return launch_rows<T, 2, 8>(op, p, nsm, st);
-  return launch_rows<T, 1, 8>(op, p, nsm, st);
+    if (word == 4) return launch_rows<OP, T, 2, 8, J>(p, nsm, st);
+  return launch_rows<OP, T, 1, 8, J>(p, nsm, st);
 }
 
-int run_rows(RowOp op, int dtype, nsk::RowParams& p, int word, void* stream) {
+template <RowOp OP>
+cudaError_t launch_type(int dtype, int word, nsk::RowParams& p, int nsm, cudaStream_t st) {
+  if (dtype == NS_DT_BF16) return launch_words<OP, __nv_bfloat16>(word, p, nsm, st);
+  if (dtype == NS_DT_FP16) return launch_words<OP, __half>(word, p, nsm, st);
+  return launch_words<OP, float>(word, p, nsm, st);
+}
+
+template <RowOp OP>
+int run_rows(int dtype, nsk::RowParams& p, int word, void* stream) {
   int dev, nsm;
   const int rc = device_setup(&dev, &p.status, &nsm);
   if (rc != NS_OK) return rc;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = counted(K_MOE, st, [&] {
-    if (dtype == NS_DT_BF16) return launch_rows_of<__nv_bfloat16>(op, word, p, nsm, st);
-    if (dtype == NS_DT_FP16) return launch_rows_of<__half>(op, word, p, nsm, st);
-    return launch_rows_of<float>(op, word, p, nsm, st);
-  });
+  const cudaError_t e = counted(K_MOE, st, [&] { return launch_type<OP>(dtype, word, p, nsm, st); });
   return e == cudaSuccess ? NS_OK : NS_ERR_CUDA;
 }
 
@@ -609,7 +631,7 @@ int ns_moe_dispatch(const void* x, int64_t x_stride, int dtype, int64_t tokens, 
   p.dim = dim;
   p.k = k;
   const int b = elem_bytes(dtype);
-  return run_rows(DISPATCH, dtype, p, common_word(b, dim, {{x, x_stride}, {out, out_stride}}), stream);
+  return run_rows<DISPATCH>(dtype, p, common_word(b, dim, {{x, x_stride}, {out, out_stride}}), stream);
 }
 
 int ns_moe_combine(const void* expert_rows, int64_t rows_stride, int dtype, int64_t tokens, int k, int64_t dim,
@@ -632,7 +654,7 @@ int ns_moe_combine(const void* expert_rows, int64_t rows_stride, int dtype, int6
   p.dim = dim;
   p.k = k;
   const int b = elem_bytes(dtype);
-  return run_rows(GATHER, dtype, p, common_word(b, dim, {{expert_rows, rows_stride}, {y, y_stride}}), stream);
+  return run_rows<GATHER>(dtype, p, common_word(b, dim, {{expert_rows, rows_stride}, {y, y_stride}}), stream);
 }
 
 int ns_moe_dispatch_grad(const void* grad_rows, int64_t rows_stride, int dtype, int64_t tokens, int k, int64_t dim,
@@ -669,7 +691,7 @@ int ns_moe_combine_grad(const void* grad_y, int64_t grad_y_stride, const void* e
   p.k = k;
   const int b = elem_bytes(dtype);
   const int word = common_word(b, dim, {{grad_y, grad_y_stride}, {expert_rows, rows_stride}, {grad_rows, grad_rows_stride}});
-  return run_rows(COMBINE_GRAD, dtype, p, word, stream);
+  return run_rows<COMBINE_GRAD>(dtype, p, word, stream);
 }
 
 }  // extern "C"
