@@ -28,6 +28,7 @@ namespace {
 constexpr int DISTILL_THREADS = 512;
 constexpr int DISTILL_WARPS = DISTILL_THREADS / 32;
 constexpr int DISTILL_MAX_TOP = 1024;
+constexpr int FEW = 4;  // entries a lane of one warp that are held in registers
 constexpr int DISTILL_MAX_CLUSTER = 8;  // the portable limit
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 
@@ -49,6 +50,7 @@ struct DistillParams {
   int places;           // of the hash table of the teacher's ids
   int cluster;          // blocks that share a token
   int slice_words;      // most words of 16 bytes of a block
+  int eager;            // few blocks: a row is read before its weight is known
   unsigned int* status;
 };
 
@@ -106,6 +108,14 @@ __device__ __forceinline__ int table_place(int id, int mask) {
   return static_cast<int>(static_cast<unsigned>(id) * 2654435761u >> 16) & mask;
 }
 
+// Entry i of all tokens' as it was given.
+__device__ __forceinline__ void entry_of(const DistillParams& p, long long i, long long* id, float* z) {
+  *id = load_index(p.ids, p.id_bytes, i);
+  *z = p.teacher_dtype == NS_DT_FP32   ? static_cast<const float*>(p.teacher)[i]
+       : p.teacher_dtype == NS_DT_BF16 ? to_float(static_cast<const __nv_bfloat16*>(p.teacher)[i])
+                                       : to_float(static_cast<const __half*>(p.teacher)[i]);
+}
+
 // Loads the entries with `n` threads, 4 at a time each so that their latencies
 // overlap; whether this thread left any in.
 template <typename T>
@@ -119,15 +129,9 @@ __device__ __forceinline__ bool load_teacher(const DistillParams& p, const Teach
 #pragma unroll
     for (int b = 0; b < B; ++b) {
       const int j = j0 + b * n;
-      const long long i = t * p.top + j;
       id[b] = -1;
       z[b] = -INFINITY;
-      if (j < p.top && weight != 0.0f) {
-        id[b] = load_index(p.ids, p.id_bytes, i);
-        z[b] = p.teacher_dtype == NS_DT_FP32   ? static_cast<const float*>(p.teacher)[i]
-               : p.teacher_dtype == NS_DT_BF16 ? to_float(static_cast<const __nv_bfloat16*>(p.teacher)[i])
-                                               : to_float(static_cast<const __half*>(p.teacher)[i]);
-      }
+      if (j < p.top && weight != 0.0f) entry_of(p, t * p.top + j, &id[b], &z[b]);
     }
 #pragma unroll
     for (int b = 0; b < B; ++b) {
@@ -199,6 +203,66 @@ __device__ __forceinline__ void teacher_probabilities(const DistillParams& p, co
     te.sums[0] = mass;
     te.sums[1] = part;
   }
+}
+
+// Both for up to 4 entries a lane, held in registers: the student's logits are
+// on their way while the probabilities are computed. Whether an entry is left.
+template <typename T>
+__device__ __forceinline__ bool few_entries(const DistillParams& p, const Teacher& te, long long t, const T* row,
+                                            float weight, int lane) {
+  long long id[FEW];
+  float z[FEW], s[FEW], pr[FEW];
+  const float given = p.teacher_lse ? p.teacher_lse[t] : 0.0f;
+#pragma unroll
+  for (int b = 0; b < FEW; ++b) {
+    const int j = lane + 32 * b;
+    id[b] = -1;
+    z[b] = -INFINITY;
+    if (j < p.top) entry_of(p, t * p.top + j, &id[b], &z[b]);  // whatever the weight: it is on its way too
+  }
+  float z0 = -INFINITY;
+  bool refused = false;
+#pragma unroll
+  for (int b = 0; b < FEW; ++b) {
+    if (weight == 0.0f) id[b] = -1;
+    refused |= id[b] >= p.vocab;
+    if (id[b] < 0 || id[b] >= p.vocab || z[b] == -INFINITY) id[b] = -1;
+    s[b] = id[b] >= 0 ? to_float(row[id[b]]) : 0.0f;
+    if (id[b] >= 0) z0 = fmaxf(z0, z[b]);
+  }
+  if (refused) atomicOr(p.status, NS_DEV_BAD_INDEX);
+  const bool any = __any_sync(0xffffffffu, id[0] >= 0 || id[1] >= 0 || id[2] >= 0 || id[3] >= 0);
+  if (!any) return false;
+  float sum = 0.0f;
+  z0 = p.teacher_lse ? 0.0f : warp_max(z0);
+#pragma unroll
+  for (int b = 0; b < FEW; ++b) {
+    z[b] = (z[b] - z0) * p.inv_tau - given;
+    pr[b] = id[b] >= 0 ? expf(z[b]) : 0.0f;
+    sum += pr[b];
+  }
+  sum = warp_sum(sum);
+  const float inv = p.teacher_lse ? 1.0f : 1.0f / sum, zlog = p.teacher_lse ? 0.0f : logf(sum);
+  float mass = 0.0f, part = 0.0f;
+#pragma unroll
+  for (int b = 0; b < FEW; ++b) {
+    const int j = lane + 32 * b;
+    pr[b] *= inv;
+    if (pr[b] != 0.0f) part += pr[b] * (z[b] - zlog - s[b] * p.inv_tau);
+    mass += pr[b];
+    if (j < p.top) {
+      te.id[j] = static_cast<int>(id[b]);
+      te.p[j] = pr[b];
+      te.s[j] = s[b];
+    }
+  }
+  mass = warp_sum(mass);
+  part = warp_sum(part);
+  if (lane == 0) {
+    te.sums[0] = mass;
+    te.sums[1] = part;
+  }
+  return true;
 }
 
 // The elements of a row that a block writes: its words, and for one block those
@@ -287,12 +351,13 @@ __global__ void __launch_bounds__(NT + 32) ns_distill_kernel(const __grid_consta
   const bool has_edge = rank == 0 && edge < vocab && (tid < head || edge >= tail);
 
   if (warp == WARPS) {
-    const bool some = load_teacher(p, te, t, row, weight, lane, 32);
-    const int any = __any_sync(0xffffffffu, some);
-    __syncwarp();
-    if (any) {
-      teacher_probabilities(p, te, t, lane);
-      if (p.grad) mark_repeated(te, p.top, p.places - 1, lane);
+    bool any;
+    if (p.top <= 32 * FEW) {
+      any = few_entries(p, te, t, row, weight, lane);
+    } else {
+      any = __any_sync(0xffffffffu, load_teacher(p, te, t, row, weight, lane, 32));
+      __syncwarp();
+      if (any) teacher_probabilities(p, te, t, lane);
     }
     if (lane == 0) *te.any = any;
     if (joins) {
@@ -319,6 +384,7 @@ __global__ void __launch_bounds__(NT + 32) ns_distill_kernel(const __grid_consta
       lse2 = p.lse[t] * LOG2E;
     }
     if (!p.grad) return;
+    mark_repeated(te, p.top, p.places - 1, lane);
     __syncthreads();  // the plain part of the gradient is written
     const int first = head + w0 * V;
     const Slice slice = {first, first + n * V, head, tail, rank == 0};
@@ -330,7 +396,7 @@ __global__ void __launch_bounds__(NT + 32) ns_distill_kernel(const __grid_consta
   const T* body = row + head + static_cast<long long>(w0) * V;
   uint4* mine = slice_smem + tid;
   const int rounds = (n + NT - 1) / NT, quarter = (rounds + 4 * B - 1) / (4 * B) * B;  // words a thread; in a copy group
-  if (weight != 0.0f) {
+  if (weight != 0.0f || p.eager) {
     for (int g = 0; g < 4; ++g) {
       for (int u = g * quarter; u < min(rounds, (g + 1) * quarter); ++u)
         if (u * NT + tid < n) nsptx::cp_async16(mine + u * NT, body + (u * NT + tid) * V);
@@ -563,6 +629,7 @@ cudaError_t launch_distill(DistillParams& p, long long tokens, int nsm, cudaStre
   p.cluster = C;
   p.slice_words = static_cast<int>((words + C - 1) / C);
   p.places = table_size(p.top);
+  p.eager = tokens * C <= 2 * nsm;
   const size_t smem = 16 * static_cast<size_t>(p.slice_words) + teacher_bytes(p.top);
   if (smem > DISTILL_MAX_SMEM || tokens * C > INT_MAX)
     return launch_pdl(ns_distill_long_kernel<T>, dim3(static_cast<unsigned>(tokens)), dim3(DISTILL_THREADS),
