@@ -12,6 +12,7 @@
 // Every value is read and written once, so the kernels are bound by memory.
 #include <algorithm>
 #include <climits>
+#include <cstdlib>
 
 #include "elem.cuh"
 #include "launch.cuh"
@@ -37,8 +38,8 @@ struct QkSide {
   const void* weight; // null: 1
   long long x_token, x_head, dy_token, dy_head, out_token, out_head;  // strides in elements
   int heads;
-  // what a step adds to each address, in bytes: x, dy, out
-  long long within[3], between[3], wrap[3];
+  // (token, head) strides of x, dy and out in bytes, where they fit
+  int token_bytes[3], head_bytes[3];
 };
 
 // A pair (token, head) of one side, in token order; steps go by a number of
@@ -190,16 +191,22 @@ __device__ __forceinline__ void load_angles(const QkParams& p, const Lane<T>& l,
   constexpr int N = Two<T>::N;
   const int half = p.rot_dim / 2;
   const int a = p.interleaved ? l.a / 2 : l.a, b = p.interleaved ? l.b / 2 : l.a + N;
-#pragma unroll
-  for (int i = 0; i < N / 2; ++i) {
-    if (l.turn_a) {
-      g.c[i] = *reinterpret_cast<const float2*>(row + a + 2 * i);
-      g.s[i] = *reinterpret_cast<const float2*>(row + half + a + 2 * i);
+  auto load = [&](float2* to, const float* from) {
+    if constexpr (N == 4) {
+      const float4 f = *reinterpret_cast<const float4*>(from);
+      to[0] = make_float2(f.x, f.y);
+      to[1] = make_float2(f.z, f.w);
+    } else {
+      to[0] = *reinterpret_cast<const float2*>(from);
     }
-    if (l.turn_b) {
-      g.c[N / 2 + i] = *reinterpret_cast<const float2*>(row + b + 2 * i);
-      g.s[N / 2 + i] = *reinterpret_cast<const float2*>(row + half + b + 2 * i);
-    }
+  };
+  if (l.turn_a) {
+    load(g.c, row + a);
+    load(g.s, row + half + a);
+  }
+  if (l.turn_b) {
+    load(g.c + N / 2, row + b);
+    load(g.s + N / 2, row + half + b);
   }
 }
 
@@ -298,20 +305,15 @@ __device__ __forceinline__ Two<T> lane_weights(const QkParams& p, const QkSide& 
 // those of the warp's next chunk.
 struct Walk {
   int t, h, left;
-  bool wrapped;  // the last step went past the token's last head
-  __device__ __forceinline__ explicit Walk(const Place& at) : t(at.t), h(at.h), left(0), wrapped(false) {}
-  // One step; whether it went to the next chunk.
-  __device__ __forceinline__ bool step(const QkParams& p, int which, int heads) {
+  __device__ __forceinline__ void step(const QkParams& p, int which, int heads) {
     const bool jump = --left == 0;
     if (jump) left = p.chunk;
     t += jump ? p.between[which].t : p.within[which].t;
     h += jump ? p.between[which].h : p.within[which].h;
-    wrapped = h >= heads;
-    if (wrapped) {
+    if (h >= heads) {
       h -= heads;
       ++t;
     }
-    return jump;
   }
 };
 
@@ -354,25 +356,30 @@ __global__ void __launch_bounds__(QK_THREADS, GRAD ? QK_GRAD_BLOCKS : QK_BLOCKS)
     if (n > 0) {
       const Two<T> g = lane_weights<T>(p, side, l);
       const Place start = place_of(first * p.chunk * H + min(group, H - 1), side.heads);
-      Walk ahead(start), at(start);  // of the copies, and of the rounds
-      const char* x_at = static_cast<const char*>(side.x) + sizeof(T) * (start.t * side.x_token + start.h * side.x_head + l.a);
-      const char* dy_at = static_cast<const char*>(side.dy) + sizeof(T) * (start.t * side.dy_token + start.h * side.dy_head + l.a);
-      char* out_at = static_cast<char*>(side.out) + sizeof(T) * (start.t * side.out_token + start.h * side.out_head + l.a);
+      Walk ahead = {start.t, start.h, p.chunk}, at = ahead;  // of the copies, and of the rounds
+      // tensor k's address of the lane's first word of a head: two wide multiply-adds
+      auto offset = [&](const Walk& w, int k) {
+        return static_cast<long long>(w.t) * side.token_bytes[k] + static_cast<long long>(w.h) * side.head_bytes[k];
+      };
+      const char* const x_base = static_cast<const char*>(side.x) + sizeof(T) * l.a;
+      const char* const dy_base = static_cast<const char*>(side.dy) + sizeof(T) * l.a;
+      char* const out_base = static_cast<char*>(side.out) + sizeof(T) * l.a;
       const int to_b = static_cast<int>(sizeof(T)) * (l.b - l.a);
       const bool takes = group < H;  // a lane left over takes no head
-      ahead.left = at.left = p.chunk;
       int fill = 0, take = 0;
       auto copy = [&](bool more) {
         if (more && takes && ahead.t < p.tokens) {
+          const char* x_at = x_base + offset(ahead, 0);
           if (l.on_a) nsptx::cp_async16(ring + fill, x_at);
           if (l.on_b) nsptx::cp_async16(ring + fill + 32, x_at + to_b);
-          if (GRAD && l.on_a) nsptx::cp_async16(ring + fill + 64, dy_at);
-          if (GRAD && l.on_b) nsptx::cp_async16(ring + fill + 96, dy_at + to_b);
+          if (GRAD) {
+            const char* dy_at = dy_base + offset(ahead, 1);
+            if (l.on_a) nsptx::cp_async16(ring + fill + 64, dy_at);
+            if (l.on_b) nsptx::cp_async16(ring + fill + 96, dy_at + to_b);
+          }
         }
         nsptx::cp_async_commit();
-        const bool jump = ahead.step(p, which, side.heads), wrap = ahead.wrapped;
-        x_at += (jump ? side.between[0] : side.within[0]) + (wrap ? side.wrap[0] : 0);
-        if (GRAD) dy_at += (jump ? side.between[1] : side.within[1]) + (wrap ? side.wrap[1] : 0);
+        ahead.step(p, which, side.heads);
         fill = fill + STAGE == STAGES * STAGE ? 0 : fill + STAGE;
       };
       for (int r = 0; r < QK_AHEAD; ++r) copy(r < n);
@@ -439,9 +446,8 @@ __global__ void __launch_bounds__(QK_THREADS, GRAD ? QK_GRAD_BLOCKS : QK_BLOCKS)
             u.b[i] = fma2(u.b[i], r2, mul2(xf.b[i], m2));
           }
         }
-        if (live) store_words<T>(out_at, to_b, l, u);
-        const bool jump = at.step(p, which, side.heads);
-        out_at += (jump ? side.between[2] : side.within[2]) + (at.wrapped ? side.wrap[2] : 0);
+        if (live) store_words<T>(out_base + offset(at, 2), to_b, l, u);
+        at.step(p, which, side.heads);
       }
       nsptx::cp_async_wait<0>();
     }
@@ -596,13 +602,6 @@ cudaError_t launch_lanes(bool grad, QkParams& p, int nsm, int* blocks, cudaStrea
     if (!p.side[i].heads) continue;
     p.within[i] = place_of(H, p.side[i].heads);
     p.between[i] = place_of(H + (*blocks * QK_WARPS - 1) * p.chunk * H, p.side[i].heads);
-    QkSide& s = p.side[i];
-    const long long token[3] = {s.x_token, s.dy_token, s.out_token}, head[3] = {s.x_head, s.dy_head, s.out_head};
-    for (int k = 0; k < 3; ++k) {
-      s.within[k] = static_cast<long long>(sizeof(T)) * (p.within[i].t * token[k] + p.within[i].h * head[k]);
-      s.between[k] = static_cast<long long>(sizeof(T)) * (p.between[i].t * token[k] + p.between[i].h * head[k]);
-      s.wrap[k] = static_cast<long long>(sizeof(T)) * (token[k] - s.heads * head[k]);
-    }
   }
   const size_t smem = sizeof(uint4) * QK_WARPS * (QK_AHEAD + 1) * (grad ? 128 : 64) +
                       (SPREAD ? sizeof(float) * QK_WARPS * 64 * Lane<T>::V : 0);
@@ -687,6 +686,13 @@ int run_qk(bool grad, const void* const* x, const void* const* dy, void* const* 
     if (grad) {
       s.dy_token = strides[8 + 2 * i];
       s.dy_head = strides[9 + 2 * i];
+    }
+    const int64_t token[3] = {s.x_token, s.dy_token, s.out_token}, head[3] = {s.x_head, s.dy_head, s.out_head};
+    for (int k = 0; k < 3; ++k) {
+      const bool fits = std::llabs(token[k]) <= INT_MAX / 4 && std::llabs(head[k]) <= INT_MAX / 4;
+      lanes = lanes && fits;
+      s.token_bytes[k] = fits ? static_cast<int>(token[k]) * b : 0;
+      s.head_bytes[k] = fits ? static_cast<int>(head[k]) * b : 0;
     }
     if (heads[i] == 0) continue;
     lanes = lanes && (reinterpret_cast<uintptr_t>(s.weight) & 15) == 0 && words_ok(s.x, s.x_token, s.x_head, b) && words_ok(s.out, s.out_token, s.out_head, b) &&
