@@ -312,8 +312,8 @@ int ns_orthogonalize_batched_fixed_ws(ns_plan_t* plan, const void* const* in, vo
  *
  * Common to all: device buffers are the caller's; strides are in elements and
  * the last dimension is contiguous; element types are NS_DT_*; sums, norms and
- * softmax statistics are in fp32 and a result is rounded to its type once;
- * results do not depend on the launch (no atomics on floating values). Buffers
+ * softmax statistics are in fp32 and a result is rounded to its type once; the
+ * same call gives the same bits (no atomics on floating values). Buffers
  * of one call must not overlap unless its text says so. A zero count (tokens,
  * heads, rows) is valid and does what the formulas say. Workspaces are scratch
  * (no contents kept between calls), 256-byte aligned. Work is asynchronous on
@@ -432,10 +432,9 @@ int ns_qk_norm_rope_grad(const void* grad_q_out, const void* grad_k_out, const v
  *                    (sum_j p_j * exp(s[v] / temperature - lse) - sum of the p_j with i_j = v).
  * weights NULL = 1. Entries with a negative id (padding) or a value of -inf
  * are left out; an id >= vocab is refused and left out. A token whose weight is
- * 0 or that has no entry left gets loss 0, lse 0 and a zero gradient, and its
- * logits are not read. grad_logits may be logits itself, with the same stride.
- * top <= 1024. A finite logit is needed in every row that is read; a row of
- * -inf gives NaN. */
+ * 0 or that has no entry left gets loss 0, lse 0 and a zero gradient, whatever
+ * its logits hold. grad_logits may be logits itself, with the same stride.
+ * top <= 1024. Any other row needs a finite logit: one of -inf gives NaN. */
 int ns_distill_loss(const void* logits, int64_t logits_stride, int dtype, int64_t tokens, int64_t vocab,
                     const void* teacher_values, int teacher_dtype, const void* teacher_ids, int id_bytes, int top,
                     const float* weights, const float* teacher_lse, float temperature, float* loss, float* lse,

@@ -11,7 +11,15 @@
 //   its gradient   dx[t]      = sum_j dxs[row(t, j)]
 //   combine        y[t]       = sum_j w[t, j] ys[row(t, j)]
 //   its gradient   dys[row_s] = w_s dy[t], dw[t, j] = <dy[t], ys[row(t, j)]>
-// Sums are in fp32 in the order of j, so results do not depend on the launch.
+// Sums over j are in fp32 in the order of j, dot products in a fixed order:
+// the same call gives the same bits.
+//
+// The sort is bound by latency: 32 x 8 slots take one launch of 2.7 us,
+// 32768 x 6 two of 6.4 us together, the second started while the first counts.
+// The rest moves whole rows and is bound by memory: 8192 x 6 rows of 2048 bf16
+// are dispatched (padded to 128 rows an expert) in 43 us, 6.3 TB/s, combined in
+// 40 us, 5.9 TB/s, and the gradient of combining them takes 68 us, 6.4 TB/s,
+// against 6.7 TB/s of the measured copy.
 #include <algorithm>
 #include <climits>
 #include <initializer_list>
@@ -281,7 +289,8 @@ __device__ __forceinline__ void clear_rows(const RowParams& p, long long group, 
 }
 
 // dispatch: a warp holds up to 32 * V * U elements of a token's row and stores
-// them to each of its rows, so x is read once.
+// them to each of its rows, so x is read once. (Bulk copies through shared
+// memory measured no faster: a row's stores are what takes the time.)
 template <typename T, int V, int U>
 __global__ void __launch_bounds__(ROW_THREADS) ns_moe_dispatch_kernel(const __grid_constant__ RowParams p) {
   nsptx::griddep_wait();
