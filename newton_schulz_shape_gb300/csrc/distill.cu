@@ -81,10 +81,11 @@ __device__ __forceinline__ long long head_of(const T* p, long long n) {
   return h < n ? h : n;
 }
 
-// Places of the hash table of `top` ids: a power of two, twice the ids or more.
+// Places of the hash table of `top` ids: a power of two, four times the ids or
+// more, which keeps searches at one or two places.
 __host__ __device__ inline int table_size(int top) {
   int n = 4;
-  while (n < 2 * top) n *= 2;
+  while (n < 4 * top) n *= 2;
   return n;
 }
 
@@ -104,8 +105,10 @@ size_t teacher_bytes(int top) { return sizeof(float) * (3 * static_cast<size_t>(
 
 constexpr int NO_ID = 0x7fffffff;  // an empty place; ids are below it
 
+// The upper bits of a multiple of the golden ratio: ids at equal distances, as
+// the lower ones would not, spread over the table.
 __device__ __forceinline__ int table_place(int id, int mask) {
-  return static_cast<int>(static_cast<unsigned>(id) * 2654435761u >> 16) & mask;
+  return static_cast<int>((static_cast<unsigned>(id) * 2654435761u) >> __clz(mask));
 }
 
 // Entry i of all tokens' as it was given.
@@ -162,7 +165,7 @@ __device__ __forceinline__ void mark_repeated(const Teacher& te, int top, int ma
   for (int j = lane; j < top; j += 32) {
     const int id = te.id[j];
     if (id < 0) continue;
-    for (int h = table_place(id, mask);; h = (h + 1) & mask) {  // ends: at least half of the places stay empty
+    for (int h = table_place(id, mask);; h = (h + 1) & mask) {  // ends: most places stay empty
       const int old = atomicCAS(&te.table[h], NO_ID, id);
       if (old == NO_ID) break;
       if ((old & 0x7fffffff) == id) {

@@ -41,7 +41,6 @@ constexpr int SORT_THREADS = 512;
 constexpr int SORT_WARPS = SORT_THREADS / 32;
 constexpr int SORT_HELD = 4;  // rounds of 32 slots that a warp keeps in registers
 constexpr int SORT_MAX_BLOCKS = 256;
-constexpr int SORT_ONE_BLOCK = 3584;  // 600 x 6 slots: 9.0 us in one block, 9.6 in two launches; 680 x 6: 10.3 and 9.5
 constexpr int ROW_THREADS = 128;
 constexpr int CLEAR_ROWS = 4;
 
@@ -461,14 +460,13 @@ int common_word(int elem, long long dim, std::initializer_list<std::pair<const v
   return elem;
 }
 
-// Slots per block and blocks of a sort. One block up to SORT_ONE_BLOCK slots
-// (more blocks need the counts first, a second launch); then blocks of what
-// their warps hold in registers, then larger blocks.
+// Slots per block and blocks of a sort: one block for as many slots as its warps
+// hold in registers, then blocks of that size (with the counts first, a second
+// launch), then larger ones.
 void sort_split(long long slots, int* chunk, int* blocks) {
   constexpr int held = nsk::SORT_THREADS * nsk::SORT_HELD;
   long long c = slots;
-  if (slots > nsk::SORT_ONE_BLOCK)
-    c = std::max<long long>(held, (slots + nsk::SORT_MAX_BLOCKS - 1) / nsk::SORT_MAX_BLOCKS);
+  if (slots > held) c = std::max<long long>(held, (slots + nsk::SORT_MAX_BLOCKS - 1) / nsk::SORT_MAX_BLOCKS);
   c = std::max<long long>(1, (c + nsk::SORT_THREADS - 1) / nsk::SORT_THREADS) * nsk::SORT_THREADS;
   *chunk = static_cast<int>(c);
   *blocks = static_cast<int>(std::max<long long>(1, (slots + c - 1) / c));

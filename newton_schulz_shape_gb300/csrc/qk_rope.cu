@@ -572,32 +572,37 @@ struct QkSumParams {
   int blocks, dim;
 };
 
-// dg: sums of the blocks' partial sums, in a fixed order.
-__global__ void __launch_bounds__(256) ns_qk_sum_kernel(const __grid_constant__ QkSumParams p) {
-  __shared__ float part[8][32];
+// dg: sums of the blocks' partial sums, in a fixed order: 32 columns a block,
+// whose 32 warps split the partial sums.
+__global__ void __launch_bounds__(1024) ns_qk_sum_kernel(const __grid_constant__ QkSumParams p) {
+  __shared__ float part[32][33];
   nsptx::griddep_wait();
   nsptx::griddep_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, col = blockIdx.x * 32 + lane;
   float sum = 0.0f;
-  if (col < 2 * p.dim)
-    for (int b = warp; b < p.blocks; b += 8) sum += p.partial[static_cast<long long>(b) * 2 * p.dim + col];
+  if (col < 2 * p.dim) {
+#pragma unroll 8
+    for (int b = warp; b < p.blocks; b += 32) sum += p.partial[static_cast<long long>(b) * 2 * p.dim + col];
+  }
   part[warp][lane] = sum;
   __syncthreads();
-  if (warp || col >= 2 * p.dim) return;
-#pragma unroll
-  for (int k = 1; k < 8; ++k) sum += part[k][lane];
-  float* out = p.out[col >= p.dim];
-  if (out) out[col >= p.dim ? col - p.dim : col] = sum;
+  // warp w sums column w's parts
+  sum = warp_sum(part[lane][warp]);
+  const int c = blockIdx.x * 32 + warp;
+  if (lane || c >= 2 * p.dim) return;
+  float* out = p.out[c >= p.dim];
+  if (out) out[c >= p.dim ? c - p.dim : c] = sum;
 }
 
 template <typename T, int G, bool SPREAD = false>
 cudaError_t launch_lanes(bool grad, QkParams& p, int nsm, int* blocks, cudaStream_t st) {
   const int H = 32 / p.lanes;
   const int most = std::min(nsm * (grad ? QK_GRAD_BLOCKS : QK_BLOCKS), QK_MAX_BLOCKS);
-  // up to 8 rounds a chunk (a token's angles serve them all: 16384 tokens of 32/8 heads take 131, 107, 97
-  // and 93 us backward with 1, 2, 4 and 8), but 4 chunks a warp, so that the warps end together
+  // a warp's rounds in equal chunks of at most 8: long ones, since a token's angles serve all of its rounds
+  // (16384 tokens of 32/8 heads take 131, 107, 97 and 93 us backward in chunks of 1, 2, 4 and 8)
   const int rounds = static_cast<int>((p.tokens * (p.side[0].heads + p.side[1].heads) + H - 1) / H);
-  p.chunk = std::min(8, std::max(1, rounds / (most * QK_WARPS * 4)));
+  const int each = (rounds + most * QK_WARPS - 1) / (most * QK_WARPS), parts = (each + 7) / 8;
+  p.chunk = std::max(1, (each + parts - 1) / std::max(1, parts));
   for (int i = 0; i < 2; ++i)
     p.chunks[i] = static_cast<int>((p.tokens * p.side[i].heads + H * p.chunk - 1) / (H * p.chunk));
   *blocks = std::min((p.chunks[0] + p.chunks[1] + QK_WARPS - 1) / QK_WARPS, most);
@@ -728,7 +733,7 @@ int run_qk(bool grad, const void* const* x, const void* const* dy, void* const* 
   if (!sums) return NS_OK;
   nsk::QkSumParams sp = {p.partial, {grad_weight[0], grad_weight[1]}, blocks, head_dim};
   const cudaError_t e = counted(K_QK, st, [&] {
-    return nsk::launch_pdl(nsk::ns_qk_sum_kernel, dim3((2 * head_dim + 31) / 32), dim3(256), 0, st, sp);
+    return nsk::launch_pdl(nsk::ns_qk_sum_kernel, dim3((2 * head_dim + 31) / 32), dim3(1024), 0, st, sp);
   });
   return e == cudaSuccess ? NS_OK : NS_ERR_CUDA;
 }
