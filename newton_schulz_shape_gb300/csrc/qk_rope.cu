@@ -455,23 +455,21 @@ __global__ void __launch_bounds__(QK_THREADS, GRAD ? QK_GRAD_BLOCKS : QK_BLOCKS)
       nsptx::cp_async_wait<0>();
     }
     if (GRAD && p.partial) {
-      float* joined = reinterpret_cast<float*>(ring_smem);  // [warps][dim]; the rings are done with
+      float* joined = reinterpret_cast<float*>(ring_smem);  // [warps][H][dim]; the rings are done with
       __syncthreads();
+      if (group < H) {
+        float* mine = joined + (warp * H + group) * p.dim;
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float mine = k < 2 ? (k ? dg.a[i].y : dg.a[i].x) : (k & 1 ? dg.b[i].y : dg.b[i].x);
-          float sum = 0.0f;
-          for (int h = 0; h < H; ++h) sum += __shfl_sync(0xffffffffu, mine, h * group_size + i_lane);
-          if (group == 0 && (k < 2 ? l.on_a : l.on_b)) joined[warp * p.dim + (k < 2 ? l.a : l.b) + 2 * i + (k & 1)] = sum;
+        for (int i = 0; i < N; ++i) {
+          if (l.on_a) *reinterpret_cast<float2*>(mine + l.a + 2 * i) = dg.a[i];
+          if (l.on_b) *reinterpret_cast<float2*>(mine + l.b + 2 * i) = dg.b[i];
         }
       }
       __syncthreads();
       for (int d = threadIdx.x; d < p.dim; d += QK_THREADS) {
         float sum = 0.0f;
-#pragma unroll
-        for (int k = 0; k < QK_WARPS; ++k) sum += joined[k * p.dim + d];
+#pragma unroll 4
+        for (int k = 0; k < QK_WARPS * H; ++k) sum += joined[k * p.dim + d];
         p.partial[(static_cast<long long>(blockIdx.x) * 2 + which) * p.dim + d] = sum;
       }
       __syncthreads();
