@@ -15,14 +15,15 @@
 // the same call gives the same bits.
 //
 // The sort is bound by latency: 32 x 8 slots take one launch of 2.7 us,
-// 32768 x 6 two of 6.4 us together, the second started while the first counts.
+// 32768 x 6 two of 6 us together, the second started while the first counts.
 // The rest moves whole rows and is bound by memory: 8192 x 6 rows of 2048 bf16
 // are dispatched (padded to 128 rows an expert) in 43 us, 6.3 TB/s, combined in
-// 40 us, 5.9 TB/s, and the gradient of combining them takes 68 us, 6.4 TB/s,
+// 38 us, 6.3 TB/s, and the gradient of combining them takes 70 us, 6.3 TB/s,
 // against 6.7 TB/s of the measured copy.
 #include <algorithm>
 #include <climits>
 #include <initializer_list>
+#include <type_traits>
 #include <utility>
 
 #include "elem.cuh"
@@ -301,21 +302,28 @@ __global__ void __launch_bounds__(ROW_THREADS) ns_moe_dispatch_kernel(const __gr
     return;
   }
   const long long t = w / p.parts;
-  const long long c0 = (w - t * p.parts) * (32 * V * U) + lane * V;
-  const T* src = static_cast<const T*>(p.src) + t * p.src_ld;
+  const int start = static_cast<int>(w - t * p.parts) * (32 * V * U), c0 = start + lane * V, dim = static_cast<int>(p.dim);
+  const T* src = static_cast<const T*>(p.src) + t * p.src_ld + c0;
   const int mine = lane_row(p, t, lane);
-  Vec<T, V> x[U];
-#pragma unroll
-  for (int u = 0; u < U; ++u)
-    if (c0 + u * 32 * V < p.dim) x[u] = load_vec<T, V>(src + c0 + u * 32 * V);
-  for (int j = 0; j < p.k; ++j) {
-    const int r = __shfl_sync(0xffffffffu, mine, j);
-    if (r < 0) continue;
-    T* dst = static_cast<T*>(p.dst) + r * p.dst_ld;
+  // `whole`: the piece ends inside the row, and needs no check of its columns
+  auto piece = [&](auto whole) {
+    Vec<T, V> x[U];
 #pragma unroll
     for (int u = 0; u < U; ++u)
-      if (c0 + u * 32 * V < p.dim) store_vec<T, V>(dst + c0 + u * 32 * V, x[u]);
-  }
+      if (decltype(whole)::value || c0 + u * 32 * V < dim) x[u] = load_vec<T, V>(src + u * 32 * V);
+    for (int j = 0; j < p.k; ++j) {
+      const int r = __shfl_sync(0xffffffffu, mine, j);
+      if (r < 0) continue;
+      T* dst = static_cast<T*>(p.dst) + r * p.dst_ld + c0;
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (decltype(whole)::value || c0 + u * 32 * V < dim) store_vec<T, V>(dst + u * 32 * V, x[u]);
+    }
+  };
+  if (start + 32 * V * U <= dim)
+    piece(std::true_type());
+  else
+    piece(std::false_type());
 }
 
 // combine and the gradient of dispatch: a warp sums 32 * V * U elements of a
@@ -328,40 +336,49 @@ __global__ void __launch_bounds__(ROW_THREADS) ns_moe_gather_kernel(const __grid
   const long long w = static_cast<long long>(blockIdx.x) * (ROW_THREADS / 32) + (threadIdx.x >> 5);
   if (w >= p.token_warps) return;
   const long long t = w / p.parts;
-  const long long c0 = (w - t * p.parts) * (32 * V * U) + lane * V;
+  const int start = static_cast<int>(w - t * p.parts) * (32 * V * U), c0 = start + lane * V, dim = static_cast<int>(p.dim);
   const int mine = lane_row(p, t, lane);
   const float my_weight = p.weights && lane < p.k ? p.weights[t * p.k + lane] : 1.0f;
-  float acc[U][V];
+  auto piece = [&](auto whole) {
+    float acc[U][V];
 #pragma unroll
-  for (int u = 0; u < U; ++u)
+    for (int u = 0; u < U; ++u)
 #pragma unroll
-    for (int i = 0; i < V; ++i) acc[u][i] = 0.0f;
-  for (int j0 = 0; j0 < p.k; j0 += J) {
-    Vec<T, V> x[J][U];
-    float wt[J];
+      for (int i = 0; i < V; ++i) acc[u][i] = 0.0f;
+    for (int j0 = 0; j0 < p.k; j0 += J) {
+      Vec<T, V> x[J][U];
+      float wt[J];
 #pragma unroll
-    for (int j = 0; j < J; ++j) {
-      const int r = j0 + j < MAX_K ? __shfl_sync(0xffffffffu, mine, j0 + j) : -1;  // -1 past the last slot too
-      wt[j] = __shfl_sync(0xffffffffu, my_weight, j0 + j);
-      if (r < 0) wt[j] = 0.0f;
-      const T* src = static_cast<const T*>(p.src) + (r < 0 ? 0 : r) * p.src_ld;
+      for (int j = 0; j < J; ++j) {
+        const int r = j0 + j < MAX_K ? __shfl_sync(0xffffffffu, mine, j0 + j) : -1;  // -1 past the last slot too
+        wt[j] = __shfl_sync(0xffffffffu, my_weight, j0 + j);
+        const T* src = static_cast<const T*>(p.src) + r * p.src_ld + c0;
+        if (r >= 0) {
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        x[j][u] = zero_vec<T, V>();
-        if (r >= 0 && c0 + u * 32 * V < p.dim) x[j][u] = load_vec<T, V>(src + c0 + u * 32 * V);
+          for (int u = 0; u < U; ++u)
+            x[j][u] = decltype(whole)::value || c0 + u * 32 * V < dim ? load_vec<T, V>(src + u * 32 * V) : zero_vec<T, V>();
+        } else {
+          wt[j] = 0.0f;
+#pragma unroll
+          for (int u = 0; u < U; ++u) x[j][u] = zero_vec<T, V>();
+        }
       }
+#pragma unroll
+      for (int j = 0; j < J; ++j)
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+          for (int i = 0; i < V; ++i) acc[u][i] = fmaf(wt[j], get(x[j][u], i), acc[u][i]);
     }
+    T* dst = static_cast<T*>(p.dst) + t * p.dst_ld + c0;
 #pragma unroll
-    for (int j = 0; j < J; ++j)
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-#pragma unroll
-        for (int i = 0; i < V; ++i) acc[u][i] = fmaf(wt[j], get(x[j][u], i), acc[u][i]);
-  }
-  T* dst = static_cast<T*>(p.dst) + t * p.dst_ld;
-#pragma unroll
-  for (int u = 0; u < U; ++u)
-    if (c0 + u * 32 * V < p.dim) store_vec<T, V>(dst + c0 + u * 32 * V, pack<T, V>(acc[u]));
+    for (int u = 0; u < U; ++u)
+      if (decltype(whole)::value || c0 + u * 32 * V < dim) store_vec<T, V>(dst + u * 32 * V, pack<T, V>(acc[u]));
+  };
+  if (start + 32 * V * U <= dim)
+    piece(std::true_type());
+  else
+    piece(std::false_type());
 }
 
 // combine's gradient: `parts` warps of one block share a token; each walks its
@@ -376,18 +393,17 @@ __global__ void __launch_bounds__(ROW_THREADS) ns_moe_combine_grad_kernel(const 
   const long long w = static_cast<long long>(blockIdx.x) * (ROW_THREADS / 32) + warp;
   const bool on = w < p.token_warps;
   const long long t = w / p.parts;
-  const int part = static_cast<int>(w - t * p.parts);
+  const int part = static_cast<int>(w - t * p.parts), dim = static_cast<int>(p.dim);
   float sum = 0.0f;
   if (on) {
     const T* dy = static_cast<const T*>(p.src) + t * p.src_ld;
     const int mine = lane_row(p, t, lane);
     const float my_weight = lane < p.k ? p.weights[t * p.k + lane] : 0.0f;
-    for (long long c0 = part * (32 * V * U) + lane * V; c0 - lane * V < p.dim; c0 += p.parts * (32 * V * U)) {
+    auto piece = [&](int c0, auto whole) {
       float g[U][V];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        Vec<T, V> x = zero_vec<T, V>();
-        if (c0 + u * 32 * V < p.dim) x = load_vec<T, V>(dy + c0 + u * 32 * V);
+        const Vec<T, V> x = decltype(whole)::value || c0 + u * 32 * V < dim ? load_vec<T, V>(dy + c0 + u * 32 * V) : zero_vec<T, V>();
 #pragma unroll
         for (int i = 0; i < V; ++i) g[u][i] = get(x, i);
       }
@@ -397,32 +413,40 @@ __global__ void __launch_bounds__(ROW_THREADS) ns_moe_combine_grad_kernel(const 
 #pragma unroll
         for (int j = 0; j < J; ++j) {
           r[j] = j0 + j < MAX_K ? __shfl_sync(0xffffffffu, mine, j0 + j) : -1;  // -1 past the last slot too
-          const T* ys = static_cast<const T*>(p.rows_in) + (r[j] < 0 ? 0 : r[j]) * p.rows_ld;
+          const T* ys = static_cast<const T*>(p.rows_in) + r[j] * p.rows_ld + c0;
+          if (r[j] >= 0) {
 #pragma unroll
-          for (int u = 0; u < U; ++u)
-            if (r[j] >= 0 && c0 + u * 32 * V < p.dim) y[j][u] = load_vec<T, V>(ys + c0 + u * 32 * V);
+            for (int u = 0; u < U; ++u)
+              if (decltype(whole)::value || c0 + u * 32 * V < dim) y[j][u] = load_vec<T, V>(ys + u * 32 * V);
+          }
         }
 #pragma unroll
         for (int j = 0; j < J; ++j) {
           if (r[j] < 0) continue;
           const float wt = __shfl_sync(0xffffffffu, my_weight, j0 + j);
-          T* out = static_cast<T*>(p.dst) + r[j] * p.dst_ld;
+          T* out = static_cast<T*>(p.dst) + r[j] * p.dst_ld + c0;
           float dot = 0.0f;
 #pragma unroll
           for (int u = 0; u < U; ++u)
-            if (c0 + u * 32 * V < p.dim) {
+            if (decltype(whole)::value || c0 + u * 32 * V < dim) {
               float o[V];
 #pragma unroll
               for (int i = 0; i < V; ++i) {
                 dot = fmaf(g[u][i], get(y[j][u], i), dot);
                 o[i] = wt * g[u][i];
               }
-              store_vec<T, V>(out + c0 + u * 32 * V, pack<T, V>(o));
+              store_vec<T, V>(out + u * 32 * V, pack<T, V>(o));
             }
           dot = warp_sum(dot);
           if (lane == j0 + j) sum += dot;
         }
       }
+    };
+    for (int start = part * (32 * V * U); start < dim; start += p.parts * (32 * V * U)) {
+      if (start + 32 * V * U <= dim)
+        piece(start + lane * V, std::true_type());
+      else
+        piece(start + lane * V, std::false_type());
     }
     if (p.parts == 1 && lane < p.k) p.grad_weights[t * p.k + lane] = sum;
   } else {
@@ -514,11 +538,12 @@ cudaError_t launch_rows(nsk::RowParams& p, int nsm, cudaStream_t st) {
 
 // Words of 16 bytes where rows allow it, else of 4 (16-bit rows of an even
 // width), else single elements: 8192 x 6 bf16 rows of 2048, 2046 and 2047 are
-// summed in 39.7, 40.6 and 56.2 us (5.9, 5.8 and 4.2 TB/s), backward in 68, 77
-// and 106 us.
+// summed in 37.7, 38.7 and 53.0 us (6.3, 6.1 and 4.4 TB/s), backward in 70, 85
+// and 100 us. Rows in flight: 3 for the sums; backward 2, or 1 of 64 bytes a lane
+// (3 of those need 163 registers and take 136 us where 1 takes 124).
 template <RowOp OP, typename T>
 cudaError_t launch_words(int word, nsk::RowParams& p, int nsm, cudaStream_t st) {
-  if (word == 16) return launch_rows<OP, T, 16 / sizeof(T), OP == GATHER ? 2 : 4, 3>(p, nsm, st);
+  if (word == 16) return launch_rows<OP, T, 16 / sizeof(T), OP == GATHER ? 2 : 4, OP == GATHER ? 3 : 1>(p, nsm, st);
   constexpr int J = OP == GATHER ? 3 : 2;
   if constexpr (sizeof(T) == 2)
     if (word == 4) return launch_rows<OP, T, 2, 8, J>(p, nsm, st);

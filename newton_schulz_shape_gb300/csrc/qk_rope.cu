@@ -10,8 +10,8 @@
 // (i, i + rot_dim / 2), or (2i, 2i + 1) when interleaved.
 //
 // Every value is read and written once, so large calls are bound by memory:
-// 16384 tokens of 32/8 heads of 128 bf16 take 61 us forward (5.7 TB/s) and 93 us
-// backward (5.5 TB/s, 0.82 of the measured copy; the rest is the instructions of
+// 16384 tokens of 32/8 heads of 128 bf16 take 61 us forward (5.7 TB/s) and 90 us
+// backward (5.7 TB/s, 0.85 of the measured copy; the rest is the instructions of
 // two reductions and a rotation for every 16 bytes). 16 tokens take 2.6 us.
 #include <algorithm>
 #include <climits>
