@@ -321,7 +321,8 @@ int ns_orthogonalize_batched_fixed_ws(ns_plan_t* plan, const void* const* in, vo
  * CUDA graph. An index that points outside its buffer is refused on the
  * device: the access is skipped and ns_check_status reports
  * NS_ERR_DEVICE_CHECK. Arguments are checked on the host: NS_ERR_ARG for null
- * pointers and values outside their domain, NS_ERR_SHAPE for sizes or strides
+ * pointers, addresses that their elements cannot have and values outside their
+ * domain, NS_ERR_SHAPE for sizes or strides
  * that do not fit each other, NS_ERR_UNSUPPORTED past a stated limit,
  * NS_ERR_WORKSPACE as elsewhere. */
 
@@ -434,7 +435,7 @@ int ns_qk_norm_rope_grad(const void* grad_q_out, const void* grad_k_out, const v
  * are left out; an id >= vocab is refused and left out. A token whose weight is
  * 0 or that has no entry left gets loss 0, lse 0 and a zero gradient, whatever
  * its logits hold. grad_logits may be logits itself, with the same stride.
- * top <= 1024. Any other row needs a finite logit: one of -inf gives NaN. */
+ * top <= 1024, temperature in [1e-30, 1e30]. Any other row needs a finite logit: one of -inf gives NaN. */
 int ns_distill_loss(const void* logits, int64_t logits_stride, int dtype, int64_t tokens, int64_t vocab,
                     const void* teacher_values, int teacher_dtype, const void* teacher_ids, int id_bytes, int top,
                     const float* weights, const float* teacher_lse, float temperature, float* loss, float* lse,

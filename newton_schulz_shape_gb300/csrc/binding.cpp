@@ -3,13 +3,14 @@
 // step the host's part is most of a call: reading the tensors here takes 1 us
 // where attribute reads and ctypes conversions in Python took 3.5 to 7.
 //
-// A tensor has to be on the GPU, of a type that the C function takes, with its
+// A tensor has to be on the current GPU, of a type that the C function takes, with its
 // last dimension contiguous: ValueError otherwise, naming the argument. The
 // library checks the rest: NsError.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
+#include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -89,24 +90,26 @@ struct Args {
     if (!THPVariable_Check(at[i])) bad(i, "a tensor");
     return THPVariable_Unpack(at[i]);
   }
+  // On the GPU that the call runs on.
+  bool here(const at::Tensor& t) const { return t.is_cuda() && t.get_device() == c10::cuda::current_device(); }
   // A GPU tensor of `dims` dimensions.
   const at::Tensor& gpu(int i, int dims) const {
     const at::Tensor& t = tensor(i);
-    if (!t.is_cuda() || t.dim() != dims) bad(i, "a GPU tensor of " + std::to_string(dims) + " dimensions");
+    if (!here(t) || t.dim() != dims) bad(i, "a GPU tensor of " + std::to_string(dims) + " dimensions");
     return t;
   }
   // The address of `numel` contiguous values; null for None.
   void* whole(int i, at::ScalarType type, int64_t numel) const {
     if (!given(i)) return nullptr;
     const at::Tensor& t = tensor(i);
-    if (!t.is_cuda() || t.scalar_type() != type || t.numel() != numel || !t.is_contiguous())
+    if (!here(t) || t.scalar_type() != type || t.numel() != numel || !t.is_contiguous())
       bad(i, std::to_string(numel) + " contiguous GPU values of " + c10::toString(type));
     return t.data_ptr();
   }
   const void* indices(int i, int64_t numel, int* bytes) const {
     const at::Tensor& t = tensor(i);
     const at::ScalarType type = t.scalar_type();
-    if (!t.is_cuda() || (type != at::kInt && type != at::kLong) || t.numel() != numel || !t.is_contiguous())
+    if (!here(t) || (type != at::kInt && type != at::kLong) || t.numel() != numel || !t.is_contiguous())
       bad(i, std::to_string(numel) + " contiguous GPU indices (int32 or int64)");
     *bytes = type == at::kLong ? 8 : 4;
     return t.data_ptr();
@@ -115,7 +118,7 @@ struct Args {
     *bytes = 0;
     if (!given(i)) return nullptr;
     const at::Tensor& t = tensor(i);
-    if (!t.is_cuda() || !t.is_contiguous()) bad(i, "a contiguous GPU tensor");
+    if (!here(t) || !t.is_contiguous()) bad(i, "a contiguous GPU tensor");
     *bytes = t.nbytes();
     return t.data_ptr();
   }

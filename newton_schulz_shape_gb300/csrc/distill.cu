@@ -651,20 +651,28 @@ using namespace nsorch;
 
 namespace {
 
-bool dtype_ok(int dtype) { return dtype == NS_DT_BF16 || dtype == NS_DT_FP16 || dtype == NS_DT_FP32; }
+using nsk::dtype_ok;
+using nsk::elem_bytes;
+using nsk::element_aligned;
 
 int run_distill(const void* logits, int64_t logits_stride, int dtype, int64_t tokens, int64_t vocab,
                 const void* teacher_values, int teacher_dtype, const void* teacher_ids, int id_bytes, int top,
                 const float* weights, const float* teacher_lse, float temperature, float* loss, float* lse,
                 void* grad_logits, int64_t grad_stride, void* stream) {
   if (!dtype_ok(dtype) || !dtype_ok(teacher_dtype) || (id_bytes != 4 && id_bytes != 8)) return NS_ERR_ARG;
-  if (tokens < 0 || vocab < 1 || top < 1 || !(temperature > 0.0f) || temperature > 3.0e38f) return NS_ERR_ARG;
+  if (tokens < 0 || vocab < 1 || top < 1 || !(temperature >= 1.0e-30f) || temperature > 1.0e30f) return NS_ERR_ARG;
   if (top > nsk::DISTILL_MAX_TOP) return NS_ERR_UNSUPPORTED;
   if (vocab > INT_MAX || tokens > INT_MAX || logits_stride < vocab || (grad_logits && grad_stride < vocab))
     return NS_ERR_SHAPE;
   if (tokens == 0) return NS_OK;
   if (!logits || !teacher_values || !teacher_ids || !lse) return NS_ERR_ARG;
   if (grad_logits == logits && grad_stride != logits_stride) return NS_ERR_ARG;
+  if (!element_aligned(logits, elem_bytes(dtype)) || !element_aligned(grad_logits, elem_bytes(dtype)) ||
+      !element_aligned(teacher_values, elem_bytes(teacher_dtype)) || !element_aligned(teacher_ids, id_bytes))
+    return NS_ERR_ARG;
+  for (const void* p : {static_cast<const void*>(weights), static_cast<const void*>(teacher_lse),
+                        static_cast<const void*>(loss), static_cast<const void*>(lse)})
+    if (!element_aligned(p, 4)) return NS_ERR_ARG;
   nsk::DistillParams p = {};
   p.logits = logits;
   p.logits_ld = logits_stride;

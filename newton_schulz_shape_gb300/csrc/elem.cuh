@@ -11,7 +11,15 @@
 
 #include <type_traits>
 
+#include "../../include/nsgb300.h"
+
 namespace nsk {
+
+// ------------------------------------------------------------ host checks
+inline bool dtype_ok(int dtype) { return dtype == NS_DT_BF16 || dtype == NS_DT_FP16 || dtype == NS_DT_FP32; }
+inline int elem_bytes(int dtype) { return dtype == NS_DT_FP32 ? 4 : 2; }
+// Whether an address can hold elements of `bytes` bytes (null can).
+inline bool element_aligned(const void* p, int bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
 
 template <typename T>
 __device__ __forceinline__ float to_float(T v);

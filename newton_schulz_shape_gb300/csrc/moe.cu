@@ -468,8 +468,13 @@ using namespace nsorch;
 
 namespace {
 
-int elem_bytes(int dtype) { return dtype == NS_DT_FP32 ? 4 : 2; }
-bool dtype_ok(int dtype) { return dtype == NS_DT_BF16 || dtype == NS_DT_FP16 || dtype == NS_DT_FP32; }
+using nsk::dtype_ok;
+using nsk::elem_bytes;
+using nsk::element_aligned;
+
+bool all_aligned(int bytes, std::initializer_list<const void*> ps) {
+  return std::all_of(ps.begin(), ps.end(), [&](const void* p) { return element_aligned(p, bytes); });
+}
 // Whether rows at p, `ld` elements apart, and their width are whole words.
 bool in_words(const void* p, long long ld, long long dim, int elem, int word) {
   return reinterpret_cast<uintptr_t>(p) % word == 0 && ld * elem % word == 0 && dim * elem % word == 0;
@@ -606,6 +611,8 @@ int ns_moe_sort(const void* expert_ids, int id_bytes, int64_t tokens, int k, int
   if (rows < need_rows || rows > nsk::MAX_SLOTS) return NS_ERR_SHAPE;
   if (!counts || !offsets || (tokens > 0 && (!expert_ids || !row_of_slot)) || (rows > 0 && !slot_of_row))
     return NS_ERR_ARG;
+  if (!element_aligned(expert_ids, id_bytes) || !all_aligned(4, {row_of_slot, slot_of_row, counts, offsets}))
+    return NS_ERR_ARG;
   nsk::SortParams p = {};
   p.ids = expert_ids;
   p.id_bytes = id_bytes;
@@ -654,6 +661,7 @@ int ns_moe_dispatch(const void* x, int64_t x_stride, int dtype, int64_t tokens, 
   if (x_stride < dim || out_stride < dim) return NS_ERR_SHAPE;
   if (rows == 0 || dim == 0) return NS_OK;
   if (!out || !slot_of_row || (tokens > 0 && (!x || !row_of_slot))) return NS_ERR_ARG;
+  if (!all_aligned(elem_bytes(dtype), {x, out}) || !all_aligned(4, {row_of_slot, slot_of_row})) return NS_ERR_ARG;
   nsk::RowParams p = {};
   p.src = x;
   p.src_ld = x_stride;
@@ -677,6 +685,7 @@ int ns_moe_combine(const void* expert_rows, int64_t rows_stride, int dtype, int6
   if (rows_stride < dim || y_stride < dim) return NS_ERR_SHAPE;
   if (tokens == 0 || dim == 0) return NS_OK;
   if (!y || !row_of_slot || (rows > 0 && !expert_rows)) return NS_ERR_ARG;
+  if (!all_aligned(elem_bytes(dtype), {expert_rows, y}) || !all_aligned(4, {row_of_slot, weights})) return NS_ERR_ARG;
   nsk::RowParams p = {};
   p.src = expert_rows;
   p.src_ld = rows_stride;
@@ -709,6 +718,9 @@ int ns_moe_combine_grad(const void* grad_y, int64_t grad_y_stride, const void* e
   if (tokens == 0 && rows == 0) return NS_OK;
   if (tokens > 0 && (!row_of_slot || !weights || !grad_weights || (dim > 0 && !grad_y))) return NS_ERR_ARG;
   if (rows > 0 && (!slot_of_row || (dim > 0 && (!expert_rows || !grad_rows)))) return NS_ERR_ARG;
+  if (!all_aligned(elem_bytes(dtype), {grad_y, expert_rows, grad_rows}) ||
+      !all_aligned(4, {row_of_slot, slot_of_row, weights, grad_weights}))
+    return NS_ERR_ARG;
   nsk::RowParams p = {};
   p.src = grad_y;
   p.src_ld = grad_y_stride;

@@ -653,7 +653,7 @@ int run_qk(bool grad, const void* const* x, const void* const* dy, void* const* 
            const void* const* weight, int weight_dtype, float* const* grad_weight, float eps, const float* table,
            int64_t table_rows, const void* positions, int position_bytes, void* workspace, uint64_t workspace_bytes,
            void* stream) {
-  if (dtype != NS_DT_BF16 && dtype != NS_DT_FP16 && dtype != NS_DT_FP32) return NS_ERR_ARG;
+  if (!nsk::dtype_ok(dtype)) return NS_ERR_ARG;
   if (weight_dtype != dtype && weight_dtype != NS_DT_FP32) return NS_ERR_ARG;
   if (tokens < 0 || heads[0] < 0 || heads[1] < 0 || head_dim < 1 || rot_dim < 0 || table_rows < 0 || !(eps >= 0.0f) || !strides)
     return NS_ERR_ARG;
@@ -669,13 +669,19 @@ int run_qk(bool grad, const void* const* x, const void* const* dy, void* const* 
   for (int i = 0; i < 2; ++i) {
     if (tokens == 0 || heads[i] == 0) continue;
     if (!x[i] || !out[i] || (grad && !dy[i])) return NS_ERR_ARG;
+    const int b = nsk::elem_bytes(dtype);
+    if (!nsk::element_aligned(x[i], b) || !nsk::element_aligned(out[i], b) || (grad && !nsk::element_aligned(dy[i], b)))
+      return NS_ERR_ARG;
+    if (!nsk::element_aligned(weight[i], nsk::elem_bytes(weight_dtype)) || (grad && !nsk::element_aligned(grad_weight[i], 4)))
+      return NS_ERR_ARG;
   }
+  if (!nsk::element_aligned(table, 4) || (positions && !nsk::element_aligned(positions, position_bytes))) return NS_ERR_ARG;
   if (sums && (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255) ||
                workspace_bytes < sizeof(float) * 2 * nsk::QK_MAX_BLOCKS * static_cast<uint64_t>(head_dim)))
     return NS_ERR_WORKSPACE;
   if ((tokens == 0 || most == 0) && !sums) return NS_OK;
   nsk::QkParams p = {};
-  const int b = dtype == NS_DT_FP32 ? 4 : 2, V = 16 / b;
+  const int b = nsk::elem_bytes(dtype), V = 16 / b;
   bool lanes = head_dim % V == 0 && head_dim / V <= 64 && (reinterpret_cast<uintptr_t>(table) & 15) == 0;
   // strides: (token, head) of x, of out and, for the gradient, of dy; queries then keys of each
   for (int i = 0; i < 2; ++i) {
