@@ -28,7 +28,8 @@ namespace {
 
 constexpr int QK_THREADS = 128;
 constexpr int QK_WARPS = QK_THREADS / 32;
-constexpr int QK_BLOCKS = 5, QK_GRAD_BLOCKS = 4;  // that share an SM
+// Blocks that share an SM, by the registers that their angles and sums take.
+constexpr int qk_blocks(bool grad, bool spread) { return 5 - (grad ? 1 : 0) - (spread ? 1 : 0); }
 constexpr int QK_AHEAD = 3;  // rounds whose words are on their way
 constexpr int QK_ANY_THREADS = 128;
 constexpr int QK_MAX_DIM = 1024;
@@ -242,35 +243,60 @@ __device__ __forceinline__ void turn(const QkParams& p, const Lane<T>& l, const 
   }
 }
 
-// The same for pairs that are not made of whole words: the other value of a
-// pair comes from its lane through `scratch` (the warp's, 2 V values a lane).
-// `first`: the group's first lane.
+// The same for pairs that are not made of whole words. Every value has its own
+// angle, with the sine's sign of its place in the pair; the other value of a
+// pair is read from `head`, the group's part of shared memory, where the lanes
+// put their words in the head's order.
 template <typename T>
-__device__ __forceinline__ void turn_spread(const QkParams& p, const Lane<T>& l, const float* row, Two<T>& x, float sign,
-                                            float* scratch, int lane, int first) {
-  constexpr int V = Lane<T>::V, N = Two<T>::N;
-  const int half = p.rot_dim / 2, words_a = (p.dim / V + 1) / 2;
+struct SpreadAngles {
+  float2 a[Lane<T>::V], b[Lane<T>::V];  // cosine, signed sine
+};
+
+// Place of the other value of value d's pair, and whether d is its second.
+__device__ __forceinline__ int other_of(const QkParams& p, int d, bool* second) {
+  const int half = p.rot_dim / 2;
+  *second = p.interleaved ? d & 1 : d >= half;
+  return p.interleaved ? d ^ 1 : (*second ? d - half : d + half);
+}
+
+template <typename T>
+__device__ __forceinline__ void load_spread(const QkParams& p, const Lane<T>& l, const float* row, SpreadAngles<T>& g) {
+  const int half = p.rot_dim / 2;
+  auto one = [&](int d) {
+    bool second;
+    other_of(p, d, &second);
+    const int angle = p.interleaved ? d >> 1 : (second ? d - half : d);
+    return make_float2(row[angle], second ? row[half + angle] : -row[half + angle]);
+  };
+#pragma unroll
+  for (int k = 0; k < Lane<T>::V; ++k) {
+    if (l.a + k < p.rot_dim) g.a[k] = one(l.a + k);
+    if (l.b + k < p.rot_dim) g.b[k] = one(l.b + k);
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ void turn_spread(const QkParams& p, const Lane<T>& l, const SpreadAngles<T>& g, Two<T>& x,
+                                            float sign, float* head) {
+  constexpr int N = Two<T>::N;
   __syncwarp();
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    reinterpret_cast<float2*>(scratch + lane * V)[i] = x.a[i];
-    reinterpret_cast<float2*>(scratch + (32 + lane) * V)[i] = x.b[i];
+    if (l.on_a && l.a < p.rot_dim) reinterpret_cast<float2*>(head + l.a)[i] = x.a[i];
+    if (l.on_b && l.b < p.rot_dim) reinterpret_cast<float2*>(head + l.b)[i] = x.b[i];
   }
   __syncwarp();
-  auto one = [&](float v, int d) {
-    if (!row || d >= p.rot_dim) return v;
-    const bool second = p.interleaved ? d & 1 : d >= half;
-    const int o = p.interleaved ? d ^ 1 : (second ? d - half : d + half);
-    const int angle = p.interleaved ? d >> 1 : (second ? d - half : d);
-    const int word = o / V, b = word >= words_a;
-    const float other = scratch[(32 * b + first + word - b * words_a) * V + o % V];
-    const float s = second ? sign * row[half + angle] : -sign * row[half + angle];
-    return v * row[angle] + other * s;
+  auto one = [&](float v, int d, const float2& cs) {
+    bool second;
+    const int o = other_of(p, d, &second);
+    return d < p.rot_dim ? v * cs.x + head[o] * (sign * cs.y) : v;
   };
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    if (l.on_a) x.a[i] = make_float2(one(x.a[i].x, l.a + 2 * i), one(x.a[i].y, l.a + 2 * i + 1));
-    if (l.on_b) x.b[i] = make_float2(one(x.b[i].x, l.b + 2 * i), one(x.b[i].y, l.b + 2 * i + 1));
+    if (l.on_a && l.a < p.rot_dim)
+      x.a[i] = make_float2(one(x.a[i].x, l.a + 2 * i, g.a[2 * i]), one(x.a[i].y, l.a + 2 * i + 1, g.a[2 * i + 1]));
+    if (l.on_b && l.b < p.rot_dim)
+      x.b[i] = make_float2(one(x.b[i].x, l.b + 2 * i, g.b[2 * i]), one(x.b[i].y, l.b + 2 * i + 1, g.b[2 * i + 1]));
   }
 }
 
@@ -328,7 +354,7 @@ struct Walk {
 // computes one. For the gradient a lane keeps the sums of its columns of dg,
 // which a block joins in a fixed order. SPREAD: see turn_spread.
 template <typename T, int G, bool GRAD, bool SPREAD>
-__global__ void __launch_bounds__(QK_THREADS, GRAD ? QK_GRAD_BLOCKS : QK_BLOCKS) ns_qk_kernel(const __grid_constant__ QkParams p) {
+__global__ void __launch_bounds__(QK_THREADS, qk_blocks(GRAD, SPREAD)) ns_qk_kernel(const __grid_constant__ QkParams p) {
   constexpr int N = Two<T>::N, STAGES = QK_AHEAD + 1, STAGE = GRAD ? 128 : 64;
   extern __shared__ uint4 ring_smem[];
   nsptx::griddep_wait();
@@ -336,8 +362,11 @@ __global__ void __launch_bounds__(QK_THREADS, GRAD ? QK_GRAD_BLOCKS : QK_BLOCKS)
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   uint4* ring = ring_smem + warp * (STAGES * STAGE) + lane;
   const int group_size = G ? G : p.lanes, H = 32 / group_size, group = lane / group_size, i_lane = lane - group * group_size;
-  const Lane<T> l = lane_of<T, SPREAD>(p, i_lane);
-  float* scratch = reinterpret_cast<float*>(ring_smem + QK_WARPS * STAGES * STAGE) + warp * 64 * Lane<T>::V;
+  const bool takes = group < H;  // a lane left over takes no head
+  Lane<T> l = lane_of<T, SPREAD>(p, i_lane);
+  if (!takes) l.on_a = l.on_b = l.turn_a = l.turn_b = false;
+  // SPREAD: the group's head (all heads of a warp fit 64 words of V values)
+  float* head = reinterpret_cast<float*>(ring_smem + QK_WARPS * STAGES * STAGE) + warp * 64 * Lane<T>::V + min(group, H - 1) * p.dim;
   const float inv_dim = 1.0f / p.dim;
   // words outside the head are zero and stay so
   for (int i = 0; i < STAGES * STAGE; i += 64) {
@@ -368,7 +397,6 @@ __global__ void __launch_bounds__(QK_THREADS, GRAD ? QK_GRAD_BLOCKS : QK_BLOCKS)
       const char* const dy_base = static_cast<const char*>(side.dy) + sizeof(T) * l.a;
       char* const out_base = static_cast<char*>(side.out) + sizeof(T) * l.a;
       const int to_b = static_cast<int>(sizeof(T)) * (l.b - l.a);
-      const bool takes = group < H;  // a lane left over takes no head
       int fill = 0, take = 0;
       auto copy = [&](bool more) {
         if (more && takes && ahead.t < p.tokens) {
@@ -389,6 +417,7 @@ __global__ void __launch_bounds__(QK_THREADS, GRAD ? QK_GRAD_BLOCKS : QK_BLOCKS)
       int angles_of = -1;
       const float* row = nullptr;
       Angles<T> angles;
+      SpreadAngles<T> spread;
       for (int r = 0; r < n; ++r) {
         copy(r + QK_AHEAD < n);
         nsptx::cp_async_wait<QK_AHEAD>();
@@ -399,6 +428,7 @@ __global__ void __launch_bounds__(QK_THREADS, GRAD ? QK_GRAD_BLOCKS : QK_BLOCKS)
         take = take + STAGE == STAGES * STAGE ? 0 : take + STAGE;
         if (p.rot_dim && live && at.t != angles_of) {
           row = table_row(p, at.t);
+          if (row && SPREAD) load_spread<T>(p, l, row, spread);
           if (row && !SPREAD) load_angles<T>(p, l, row, angles);
           angles_of = at.t;
         }
@@ -418,12 +448,12 @@ __global__ void __launch_bounds__(QK_THREADS, GRAD ? QK_GRAD_BLOCKS : QK_BLOCKS)
             u.b[i] = mul2(xf.b[i], mul2(g.b[i], r2));
           }
           if (SPREAD)
-            turn_spread<T>(p, l, row, u, 1.0f, scratch, lane, lane - i_lane);
+            turn_spread<T>(p, l, spread, u, 1.0f, head);
           else
             turn<T>(p, l, angles, u, 1.0f);
         } else {
           if (SPREAD)
-            turn_spread<T>(p, l, row, u, -1.0f, scratch, lane, lane - i_lane);
+            turn_spread<T>(p, l, spread, u, -1.0f, head);
           else
             turn<T>(p, l, angles, u, -1.0f);
           if (live) {
@@ -595,7 +625,7 @@ __global__ void __launch_bounds__(1024) ns_qk_sum_kernel(const __grid_constant__
 template <typename T, int G, bool SPREAD = false>
 cudaError_t launch_lanes(bool grad, QkParams& p, int nsm, int* blocks, cudaStream_t st) {
   const int H = 32 / p.lanes;
-  const int most = std::min(nsm * (grad ? QK_GRAD_BLOCKS : QK_BLOCKS), QK_MAX_BLOCKS);
+  const int most = std::min(nsm * qk_blocks(grad, SPREAD), QK_MAX_BLOCKS);
   // a warp's rounds in equal chunks of at most 8: long ones, since a token's angles serve all of its rounds
   // (16384 tokens of 32/8 heads take 131, 107, 97 and 93 us backward in chunks of 1, 2, 4 and 8)
   const int rounds = static_cast<int>((p.tokens * (p.side[0].heads + p.side[1].heads) + H - 1) / H);
