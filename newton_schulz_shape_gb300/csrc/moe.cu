@@ -548,11 +548,29 @@ cudaError_t launch_rows(nsk::RowParams& p, int nsm, cudaStream_t st) {
 // (3 of those need 163 registers and take 136 us where 1 takes 124).
 template <RowOp OP, typename T>
 cudaError_t launch_words(int word, nsk::RowParams& p, int nsm, cudaStream_t st) {
-  if (word == 16) return launch_rows<OP, T, 16 / sizeof(T), OP == GATHER ? 2 : 4, OP == GATHER ? 3 : 1>(p, nsm, st);
-  constexpr int J = OP == GATHER ? 3 : 2;
-  if constexpr (sizeof(T) == 2)
-    if (word == 4) return launch_rows<OP, T, 2, 8, J>(p, nsm, st);
-  return launch_rows<OP, T, 1, 8, J>(p, nsm, st);
+  constexpr int V = 16 / sizeof(T);
+  if constexpr (OP == GATHER) {
+    // few slots: more of each row at a time instead of more rows (16384 tokens of 1, 2 and 4 rows of 2048 bf16
+    // in 24.6, 34.1 and 52.7 us against 34.5, 39.8 and 57.0; of 2047 columns, 1 and 2 rows in 37 and 44 against
+    // 54 and 60, but three fp32 rows of 1001 in 10.0 against 9.5), where the row reaches the last of a lane's
+    // words (8192 tokens of 2 rows of 512 take 5.9 us against 5.3, of 255 columns 5.3 against 4.5) and, for the
+    // wide words, where the tokens fill the GPU (1216 tokens of 4 rows of 2048 take 4.9 us against 4.6, 2432
+    // tokens 10.3 against 11.6)
+    const auto reaches = [&](int v, int u) { return p.dim > 32 * v * (u - 1); };
+    if (word == 16 && p.k <= 4 && reaches(V, 4) && p.tokens >= 16 * nsm) return launch_rows<OP, T, V, 4, 1>(p, nsm, st);
+    if (word == 16) return launch_rows<OP, T, V, 2, 3>(p, nsm, st);
+    if constexpr (sizeof(T) == 2) {
+      if (word == 4 && p.k <= 2 && reaches(2, 16)) return launch_rows<OP, T, 2, 16, 2>(p, nsm, st);
+      if (word == 4) return launch_rows<OP, T, 2, 8, 3>(p, nsm, st);
+    }
+    if (p.k <= 2 && reaches(1, 16)) return launch_rows<OP, T, 1, 16, 2>(p, nsm, st);
+    return launch_rows<OP, T, 1, 8, 3>(p, nsm, st);
+  } else {
+    if (word == 16) return launch_rows<OP, T, V, 4, 1>(p, nsm, st);
+    if constexpr (sizeof(T) == 2)
+      if (word == 4) return launch_rows<OP, T, 2, 8, 2>(p, nsm, st);
+    return launch_rows<OP, T, 1, 8, 2>(p, nsm, st);
+  }
 }
 
 template <RowOp OP>

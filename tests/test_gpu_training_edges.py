@@ -167,6 +167,30 @@ def test_infinite_weights_and_rows_stay_where_they_are():
     assert grad_rows[2].isinf().all() and (grad_rows[[0, 1, 3, 4]] == 1).all()
 
 
+FEW_ROWS = [  # tokens, k, dim: on both sides of the limits at which a lane takes more of a row
+    (2500, 1, 2048), (2500, 4, 776), (2500, 2, 768), (2500, 5, 1032), (2400, 4, 1024), (2431, 3, 392), (2440, 4, 384),
+    (61, 1, 481), (61, 2, 480), (61, 2, 962), (61, 1, 960), (61, 3, 1023), (61, 2, 1541), (61, 1, 3001), (700, 2, 2046),
+]
+
+
+@pytest.mark.parametrize("T,k,D", FEW_ROWS)
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+def test_sums_of_few_rows(T, k, D, dtype):
+    g = gen(T + k + D)
+    R = T * k + 5
+    row = torch.randint(-1, R, (T, k), generator=g, device=DEV, dtype=torch.int32)
+    ys, w = randn(g, R, D, dtype=dtype), randn(g, T, k)
+    y, dx = (torch.full((T, D), float("nan"), dtype=dtype, device=DEV) for _ in range(2))
+    nsg.ns_moe_combine(ys, w, row, y)
+    nsg.ns_moe_dispatch_grad(ys, row, dx)
+    ok()
+    r, v, wv = row.cpu().numpy(), f64(ys), f64(w)
+    U, tiny = torch.finfo(dtype).eps / 2, float(torch.finfo(dtype).tiny) * float(torch.finfo(dtype).eps)
+    for got, want, size in ((y, ot.moe_combine(v, wv, r), ot.moe_combine(np.abs(v), np.abs(wv), r)),
+                            (dx, ot.moe_dispatch_grad(v, r), ot.moe_dispatch_grad(np.abs(v), r))):
+        assert (np.abs(f64(got) - want) <= (k + 2) * u * size + U * np.abs(want) * (1 + 1e-6) + tiny + U * (k + 2) * u * size).all()
+
+
 def test_launch_counts():
     nsg.ns_profile_read_training(reset=True)
     x = torch.ones(4, 2, 64, device=DEV)
