@@ -368,11 +368,6 @@ __global__ void __launch_bounds__(QK_THREADS, qk_blocks(GRAD, SPREAD)) ns_qk_ker
   // SPREAD: the group's head (all heads of a warp fit 64 words of V values)
   float* head = reinterpret_cast<float*>(ring_smem + QK_WARPS * STAGES * STAGE) + warp * 64 * Lane<T>::V + min(group, H - 1) * p.dim;
   const float inv_dim = 1.0f / p.dim;
-  // words outside the head are zero and stay so
-  for (int i = 0; i < STAGES * STAGE; i += 64) {
-    if (!l.on_a) ring[i] = make_uint4(0, 0, 0, 0);
-    if (!l.on_b) ring[i + 32] = make_uint4(0, 0, 0, 0);
-  }
   const int warps = gridDim.x * QK_WARPS, me = blockIdx.x * QK_WARPS + warp;
   int chunk = me;  // this warp's next, in those of the queries and then of the keys
   for (int which = 0; which < 2; ++which) {
@@ -386,6 +381,11 @@ __global__ void __launch_bounds__(QK_THREADS, qk_blocks(GRAD, SPREAD)) ns_qk_ker
       for (int i = 0; i < N; ++i) dg.a[i] = dg.b[i] = make_float2(0.0f, 0.0f);
     }
     if (n > 0) {
+      // words outside the head are zero for the whole side (the sums of the other side lay in the ring)
+      for (int i = 0; i < STAGES * STAGE; i += 64) {
+        if (!l.on_a) ring[i] = make_uint4(0, 0, 0, 0);
+        if (!l.on_b) ring[i + 32] = make_uint4(0, 0, 0, 0);
+      }
       const Two<T> g = lane_weights<T>(p, side, l);
       const Place start = place_of(first * p.chunk * H + min(group, H - 1), side.heads);
       Walk ahead = {start.t, start.h, p.chunk}, at = ahead;  // of the copies, and of the rounds

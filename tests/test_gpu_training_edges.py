@@ -103,6 +103,21 @@ def test_rotations_of_any_even_width(D, rot, interleaved, dtype, T, H, K):
         assert (np.abs(f64(dw) - want_w) <= ((T * x.shape[1] + 2) * u + c) * (ua * np.abs(xv) * r).sum((0, 1)) + u).all()
 
 
+# Many heads, so that the same warps take queries and then keys: heads of an odd
+# number of 16-byte words (3, 9, 5) beside one of an even number.
+MANY_HEADS = [  # T, H, K, dim, rot, interleaved, dtype
+    (100, 2000, 1500, 24, 16, False, torch.bfloat16), (100, 2000, 1500, 24, 24, True, torch.float16),
+    (100, 2000, 1500, 24, 24, False, torch.bfloat16), (100, 2000, 1500, 12, 8, False, torch.float32),
+    (100, 2000, 1500, 12, 12, False, torch.float32), (100, 800, 900, 72, 64, False, torch.bfloat16),
+    (100, 1200, 1300, 40, 16, False, torch.float16), (100, 1000, 800, 64, 64, False, torch.bfloat16),
+]
+
+
+@pytest.mark.parametrize("T,H,K,D,rot,interleaved,dtype", MANY_HEADS)
+def test_rotations_of_many_heads(T, H, K, D, rot, interleaved, dtype):
+    test_rotations_of_any_even_width(D, rot, interleaved, dtype, T, H, K)
+
+
 @pytest.mark.parametrize("dtype,V", [(torch.bfloat16, 900001), (torch.float32, 450000)])
 def test_rows_too_long_for_a_cluster(dtype, V):
     g = gen(V)
