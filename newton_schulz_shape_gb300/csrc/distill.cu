@@ -451,6 +451,8 @@ __global__ void __launch_bounds__(NT + 32) ns_distill_kernel(const __grid_consta
         for (; u + B <= min(end, full); u += B) take(u, std::true_type());
         for (; u < end; u += B) take(u, std::false_type());
       }
+    } else {
+      nsptx::cp_async_wait<0>();  // a row that was read before its weight was known
     }
     o = join_warp(o);
     if (joins) nsptx::cluster_wait();
