@@ -698,13 +698,13 @@ int run_qk(bool grad, const void* const* x, const void* const* dy, void* const* 
   if (both > 0 && tokens > INT_MAX / 2 / both) return NS_ERR_SHAPE;
   const bool sums = grad && (grad_weight[0] || grad_weight[1]);
   for (int i = 0; i < 2; ++i) {
+    if (grad && !nsk::element_aligned(grad_weight[i], 4)) return NS_ERR_ARG;  // written without tokens too
     if (tokens == 0 || heads[i] == 0) continue;
     if (!x[i] || !out[i] || (grad && !dy[i])) return NS_ERR_ARG;
     const int b = nsk::elem_bytes(dtype);
     if (!nsk::element_aligned(x[i], b) || !nsk::element_aligned(out[i], b) || (grad && !nsk::element_aligned(dy[i], b)))
       return NS_ERR_ARG;
-    if (!nsk::element_aligned(weight[i], nsk::elem_bytes(weight_dtype)) || (grad && !nsk::element_aligned(grad_weight[i], 4)))
-      return NS_ERR_ARG;
+    if (!nsk::element_aligned(weight[i], nsk::elem_bytes(weight_dtype))) return NS_ERR_ARG;
   }
   if (!nsk::element_aligned(table, 4) || (positions && !nsk::element_aligned(positions, position_bytes))) return NS_ERR_ARG;
   if (sums && (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255) ||

@@ -30,6 +30,12 @@ def test_misaligned_addresses(name, base, changed):
     assert call(name, base, **changed) == nsg.NS_ERR_ARG
 
 
+@pytest.mark.parametrize("none", [dict(tokens=0), dict(q_heads=0, k_heads=0), dict(k_heads=0)])
+def test_weight_gradients_are_checked_without_tokens_too(none):
+    for off in (dict(dqw=P + 2), dict(dkw=P + 1)):
+        assert call("ns_qk_norm_rope_grad", QK_GRAD, **none, **off) == nsg.NS_ERR_ARG
+
+
 def test_temperatures_whose_inverse_is_not_finite():
     for t in (1e-40, 1e-31, 2e30, float("inf"), -1.0):
         assert call("ns_distill_loss", LOSS, temperature=t) == nsg.NS_ERR_ARG
