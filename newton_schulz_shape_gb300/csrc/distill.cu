@@ -54,6 +54,7 @@ struct DistillParams {
   unsigned int* status;
 };
 
+// Powers below the smallest normal number become 0.
 __device__ __forceinline__ float exp2_fast(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -158,22 +159,29 @@ __device__ __forceinline__ bool load_teacher(const DistillParams& p, const Teach
   return some;
 }
 
-// Enters the ids in the hash table, by one warp.
+// Enters the ids in the hash table, by one warp, whose lanes stay together: a
+// loop that each leaves by itself, on what its exchange returned, would leave
+// them apart to the block's barriers, where the first to arrive counted for
+// all.
 __device__ __forceinline__ void mark_repeated(const Teacher& te, int top, int mask, int lane) {
   for (int i = lane; i <= mask; i += 32) te.table[i] = NO_ID;
   __syncwarp();
-  for (int j = lane; j < top; j += 32) {
-    const int id = te.id[j];
-    if (id < 0) continue;
-    for (int h = table_place(id, mask);; h = (h + 1) & mask) {  // ends: most places stay empty
-      const int old = atomicCAS(&te.table[h], NO_ID, id);
-      if (old == NO_ID) break;
-      if ((old & 0x7fffffff) == id) {
-        atomicOr(&te.table[h], 0x80000000);
-        break;
+  for (int j0 = 0; j0 < top; j0 += 32) {
+    const int id = j0 + lane < top ? te.id[j0 + lane] : -1;
+    int h = table_place(id, mask);
+    bool open = id >= 0;
+    while (__any_sync(0xffffffffu, open)) {  // ends: most places stay empty
+      if (open) {
+        const int old = atomicCAS(&te.table[h], NO_ID, id);
+        const bool again = old != NO_ID && (old & 0x7fffffff) == id;
+        if (again) atomicOr(&te.table[h], 0x80000000);
+        open = old != NO_ID && !again;
+        h = (h + 1) & mask;
       }
+      __syncwarp();
     }
   }
+  __syncwarp();
 }
 
 // Probabilities and their sums, by one warp; visible to the block after its
@@ -289,7 +297,7 @@ __device__ __forceinline__ void write_entries(const DistillParams& p, const Teac
     const int id = te.id[j];
     if (id < 0 || !slice.has(id)) continue;
     int h = table_place(id, mask);
-    while ((te.table[h] & 0x7fffffff) != id) h = (h + 1) & mask;
+    for (int i = 0; i < mask && (te.table[h] & 0x7fffffff) != id; ++i) h = (h + 1) & mask;
     float sum = te.p[j];
     if (te.table[h] < 0) {
       sum = 0.0f;
@@ -521,7 +529,7 @@ __global__ void __launch_bounds__(NT + 32) ns_distill_kernel(const __grid_consta
   __syncthreads();
 }
 
-// Rows too long for the registers of a cluster: one block takes one token in
+// Rows too long for the shared memory of a cluster: one block takes one token in
 // two passes over its logits.
 template <typename T>
 __global__ void __launch_bounds__(DISTILL_THREADS) ns_distill_long_kernel(const __grid_constant__ DistillParams p) {

@@ -137,6 +137,34 @@ def test_rows_too_long_for_a_cluster(dtype, V):
         assert (np.abs(f64(got) - want) <= U * np.abs(want) + 4 * e * (np.abs(want) + 1e-3)).all()
 
 
+# Every entry's gradient where a warp that enters the ids also computes, and
+# where it has to be done before a short row is.
+@pytest.mark.parametrize("dtype,V,K", [(torch.float32, 512296, 1024), (torch.bfloat16, 1011385, 1024), (torch.float16, 830001, 200),
+                                       (torch.bfloat16, 1200, 1024), (torch.float32, 50021, 1000), (torch.bfloat16, 151, 129)])
+def test_gradients_of_many_entries(dtype, V, K):
+    g = gen(V)
+    T = 5
+    logits = randn(g, T, V, dtype=dtype)
+    ids, values = torch.randint(0, V, (T, K), generator=g, device=DEV), randn(g, T, K)
+    loss, lse, grad, later = empty(T), empty(T), empty(T, V, dtype=dtype), empty(T, V, dtype=dtype)
+    nsg.ns_distill_loss(logits, values, ids, loss, lse, grad_logits=grad, temperature=0.8)
+    nsg.ns_distill_grad(logits, values, ids, lse, later, temperature=0.8)
+    ok()
+    want_loss, want_lse, want = ot.distill(f64(logits), f64(values), ids.cpu().numpy(), None, None, 0.8)
+    e = (V / 128 + 64) * u
+    assert np.abs(f64(lse) - want_lse).max() <= e * 20 and np.abs(f64(loss) - want_loss).max() <= e * 40
+    U = torch.finfo(dtype).eps / 2
+    sums = np.zeros((T, V))                                     # what is subtracted: its sum in fp32 has its own error
+    p = np.exp(f64(values) / 0.8)
+    np.add.at(sums, (np.arange(T)[:, None], ids.cpu().numpy()), p / p.sum(1, keepdims=True) / 0.8)
+    for got in (grad, later):
+        assert (np.abs(f64(got) - want) <= U * np.abs(want) + 4 * e * (np.abs(want) + sums + 1e-6) + 2.0 ** -25).all()
+    again = logits.clone()
+    nsg.ns_distill_loss(again, values, ids, loss, lse, grad_logits=again, temperature=0.8)
+    ok()
+    assert torch.equal(again, grad)
+
+
 def test_the_most_teacher_entries_with_every_one_repeated():
     g = gen(3)
     T, V, K = 5, 2000, 1024
