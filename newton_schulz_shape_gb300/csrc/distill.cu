@@ -621,7 +621,7 @@ constexpr int DISTILL_MAX_SMEM = 200 * 1024;
 
 template <typename T, int NT>
 cudaError_t launch_slices(const DistillParams& p, long long tokens, size_t smem, cudaStream_t st) {
-  if (smem > 48 * 1024) {
+  if (smem > SMEM_WITHOUT_ASKING) {
     const cudaError_t e = cudaFuncSetAttribute(ns_distill_kernel<T, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                DISTILL_MAX_SMEM);
     if (e != cudaSuccess) return e;

@@ -7,6 +7,10 @@
 
 namespace nsk {
 
+// Dynamic shared memory that a kernel with at most 8 KB of its own gets without
+// asking: the default limit of 48 KB is on both together.
+constexpr size_t SMEM_WITHOUT_ASKING = 40 * 1024;
+
 template <typename P>
 cudaError_t launch_pdl(void (*kern)(P), dim3 grid, dim3 block, size_t smem, cudaStream_t st, const P& p) {
   cudaLaunchConfig_t cfg = {};

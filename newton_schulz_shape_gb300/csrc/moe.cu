@@ -662,7 +662,7 @@ int ns_moe_sort(const void* expert_ids, int id_bytes, int64_t tokens, int k, int
   const size_t smem = (static_cast<size_t>(nsk::SORT_WARPS + 3) * experts + 1) * sizeof(int);
   void (*const place)(nsk::SortParams) = p.chunk <= nsk::SORT_THREADS * nsk::SORT_HELD ? nsk::ns_moe_place_kernel<true>
                                                                                       : nsk::ns_moe_place_kernel<false>;
-  if (smem > 48 * 1024 &&
+  if (smem > nsk::SMEM_WITHOUT_ASKING &&
       cudaFuncSetAttribute(place, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
     return NS_ERR_CUDA;
   const cudaError_t e = counted(K_MOE, st, [&] {

@@ -3,6 +3,10 @@ odd rotations, rows too long for shared memory, many teacher entries, calls on
 the same buffers in a row. Against the float64 oracle; tolerances as in
 test_gpu_training_ops.py (u = 2^-24, U half the output type's eps)."""
 
+import subprocess
+import sys
+from pathlib import Path
+
 import numpy as np
 import pytest
 import torch
@@ -232,6 +236,26 @@ def test_sums_of_few_rows(T, k, D, dtype):
     for got, want, size in ((y, ot.moe_combine(v, wv, r), ot.moe_combine(np.abs(v), np.abs(wv), r)),
                             (dx, ot.moe_dispatch_grad(v, r), ot.moe_dispatch_grad(np.abs(v), r))):
         assert (np.abs(f64(got) - want) <= (k + 2) * u * size + U * np.abs(want) * (1 + 1e-6) + tiny + U * (k + 2) * u * size).all()
+
+
+FIRST_CALLS = {  # dynamic shared memory just below 48 KB, which the static part takes past it
+    "distill": "V, K = 192289, 32\n"
+               "x, z, ids = torch.randn(2, V, device='cuda').half(), torch.randn(2, K, device='cuda'), torch.zeros(2, K, dtype=torch.int64, device='cuda')\n"
+               "out = torch.empty(2, 2, device='cuda')\n"
+               "nsg.ns_distill_loss(x, z, ids, out[0], out[1], grad_logits=torch.empty_like(x))\n",
+    "sort": "E = 646\n"
+            "ids = torch.arange(64, device='cuda').view(32, 2)\n"
+            "i = [torch.empty(n, dtype=torch.int32, device='cuda') for n in (64, 64, E, E + 1)]\n"
+            "nsg.ns_moe_sort(ids, E, i[0].view(32, 2), *i[1:], None)\n"
+            "assert torch.equal(i[0], torch.arange(64, device='cuda', dtype=torch.int32))\n",
+}
+
+
+@pytest.mark.parametrize("name", FIRST_CALLS)
+def test_first_call_of_a_process_near_the_shared_memory_limit(name):
+    code = "import torch, newton_schulz_shape_gb300 as nsg\n" + FIRST_CALLS[name] + "assert nsg.ns_check_status() == nsg.NS_OK\n"
+    run = subprocess.run([sys.executable, "-c", code], cwd=Path(__file__).resolve().parent.parent, capture_output=True, text=True, timeout=300)
+    assert run.returncode == 0, run.stderr[-2000:]
 
 
 def test_launch_counts():
