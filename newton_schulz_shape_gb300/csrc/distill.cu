@@ -106,10 +106,13 @@ size_t teacher_bytes(int top) { return sizeof(float) * (3 * static_cast<size_t>(
 
 constexpr int NO_ID = 0x7fffffff;  // an empty place; ids are below it
 
-// The upper bits of a multiple of the golden ratio: ids at equal distances, as
-// the lower ones would not, spread over the table.
+// The upper bits of a multiple of the golden ratio, mixed and multiplied once
+// more: a single multiple puts ids whose distance is near a Fibonacci number in
+// each other's way (64 ids 377 apart: 18 us a call where 5.3 are usual).
 __device__ __forceinline__ int table_place(int id, int mask) {
-  return static_cast<int>((static_cast<unsigned>(id) * 2654435761u) >> __clz(mask));
+  unsigned h = static_cast<unsigned>(id) * 2654435761u;
+  h = (h ^ (h >> 15)) * 2654435761u;
+  return static_cast<int>(h >> __clz(mask));
 }
 
 // Entry i of all tokens' as it was given.

@@ -28,8 +28,11 @@ namespace {
 
 constexpr int QK_THREADS = 128;
 constexpr int QK_WARPS = QK_THREADS / 32;
+// What is rotated: whole words (or nothing); interleaved pairs that end inside a
+// word; pairs (i, i + rot_dim / 2) that are not made of whole words.
+enum QkTurn { WHOLE, PARTIAL, SPREAD };
 // Blocks that share an SM, by the registers that their angles and sums take.
-constexpr int qk_blocks(bool grad, bool spread) { return 5 - (grad ? 1 : 0) - (spread ? 1 : 0); }
+constexpr int qk_blocks(bool grad, QkTurn mode) { return 5 - (grad ? 1 : 0) - (mode == SPREAD ? 1 : 0); }
 constexpr int QK_AHEAD = 3;  // rounds whose words are on their way
 constexpr int QK_ANY_THREADS = 128;
 constexpr int QK_MAX_DIM = 1024;
@@ -118,14 +121,17 @@ struct Lane {
   bool turn_a, turn_b; // rotated
 };
 
-// Lane i of a head's group. SPREAD: the pairs are not made of whole words, so
-// the words are taken in order.
-template <typename T, bool SPREAD>
+// SPREAD: places of a warp's heads, at most 64 words and 32 heads.
+__host__ __device__ constexpr int spread_places(int V) { return 64 * V + 64; }
+
+// Lane i of a head's group. Where the pairs (i, i + rot_dim / 2) are not made of
+// whole words the words are taken in order, as they are for interleaved pairs.
+template <typename T, QkTurn MODE>
 __device__ __forceinline__ Lane<T> lane_of(const QkParams& p, int i) {
   constexpr int V = Lane<T>::V;
   Lane<T> l;
-  const int words = p.dim / V, turned = p.rot_dim / V;
-  if (SPREAD || p.interleaved) {
+  const int words = p.dim / V, turned = (p.rot_dim + V - 1) / V;
+  if (MODE != WHOLE || p.interleaved) {
     const int a = i, b = i + (words + 1) / 2;
     l.on_a = a < (words + 1) / 2;
     l.on_b = l.on_a && b < words;
@@ -190,10 +196,28 @@ struct Angles {
   float2 c[Two<T>::N], s[Two<T>::N];
 };
 
-template <typename T>
+template <typename T, QkTurn MODE>
 __device__ __forceinline__ void load_angles(const QkParams& p, const Lane<T>& l, const float* row, Angles<T>& g) {
   constexpr int N = Two<T>::N;
   const int half = p.rot_dim / 2;
+  if constexpr (MODE == PARTIAL) {
+    // interleaved pairs up to the middle of a word, whose others stay as they are; no row of the table need
+    // start at a vector's boundary
+    auto some = [&](float2* c, float2* s, int first) {
+      float* const cf = reinterpret_cast<float*>(c);
+      float* const sf = reinterpret_cast<float*>(s);
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        if (first + i < half) {
+          cf[i] = row[first + i];
+          sf[i] = row[half + first + i];
+        }
+      }
+    };
+    if (l.turn_a) some(g.c, g.s, l.a / 2);
+    if (l.turn_b) some(g.c + N / 2, g.s + N / 2, l.b / 2);
+    return;
+  }
   const int a = p.interleaved ? l.a / 2 : l.a, b = p.interleaved ? l.b / 2 : l.a + N;
   auto load = [&](float2* to, const float* from) {
     if constexpr (N == 4) {
@@ -215,23 +239,27 @@ __device__ __forceinline__ void load_angles(const QkParams& p, const Lane<T>& l,
 }
 
 // Rotates the lane's pairs, forward (sign 1) or back (sign -1).
-template <typename T>
+template <typename T, QkTurn MODE>
 __device__ __forceinline__ void turn(const QkParams& p, const Lane<T>& l, const Angles<T>& g, Two<T>& x, float sign) {
   constexpr int N = Two<T>::N;
-  if (p.interleaved) {
+  if (MODE == PARTIAL || p.interleaved) {
     // pair i of a word: cosine and sine i of the word's N
     auto one = [&](float2& v, float c, float s) { v = make_float2(v.x * c - v.y * s, v.y * c + v.x * s); };
+    auto word = [&](float2* v, const float2* c, const float2* s, int pairs) {
 #pragma unroll
-    for (int i = 0; i < N; i += 2) {
-      const int k = i / 2;
-      if (l.turn_a) {
-        one(x.a[i], g.c[k].x, sign * g.s[k].x);
-        one(x.a[i + 1], g.c[k].y, sign * g.s[k].y);
+      for (int i = 0; i < N; i += 2) {
+        const int k = i / 2;
+        if (i < pairs) one(v[i], c[k].x, sign * s[k].x);
+        if (i + 1 < pairs) one(v[i + 1], c[k].y, sign * s[k].y);
       }
-      if (l.turn_b) {
-        one(x.b[i], g.c[N / 2 + k].x, sign * g.s[N / 2 + k].x);
-        one(x.b[i + 1], g.c[N / 2 + k].y, sign * g.s[N / 2 + k].y);
-      }
+    };
+    const int half = p.rot_dim / 2;
+    if (MODE == PARTIAL) {
+      if (l.turn_a) word(x.a, g.c, g.s, half - l.a / 2);
+      if (l.turn_b) word(x.b, g.c + N / 2, g.s + N / 2, half - l.b / 2);
+    } else {
+      if (l.turn_a) word(x.a, g.c, g.s, N);
+      if (l.turn_b) word(x.b, g.c + N / 2, g.s + N / 2, N);
     }
   } else if (l.turn_a) {
 #pragma unroll
@@ -244,60 +272,69 @@ __device__ __forceinline__ void turn(const QkParams& p, const Lane<T>& l, const 
 }
 
 // The same for pairs that are not made of whole words. Every value has its own
-// angle, with the sine's sign of its place in the pair; the other value of a
-// pair is read from `head`, the group's part of shared memory, where the lanes
-// put their words in the head's order.
+// angle, with the sine's sign of its place in the pair. The other value of value
+// d's pair is the (d + rot_dim / 2)-th modulo rot_dim: the lanes put their words
+// in the head's order in `head`, the group's part of shared memory, the first
+// value once more behind the last, so that the others of two neighbours lie side
+// by side, at even places (all are moved by one where rot_dim / 2 is odd). Read in
+// pairs: 16384 tokens of 32/8 heads of 72, all rotated, 159 us backward value by
+// value, 125 so.
 template <typename T>
 struct SpreadAngles {
-  float2 a[Lane<T>::V], b[Lane<T>::V];  // cosine, signed sine
+  float2 ca[Two<T>::N], sa[Two<T>::N], cb[Two<T>::N], sb[Two<T>::N];
 };
 
-// Place of the other value of value d's pair, and whether d is its second.
-__device__ __forceinline__ int other_of(const QkParams& p, int d, bool* second) {
-  const int half = p.rot_dim / 2;
-  *second = p.interleaved ? d & 1 : d >= half;
-  return p.interleaved ? d ^ 1 : (*second ? d - half : d + half);
-}
-
+// The sines with `sign`: 1 forward, -1 back.
 template <typename T>
-__device__ __forceinline__ void load_spread(const QkParams& p, const Lane<T>& l, const float* row, SpreadAngles<T>& g) {
+__device__ __forceinline__ void load_spread(const QkParams& p, const Lane<T>& l, const float* row, SpreadAngles<T>& g,
+                                            float sign) {
   const int half = p.rot_dim / 2;
-  auto one = [&](int d) {
-    bool second;
-    other_of(p, d, &second);
-    const int angle = p.interleaved ? d >> 1 : (second ? d - half : d);
-    return make_float2(row[angle], second ? row[half + angle] : -row[half + angle]);
-  };
+  auto word = [&](float2* c, float2* s, int first) {
 #pragma unroll
-  for (int k = 0; k < Lane<T>::V; ++k) {
-    if (l.a + k < p.rot_dim) g.a[k] = one(l.a + k);
-    if (l.b + k < p.rot_dim) g.b[k] = one(l.b + k);
-  }
+    for (int i = 0; i < Two<T>::N; ++i) {
+      const int d = first + 2 * i;
+      if (d >= p.rot_dim) continue;
+      const int a = d < half ? d : d - half, b = d + 1 < half ? d + 1 : d + 1 - half;
+      c[i] = make_float2(row[a], row[b]);
+      s[i] = make_float2(d < half ? -sign * row[half + a] : sign * row[half + a],
+                         d + 1 < half ? -sign * row[half + b] : sign * row[half + b]);
+    }
+  };
+  word(g.ca, g.sa, l.a);
+  word(g.cb, g.sb, l.b);
 }
 
 template <typename T>
 __device__ __forceinline__ void turn_spread(const QkParams& p, const Lane<T>& l, const SpreadAngles<T>& g, Two<T>& x,
-                                            float sign, float* head) {
-  constexpr int N = Two<T>::N;
-  __syncwarp();
+                                            float* head) {
+  const int half = p.rot_dim / 2, odd = half & 1;
+  auto put = [&](const float2* v, int first, bool on) {
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    if (l.on_a && l.a < p.rot_dim) reinterpret_cast<float2*>(head + l.a)[i] = x.a[i];
-    if (l.on_b && l.b < p.rot_dim) reinterpret_cast<float2*>(head + l.b)[i] = x.b[i];
-  }
-  __syncwarp();
-  auto one = [&](float v, int d, const float2& cs) {
-    bool second;
-    const int o = other_of(p, d, &second);
-    return d < p.rot_dim ? v * cs.x + head[o] * (sign * cs.y) : v;
+    for (int i = 0; i < Two<T>::N; ++i) {
+      float* const to = head + odd + first + 2 * i;
+      if (!on || first + 2 * i >= p.rot_dim) continue;
+      if (odd) {
+        to[0] = v[i].x;
+        to[1] = v[i].y;
+      } else {
+        *reinterpret_cast<float2*>(to) = v[i];
+      }
+    }
   };
+  auto get = [&](float2* v, const float2* c, const float2* s, int first, bool on) {
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    if (l.on_a && l.a < p.rot_dim)
-      x.a[i] = make_float2(one(x.a[i].x, l.a + 2 * i, g.a[2 * i]), one(x.a[i].y, l.a + 2 * i + 1, g.a[2 * i + 1]));
-    if (l.on_b && l.b < p.rot_dim)
-      x.b[i] = make_float2(one(x.b[i].x, l.b + 2 * i, g.b[2 * i]), one(x.b[i].y, l.b + 2 * i + 1, g.b[2 * i + 1]));
-  }
+    for (int i = 0; i < Two<T>::N; ++i) {
+      const int d = first + 2 * i, o = d + half < p.rot_dim ? d + half : d - half;
+      if (on && d < p.rot_dim) v[i] = fma2(v[i], c[i], mul2(*reinterpret_cast<const float2*>(head + odd + o), s[i]));
+    }
+  };
+  __syncwarp();
+  put(x.a, l.a, l.on_a);
+  put(x.b, l.b, l.on_b);
+  if (l.on_a && l.a == 0) head[odd + p.rot_dim] = x.a[0].x;
+  __syncwarp();
+  get(x.a, g.ca, g.sa, l.a, l.on_a);
+  get(x.b, g.cb, g.sb, l.b, l.on_b);
 }
 
 // The weights of one of the lane's words.
@@ -352,9 +389,9 @@ struct Walk {
 // p.chunk rounds at a time, so that together they walk through memory in order;
 // a warp copies the words of its next QK_AHEAD rounds to shared memory while it
 // computes one. For the gradient a lane keeps the sums of its columns of dg,
-// which a block joins in a fixed order. SPREAD: see turn_spread.
-template <typename T, int G, bool GRAD, bool SPREAD>
-__global__ void __launch_bounds__(QK_THREADS, qk_blocks(GRAD, SPREAD)) ns_qk_kernel(const __grid_constant__ QkParams p) {
+// which a block joins in a fixed order.
+template <typename T, int G, bool GRAD, QkTurn MODE>
+__global__ void __launch_bounds__(QK_THREADS, qk_blocks(GRAD, MODE)) ns_qk_kernel(const __grid_constant__ QkParams p) {
   constexpr int N = Two<T>::N, STAGES = QK_AHEAD + 1, STAGE = GRAD ? 128 : 64;
   extern __shared__ uint4 ring_smem[];
   nsptx::griddep_wait();
@@ -363,10 +400,10 @@ __global__ void __launch_bounds__(QK_THREADS, qk_blocks(GRAD, SPREAD)) ns_qk_ker
   uint4* ring = ring_smem + warp * (STAGES * STAGE) + lane;
   const int group_size = G ? G : p.lanes, H = 32 / group_size, group = lane / group_size, i_lane = lane - group * group_size;
   const bool takes = group < H;  // a lane left over takes no head
-  Lane<T> l = lane_of<T, SPREAD>(p, i_lane);
+  Lane<T> l = lane_of<T, MODE>(p, i_lane);
   if (!takes) l.on_a = l.on_b = l.turn_a = l.turn_b = false;
-  // SPREAD: the group's head (all heads of a warp fit 64 words of V values)
-  float* head = reinterpret_cast<float*>(ring_smem + QK_WARPS * STAGES * STAGE) + warp * 64 * Lane<T>::V + min(group, H - 1) * p.dim;
+  // SPREAD: the group's head, of dim + 2 places
+  float* head = reinterpret_cast<float*>(ring_smem + QK_WARPS * STAGES * STAGE) + warp * spread_places(Lane<T>::V) + min(group, H - 1) * (p.dim + 2);
   const float inv_dim = 1.0f / p.dim;
   const int warps = gridDim.x * QK_WARPS, me = blockIdx.x * QK_WARPS + warp;
   int chunk = me;  // this warp's next, in those of the queries and then of the keys
@@ -428,8 +465,8 @@ __global__ void __launch_bounds__(QK_THREADS, qk_blocks(GRAD, SPREAD)) ns_qk_ker
         take = take + STAGE == STAGES * STAGE ? 0 : take + STAGE;
         if (p.rot_dim && live && at.t != angles_of) {
           row = table_row(p, at.t);
-          if (row && SPREAD) load_spread<T>(p, l, row, spread);
-          if (row && !SPREAD) load_angles<T>(p, l, row, angles);
+          if (row && MODE == SPREAD) load_spread<T>(p, l, row, spread, GRAD ? -1.0f : 1.0f);
+          if (row && MODE != SPREAD) load_angles<T, MODE>(p, l, row, angles);
           angles_of = at.t;
         }
         if (p.rot_dim && !row) live = false;
@@ -447,15 +484,15 @@ __global__ void __launch_bounds__(QK_THREADS, qk_blocks(GRAD, SPREAD)) ns_qk_ker
             u.a[i] = mul2(xf.a[i], mul2(g.a[i], r2));
             u.b[i] = mul2(xf.b[i], mul2(g.b[i], r2));
           }
-          if (SPREAD)
-            turn_spread<T>(p, l, spread, u, 1.0f, head);
+          if (MODE == SPREAD)
+            turn_spread<T>(p, l, spread, u, head);
           else
-            turn<T>(p, l, angles, u, 1.0f);
+            turn<T, MODE>(p, l, angles, u, 1.0f);
         } else {
-          if (SPREAD)
-            turn_spread<T>(p, l, spread, u, -1.0f, head);
+          if (MODE == SPREAD)
+            turn_spread<T>(p, l, spread, u, head);
           else
-            turn<T>(p, l, angles, u, -1.0f);
+            turn<T, MODE>(p, l, angles, u, -1.0f);
           if (live) {
 #pragma unroll
             for (int i = 0; i < N; ++i) {
@@ -623,10 +660,10 @@ __global__ void __launch_bounds__(1024) ns_qk_sum_kernel(const __grid_constant__
   if (out) out[c >= p.dim ? c - p.dim : c] = sum;
 }
 
-template <typename T, int G, bool SPREAD = false>
+template <typename T, int G, QkTurn MODE>
 cudaError_t launch_lanes(bool grad, QkParams& p, int nsm, int* blocks, cudaStream_t st) {
   const int H = 32 / p.lanes;
-  const int most = std::min(nsm * qk_blocks(grad, SPREAD), QK_MAX_BLOCKS);
+  const int most = std::min(nsm * qk_blocks(grad, MODE), QK_MAX_BLOCKS);
   // a warp's rounds in equal chunks of at most 8: long ones, since a token's angles serve all of its rounds
   // (16384 tokens of 32/8 heads take 131, 107, 97 and 93 us backward in chunks of 1, 2, 4 and 8)
   const int rounds = static_cast<int>((p.tokens * (p.side[0].heads + p.side[1].heads) + H - 1) / H);
@@ -641,12 +678,12 @@ cudaError_t launch_lanes(bool grad, QkParams& p, int nsm, int* blocks, cudaStrea
     p.between[i] = place_of(H + (*blocks * QK_WARPS - 1) * p.chunk * H, p.side[i].heads);
   }
   const size_t smem = sizeof(uint4) * QK_WARPS * (QK_AHEAD + 1) * (grad ? 128 : 64) +
-                      (SPREAD ? sizeof(float) * QK_WARPS * 64 * Lane<T>::V : 0);
-  if (!grad) return launch_pdl(ns_qk_kernel<T, G, false, SPREAD>, dim3(*blocks), dim3(QK_THREADS), smem, st, p);
-  const cudaError_t e = cudaFuncSetAttribute(ns_qk_kernel<T, G, true, SPREAD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                      (MODE == SPREAD ? sizeof(float) * QK_WARPS * spread_places(Lane<T>::V) : 0);
+  if (!grad) return launch_pdl(ns_qk_kernel<T, G, false, MODE>, dim3(*blocks), dim3(QK_THREADS), smem, st, p);
+  const cudaError_t e = cudaFuncSetAttribute(ns_qk_kernel<T, G, true, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              static_cast<int>(smem));
   if (e != cudaSuccess) return e;
-  return launch_pdl(ns_qk_kernel<T, G, true, SPREAD>, dim3(*blocks), dim3(QK_THREADS), smem, st, p);
+  return launch_pdl(ns_qk_kernel<T, G, true, MODE>, dim3(*blocks), dim3(QK_THREADS), smem, st, p);
 }
 
 template <typename T>
@@ -654,10 +691,11 @@ cudaError_t launch_qk(bool grad, bool lanes, QkParams& p, int nsm, int* blocks, 
   constexpr int V = Lane<T>::V;
   if (lanes) {
     p.lanes = (p.dim / V + 1) / 2;
-    if (p.rot_dim % (p.interleaved ? V : 2 * V)) return launch_lanes<T, 0, true>(grad, p, nsm, blocks, st);
-    if (p.lanes == 8) return launch_lanes<T, 8>(grad, p, nsm, blocks, st);
-    if (p.lanes == 16) return launch_lanes<T, 16>(grad, p, nsm, blocks, st);
-    return launch_lanes<T, 0>(grad, p, nsm, blocks, st);
+    if (p.interleaved && p.rot_dim % V) return launch_lanes<T, 0, PARTIAL>(grad, p, nsm, blocks, st);
+    if (!p.interleaved && p.rot_dim % (2 * V)) return launch_lanes<T, 0, SPREAD>(grad, p, nsm, blocks, st);
+    if (p.lanes == 8) return launch_lanes<T, 8, WHOLE>(grad, p, nsm, blocks, st);
+    if (p.lanes == 16) return launch_lanes<T, 16, WHOLE>(grad, p, nsm, blocks, st);
+    return launch_lanes<T, 0, WHOLE>(grad, p, nsm, blocks, st);
   }
   constexpr int WARPS = QK_ANY_THREADS / 32;
   const long long pairs = p.tokens * std::max(p.side[0].heads, p.side[1].heads);
