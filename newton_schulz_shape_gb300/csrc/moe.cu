@@ -43,7 +43,7 @@ constexpr int SORT_WARPS = SORT_THREADS / 32;
 constexpr int SORT_HELD = 4;  // rounds of 32 slots that a warp keeps in registers
 constexpr int SORT_MAX_BLOCKS = 256;
 constexpr int ROW_THREADS = 128;
-constexpr int CLEAR_ROWS = 4;
+constexpr int CLEAR_ROWS = 4;  // twice as many where they are short (28351 x 2 rows of 128 dispatched in 10.5 us against 12.5)
 
 // Counts of a block, a whole number of 16-byte words.
 __host__ __device__ inline int count_stride(int experts) { return (experts + 3) / 4 * 4; }
@@ -257,6 +257,7 @@ struct RowParams {
   long long tokens, rows, dim;
   int k;
   int parts;                // warps that share one token
+  int clear;                // rows that a warp clears, where they hold no slot
   long long token_warps;    // warps before the ones that clear rows without a slot
   unsigned int* status;
 };
@@ -273,17 +274,17 @@ __device__ __forceinline__ int lane_row(const RowParams& p, long long t, int lan
   return r;
 }
 
-// Clears those of CLEAR_ROWS rows that hold no slot. Few rows a warp: they come
+// Clears those of p.clear rows that hold no slot. Few rows a warp: they come
 // in runs (the ends of segments), and a warp with 32 of them to clear would end
 // long after the others.
 template <typename T, int V>
 __device__ __forceinline__ void clear_rows(const RowParams& p, long long group, int lane) {
-  const long long r = group * CLEAR_ROWS + lane;
-  unsigned todo = __ballot_sync(0xffffffffu, lane < CLEAR_ROWS && r < p.rows && p.slot_of_row[r] < 0);
+  const long long r = group * p.clear + lane;
+  unsigned todo = __ballot_sync(0xffffffffu, lane < p.clear && r < p.rows && p.slot_of_row[r] < 0);
   while (todo) {
     const int i = __ffs(todo) - 1;
     todo &= todo - 1;
-    T* row = static_cast<T*>(p.dst) + (group * CLEAR_ROWS + i) * p.dst_ld;
+    T* row = static_cast<T*>(p.dst) + (group * p.clear + i) * p.dst_ld;
     for (long long c = lane * V; c < p.dim; c += 32 * V) store_vec<T, V>(row + c, zero_vec<T, V>());
   }
 }
@@ -532,7 +533,8 @@ cudaError_t launch_rows(nsk::RowParams& p, int nsm, cudaStream_t st) {
     p.parts = static_cast<int>(pieces);
   }
   p.token_warps = p.tokens * p.parts;
-  const long long all = p.token_warps + (OP == GATHER ? 0 : (p.rows + CLEAR_ROWS - 1) / CLEAR_ROWS);
+  p.clear = p.dim * sizeof(T) <= 512 ? 2 * CLEAR_ROWS : CLEAR_ROWS;
+  const long long all = p.token_warps + (OP == GATHER ? 0 : (p.rows + p.clear - 1) / p.clear);
   const long long blocks = (all + warps - 1) / warps;
   if (blocks > INT_MAX) return cudaErrorInvalidValue;
   const dim3 grid(static_cast<unsigned>(blocks)), block(ROW_THREADS);
@@ -544,11 +546,17 @@ cudaError_t launch_rows(nsk::RowParams& p, int nsm, cudaStream_t st) {
 // Words of 16 bytes where rows allow it, else of 4 (16-bit rows of an even
 // width), else single elements: 8192 x 6 bf16 rows of 2048, 2046 and 2047 are
 // summed in 37.7, 38.7 and 53.0 us (6.3, 6.1 and 4.4 TB/s), backward in 70, 85
-// and 100 us. Rows in flight: 3 for the sums; backward 2, or 1 of 64 bytes a lane
-// (3 of those need 163 registers and take 136 us where 1 takes 124).
+// and 100 us. U, the words of a row that a lane takes at once, is what a short
+// row has for it, so that more warps fit (28351 x 2 rows of 256 bf16 backward
+// 21 us with one word, 34 with the four of long rows; of 512, 31 with two against
+// 41; of 70, 13 against 19). J, the rows in flight: 3 for the sums; backward 2, or 1
+// of 32 or 64 bytes a lane (3 of those need 163 registers and take 136 us where 1
+// takes 124).
 template <RowOp OP, typename T>
 cudaError_t launch_words(int word, nsk::RowParams& p, int nsm, cudaStream_t st) {
   constexpr int V = 16 / sizeof(T);
+  // whether a row has more than u words of v elements for a lane
+  const auto longer = [&](int v, int u) { return p.dim > 32LL * v * u; };
   if constexpr (OP == GATHER) {
     // few slots: more of each row at a time instead of more rows (16384 tokens of 1, 2 and 4 rows of 2048 bf16
     // in 24.6, 34.1 and 52.7 us against 34.5, 39.8 and 57.0; of 2047 columns, 1 and 2 rows in 37 and 44 against
@@ -556,20 +564,40 @@ cudaError_t launch_words(int word, nsk::RowParams& p, int nsm, cudaStream_t st) 
     // words (8192 tokens of 2 rows of 512 take 5.9 us against 5.3, of 255 columns 5.3 against 4.5) and, for the
     // wide words, where the tokens fill the GPU (1216 tokens of 4 rows of 2048 take 4.9 us against 4.6, 2432
     // tokens 10.3 against 11.6)
-    const auto reaches = [&](int v, int u) { return p.dim > 32 * v * (u - 1); };
-    if (word == 16 && p.k <= 4 && reaches(V, 4) && p.tokens >= 16 * nsm) return launch_rows<OP, T, V, 4, 1>(p, nsm, st);
-    if (word == 16) return launch_rows<OP, T, V, 2, 3>(p, nsm, st);
-    if constexpr (sizeof(T) == 2) {
-      if (word == 4 && p.k <= 2 && reaches(2, 16)) return launch_rows<OP, T, 2, 16, 2>(p, nsm, st);
-      if (word == 4) return launch_rows<OP, T, 2, 8, 3>(p, nsm, st);
+    if (word == 16) {
+      if (p.k <= 4 && longer(V, 3) && p.tokens >= 16 * nsm) return launch_rows<OP, T, V, 4, 1>(p, nsm, st);
+      if (longer(V, 1)) return launch_rows<OP, T, V, 2, 3>(p, nsm, st);
+      return launch_rows<OP, T, V, 1, 3>(p, nsm, st);
     }
-    if (p.k <= 2 && reaches(1, 16)) return launch_rows<OP, T, 1, 16, 2>(p, nsm, st);
-    return launch_rows<OP, T, 1, 8, 3>(p, nsm, st);
+    const auto narrow = [&](auto v) {
+      constexpr int W = decltype(v)::value;
+      if (p.k <= 2 && longer(W, 15)) return launch_rows<OP, T, W, 16, 2>(p, nsm, st);
+      if (longer(W, 4)) return launch_rows<OP, T, W, 8, 3>(p, nsm, st);
+      return launch_rows<OP, T, W, 4, 3>(p, nsm, st);
+    };
+    if constexpr (sizeof(T) == 2)
+      if (word == 4) return narrow(std::integral_constant<int, 2>());
+    return narrow(std::integral_constant<int, 1>());
+  } else if constexpr (OP == COMBINE_GRAD) {
+    if (word == 16) {
+      if (longer(V, 2)) return launch_rows<OP, T, V, 4, 1>(p, nsm, st);
+      if (longer(V, 1)) return launch_rows<OP, T, V, 2, 1>(p, nsm, st);
+      return launch_rows<OP, T, V, 1, 2>(p, nsm, st);
+    }
+    const auto narrow = [&](auto v) {
+      constexpr int W = decltype(v)::value;
+      if (longer(W, 4)) return launch_rows<OP, T, W, 8, 2>(p, nsm, st);
+      if (longer(W, 2)) return launch_rows<OP, T, W, 4, 2>(p, nsm, st);
+      return launch_rows<OP, T, W, 2, 2>(p, nsm, st);
+    };
+    if constexpr (sizeof(T) == 2)
+      if (word == 4) return narrow(std::integral_constant<int, 2>());
+    return narrow(std::integral_constant<int, 1>());
   } else {
     if (word == 16) return launch_rows<OP, T, V, 4, 1>(p, nsm, st);
     if constexpr (sizeof(T) == 2)
-      if (word == 4) return launch_rows<OP, T, 2, 8, 2>(p, nsm, st);
-    return launch_rows<OP, T, 1, 8, 2>(p, nsm, st);
+      if (word == 4) return launch_rows<OP, T, 2, 8, 1>(p, nsm, st);
+    return launch_rows<OP, T, 1, 8, 1>(p, nsm, st);
   }
 }
 

@@ -11,6 +11,7 @@ import numpy as np
 import pytest
 import torch
 
+import test_gpu_training_ops as ops
 from oracle import training as ot
 
 pytestmark = pytest.mark.gpu
@@ -236,6 +237,15 @@ def test_sums_of_few_rows(T, k, D, dtype):
     for got, want, size in ((y, ot.moe_combine(v, wv, r), ot.moe_combine(np.abs(v), np.abs(wv), r)),
                             (dx, ot.moe_dispatch_grad(v, r), ot.moe_dispatch_grad(np.abs(v), r))):
         assert (np.abs(f64(got) - want) <= (k + 2) * u * size + U * np.abs(want) * (1 + 1e-6) + tiny + U * (k + 2) * u * size).all()
+
+
+# Widths on both sides of those at which a lane takes more words of a row.
+@pytest.mark.parametrize("D", [256, 264, 512, 520, 64, 66, 128, 130, 258, 32, 33, 65, 129, 124, 132])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("k", [2, 5])
+def test_rows_of_few_words(D, dtype, k):
+    ops.test_combine_and_gradient(41, k, 6, D, 4, 0, 0, 0, dtype)
+    ops.test_dispatch_and_gradient(41, k, 6, D, 4, 0, 0, 0, dtype)
 
 
 FIRST_CALLS = {  # dynamic shared memory just below 48 KB, which the static part takes past it
