@@ -75,13 +75,6 @@ struct Online {
   }
 };
 
-// Elements before the first 16-byte boundary of p, at most n.
-template <typename T>
-__device__ __forceinline__ long long head_of(const T* p, long long n) {
-  const long long h = ((16 - (reinterpret_cast<uintptr_t>(p) & 15)) & 15) / sizeof(T);
-  return h < n ? h : n;
-}
-
 // Places of the hash table of `top` ids: a power of two, four times the ids or
 // more, which keeps searches at one or two places.
 __host__ __device__ inline int table_size(int top) {

@@ -176,6 +176,13 @@ __device__ __forceinline__ void store_once(T* p, const Vec<T, 16 / sizeof(T)>& x
   __stcs(reinterpret_cast<uint4*>(p), *reinterpret_cast<const uint4*>(&x));
 }
 
+// Elements before the first 16-byte boundary of p, at most n.
+template <typename T>
+__device__ __forceinline__ long long head_of(const T* p, long long n) {
+  const long long h = ((16 - (reinterpret_cast<uintptr_t>(p) & 15)) & 15) / sizeof(T);
+  return h < n ? h : n;
+}
+
 __device__ __forceinline__ float warp_sum(float x) {
 #pragma unroll
   for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);

@@ -43,6 +43,7 @@ constexpr int SORT_WARPS = SORT_THREADS / 32;
 constexpr int SORT_HELD = 4;  // rounds of 32 slots that a warp keeps in registers
 constexpr int SORT_MAX_BLOCKS = 256;
 constexpr int ROW_THREADS = 128;
+constexpr int MANY_WARPS = 16;  // of a block where many share a token
 constexpr int CLEAR_ROWS = 4;  // twice as many where they are short (28351 x 2 rows of 128 dispatched in 10.5 us against 12.5)
 
 // Counts of a block, a whole number of 16-byte words.
@@ -285,7 +286,16 @@ __device__ __forceinline__ void clear_rows(const RowParams& p, long long group, 
     const int i = __ffs(todo) - 1;
     todo &= todo - 1;
     T* row = static_cast<T*>(p.dst) + (group * p.clear + i) * p.dst_ld;
-    for (long long c = lane * V; c < p.dim; c += 32 * V) store_vec<T, V>(row + c, zero_vec<T, V>());
+    if (V == 1 && p.dim >= 512) {
+      // zeros need no words of the row's own: 16 bytes at a time between its ends (8192 x 6 rows of 2047 bf16
+      // among their padding dispatched in 47 us, element by element 53; 4-byte words lose by it, and short rows)
+      constexpr int W = 16 / sizeof(T);
+      const long long head = head_of(row, p.dim), words = (p.dim - head) / W, ends = p.dim - words * W;
+      for (long long c = lane; c < words; c += 32) store_vec<T, W>(row + head + c * W, zero_vec<T, W>());
+      for (long long c = lane; c < ends; c += 32) row[c < head ? c : words * W + c] = from_float<T>(0.0f);
+    } else {
+      for (long long c = lane * V; c < p.dim; c += 32 * V) store_vec<T, V>(row + c, zero_vec<T, V>());
+    }
   }
 }
 
@@ -385,13 +395,13 @@ __global__ void __launch_bounds__(ROW_THREADS) ns_moe_gather_kernel(const __grid
 // combine's gradient: `parts` warps of one block share a token; each walks its
 // pieces of the row, writes w dy and sums dy ys, slot j's sum in lane j, with
 // the pieces of J rows on their way at once.
-template <typename T, int V, int U, int J>
-__global__ void __launch_bounds__(ROW_THREADS) ns_moe_combine_grad_kernel(const __grid_constant__ RowParams p) {
-  __shared__ float part_sum[ROW_THREADS / 32][MAX_K];
+template <typename T, int V, int U, int J, int WARPS>
+__global__ void __launch_bounds__(32 * WARPS) ns_moe_combine_grad_kernel(const __grid_constant__ RowParams p) {
+  __shared__ float part_sum[WARPS][MAX_K];
   nsptx::griddep_wait();
   nsptx::griddep_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const long long w = static_cast<long long>(blockIdx.x) * (ROW_THREADS / 32) + warp;
+  const long long w = static_cast<long long>(blockIdx.x) * WARPS + warp;
   const bool on = w < p.token_warps;
   const long long t = w / p.parts;
   const int part = static_cast<int>(w - t * p.parts), dim = static_cast<int>(p.dim);
@@ -519,28 +529,27 @@ int row_args(int dtype, int64_t tokens, int k, int64_t dim, int64_t rows) {
 
 enum RowOp { DISPATCH, GATHER, COMBINE_GRAD };
 
-// J: rows on their way at once, see the kernels.
-template <RowOp OP, typename T, int V, int U, int J>
+// J: rows on their way at once, see the kernels. WARPS of a block.
+template <RowOp OP, typename T, int V, int U, int J, int WARPS = nsk::ROW_THREADS / 32>
 cudaError_t launch_rows(nsk::RowParams& p, int nsm, cudaStream_t st) {
   using namespace nsk;
-  const int warps = ROW_THREADS / 32;
   const long long pieces = (p.dim + 32 * V * U - 1) / (32 * V * U);
   if (OP == COMBINE_GRAD) {
     // a token's warps sit in one block; few tokens are shared by more warps
     p.parts = 1;
-    while (p.parts < warps && p.parts < pieces && p.tokens * p.parts < nsm * 16) p.parts *= 2;
+    while (p.parts < WARPS && p.parts < pieces && p.tokens * p.parts < nsm * 16) p.parts *= 2;
   } else {
     p.parts = static_cast<int>(pieces);
   }
   p.token_warps = p.tokens * p.parts;
   p.clear = p.dim * sizeof(T) <= 512 ? 2 * CLEAR_ROWS : CLEAR_ROWS;
   const long long all = p.token_warps + (OP == GATHER ? 0 : (p.rows + p.clear - 1) / p.clear);
-  const long long blocks = (all + warps - 1) / warps;
+  const long long blocks = (all + WARPS - 1) / WARPS;
   if (blocks > INT_MAX) return cudaErrorInvalidValue;
-  const dim3 grid(static_cast<unsigned>(blocks)), block(ROW_THREADS);
+  const dim3 grid(static_cast<unsigned>(blocks)), block(32 * WARPS);
   if constexpr (OP == DISPATCH) return launch_pdl(ns_moe_dispatch_kernel<T, V, U>, grid, block, 0, st, p);
   if constexpr (OP == GATHER) return launch_pdl(ns_moe_gather_kernel<T, V, U, J>, grid, block, 0, st, p);
-  if constexpr (OP == COMBINE_GRAD) return launch_pdl(ns_moe_combine_grad_kernel<T, V, U, J>, grid, block, 0, st, p);
+  if constexpr (OP == COMBINE_GRAD) return launch_pdl(ns_moe_combine_grad_kernel<T, V, U, J, WARPS>, grid, block, 0, st, p);
 }
 
 // Words of 16 bytes where rows allow it, else of 4 (16-bit rows of an even
@@ -579,13 +588,21 @@ cudaError_t launch_words(int word, nsk::RowParams& p, int nsm, cudaStream_t st) 
       if (word == 4) return narrow(std::integral_constant<int, 2>());
     return narrow(std::integral_constant<int, 1>());
   } else if constexpr (OP == COMBINE_GRAD) {
+    // few tokens of long rows: more than the 4 warps of a block for each (13 x 8 rows of 3761 fp16 take 6.1 us
+    // against 12.3, 7 x 8 of 6399 fp32 9.2 against 19; blocks this large cost 8 % where the tokens are many)
+    const bool few = p.tokens < 4 * nsm;
     if (word == 16) {
+      if (few && longer(V, 16)) return launch_rows<OP, T, V, 4, 1, nsk::MANY_WARPS>(p, nsm, st);
       if (longer(V, 2)) return launch_rows<OP, T, V, 4, 1>(p, nsm, st);
       if (longer(V, 1)) return launch_rows<OP, T, V, 2, 1>(p, nsm, st);
       return launch_rows<OP, T, V, 1, 2>(p, nsm, st);
     }
     const auto narrow = [&](auto v) {
       constexpr int W = decltype(v)::value;
+      if (few && longer(W, 32)) return launch_rows<OP, T, W, 8, 2, nsk::MANY_WARPS>(p, nsm, st);
+      // one or two slots leave registers for more of the row: 6000 x 1 rows of 5527 bf16 in 48 us against 70, x 2 in 74
+      // against 91; of 5526 38 against 47, x 2 in 60 against 63
+      if (p.k <= 2 && longer(W, 15)) return launch_rows<OP, T, W, 16, 1>(p, nsm, st);
       if (longer(W, 4)) return launch_rows<OP, T, W, 8, 2>(p, nsm, st);
       if (longer(W, 2)) return launch_rows<OP, T, W, 4, 2>(p, nsm, st);
       return launch_rows<OP, T, W, 2, 2>(p, nsm, st);

@@ -248,6 +248,14 @@ def test_rows_of_few_words(D, dtype, k):
     ops.test_dispatch_and_gradient(41, k, 6, D, 4, 0, 0, 0, dtype)
 
 
+# Few tokens whose rows many warps share, and one or two slots of long rows.
+@pytest.mark.parametrize("T,k,D", [(13, 8, 3761), (7, 3, 6402), (1, 8, 4104), (3, 32, 5001), (9, 2, 8192), (650, 1, 1001), (650, 2, 1002), (650, 2, 483)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("align", [1, 16])
+def test_gradients_of_long_rows(T, k, D, dtype, align):
+    ops.test_combine_and_gradient(T, k, 6, D, align, 0, 0, 0, dtype)
+
+
 FIRST_CALLS = {  # dynamic shared memory just below 48 KB, which the static part takes past it
     "distill": "V, K = 192289, 32\n"
                "x, z, ids = torch.randn(2, V, device='cuda').half(), torch.randn(2, K, device='cuda'), torch.zeros(2, K, dtype=torch.int64, device='cuda')\n"
