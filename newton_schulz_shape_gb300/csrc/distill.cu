@@ -76,24 +76,25 @@ struct Online {
 };
 
 // Places of the hash table of `top` ids: a power of two, four times the ids or
-// more, which keeps searches at one or two places.
+// more, which keeps searches at one or two places, and twice that where it is
+// small.
 __host__ __device__ inline int table_size(int top) {
   int n = 4;
-  while (n < 4 * top) n *= 2;
+  while (n < (top <= 128 ? 8 : 4) * top) n *= 2;
   return n;
 }
 
 // The teacher's entries of a token, in shared memory.
 struct Teacher {
+  int* table;  // hash table of the ids; bit 31 marks one that is named more than once
   float* p;    // [top] probability
   float* s;    // [top] the student's logit at the entry
   int* id;     // [top] the entry, -1 if left out
-  int* table;  // hash table of the ids; bit 31 marks one that is named more than once
   float* sums; // [2] sum of the probabilities, sum of p (log p - s / tau)
   int* any;    // whether an entry is left
   __device__ __forceinline__ Teacher(void* at, int top, int places)
-      : p(static_cast<float*>(at)), s(p + top), id(reinterpret_cast<int*>(s + top)), table(id + top),
-        sums(reinterpret_cast<float*>(table + places)), any(reinterpret_cast<int*>(sums + 2)) {}
+      : table(static_cast<int*>(at)), p(reinterpret_cast<float*>(table + places)), s(p + top),
+        id(reinterpret_cast<int*>(s + top)), sums(reinterpret_cast<float*>(id + top)), any(reinterpret_cast<int*>(sums + 2)) {}
 };
 size_t teacher_bytes(int top) { return sizeof(float) * (3 * static_cast<size_t>(top) + table_size(top) + 4); }
 
@@ -160,7 +161,7 @@ __device__ __forceinline__ bool load_teacher(const DistillParams& p, const Teach
 // them apart to the block's barriers, where the first to arrive counted for
 // all.
 __device__ __forceinline__ void mark_repeated(const Teacher& te, int top, int mask, int lane) {
-  for (int i = lane; i <= mask; i += 32) te.table[i] = NO_ID;
+  for (int i = lane; i <= mask / 4; i += 32) reinterpret_cast<int4*>(te.table)[i] = make_int4(NO_ID, NO_ID, NO_ID, NO_ID);
   __syncwarp();
   for (int j0 = 0; j0 < top; j0 += 32) {
     const int id = j0 + lane < top ? te.id[j0 + lane] : -1;
