@@ -44,7 +44,9 @@ constexpr int SORT_HELD = 4;  // rounds of 32 slots that a warp keeps in registe
 constexpr int SORT_MAX_BLOCKS = 256;
 constexpr int ROW_THREADS = 128;
 constexpr int MANY_WARPS = 16;  // of a block where many share a token
-constexpr int CLEAR_ROWS = 4;  // twice as many where they are short (28351 x 2 rows of 128 dispatched in 10.5 us against 12.5)
+// Rows that a warp clears; twice as many where they are short (28351 x 2 rows of 128
+// dispatched in 10.5 us against 12.5).
+constexpr int CLEAR_ROWS = 4;
 
 // Counts of a block, a whole number of 16-byte words.
 __host__ __device__ inline int count_stride(int experts) { return (experts + 3) / 4 * 4; }
@@ -116,7 +118,10 @@ __global__ void __launch_bounds__(SORT_THREADS) ns_moe_place_kernel(const __grid
   int held[SORT_HELD], rank[SORT_HELD];
   if (HELD) {
 #pragma unroll
-    for (int i = 0; i < SORT_HELD; ++i) held[i] = w0 + i * 32 + lane < w1 ? slot_expert(p, w0 + i * 32 + lane, &refused) : -1;
+    for (int i = 0; i < SORT_HELD; ++i) {
+      const int s = w0 + i * 32 + lane;
+      held[i] = s < w1 ? slot_expert(p, s, &refused) : -1;
+    }
   }
   __syncthreads();
   // rank of a slot among this warp's of its expert so far, counted on top of
@@ -313,7 +318,8 @@ __global__ void __launch_bounds__(ROW_THREADS) ns_moe_dispatch_kernel(const __gr
     return;
   }
   const long long t = w / p.parts;
-  const int start = static_cast<int>(w - t * p.parts) * (32 * V * U), c0 = start + lane * V, dim = static_cast<int>(p.dim);
+  const int start = static_cast<int>(w - t * p.parts) * (32 * V * U), c0 = start + lane * V;
+  const int dim = static_cast<int>(p.dim);
   const T* src = static_cast<const T*>(p.src) + t * p.src_ld + c0;
   const int mine = lane_row(p, t, lane);
   // `whole`: the piece ends inside the row, and needs no check of its columns
@@ -347,7 +353,8 @@ __global__ void __launch_bounds__(ROW_THREADS) ns_moe_gather_kernel(const __grid
   const long long w = static_cast<long long>(blockIdx.x) * (ROW_THREADS / 32) + (threadIdx.x >> 5);
   if (w >= p.token_warps) return;
   const long long t = w / p.parts;
-  const int start = static_cast<int>(w - t * p.parts) * (32 * V * U), c0 = start + lane * V, dim = static_cast<int>(p.dim);
+  const int start = static_cast<int>(w - t * p.parts) * (32 * V * U), c0 = start + lane * V;
+  const int dim = static_cast<int>(p.dim);
   const int mine = lane_row(p, t, lane);
   const float my_weight = p.weights && lane < p.k ? p.weights[t * p.k + lane] : 1.0f;
   auto piece = [&](auto whole) {
@@ -367,7 +374,8 @@ __global__ void __launch_bounds__(ROW_THREADS) ns_moe_gather_kernel(const __grid
         if (r >= 0) {
 #pragma unroll
           for (int u = 0; u < U; ++u)
-            x[j][u] = decltype(whole)::value || c0 + u * 32 * V < dim ? load_vec<T, V>(src + u * 32 * V) : zero_vec<T, V>();
+            x[j][u] =
+                decltype(whole)::value || c0 + u * 32 * V < dim ? load_vec<T, V>(src + u * 32 * V) : zero_vec<T, V>();
         } else {
           wt[j] = 0.0f;
 #pragma unroll
@@ -414,7 +422,8 @@ __global__ void __launch_bounds__(32 * WARPS) ns_moe_combine_grad_kernel(const _
       float g[U][V];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const Vec<T, V> x = decltype(whole)::value || c0 + u * 32 * V < dim ? load_vec<T, V>(dy + c0 + u * 32 * V) : zero_vec<T, V>();
+        const Vec<T, V> x =
+            decltype(whole)::value || c0 + u * 32 * V < dim ? load_vec<T, V>(dy + c0 + u * 32 * V) : zero_vec<T, V>();
 #pragma unroll
         for (int i = 0; i < V; ++i) g[u][i] = get(x, i);
       }

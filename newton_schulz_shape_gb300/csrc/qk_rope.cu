@@ -398,12 +398,14 @@ __global__ void __launch_bounds__(QK_THREADS, qk_blocks(GRAD, MODE)) ns_qk_kerne
   nsptx::griddep_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   uint4* ring = ring_smem + warp * (STAGES * STAGE) + lane;
-  const int group_size = G ? G : p.lanes, H = 32 / group_size, group = lane / group_size, i_lane = lane - group * group_size;
+  const int group_size = G ? G : p.lanes, H = 32 / group_size;
+  const int group = lane / group_size, i_lane = lane - group * group_size;
   const bool takes = group < H;  // a lane left over takes no head
   Lane<T> l = lane_of<T, MODE>(p, i_lane);
   if (!takes) l.on_a = l.on_b = l.turn_a = l.turn_b = false;
   // SPREAD: the group's head, of dim + 2 places
-  float* head = reinterpret_cast<float*>(ring_smem + QK_WARPS * STAGES * STAGE) + warp * spread_places(Lane<T>::V) + min(group, H - 1) * (p.dim + 2);
+  float* head = reinterpret_cast<float*>(ring_smem + QK_WARPS * STAGES * STAGE) + warp * spread_places(Lane<T>::V) +
+                min(group, H - 1) * (p.dim + 2);
   const float inv_dim = 1.0f / p.dim;
   const int warps = gridDim.x * QK_WARPS, me = blockIdx.x * QK_WARPS + warp;
   int chunk = me;  // this warp's next, in those of the queries and then of the keys
@@ -724,8 +726,8 @@ int run_qk(bool grad, const void* const* x, const void* const* dy, void* const* 
            void* stream) {
   if (!nsk::dtype_ok(dtype)) return NS_ERR_ARG;
   if (weight_dtype != dtype && weight_dtype != NS_DT_FP32) return NS_ERR_ARG;
-  if (tokens < 0 || heads[0] < 0 || heads[1] < 0 || head_dim < 1 || rot_dim < 0 || table_rows < 0 || !(eps >= 0.0f) || !strides)
-    return NS_ERR_ARG;
+  if (tokens < 0 || heads[0] < 0 || heads[1] < 0 || head_dim < 1 || rot_dim < 0 || table_rows < 0) return NS_ERR_ARG;
+  if (!(eps >= 0.0f) || !strides) return NS_ERR_ARG;
   if (rot_dim > head_dim || rot_dim % 2) return NS_ERR_SHAPE;
   if (head_dim > nsk::QK_MAX_DIM) return NS_ERR_UNSUPPORTED;
   if (interleaved != 0 && interleaved != 1) return NS_ERR_ARG;
@@ -760,13 +762,16 @@ int run_qk(bool grad, const void* const* x, const void* const* dy, void* const* 
     s.dy = grad ? dy[i] : nullptr;
     s.weight = weight[i];
     s.heads = heads[i];
-    s.x_token = strides[2 * i];
-    s.x_head = strides[2 * i + 1];
-    s.out_token = strides[4 + 2 * i];
-    s.out_head = strides[5 + 2 * i];
+    // the stride of one token, or of one head, reaches nothing
+    auto token_stride = [&](int k) { return tokens > 1 ? strides[k] : 0; };
+    auto head_stride = [&](int k) { return heads[i] > 1 ? strides[k] : 0; };
+    s.x_token = token_stride(2 * i);
+    s.x_head = head_stride(2 * i + 1);
+    s.out_token = token_stride(4 + 2 * i);
+    s.out_head = head_stride(5 + 2 * i);
     if (grad) {
-      s.dy_token = strides[8 + 2 * i];
-      s.dy_head = strides[9 + 2 * i];
+      s.dy_token = token_stride(8 + 2 * i);
+      s.dy_head = head_stride(9 + 2 * i);
     }
     const int64_t token[3] = {s.x_token, s.dy_token, s.out_token}, head[3] = {s.x_head, s.dy_head, s.out_head};
     for (int k = 0; k < 3; ++k) {
@@ -776,8 +781,8 @@ int run_qk(bool grad, const void* const* x, const void* const* dy, void* const* 
       s.head_bytes[k] = fits ? static_cast<int>(head[k]) * b : 0;
     }
     if (heads[i] == 0) continue;
-    lanes = lanes && (reinterpret_cast<uintptr_t>(s.weight) & 15) == 0 && words_ok(s.x, s.x_token, s.x_head, b) && words_ok(s.out, s.out_token, s.out_head, b) &&
-            (!grad || words_ok(s.dy, s.dy_token, s.dy_head, b));
+    lanes = lanes && (reinterpret_cast<uintptr_t>(s.weight) & 15) == 0 && words_ok(s.x, s.x_token, s.x_head, b) &&
+            words_ok(s.out, s.out_token, s.out_head, b) && (!grad || words_ok(s.dy, s.dy_token, s.dy_head, b));
   }
   p.tokens = tokens;
   p.dim = head_dim;

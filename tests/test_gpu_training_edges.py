@@ -276,6 +276,20 @@ def test_first_call_of_a_process_near_the_shared_memory_limit(name):
     assert run.returncode == 0, run.stderr[-2000:]
 
 
+def test_strides_of_one_token_and_one_head_reach_nothing():
+    g = gen(12)
+    for shape, odd in (((1, 5, 64), (331, 64, 1)), ((7, 1, 64), (64, 99, 1))):
+        q, k = randn(g, *shape, dtype=torch.bfloat16), randn(g, *shape, dtype=torch.bfloat16)
+        qs, ks, qo, ko = (torch.empty_strided(shape, odd, dtype=torch.bfloat16, device=DEV) for _ in range(4))
+        qs.copy_(q)
+        ks.copy_(k)
+        want_q, want_k = torch.empty_like(q), torch.empty_like(k)
+        nsg.ns_qk_norm_rope(q, k, want_q, want_k)
+        nsg.ns_qk_norm_rope(qs, ks, qo, ko)
+        assert torch.equal(qo, want_q) and torch.equal(ko, want_k)
+    ok()
+
+
 def test_launch_counts():
     nsg.ns_profile_read_training(reset=True)
     x = torch.ones(4, 2, 64, device=DEV)
