@@ -370,6 +370,7 @@ __global__ void __launch_bounds__(NT + 32) ns_distill_kernel(const __grid_consta
       if (any) teacher_probabilities(p, te, t, lane);
     }
     if (lane == 0) *te.any = any;
+    __syncwarp();
     if (joins) {
       nsptx::cluster_wait();
       nsptx::cluster_sync_all();
@@ -523,6 +524,7 @@ __global__ void __launch_bounds__(NT + 32) ns_distill_kernel(const __grid_consta
   for (; u + B <= full; u += B) give(u, std::true_type());
   for (; u < rounds; u += B) give(u, std::false_type());
   if (has_edge) grad[edge] = from_float<T>(mass * exp2_fast(fmaf(ex, c, -lse2)));
+  __syncwarp();  // lanes leave the last round of words one by one
   __syncthreads();
 }
 

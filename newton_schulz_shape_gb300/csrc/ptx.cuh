@@ -199,10 +199,13 @@ __device__ __forceinline__ uint32_t cluster_count_x() {
 }
 // The barrier below in two halves, without ordering of memory: after the wait,
 // every CTA of the cluster has started (its shared memory may be written).
+// As in all of these, a warp's lanes have to come to it together.
 __device__ __forceinline__ void cluster_arrive_relaxed() {
+  __syncwarp();
   asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
 }
 __device__ __forceinline__ void cluster_wait() {
+  __syncwarp();
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 // Whole-cluster barrier (every thread of every CTA, warps converged).
