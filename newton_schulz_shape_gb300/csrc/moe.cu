@@ -107,9 +107,8 @@ __global__ void __launch_bounds__(SORT_THREADS) ns_moe_place_kernel(const __grid
   int* total = before + E;              // [E]
   int* offset = total + E;              // [E + 1]
   for (int i = threadIdx.x; i < (SORT_WARPS + 2) * E; i += SORT_THREADS) sm[i] = 0;
-  // after ns_moe_count_kernel, which starts this one only once all before it has
-  // completed, the ids can be read while it still counts
-  if (p.blocks == 1) nsptx::griddep_wait();
+  nsptx::griddep_wait();
+  nsptx::griddep_launch_dependents();
 
   const int per_warp = p.chunk / SORT_WARPS;
   const int w0 = min(p.slots, static_cast<int>(blockIdx.x) * p.chunk + warp * per_warp);
@@ -145,8 +144,6 @@ __global__ void __launch_bounds__(SORT_THREADS) ns_moe_place_kernel(const __grid
       if (e >= 0) atomicAdd(&next[warp * E + e], 1);
     }
   }
-  if (p.blocks > 1) nsptx::griddep_wait();
-  nsptx::griddep_launch_dependents();
   if (refused) atomicOr(p.status, NS_DEV_BAD_INDEX);
   if (p.blocks > 1) {
     // four experts a thread; the threads that share them split the blocks

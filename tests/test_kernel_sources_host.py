@@ -46,3 +46,26 @@ def test_warps_are_together_at_the_barriers_of_the_distillation_kernel():
     text = without_comments((CSRC / "distill.cu").read_text())
     assert re.search(r"if \(lane == 0\) \*te\.any = any;\s*__syncwarp\(\);", text)
     assert re.search(r"if \(has_edge\) grad\[edge\] = from_float<T>\(mass[^\n]*\s*__syncwarp\(\);\s*__syncthreads\(\);", text)
+
+
+# A kernel that starts while its predecessor runs may touch no data before its
+# wait, which alone promises that what earlier kernels wrote is seen.
+KERNELS = {name: body for f in ("moe.cu", "qk_rope.cu", "distill.cu")
+           for name, body in bodies(without_comments((CSRC / f).read_text()), r"__global__ void __launch_bounds__\(.*\) (\w+)\(const __grid_constant__")}
+DATA = r"slot_expert|load_index|load_teacher|few_entries|table_row|lane_row|lane_weights|cp_async16|load_vec|atomicOr\(p\.status" \
+       r"|p\.(ids|block_counts|row_of_slot|slot_of_row|src|rows_in|weights|side|positions|partial|logits|teacher|lse)\b"
+
+
+def test_the_kernels_are_found():
+    assert len(KERNELS) == 10
+
+
+@pytest.mark.parametrize("name", KERNELS)
+def test_no_data_before_the_wait(name):
+    body = KERNELS[name]
+    waits = [m.start() for m in re.finditer(r"griddep_wait\(\);", body)]
+    assert len(waits) == 1
+    line = body[:waits[0]].rsplit("\n", 1)[1]
+    assert line.strip() == "nsptx::"                       # on no condition
+    assert not re.search(DATA, body[:waits[0]])
+    assert body.index("griddep_launch_dependents") > waits[0]
