@@ -5,7 +5,7 @@
 // R over the first `rot_dim` of them:
 //   r = (mean(x^2) + eps)^(-1/2),  y = R_pos (x r g)
 // and backward, with u = R_pos^T dy and h = u g:
-//   dx = r (h - x r^2 mean(h x)),  dg = sum over tokens and heads of u x r.
+//   dx = r (h - n mean(h n)), n = x r,  dg = sum over tokens and heads of u n.
 // The rotation turns pairs (a, b) -> (a c - b s, b c + a s); the pairs are
 // (i, i + rot_dim / 2), or (2i, 2i + 1) when interleaved.
 //
@@ -461,7 +461,7 @@ __global__ void __launch_bounds__(QK_THREADS, qk_blocks(GRAD, MODE)) ns_qk_kerne
         copy(r + QK_AHEAD < n);
         nsptx::cp_async_wait<QK_AHEAD>();
         bool live = takes && at.t < p.tokens;  // of a whole group of lanes; the others' values go nowhere
-        const Two<T> xf = unpack<T>(ring + take);
+        Two<T> xf = unpack<T>(ring + take);
         Two<T> u;
         if (GRAD) u = unpack<T>(ring + take + 64);
         take = take + STAGE == STAGES * STAGE ? 0 : take + STAGE;
@@ -495,11 +495,17 @@ __global__ void __launch_bounds__(QK_THREADS, qk_blocks(GRAD, MODE)) ns_qk_kerne
             turn_spread<T>(p, l, spread, u, head);
           else
             turn<T, MODE>(p, l, angles, u, -1.0f);
+          // from here on x stands for n = x r: r^2 and r^3 leave fp32's range long before the results do
+#pragma unroll
+          for (int i = 0; i < N; ++i) {
+            xf.a[i] = mul2(xf.a[i], r2);
+            xf.b[i] = mul2(xf.b[i], r2);
+          }
           if (live) {
 #pragma unroll
             for (int i = 0; i < N; ++i) {
-              dg.a[i] = fma2(u.a[i], mul2(xf.a[i], r2), dg.a[i]);
-              dg.b[i] = fma2(u.b[i], mul2(xf.b[i], r2), dg.b[i]);
+              dg.a[i] = fma2(u.a[i], xf.a[i], dg.a[i]);
+              dg.b[i] = fma2(u.b[i], xf.b[i], dg.b[i]);
             }
           }
           float2 d2 = make_float2(0.0f, 0.0f);
@@ -510,7 +516,7 @@ __global__ void __launch_bounds__(QK_THREADS, qk_blocks(GRAD, MODE)) ns_qk_kerne
             d2 = fma2(u.a[i], xf.a[i], d2);
             d2 = fma2(u.b[i], xf.b[i], d2);
           }
-          const float m = -r_norm * r_norm * r_norm * (group_sum<G>(d2.x + d2.y, group_size, i_lane) * inv_dim);
+          const float m = -r_norm * (group_sum<G>(d2.x + d2.y, group_size, i_lane) * inv_dim);
           const float2 m2 = make_float2(m, m);
 #pragma unroll
           for (int i = 0; i < N; ++i) {
@@ -612,11 +618,12 @@ __global__ void __launch_bounds__(QK_ANY_THREADS) ns_qk_any_kernel(const __grid_
             u = u * c - to_float(dy[o]) * s;
           }
           us[d] = u;
-          dot = fmaf(u * weight_at<T>(p, side.weight, d), xs[d], dot);
-          dg[d] = fmaf(u, xs[d] * r, dg[d]);
+          const float n = xs[d] * r;
+          xs[d] = n;
+          dot = fmaf(u * weight_at<T>(p, side.weight, d), n, dot);
+          dg[d] = fmaf(u, n, dg[d]);
         }
-        dot = warp_sum(dot);
-        const float m = r * r * (dot / D);
+        const float m = warp_sum(dot) / D;
         __syncwarp();  // dx may take the place of dy
         for (int d = lane; d < D; d += 32)
           out[d] = from_float<T>(r * (us[d] * weight_at<T>(p, side.weight, d) - xs[d] * m));
