@@ -483,8 +483,8 @@ __global__ void __launch_bounds__(QK_THREADS, qk_blocks(GRAD, MODE)) ns_qk_kerne
         if (!GRAD) {
 #pragma unroll
           for (int i = 0; i < N; ++i) {
-            u.a[i] = mul2(xf.a[i], mul2(g.a[i], r2));
-            u.b[i] = mul2(xf.b[i], mul2(g.b[i], r2));
+            u.a[i] = mul2(mul2(xf.a[i], r2), g.a[i]);
+            u.b[i] = mul2(mul2(xf.b[i], r2), g.b[i]);
           }
           if (MODE == SPREAD)
             turn_spread<T>(p, l, spread, u, head);

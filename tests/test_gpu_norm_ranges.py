@@ -50,3 +50,27 @@ def test_gradient(scale, eps, D, rot, interleaved, offset, dtype):
         want, want_w = ot.norm_rope_grad(dyv, xv, wv, *at)
         near(dx, want, 2 * c * (r * h + np.abs(xv) * r ** 3 * (h * np.abs(xv)).mean(-1, keepdims=True)), dtype)
         near(dw, want_w, ((T * x.shape[1] + 2) * u + c) * (ua * np.abs(xv) * r).sum((0, 1)), torch.float32)
+
+
+# Scale of x, eps, scale of the weights: their product with r alone has no value in fp32.
+WEIGHTS = [(1e15, 1e-6, 1e-28), (2e17, 1e-6, 1e-25), (1e-18, 0.0, 1e22)]
+
+
+@pytest.mark.parametrize("scale,eps,weight", WEIGHTS)
+@pytest.mark.parametrize("D,rot,interleaved,offset", FORMS)
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_forward(scale, eps, weight, D, rot, interleaved, offset, dtype):
+    g = gen(D + rot)
+    T, H, K = 21, 4, 2
+    q, k = heads(g, T, H, D, scale, dtype, offset), heads(g, T, K, D, scale, dtype, offset)
+    qw, kw = (randn(g, D) * weight).to(dtype), (randn(g, D) * weight).to(dtype)
+    table = rotation_table(T, rot)
+    qo, ko = torch.full_like(q, 7), torch.full_like(k, 7)
+    nsg.ns_qk_norm_rope(q, k, qo, ko, qw, kw, table, eps=eps, interleaved=interleaved)
+    assert status() == nsg.NS_OK
+    at = (f64(table), np.arange(T), rot, eps, interleaved)
+    R = np.abs(ot._rotation(at[0], at[1], rot, D, interleaved))
+    for x, y, w in ((q, qo, qw), (k, ko, kw)):
+        xv, wv = f64(x), f64(w)
+        r = 1 / np.sqrt((xv * xv).mean(-1, keepdims=True) + eps)
+        near(y, ot.norm_rope(xv, wv, *at), (D + 16) * u * np.einsum("tab,thb->tha", R, np.abs(xv * r * wv)), dtype)
