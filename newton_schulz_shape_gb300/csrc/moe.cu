@@ -525,6 +525,11 @@ int sort_args(int64_t tokens, int k, int experts) {
   return NS_OK;
 }
 
+// Dynamic shared memory of ns_moe_place_kernel.
+constexpr size_t place_smem(int experts) {
+  return (static_cast<size_t>(nsk::SORT_WARPS + 3) * experts + 1) * sizeof(int);
+}
+
 // Checks shared by the four row operators.
 int row_args(int dtype, int64_t tokens, int k, int64_t dim, int64_t rows) {
   if (!dtype_ok(dtype) || tokens < 0 || k < 1 || dim < 0 || rows < 0) return NS_ERR_ARG;
@@ -710,11 +715,13 @@ int ns_moe_sort(const void* expert_ids, int id_bytes, int64_t tokens, int k, int
     });
     if (e != cudaSuccess) return NS_ERR_CUDA;
   }
-  const size_t smem = (static_cast<size_t>(nsk::SORT_WARPS + 3) * experts + 1) * sizeof(int);
+  const size_t smem = place_smem(experts);
   void (*const place)(nsk::SortParams) = p.chunk <= nsk::SORT_THREADS * nsk::SORT_HELD ? nsk::ns_moe_place_kernel<true>
                                                                                       : nsk::ns_moe_place_kernel<false>;
+  // the same limit in every call: a smaller one that another thread sets before this launch would refuse it
   if (smem > nsk::SMEM_WITHOUT_ASKING &&
-      cudaFuncSetAttribute(place, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
+      cudaFuncSetAttribute(place, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           static_cast<int>(place_smem(nsk::MAX_EXPERTS))) != cudaSuccess)
     return NS_ERR_CUDA;
   const cudaError_t e = counted(K_MOE, st, [&] {
     return nsk::launch_pdl(place, dim3(p.blocks), dim3(nsk::SORT_THREADS), smem, st, p);
