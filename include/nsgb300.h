@@ -435,7 +435,8 @@ int ns_qk_norm_rope_grad(const void* grad_q_out, const void* grad_k_out, const v
  * are left out; an id >= vocab is refused and left out. A token whose weight is
  * 0 or that has no entry left gets loss 0, lse 0 and a zero gradient, whatever
  * its logits hold. grad_logits may be logits itself, with the same stride.
- * top <= 1024, temperature in [1e-30, 1e30]. Any other row needs a finite logit: one of -inf gives NaN. */
+ * top <= 1024, temperature in [1e-30, 1e30]. Any other row needs a finite logit, of whatever size: one of -inf
+ * gives NaN. Where s / temperature leaves fp32's range lse is infinite; loss and grad_logits are not affected. */
 int ns_distill_loss(const void* logits, int64_t logits_stride, int dtype, int64_t tokens, int64_t vocab,
                     const void* teacher_values, int teacher_dtype, const void* teacher_ids, int id_bytes, int top,
                     const float* weights, const float* teacher_lse, float temperature, float* loss, float* lse,

@@ -12,7 +12,13 @@
 // or that has no entry left has loss 0, lse 0 and a zero gradient, whatever its
 // logits hold (NaN included); those of a weight of 0 need not be read.
 // The maximum, the sums and the logarithm are in fp32; a gradient value is
-// rounded once, when it is stored.
+// rounded once, when it is stored. The maximum m of the logits is kept as it is
+// and subtracted before anything is scaled: exp(s / tau - lse) is
+// 2^((s - m) c - l) with c = log2(e) / tau and l the log2 of the sum of
+// 2^((s - m) c), and the loss is taken from the largest logit s0 at the entries:
+// sum_j p_j (log p_j + (s0 - s_{i_j}) / tau) + P ((m - s0) / tau + l ln 2).
+// So finite logits of any size, the type's lowest among them, and rows far from
+// zero lose nothing.
 #include <algorithm>
 #include <climits>
 
@@ -44,7 +50,7 @@ struct DistillParams {
   int id_bytes, top;
   const float* weights;      // null: 1
   const float* teacher_lse;  // null: over the top entries
-  float inv_tau;
+  float tau, inv_tau;
   float* loss;          // null: the log-sum-exp is given
   float* lse;
   int places;           // of the hash table of the teacher's ids
@@ -64,16 +70,24 @@ __device__ __forceinline__ float exp2_fast(float x) {
 // Maximum and sum of exp2((x - max) c) of what was seen so far.
 struct Online {
   float m = -INFINITY, s = 0.0f;
-  __device__ __forceinline__ void join(float m2, float s2) {
+  __device__ __forceinline__ void join(float m2, float s2, float c) {
     const float n = fmaxf(m, m2);
     if (n == -INFINITY) {
       s += s2;  // 0, or NaN
       return;
     }
-    s = s * exp2_fast(m - n) + s2 * exp2_fast(m2 - n);
+    s = s * exp2_fast((m - n) * c) + s2 * exp2_fast((m2 - n) * c);
     m = n;
   }
 };
+
+// What a logit x is compared with: exp(x / tau - lse) = exp2((x - m) c - l).
+struct RowSum {
+  float m, l;
+  __device__ __forceinline__ float power(float x, float c) const { return exp2_fast(fmaf(x - m, c, -l)); }
+};
+// From a log-sum-exp that was given.
+__device__ __forceinline__ RowSum given_sum(const DistillParams& p, long long t) { return {p.lse[t] * p.tau, 0.0f}; }
 
 // Places of the hash table of `top` ids: a power of two, four times the ids or
 // more, which keeps searches at one or two places, and twice that where it is
@@ -90,11 +104,11 @@ struct Teacher {
   float* p;    // [top] probability
   float* s;    // [top] the student's logit at the entry
   int* id;     // [top] the entry, -1 if left out
-  float* sums; // [2] sum of the probabilities, sum of p (log p - s / tau)
+  float* sums; // [3] sum of the probabilities, sum of p (log p - (s - s0) / tau), s0
   int* any;    // whether an entry is left
   __device__ __forceinline__ Teacher(void* at, int top, int places)
       : table(static_cast<int*>(at)), p(reinterpret_cast<float*>(table + places)), s(p + top),
-        id(reinterpret_cast<int*>(s + top)), sums(reinterpret_cast<float*>(id + top)), any(reinterpret_cast<int*>(sums + 2)) {}
+        id(reinterpret_cast<int*>(s + top)), sums(reinterpret_cast<float*>(id + top)), any(reinterpret_cast<int*>(sums + 3)) {}
 };
 size_t teacher_bytes(int top) { return sizeof(float) * (3 * static_cast<size_t>(top) + table_size(top) + 4); }
 
@@ -181,6 +195,14 @@ __device__ __forceinline__ void mark_repeated(const Teacher& te, int top, int ma
   __syncwarp();
 }
 
+// What the student's logits at the entries are measured from: the largest of
+// all lanes' s0, or 0 where none is finite.
+__device__ __forceinline__ float origin(float s0) {
+  float m;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(s0));
+  return m > -INFINITY ? m : 0.0f;
+}
+
 // Probabilities and their sums, by one warp; visible to the block after its
 // next barrier.
 __device__ __forceinline__ void teacher_probabilities(const DistillParams& p, const Teacher& te, long long t, int lane) {
@@ -197,19 +219,27 @@ __device__ __forceinline__ void teacher_probabilities(const DistillParams& p, co
     for (int j = lane; j < p.top; j += 32) sum += te.id[j] >= 0 ? expf((te.p[j] - z0) * p.inv_tau) : 0.0f;
     zlog = logf(warp_sum(sum));
   }
-  float mass = 0.0f, part = 0.0f;
+  float mass = 0.0f, part = 0.0f, s0 = -INFINITY;
   for (int j = lane; j < p.top; j += 32) {
     const float logp = (te.p[j] - z0) * p.inv_tau - zlog;
     const float pr = te.id[j] >= 0 ? expf(logp) : 0.0f;
-    if (pr != 0.0f) part += pr * (logp - te.s[j] * p.inv_tau);
+    if (pr != 0.0f) {
+      part += pr * logp;
+      s0 = fmaxf(s0, te.s[j]);
+    }
     mass += pr;
     te.p[j] = pr;
   }
+  s0 = origin(s0);
+  float apart = 0.0f;
+  for (int j = lane; j < p.top; j += 32)
+    if (te.p[j] != 0.0f) apart += te.p[j] * (s0 - te.s[j]);
   mass = warp_sum(mass);
-  part = warp_sum(part);
+  part = warp_sum(fmaf(apart, p.inv_tau, part));
   if (lane == 0) {
     te.sums[0] = mass;
     te.sums[1] = part;
+    te.sums[2] = s0;
   }
 }
 
@@ -251,12 +281,17 @@ __device__ __forceinline__ bool few_entries(const DistillParams& p, const Teache
   }
   sum = warp_sum(sum);
   const float inv = p.teacher_lse ? 1.0f : 1.0f / sum, zlog = p.teacher_lse ? 0.0f : logf(sum);
-  float mass = 0.0f, part = 0.0f;
+  float mass = 0.0f, part = 0.0f, s0 = -INFINITY;
+#pragma unroll
+  for (int b = 0; b < FEW; ++b) {
+    pr[b] *= inv;
+    if (pr[b] != 0.0f) s0 = fmaxf(s0, s[b]);
+  }
+  s0 = origin(s0);
 #pragma unroll
   for (int b = 0; b < FEW; ++b) {
     const int j = lane + 32 * b;
-    pr[b] *= inv;
-    if (pr[b] != 0.0f) part += pr[b] * (z[b] - zlog - s[b] * p.inv_tau);
+    if (pr[b] != 0.0f) part += pr[b] * fmaf(s0 - s[b], p.inv_tau, z[b] - zlog);
     mass += pr[b];
     if (j < p.top) {
       te.id[j] = static_cast<int>(id[b]);
@@ -269,8 +304,17 @@ __device__ __forceinline__ bool few_entries(const DistillParams& p, const Teache
   if (lane == 0) {
     te.sums[0] = mass;
     te.sums[1] = part;
+    te.sums[2] = s0;
   }
   return true;
+}
+
+// The loss of a token and its log-sum-exp.
+__device__ __forceinline__ void write_loss(const DistillParams& p, const Teacher& te, long long t, float weight,
+                                           const RowSum& r) {
+  const float log_sum = r.l * LN2;
+  p.loss[t] = weight * (te.sums[1] + te.sums[0] * fmaf(r.m - te.sums[2], p.inv_tau, log_sum));
+  p.lse[t] = fmaf(r.m, p.inv_tau, log_sum);
 }
 
 // The elements of a row that a block writes: its words, and for one block those
@@ -288,7 +332,7 @@ struct Slice {
 // that names it; once the rest of the slice is written.
 template <typename T>
 __device__ __forceinline__ void write_entries(const DistillParams& p, const Teacher& te, const Slice& slice, T* grad,
-                                              float c, float lse2, float scale, int start, int n) {
+                                              float c, const RowSum& r, float scale, int start, int n) {
   const int mask = p.places - 1;
   for (int j = start; j < p.top; j += n) {
     const int id = te.id[j];
@@ -300,27 +344,27 @@ __device__ __forceinline__ void write_entries(const DistillParams& p, const Teac
       sum = 0.0f;
       for (int i = 0; i < p.top; ++i) sum += te.id[i] == id ? te.p[i] : 0.0f;
     }
-    grad[id] = from_float<T>(scale * te.sums[0] * exp2_fast(fmaf(te.s[j], c, -lse2)) - scale * sum);
+    grad[id] = from_float<T>(scale * te.sums[0] * r.power(te.s[j], c) - scale * sum);
   }
 }
 
 // The maximum and sum of a warp's threads, in all of them.
-__device__ __forceinline__ Online join_warp(Online o) {
+__device__ __forceinline__ Online join_warp(Online o, float c) {
   // one rescaling to the warp's maximum, then plain sums
   const float m = warp_max(o.m);
-  o.s = m == -INFINITY ? o.s : o.s * exp2_fast(o.m - m);
+  o.s = m == -INFINITY ? o.s : o.s * exp2_fast((o.m - m) * c);
   o.m = m;
   o.s = warp_sum(o.s);
   return o;
 }
 
-// log2 of the sum over all parts of a token, in every lane.
+// The sum over all parts of a token, in every lane.
 template <int WARPS>
-__device__ __forceinline__ float join_parts(const float2* parts, int C, int lane) {
+__device__ __forceinline__ RowSum join_parts(const float2* parts, int C, int lane, float c) {
   Online o;
-  for (int i = lane; i < C * WARPS; i += 32) o.join(parts[i].x, parts[i].y);
-  o = join_warp(o);
-  return o.m + log2f(o.s);
+  for (int i = lane; i < C * WARPS; i += 32) o.join(parts[i].x, parts[i].y, c);
+  o = join_warp(o, c);
+  return {o.m, log2f(o.s)};
 }
 
 // A cluster of blocks takes one token. NT threads of a block copy its logits to
@@ -384,22 +428,19 @@ __global__ void __launch_bounds__(NT + 32) ns_distill_kernel(const __grid_consta
       }
       return;
     }
-    float lse2;
+    RowSum r;
     if (p.loss) {
-      lse2 = join_parts<WARPS>(parts, C, lane);
-      if (rank == 0 && lane == 0) {
-        p.loss[t] = weight * (te.sums[1] + te.sums[0] * (lse2 * LN2));
-        p.lse[t] = lse2 * LN2;
-      }
+      r = join_parts<WARPS>(parts, C, lane, c);
+      if (rank == 0 && lane == 0) write_loss(p, te, t, weight, r);
     } else {
-      lse2 = p.lse[t] * LOG2E;
+      r = given_sum(p, t);
     }
     if (!p.grad) return;
     mark_repeated(te, p.top, p.places - 1, lane);
     __syncthreads();  // the plain part of the gradient is written
     const int first = head + w0 * V;
     const Slice slice = {first, first + n * V, head, tail, rank == 0};
-    write_entries<T>(p, te, slice, grad, c, lse2, weight * p.inv_tau, lane, 32);
+    write_entries<T>(p, te, slice, grad, c, r, weight * p.inv_tau, lane, 32);
     return;
   }
 
@@ -424,12 +465,12 @@ __global__ void __launch_bounds__(NT + 32) ns_distill_kernel(const __grid_consta
                                                               : fill_vec<T, V>(-INFINITY);
   };
   const float2 c2 = make_float2(c, c);
-  float lse2 = 0.0f;
+  RowSum r;
   if (p.loss) {
     Online o;
     if (weight != 0.0f) {
-      o.m = ex * c;
-      o.s = o.m == -INFINITY ? 0.0f : exp2_fast(o.m - o.m);
+      o.m = ex;
+      o.s = ex == -INFINITY ? 0.0f : exp2_fast(ex - ex);  // 1, or NaN
       for (int g = 0; g < 4; ++g) {
         if (g == 0) nsptx::cp_async_wait<3>();
         if (g == 1) nsptx::cp_async_wait<2>();
@@ -438,15 +479,15 @@ __global__ void __launch_bounds__(NT + 32) ns_distill_kernel(const __grid_consta
         auto take = [&](int u, auto whole) {
           Vec<T, V> x[B];
           words_at(u, x, whole);
-          const float m = max_of(max_vec(max_vec(x[0], x[1]), max_vec(x[2], x[3]))) * c;
+          const float m = max_of(max_vec(max_vec(x[0], x[1]), max_vec(x[2], x[3])));
           const float top = fmaxf(o.m, m), base = top == -INFINITY ? 0.0f : top;
           const float2 b2 = make_float2(-base, -base);
-          float2 sum = make_float2(o.s * exp2_fast(o.m - base), 0.0f);
+          float2 sum = make_float2(o.s * exp2_fast((o.m - base) * c), 0.0f);
 #pragma unroll
           for (int i = 0; i < B; ++i)
 #pragma unroll
             for (int k = 0; k < V; k += 2) {
-              const float2 a = fma2(make_float2(get(x[i], k), get(x[i], k + 1)), c2, b2);
+              const float2 a = mul2(add2(make_float2(get(x[i], k), get(x[i], k + 1)), b2), c2);
               sum = add2(sum, make_float2(exp2_fast(a.x), exp2_fast(a.y)));
             }
           o.m = top;
@@ -460,7 +501,7 @@ __global__ void __launch_bounds__(NT + 32) ns_distill_kernel(const __grid_consta
     } else {
       nsptx::cp_async_wait<0>();  // a row that was read before its weight was known
     }
-    o = join_warp(o);
+    o = join_warp(o, c);
     if (joins) nsptx::cluster_wait();
     if (C == 1) {
       if (lane == 0) parts[warp] = make_float2(o.m, o.s);
@@ -472,11 +513,11 @@ __global__ void __launch_bounds__(NT + 32) ns_distill_kernel(const __grid_consta
       nsptx::cluster_sync_all();
     else
       __syncthreads();
-    lse2 = join_parts<WARPS>(parts, C, lane);
+    r = join_parts<WARPS>(parts, C, lane, c);
   } else {
     nsptx::cp_async_wait<0>();
     __syncthreads();
-    lse2 = p.lse[t] * LOG2E;
+    r = given_sum(p, t);
   }
   if (!p.grad) return;
 
@@ -497,7 +538,7 @@ __global__ void __launch_bounds__(NT + 32) ns_distill_kernel(const __grid_consta
     return;
   }
   const float mass = weight * p.inv_tau * te.sums[0];
-  const float2 b2 = make_float2(-lse2, -lse2), m2 = make_float2(mass, mass);
+  const float2 b2 = make_float2(-r.m, -r.m), l2 = make_float2(-r.l, -r.l), m2 = make_float2(mass, mass);
   auto give = [&](int u, auto whole) {
     Vec<T, V> x[B];
     words_at(u, x, whole);
@@ -507,7 +548,7 @@ __global__ void __launch_bounds__(NT + 32) ns_distill_kernel(const __grid_consta
       float y[V];
 #pragma unroll
       for (int k = 0; k < V; k += 2) {
-        const float2 a = fma2(make_float2(get(x[i], k), get(x[i], k + 1)), c2, b2);
+        const float2 a = fma2(add2(make_float2(get(x[i], k), get(x[i], k + 1)), b2), c2, l2);
         const float2 b = mul2(m2, make_float2(exp2_fast(a.x), exp2_fast(a.y)));
         y[k] = b.x;
         y[k + 1] = b.y;
@@ -523,7 +564,7 @@ __global__ void __launch_bounds__(NT + 32) ns_distill_kernel(const __grid_consta
   int u = 0;
   for (; u + B <= full; u += B) give(u, std::true_type());
   for (; u < rounds; u += B) give(u, std::false_type());
-  if (has_edge) grad[edge] = from_float<T>(mass * exp2_fast(fmaf(ex, c, -lse2)));
+  if (has_edge) grad[edge] = from_float<T>(mass * r.power(ex, c));
   __syncwarp();  // lanes leave the last round of words one by one
   __syncthreads();
 }
@@ -563,33 +604,30 @@ __global__ void __launch_bounds__(DISTILL_THREADS) ns_distill_long_kernel(const 
   }
 
   const long long head = head_of(row, p.vocab), words = (p.vocab - head) / V, edges = p.vocab - words * V;
-  float lse2;
+  RowSum r;
   if (p.loss) {
     Online o;
     for (long long i = tid; i < words; i += DISTILL_THREADS) {
       const Vec<T, V> x = load_vec<T, V>(row + head + i * V);
       float m = -INFINITY, s = 0.0f;
 #pragma unroll
-      for (int k = 0; k < V; ++k) m = fmaxf(m, get(x, k) * c);
+      for (int k = 0; k < V; ++k) m = fmaxf(m, get(x, k));
       const float base = m == -INFINITY ? 0.0f : m;
 #pragma unroll
-      for (int k = 0; k < V; ++k) s += exp2_fast(fmaf(get(x, k), c, -base));
-      o.join(m, s);
+      for (int k = 0; k < V; ++k) s += exp2_fast((get(x, k) - base) * c);
+      o.join(m, s, c);
     }
     for (long long i = tid; i < edges; i += DISTILL_THREADS) {
-      const float v = to_float(row[i < head ? i : words * V + i]) * c;
-      o.join(v, v == -INFINITY ? 0.0f : exp2_fast(v - v));
+      const float v = to_float(row[i < head ? i : words * V + i]);
+      o.join(v, v == -INFINITY ? 0.0f : exp2_fast(v - v), c);
     }
-    o = join_warp(o);
+    o = join_warp(o, c);
     if (lane == 0) parts[warp] = make_float2(o.m, o.s);
     __syncthreads();
-    lse2 = join_parts<DISTILL_WARPS>(parts, 1, lane);
-    if (tid == 0) {
-      p.loss[t] = weight * (te.sums[1] + te.sums[0] * (lse2 * LN2));
-      p.lse[t] = lse2 * LN2;
-    }
+    r = join_parts<DISTILL_WARPS>(parts, 1, lane, c);
+    if (tid == 0) write_loss(p, te, t, weight, r);
   } else {
-    lse2 = p.lse[t] * LOG2E;
+    r = given_sum(p, t);
     __syncthreads();
   }
   if (!p.grad) return;
@@ -600,20 +638,20 @@ __global__ void __launch_bounds__(DISTILL_THREADS) ns_distill_long_kernel(const 
       const Vec<T, V> x = load_vec<T, V>(row + head + i * V);
       float y[V];
 #pragma unroll
-      for (int k = 0; k < V; ++k) y[k] = mass * exp2_fast(fmaf(get(x, k), c, -lse2));
+      for (int k = 0; k < V; ++k) y[k] = mass * r.power(get(x, k), c);
       store_vec<T, V>(grad + head + i * V, pack<T, V>(y));
     }
     for (long long i = tid; i < edges; i += DISTILL_THREADS) {
       const long long v = i < head ? i : words * V + i;
-      grad[v] = from_float<T>(mass * exp2_fast(fmaf(to_float(row[v]), c, -lse2)));
+      grad[v] = from_float<T>(mass * r.power(to_float(row[v]), c));
     }
   } else {
     for (long long v = tid; v < p.vocab; v += DISTILL_THREADS)
-      grad[v] = from_float<T>(mass * exp2_fast(fmaf(to_float(row[v]), c, -lse2)));
+      grad[v] = from_float<T>(mass * r.power(to_float(row[v]), c));
   }
   __syncthreads();
   const Slice slice = {0, p.vocab, 0, p.vocab, false};
-  write_entries<T>(p, te, slice, grad, c, lse2, scale, tid, DISTILL_THREADS);
+  write_entries<T>(p, te, slice, grad, c, r, scale, tid, DISTILL_THREADS);
 }
 
 constexpr int DISTILL_MAX_SMEM = 200 * 1024;
@@ -695,6 +733,7 @@ int run_distill(const void* logits, int64_t logits_stride, int dtype, int64_t to
   p.top = top;
   p.weights = weights;
   p.teacher_lse = teacher_lse;
+  p.tau = temperature;
   p.inv_tau = 1.0f / temperature;
   p.loss = loss;
   p.lse = lse;
