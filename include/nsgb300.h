@@ -443,7 +443,9 @@ int ns_distill_loss(const void* logits, int64_t logits_stride, int dtype, int64_
                     void* grad_logits, int64_t grad_stride, void* stream);
 
 /* The gradient alone, from the lse that ns_distill_loss wrote for the same
- * logits: for a backward pass that comes later, with other weights. */
+ * logits: for a backward pass that comes later, with other weights. A token
+ * that ns_distill_loss left out has no lse (it wrote -0 there): where such a
+ * token has a weight and entries now, its gradient is NaN. */
 int ns_distill_grad(const void* logits, int64_t logits_stride, int dtype, int64_t tokens, int64_t vocab,
                     const void* teacher_values, int teacher_dtype, const void* teacher_ids, int id_bytes, int top,
                     const float* weights, const float* teacher_lse, float temperature, const float* lse,

@@ -457,7 +457,8 @@ PyMethodDef g_methods[] = {
     NS_METHOD(8, distill_grad,
               "ns_distill_grad(logits, teacher_values, teacher_ids, lse, grad_logits, weights=None, "
               "teacher_lse=None, temperature=1.0, stream=None)\n--\n\n"
-              "The gradient alone, from the lse that ns_distill_loss wrote."),
+              "The gradient alone, from the lse that ns_distill_loss wrote; other weights are fine, but the gradient of a\n"
+              "token that the loss left out (weight 0 or no entry) is NaN once it counts."),
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_training", "Calls of the training-step operators on torch tensors.", -1,

@@ -86,8 +86,14 @@ struct RowSum {
   float m, l;
   __device__ __forceinline__ float power(float x, float c) const { return exp2_fast(fmaf(x - m, c, -l)); }
 };
-// From a log-sum-exp that was given.
-__device__ __forceinline__ RowSum given_sum(const DistillParams& p, long long t) { return {p.lse[t] * p.tau, 0.0f}; }
+// A token that the loss leaves out gets lse -0: equal to 0, but no log-sum-exp
+// that was computed, so that a gradient with another weight can tell.
+constexpr unsigned LEFT_OUT = 0x80000000u;
+// From a log-sum-exp that was given; NaN for a token that had none.
+__device__ __forceinline__ RowSum given_sum(const DistillParams& p, long long t) {
+  const float lse = p.lse[t];
+  return {__float_as_uint(lse) == LEFT_OUT ? __uint_as_float(0x7fc00000u) : lse * p.tau, 0.0f};
+}
 
 // Places of the hash table of `top` ids: a power of two, four times the ids or
 // more, which keeps searches at one or two places, and twice that where it is
@@ -314,7 +320,7 @@ __device__ __forceinline__ void write_loss(const DistillParams& p, const Teacher
                                            const RowSum& r) {
   const float log_sum = r.l * LN2;
   p.loss[t] = weight * (te.sums[1] + te.sums[0] * fmaf(r.m - te.sums[2], p.inv_tau, log_sum));
-  p.lse[t] = fmaf(r.m, p.inv_tau, log_sum);
+  p.lse[t] = fmaf(r.m, p.inv_tau, log_sum) + 0.0f;  // never -0
 }
 
 // The elements of a row that a block writes: its words, and for one block those
@@ -424,7 +430,7 @@ __global__ void __launch_bounds__(NT + 32) ns_distill_kernel(const __grid_consta
     if (!any) {
       if (p.loss && rank == 0 && lane == 0) {
         p.loss[t] = 0.0f;
-        p.lse[t] = 0.0f;
+        p.lse[t] = __uint_as_float(LEFT_OUT);
       }
       return;
     }
@@ -588,7 +594,7 @@ __global__ void __launch_bounds__(DISTILL_THREADS) ns_distill_long_kernel(const 
   if (!__syncthreads_or(load_teacher(p, te, t, row, weight, tid, DISTILL_THREADS))) {
     if (p.loss && tid == 0) {
       p.loss[t] = 0.0f;
-      p.lse[t] = 0.0f;
+      p.lse[t] = __uint_as_float(LEFT_OUT);
     }
     if (p.grad) {
       const long long head = head_of(grad, p.vocab), words = (p.vocab - head) / V;
