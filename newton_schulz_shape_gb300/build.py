@@ -43,9 +43,12 @@ def _deps() -> list:
 
 
 def _torch_dir():
-    """Where torch is installed, without importing it; None if it is not."""
+    """Where torch is installed, without importing it; None if it is not, or
+    not for CUDA: the library needs no torch, and no such torch has a use for
+    the binding."""
     spec = importlib.util.find_spec("torch")
-    return os.path.dirname(spec.origin) if spec and spec.origin else None
+    where = os.path.dirname(spec.origin) if spec and spec.origin else None
+    return where if where and os.path.exists(os.path.join(where, "lib", "libc10_cuda.so")) else None
 
 
 def _stale() -> bool:
