@@ -3,7 +3,8 @@ its training-step operators (_training.so) against the installed torch.
 
 Each translation unit compiles in parallel into ``_build/``; the shared
 library lands next to this file. Rebuilds only when a source or header is
-newer than the library. No cmake, one -gencode.
+newer than the library, or the binding was built against another torch or
+Python. No cmake, one -gencode.
 """
 
 from __future__ import annotations
@@ -51,10 +52,25 @@ def _torch_dir():
     return where if where and os.path.exists(os.path.join(where, "lib", "libc10_cuda.so")) else None
 
 
+def _binding_of() -> str:
+    """What a binding is compiled against: this torch and this Python."""
+    with open(os.path.join(_torch_dir(), "version.py")) as f:
+        return f"{sysconfig.get_config_var('SOABI')}\n{_torch_dir()}\n{f.read()}"
+
+
+def _stamp() -> str:
+    return os.path.join(BUILD, "binding.txt")
+
+
 def _stale() -> bool:
-    made = [LIB] + ([BINDING] if _torch_dir() else [])
+    made = [LIB] + ([BINDING, _stamp()] if _torch_dir() else [])
     if not all(os.path.exists(f) for f in made):
         return True
+    if _torch_dir():
+        with open(_stamp()) as f:
+            if f.read() != _binding_of():
+                return True
+    made = made[:2]
     t = min(os.path.getmtime(f) for f in made)
     return any(os.path.getmtime(f) > t for f in _deps())
 
@@ -82,6 +98,8 @@ def _link_binding(obj: str) -> None:
     _run(["g++", "-shared", obj, "-o", tmp, "-L", PKG, "-l:libnsgb300.so", "-Wl,-rpath,$ORIGIN",
           "-L", os.path.join(_torch_dir(), "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"], "link of _training.so")
     os.replace(tmp, BINDING)
+    with open(_stamp(), "w") as f:
+        f.write(_binding_of())
 
 
 def build(force: bool = False, verbose: bool = False) -> str:

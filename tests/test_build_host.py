@@ -98,3 +98,25 @@ def test_entry_point_imports_what_was_built(monkeypatch):
     entry.build()
     monkeypatch.undo()
     assert seen and "newton_schulz_shape_gb300.training" not in seen
+
+
+def test_another_torch_or_python_makes_the_binding_stale(build, tmp_path, monkeypatch):
+    fake_torch(tmp_path, monkeypatch, build)
+    pretend_to_build(build, monkeypatch)
+    assert not build._stale()
+    fake_torch(tmp_path, monkeypatch, build, version="1.1")
+    assert build._stale()
+    pretend_to_build(build, monkeypatch)
+    assert not build._stale()
+    monkeypatch.setattr(build.sysconfig, "get_config_var", lambda name: "cpython-399-nowhere" if name == "SOABI" else None)
+    assert build._stale()
+    pretend_to_build(build, monkeypatch)
+    assert not build._stale()
+
+
+def test_a_binding_of_unknown_origin_is_stale(build, tmp_path, monkeypatch):
+    fake_torch(tmp_path, monkeypatch, build)
+    pretend_to_build(build, monkeypatch)
+    for f in os.listdir(build.BUILD):
+        os.remove(os.path.join(build.BUILD, f))
+    assert build._stale()
