@@ -4,12 +4,14 @@
 // where attribute reads and ctypes conversions in Python took 3.5 to 7.
 //
 // A tensor has to be on the current GPU, of a type that the C function takes, with its
-// last dimension contiguous: ValueError otherwise, naming the argument. The
-// library checks the rest: NsError.
+// last dimension contiguous, and may require gradients only where none are
+// recorded: ValueError otherwise, naming the argument. The library checks the
+// rest: NsError.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
+#include <c10/core/GradMode.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -98,13 +100,19 @@ struct Args {
     if (!here(t) || t.dim() != dims) bad(i, "a GPU tensor of " + std::to_string(dims) + " dimensions");
     return t;
   }
+  // The address of a tensor's values. The calls record nothing: a graph would end here without a word.
+  void* address(int i, const at::Tensor& t) const {
+    if (t.requires_grad() && c10::GradMode::is_enabled())
+      bad(i, "a tensor without gradients to record (detached, under no_grad or in an autograd.Function)");
+    return t.data_ptr();
+  }
   // The address of `numel` contiguous values; null for None.
   void* whole(int i, at::ScalarType type, int64_t numel) const {
     if (!given(i)) return nullptr;
     const at::Tensor& t = tensor(i);
     if (!here(t) || t.scalar_type() != type || t.numel() != numel || !t.is_contiguous())
       bad(i, std::to_string(numel) + " contiguous GPU values of " + c10::toString(type));
-    return t.data_ptr();
+    return address(i, t);
   }
   const void* indices(int i, int64_t numel, int* bytes) const {
     const at::Tensor& t = tensor(i);
@@ -143,7 +151,7 @@ struct Args {
     }
     if (t.stride(1) != 1 && d > 1) bad(i, "contiguous rows");
     *stride = n > 1 ? t.stride(0) : std::max(t.stride(0), d);
-    return t.data_ptr();
+    return address(i, t);
   }
   int64_t number(int i, int64_t otherwise) const {
     if (!at[i]) return otherwise;
@@ -282,7 +290,7 @@ struct Heads {
       a.bad(i, std::string(c10::toString(type)) + " [" + std::to_string(tokens) + ", " + std::to_string(heads[side]) +
                    ", " + std::to_string(dim) + "]");
     if (t.stride(2) != 1 && dim > 1) a.bad(i, "contiguous heads");
-    at[n] = t.data_ptr();
+    at[n] = a.address(i, t);
     strides[2 * n] = t.stride(0);
     strides[2 * n + 1] = t.stride(1);
     ++n;

@@ -8,6 +8,11 @@ its type one the C function takes and its last dimension contiguous
 (ValueError otherwise); the library checks the rest (NsError). Streams default
 to torch's current stream.
 
+The calls record nothing for autograd: a tensor that requires gradients is
+refused where they are recorded (ValueError). Under ``torch.no_grad`` and inside
+an ``autograd.Function`` (examples/muon_moe_step.py has one for each operator)
+it is taken.
+
 The calls on tensors are an extension module (csrc/binding.cpp, built with the
 library; missing it is an ImportError): ``help`` on each shows its arguments.
 """
