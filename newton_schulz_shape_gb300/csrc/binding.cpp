@@ -19,6 +19,7 @@
 #include <algorithm>
 #include <climits>
 #include <exception>
+#include <initializer_list>
 #include <sstream>
 #include <string>
 
@@ -185,8 +186,16 @@ struct Args {
     if (!p && PyErr_Occurred()) throw Refused();
     return p;
   }
-  PyObject* result(int rc) const {
-    if (rc == NS_OK) Py_RETURN_NONE;
+  // What the call returns; the arguments that it wrote count one write more for autograd.
+  PyObject* result(int rc, std::initializer_list<int> written) const {
+    if (rc == NS_OK) {
+      for (int i : written)
+        if (given(i)) {
+          const at::Tensor& t = THPVariable_Unpack(at[i]);
+          if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+        }
+      Py_RETURN_NONE;
+    }
     return PyObject_CallFunction(g_check, "is", rc, sig.function);
   }
 };
@@ -215,7 +224,8 @@ PyObject* moe_sort(const Args& a) {
                               static_cast<int*>(a.whole(3, at::kInt, rows)),
                               static_cast<int*>(a.whole(4, at::kInt, experts)),
                               static_cast<int*>(a.whole(5, at::kInt, static_cast<int64_t>(experts) + 1)), ws, ws_bytes,
-                              a.stream()));
+                              a.stream()),
+                  {2, 3, 4, 5});
 }
 
 PyObject* moe_dispatch(const Args& a) {
@@ -227,7 +237,8 @@ PyObject* moe_dispatch(const Args& a) {
   const int* slot_of_row = static_cast<int*>(a.whole(2, at::kInt, rows));
   void* out = a.matrix(3, type, rows, dim, &out_ld);
   return a.result(ns_moe_dispatch(x, x_ld, a.dtype(0), tokens, as_int(k), dim, row_of_slot, slot_of_row, rows, out,
-                                  out_ld, a.stream()));
+                                  out_ld, a.stream()),
+                  {3});
 }
 
 PyObject* moe_dispatch_grad(const Args& a) {
@@ -238,7 +249,8 @@ PyObject* moe_dispatch_grad(const Args& a) {
   const int64_t rows = a.tensor(0).size(0), dim = a.tensor(0).size(1);
   void* grad_x = a.matrix(2, type, tokens, dim, &x_ld);
   return a.result(ns_moe_dispatch_grad(grad_rows, rows_ld, a.dtype(0), tokens, as_int(k), dim, row_of_slot, rows,
-                                       grad_x, x_ld, a.stream()));
+                                       grad_x, x_ld, a.stream()),
+                  {2});
 }
 
 PyObject* moe_combine(const Args& a) {
@@ -250,7 +262,8 @@ PyObject* moe_combine(const Args& a) {
   const float* weights = static_cast<float*>(a.whole(1, at::kFloat, tokens * k));
   void* y = a.matrix(3, type, tokens, dim, &y_ld);
   return a.result(ns_moe_combine(expert_rows, rows_ld, a.dtype(0), tokens, as_int(k), dim, row_of_slot, weights, rows,
-                                 y, y_ld, a.stream()));
+                                 y, y_ld, a.stream()),
+                  {3});
 }
 
 PyObject* moe_combine_grad(const Args& a) {
@@ -267,7 +280,8 @@ PyObject* moe_combine_grad(const Args& a) {
   float* grad_weights = static_cast<float*>(a.whole(6, at::kFloat, tokens * k));
   return a.result(ns_moe_combine_grad(grad_y, y_ld, expert_rows, rows_ld, a.dtype(1), tokens, as_int(k), dim,
                                       row_of_slot, slot_of_row, weights, rows, grad_rows, grad_ld, grad_weights,
-                                      a.stream()));
+                                      a.stream()),
+                  {5, 6});
 }
 
 // Queries, keys and what has their shapes: addresses, and (token, head) strides.
@@ -328,7 +342,8 @@ PyObject* qk_norm_rope(const Args& a) {
   return a.result(ns_qk_norm_rope(h.at[0], h.at[1], h.at[2], h.at[3], h.strides, a.dtype(0), h.tokens,
                                   as_int(h.heads[0]), as_int(h.heads[1]), as_int(h.dim), as_int(r.rot_dim), a.flag(9),
                                   r.q_weight, r.k_weight, r.weight_dtype, a.real(8, 1e-6f), r.table, r.table_rows,
-                                  r.positions, r.position_bytes, a.stream()));
+                                  r.positions, r.position_bytes, a.stream()),
+                  {2, 3});
 }
 
 PyObject* qk_norm_rope_grad(const Args& a) {
@@ -341,7 +356,8 @@ PyObject* qk_norm_rope_grad(const Args& a) {
       h.at[4], h.at[5], h.at[0], h.at[1], h.at[2], h.at[3], h.strides, a.dtype(2), h.tokens, as_int(h.heads[0]),
       as_int(h.heads[1]), as_int(h.dim), as_int(r.rot_dim), a.flag(14), r.q_weight, r.k_weight, r.weight_dtype,
       static_cast<float*>(a.whole(8, at::kFloat, h.dim)), static_cast<float*>(a.whole(9, at::kFloat, h.dim)),
-      a.real(13, 1e-6f), r.table, r.table_rows, r.positions, r.position_bytes, ws, ws_bytes, a.stream()));
+      a.real(13, 1e-6f), r.table, r.table_rows, r.positions, r.position_bytes, ws, ws_bytes, a.stream()),
+                  {4, 5, 8, 9});
 }
 
 // The student's and the teacher's logits, from arguments 0, 1 and 2.
@@ -374,7 +390,8 @@ PyObject* distill_loss(const Args& a) {
                                   l.id_bytes, as_int(l.top), static_cast<float*>(a.whole(6, at::kFloat, l.tokens)),
                                   static_cast<float*>(a.whole(7, at::kFloat, l.tokens)), a.real(8, 1.0f),
                                   static_cast<float*>(a.whole(3, at::kFloat, l.tokens)),
-                                  static_cast<float*>(a.whole(4, at::kFloat, l.tokens)), grad, grad_ld, a.stream()));
+                                  static_cast<float*>(a.whole(4, at::kFloat, l.tokens)), grad, grad_ld, a.stream()),
+                  {3, 4, 5});
 }
 
 PyObject* distill_grad(const Args& a) {
@@ -384,7 +401,8 @@ PyObject* distill_grad(const Args& a) {
   return a.result(ns_distill_grad(l.logits, l.stride, l.dtype, l.tokens, l.vocab, l.values, l.values_dtype, l.ids,
                                   l.id_bytes, as_int(l.top), static_cast<float*>(a.whole(5, at::kFloat, l.tokens)),
                                   static_cast<float*>(a.whole(6, at::kFloat, l.tokens)), a.real(7, 1.0f),
-                                  static_cast<float*>(a.whole(3, at::kFloat, l.tokens)), grad, grad_ld, a.stream()));
+                                  static_cast<float*>(a.whole(3, at::kFloat, l.tokens)), grad, grad_ld, a.stream()),
+                  {4});
 }
 
 Signature g_signatures[] = {

@@ -55,3 +55,43 @@ def test_tensors_that_require_gradients_are_refused_where_a_graph_is_recorded(na
             op(**given, **rest)
     torch.cuda.synchronize()
     assert nsg.ns_check_status() == nsg.NS_OK
+
+
+@pytest.mark.parametrize("name", NAMES + ["ns_moe_sort"])
+def test_outputs_count_as_written(name):
+    # so that autograd can tell that what it saved is no longer there
+    if name == "ns_moe_sort":
+        i32 = [torch.empty(n, dtype=torch.int32, device=DEV) for n in ((2, 2), 4, 3, 4)]
+        floats = dict(zip(("row_of_slot", "slot_of_row", "counts", "offsets"), i32))
+        rest = dict(expert_ids=torch.zeros(2, 2, dtype=torch.int64, device=DEV), experts=3, workspace=None)
+        written = list(floats)
+    else:
+        _, floats, rest, written = next(c for c in calls() if c[0] == name)
+    op = getattr(nsg, name)
+    before = {k: v._version for k, v in floats.items()}
+    op(**floats, **rest)
+    assert {k for k, v in floats.items() if v._version != before[k]} == set(written)
+    # a view counts for what it is a view of, a refused call for nothing
+    big = {k: torch.empty(2, *v.shape, dtype=v.dtype, device=DEV) for k, v in floats.items() if k in written}
+    op(**{**floats, **{k: v[0] for k, v in big.items()}}, **rest)
+    assert all(v._version == 1 for v in big.values())
+    before = {k: v._version for k, v in floats.items()}
+    with pytest.raises(ValueError):
+        op(**{**floats, written[-1]: floats[written[-1]].cpu()}, **rest)
+    assert all(v._version == before[k] for k, v in floats.items())
+    # tensors of inference mode have no count
+    with torch.inference_mode():
+        made = {k: v.clone() for k, v in floats.items()}
+    op(**made, **rest)
+    torch.cuda.synchronize()
+    assert nsg.ns_check_status() == nsg.NS_OK
+
+
+def test_a_saved_tensor_that_was_written_over_stops_the_backward_pass():
+    x = torch.ones(2, 2, 16, device=DEV, requires_grad=True)
+    y = x * 2
+    z = (y * y).sum()                    # saves y
+    with torch.no_grad():
+        nsg.ns_qk_norm_rope(y.detach(), y.detach(), y.detach(), torch.empty_like(y))
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        z.backward()
