@@ -397,7 +397,8 @@ int ns_moe_combine_grad(const void* grad_y, int64_t grad_y_stride, const void* e
  * table[pos][rot_dim / 2 + i] (fp32 [table_rows][rot_dim]). positions[t] is
  * int32 or int64 (position_bytes 4 or 8), NULL = t; a token whose position is
  * outside the table is refused (its outputs are not written). head_dim <= 1024,
- * tokens * (q_heads + k_heads) < 2^30.
+ * tokens * (q_heads + k_heads) < 2^30. The sum of a head's squares is in fp32:
+ * a root mean square above 1e18 (of 128 values) has no norm there.
  * q_out may be q and k_out may be k, with the same strides. */
 int ns_qk_norm_rope(const void* q, const void* k, void* q_out, void* k_out, const int64_t* strides, int dtype,
                     int64_t tokens, int q_heads, int k_heads, int head_dim, int rot_dim, int interleaved,

@@ -9,8 +9,8 @@
 //   loss = w sum_j p_j (log p_j - s_{i_j} / tau + lse)
 //   dloss/ds_v = (w / tau) (P exp(s_v / tau - lse) - sum_{j: i_j = v} p_j), P = sum_j p_j
 // Entries with i_j < 0 or z_j = -inf are left out. A token whose weight is 0
-// or that has no entry left has loss 0, lse 0 and a zero gradient, whatever its
-// logits hold (NaN included); those of a weight of 0 need not be read.
+// or that has no entry left has loss 0, lse 0 (as -0) and a zero gradient, whatever
+// its logits hold (NaN included); those of a weight of 0 need not be read.
 // The maximum, the sums and the logarithm are in fp32; a gradient value is
 // rounded once, when it is stored. The maximum m of the logits is kept as it is
 // and subtracted before anything is scaled: exp(s / tau - lse) is
@@ -381,8 +381,9 @@ __device__ __forceinline__ RowSum join_parts(const float2* parts, int C, int lan
 // memory, so that one barrier joins them. The copies of a block are all in
 // flight at once, and the blocks that share an SM overlap their phases: with
 // slices of 64 KB there are three of them.
-// Bound by memory: 4096 rows of 131072 bf16, loss and gradient, 338 us, 6.35 TB/s
-// (0.95 of the measured copy). Two passes of one block a row took 564 us (the
+// Bound by memory: 4096 rows of 131072 bf16, loss and gradient, 342 us, 6.3 TB/s
+// (0.94 of the measured copy); the loss alone 198 us, 5.4 TB/s, bound by its
+// instructions. Two passes of one block a row took 564 us (the
 // second read came from L2, but the phases of a row did not overlap), slices
 // kept in registers 453 us (two blocks an SM at 56 registers). 8 such rows take
 // 5.4 us, 2.5 of them the launch: 64 blocks, whose chain of loads is a token's

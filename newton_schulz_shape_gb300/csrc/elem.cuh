@@ -164,13 +164,7 @@ template <typename T, int V>
 __device__ __forceinline__ void store_vec(T* p, const Vec<T, V>& x) {
   *reinterpret_cast<Vec<T, V>*>(p) = x;
 }
-// The same for 16 bytes that are read or written once (evicted first).
-template <typename T>
-__device__ __forceinline__ Vec<T, 16 / sizeof(T)> load_once(const T* p) {
-  Vec<T, 16 / sizeof(T)> x;
-  *reinterpret_cast<uint4*>(&x) = __ldcs(reinterpret_cast<const uint4*>(p));
-  return x;
-}
+// The same for 16 bytes that are written once (evicted first).
 template <typename T>
 __device__ __forceinline__ void store_once(T* p, const Vec<T, 16 / sizeof(T)>& x) {
   __stcs(reinterpret_cast<uint4*>(p), *reinterpret_cast<const uint4*>(&x));

@@ -8,6 +8,9 @@ its type one the C function takes and its last dimension contiguous
 (ValueError otherwise); the library checks the rest (NsError). Streams default
 to torch's current stream.
 
+A call on another stream (``stream=`` a torch stream or a handle) holds no
+reference to its tensors: keep them until it is done, or ``record_stream`` them.
+
 The calls record nothing for autograd: a tensor that requires gradients is
 refused where they are recorded (ValueError). Under ``torch.no_grad`` and inside
 an ``autograd.Function`` (examples/muon_moe_step.py has one for each operator)
