@@ -138,7 +138,9 @@ __device__ __forceinline__ void entry_of(const DistillParams& p, long long i, lo
 }
 
 // Loads the entries with `n` threads, 4 at a time each so that their latencies
-// overlap; whether this thread left any in.
+// overlap; whether this thread left any in. In the gradient alone in place of the
+// logits, another block may have written its slice by then: of the logits read
+// there only those of the block's own slice are used.
 template <typename T>
 __device__ __forceinline__ bool load_teacher(const DistillParams& p, const Teacher& te, long long t, const T* row,
                                              float weight, int first, int n) {
