@@ -452,6 +452,94 @@ int ns_distill_grad(const void* logits, int64_t logits_stride, int dtype, int64_
                     const float* weights, const float* teacher_lse, float temperature, const float* lse,
                     void* grad_logits, int64_t grad_stride, void* stream);
 
+/* ---- gradient norm and clipping. Tensors are given as arrays of `count`
+ * addresses, numbers of values and types (NS_DT_*, which may differ from tensor
+ * to tensor): host arrays that are read before the call returns. A tensor's
+ * values are contiguous in memory, at any address that they can have; it may
+ * be empty. At most 2^20 tensors, 2^43 bytes together. Tensors of one call must
+ * not overlap. */
+
+/* Bytes of device workspace of ns_grad_norm. Host only. */
+int ns_grad_norm_workspace_bytes(int count, uint64_t* bytes);
+
+/* *norm (device, fp32) = sqrt(sum of squares of all values of all tensors), 0
+ * without any. Squares that leave fp32's range are summed in 64 bits, so that
+ * finite values have their norm whatever their size; one above fp32's largest
+ * value is infinite. An infinite value makes it infinite, a NaN makes it NaN. */
+int ns_grad_norm(const void* const* grads, const int64_t* numels, const int* dtypes, int count, float* norm,
+                 void* workspace, uint64_t workspace_bytes, void* stream);
+
+/* outs[i] = c * grads[i], c = min(1, max_norm / (*norm + eps)), rounded once.
+ * *norm is on the device: what ns_grad_norm wrote, or the norm over several
+ * calls or ranks. outs[i] may be grads[i] itself, and is not touched then if
+ * c = 1. An infinite norm gives c = 0 (infinite values become NaN), a norm that
+ * is NaN makes every value NaN. max_norm >= 0, eps >= 0 and finite. */
+int ns_grad_clip(const void* const* grads, void* const* outs, const int64_t* numels, const int* dtypes, int count,
+                 const float* norm, float max_norm, float eps, void* stream);
+
+/* The norms after and before a block of a residual network, with the block's
+ * gate and the residual's scale. For each token, with the block's output b and
+ * the residual x of dim values:
+ *   u = b / sqrt(mean(b^2) + eps) * branch_weight (post_norm = 0: b * branch_weight)
+ *   h = residual_scale * x + branch_scale * gate * u      -> residual_out
+ *   n = h / sqrt(mean(h^2) + eps) * weight                -> out
+ * branch, out and the weights' type is dtype, the residual's residual_dtype
+ * (dtype or fp32); branch_weight and weight (NULL = 1) have dim values of
+ * weight_dtype (dtype or fp32). gate_kind 0: no gate; 1: fp32 [tokens], one for
+ * each token; 2: [tokens][dim] of dtype. branch NULL: h = residual_scale * x
+ * (the norm before the first block; the gate is not used). residual_out NULL or
+ * out NULL: not wanted; n is computed from h before h is rounded. strides[5]:
+ * row strides of branch, residual, residual_out, out and gate. residual_out may
+ * be residual and out may be branch or gate, with the same stride. dim at most
+ * 2^20, tokens * dim at most 2^40. Sums of squares are in fp32: a root mean
+ * square above 1e17 has no norm there. */
+int ns_block_norm(const void* branch, const void* residual, void* residual_out, void* out, const int64_t* strides,
+                  int dtype, int residual_dtype, int64_t tokens, int64_t dim, const void* branch_weight,
+                  const void* weight, int weight_dtype, const void* gate, int gate_kind, int post_norm,
+                  float residual_scale, float branch_scale, float eps, void* stream);
+
+/* Bytes of device workspace of ns_block_norm_grad (needed only with a weight
+ * gradient). Host only. */
+int ns_block_norm_grad_workspace_bytes(int64_t dim, uint64_t* bytes);
+
+/* Gradient of ns_block_norm, from the gradients of residual_out and of out
+ * (either may be NULL: zero) and the forward's branch, gate and residual_out (h
+ * as it was stored; with residual_scale 1 and no branch that is residual): the
+ * gradients of branch, residual and gate, and the weights' (fp32 [dim], sums over
+ * tokens); each may be NULL: not wanted. The gate's gradient has the gate's form
+ * and type. strides[8]: row strides of branch, residual_out, grad_branch,
+ * grad_residual, grad_residual_out, grad_out, gate and grad_gate. Outputs may be
+ * inputs of the same type and shape with the same stride (grad_residual may be
+ * grad_residual_out, grad_branch may be grad_out or branch, grad_gate may be
+ * gate), each input at most once. */
+int ns_block_norm_grad(const void* grad_residual_out, const void* grad_out, const void* branch, const void* residual_out,
+                       void* grad_branch, void* grad_residual, const int64_t* strides, int dtype, int residual_dtype,
+                       int64_t tokens, int64_t dim, const void* branch_weight, const void* weight, int weight_dtype,
+                       const void* gate, int gate_kind, float* grad_branch_weight, float* grad_weight, void* grad_gate,
+                       int post_norm, float residual_scale, float branch_scale, float eps, void* workspace,
+                       uint64_t workspace_bytes, void* stream);
+
+/* Bytes of device workspace of ns_moe_few_tokens. Host only. */
+int ns_moe_few_tokens_workspace_bytes(int64_t tokens, int k, int64_t dim, int64_t ffn, uint64_t* bytes);
+
+/* A whole mixture-of-experts layer for a few tokens (a decoding step), without
+ * sorting them: for every slot s = t * k + j with expert e = expert_ids[s]
+ *   h_s = silu(G_e x_t) * (U_e x_t),  silu(a) = a / (1 + exp(-a))
+ *   y_t = sum over t's slots of weights[s] * D_e h_s
+ * where gate_up is [experts][2 * ffn][dim], G_e its first ffn rows of expert e
+ * and U_e the others, and down is [experts][dim][ffn], all contiguous. Ids are
+ * int32 or int64; a negative one goes nowhere, one >= experts is refused and goes
+ * nowhere; a token may name an expert more than once. weights fp32
+ * [tokens][k], NULL = 1; the weight of a slot that goes nowhere is not used,
+ * whatever it holds, and the weights of experts that no token names are not
+ * read. y may be x itself. tokens <= 256, 1 <= k <= 32, 1 <= experts <= 1024,
+ * dim and ffn < 2^20, ffn >= 1; for more tokens: ns_moe_sort, ns_moe_dispatch
+ * and ns_moe_combine. */
+int ns_moe_few_tokens(const void* x, int64_t x_stride, int dtype, int64_t tokens, int k, int64_t dim, int64_t ffn,
+                      int experts, const void* expert_ids, int id_bytes, const float* weights, const void* gate_up,
+                      const void* down, void* y, int64_t y_stride, void* workspace, uint64_t workspace_bytes,
+                      void* stream);
+
 /* ---------------------------------------------------------- test support
  * No counterpart on the pages: hooks with which tests drive the library's
  * device-side error paths without faulting or hanging the GPU. */
@@ -528,8 +616,13 @@ int ns_profile_enable(int enable);
 int ns_profile_read(int reset, int64_t* launches, double* gpu_ms);
 
 /* The same for the training-step operators, launches[3] and gpu_ms[3]:
- * 0 = sort, dispatch and combine, 1 = norms and rotation, 2 = distillation. */
+ * 0 = sort, dispatch, combine and the layer for a few tokens, 1 = head norms and
+ * rotation, 2 = distillation. */
 int ns_profile_read_training(int reset, int64_t* launches, double* gpu_ms);
+
+/* The same, launches[2] and gpu_ms[2]: 0 = gradient norm and clipping, 1 = block
+ * norms. */
+int ns_profile_read_blocks(int reset, int64_t* launches, double* gpu_ms);
 
 #ifdef __cplusplus
 }

@@ -8,8 +8,8 @@ the import fails.
 
 Buffers are torch CUDA tensors (or raw device addresses as ints); streams
 default to torch's current stream. The operators of the training step
-(``ns_moe_*``, ``ns_qk_norm_rope*``, ``ns_distill_*``) take torch tensors and
-are in ``training.py``.
+(``ns_moe_*``, ``ns_qk_norm_rope*``, ``ns_distill_*``, ``ns_grad_*``,
+``ns_block_norm*``) take torch tensors and are in ``training.py``.
 """
 
 from __future__ import annotations
@@ -27,7 +27,10 @@ A_COEF, B_COEF, C_COEF = 3.4445, -4.7750, 2.0315
 # imported when one is first used, so that the rest needs no torch.
 _TRAINING = ("ns_moe_rows", "ns_moe_sort_workspace_bytes", "ns_moe_sort", "ns_moe_dispatch", "ns_moe_dispatch_grad",
              "ns_moe_combine", "ns_moe_combine_grad", "ns_qk_norm_rope", "ns_qk_norm_rope_grad_workspace_bytes",
-             "ns_qk_norm_rope_grad", "ns_distill_loss", "ns_distill_grad", "ns_profile_read_training")
+             "ns_qk_norm_rope_grad", "ns_distill_loss", "ns_distill_grad", "ns_profile_read_training",
+             "ns_grad_norm_workspace_bytes", "ns_grad_norm", "ns_grad_clip", "ns_block_norm",
+             "ns_block_norm_grad_workspace_bytes", "ns_block_norm_grad", "ns_moe_few_tokens_workspace_bytes",
+             "ns_moe_few_tokens", "ns_profile_read_blocks")
 
 
 def __getattr__(name):

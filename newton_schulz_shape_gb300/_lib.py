@@ -104,6 +104,18 @@ _SIGS = {
                                _ptr, _ptr, _i64, _ptr]),
     "ns_distill_grad": (_int, [_ptr, _i64, _int, _i64, _i64, _ptr, _int, _ptr, _int, _int, _ptr, _ptr, _f32, _ptr,
                                _ptr, _i64, _ptr]),
+    "ns_grad_norm_workspace_bytes": (_int, [_int, _u64p]),
+    "ns_grad_norm": (_int, [_vpp, _i64p, _i32p, _int, _ptr, _ptr, ctypes.c_uint64, _ptr]),
+    "ns_grad_clip": (_int, [_vpp, _vpp, _i64p, _i32p, _int, _ptr, _f32, _f32, _ptr]),
+    "ns_block_norm": (_int, [_ptr, _ptr, _ptr, _ptr, _ptr, _int, _int, _i64, _i64, _ptr, _ptr, _int, _ptr, _int, _int,
+                             _f32, _f32, _f32, _ptr]),
+    "ns_block_norm_grad_workspace_bytes": (_int, [_i64, _u64p]),
+    "ns_block_norm_grad": (_int, [_ptr, _ptr, _ptr, _ptr, _ptr, _ptr, _ptr, _int, _int, _i64, _i64, _ptr, _ptr, _int,
+                                  _ptr, _int, _ptr, _ptr, _ptr, _int, _f32, _f32, _f32, _ptr, ctypes.c_uint64, _ptr]),
+    "ns_moe_few_tokens_workspace_bytes": (_int, [_i64, _int, _i64, _i64, _u64p]),
+    "ns_moe_few_tokens": (_int, [_ptr, _i64, _int, _i64, _int, _i64, _i64, _int, _ptr, _int, _ptr, _ptr, _ptr, _ptr,
+                                 _i64, _ptr, ctypes.c_uint64, _ptr]),
+    "ns_profile_read_blocks": (_int, [_int, _i64p, ctypes.POINTER(ctypes.c_double)]),
     "ns_profile_read_training": (_int, [_int, _i64p, ctypes.POINTER(ctypes.c_double)]),
     "ns_profile_read": (ctypes.c_int, [ctypes.c_int, _i64p, ctypes.POINTER(ctypes.c_double)]),
 }

@@ -25,7 +25,7 @@ LIB = os.path.join(PKG, "libnsgb300.so")
 BINDING = os.path.join(PKG, "_training.so")
 SOURCES = ["planner.cpp", "api.cu", "runtime.cu", "route.cu", "ns_bf16.cu", "ns_fp32.cu", "pipeline.cu",
            "gemm.cu", "gemm2sm.cu", "gemm32.cu", "prologue.cu", "pack.cu", "small.cu", "noalloc.cu",
-           "moe.cu", "qk_rope.cu", "distill.cu"]
+           "moe.cu", "qk_rope.cu", "distill.cu", "grad_norm.cu", "block_norm.cu", "moe_few.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -22,6 +22,7 @@
 #include <initializer_list>
 #include <sstream>
 #include <string>
+#include <vector>
 
 #include "nsgb300.h"
 
@@ -31,7 +32,7 @@ PyObject* g_check = nullptr;  // _lib.check
 
 struct Refused {};  // the Python error is set
 
-constexpr int kMaxArgs = 16;
+constexpr int kMaxArgs = 20;
 
 // Names of a call's arguments, the first `required` of them without a default.
 struct Signature {
@@ -170,8 +171,8 @@ struct Args {
     if (v == -1.0 && PyErr_Occurred()) throw Refused();
     return static_cast<float>(v);
   }
-  bool flag(int i) const {
-    const int v = at[i] ? PyObject_IsTrue(at[i]) : 0;
+  bool flag(int i, bool otherwise = false) const {
+    const int v = at[i] ? PyObject_IsTrue(at[i]) : otherwise;
     if (v < 0) throw Refused();
     return v != 0;
   }
@@ -186,14 +187,45 @@ struct Args {
     if (!p && PyErr_Occurred()) throw Refused();
     return p;
   }
+  // The tensors of a list or tuple.
+  std::vector<at::Tensor> tensors(int i) const {
+    PyObject* items = PySequence_Fast(at[i], sig.names[i]);
+    if (!items) {
+      PyErr_Clear();
+      bad(i, "a list of tensors");
+    }
+    std::vector<at::Tensor> found;
+    for (Py_ssize_t j = 0; j < PySequence_Fast_GET_SIZE(items); ++j) {
+      PyObject* item = PySequence_Fast_GET_ITEM(items, j);
+      if (!THPVariable_Check(item)) {
+        const std::string what = Py_TYPE(item)->tp_name;
+        Py_DECREF(items);
+        bad_item(i, j, "a tensor", what);
+      }
+      found.push_back(THPVariable_Unpack(item));
+    }
+    Py_DECREF(items);
+    return found;
+  }
+  [[noreturn]] void bad_item(int i, Py_ssize_t j, const std::string& want, const std::string& got) const {
+    PyErr_SetString(PyExc_ValueError,
+                    (std::string(sig.names[i]) + "[" + std::to_string(j) + "]: " + want + ", got " + got).c_str());
+    throw Refused();
+  }
+  [[noreturn]] void bad_item(int i, Py_ssize_t j, const std::string& want, const at::Tensor& t) const {
+    std::ostringstream m;
+    m << t.dtype().name() << " " << t.sizes() << " with strides " << t.strides() << " on " << t.device();
+    bad_item(i, j, want, m.str());
+  }
+
+  static void count_write(const at::Tensor& t) {
+    if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+  }
   // What the call returns; the arguments that it wrote count one write more for autograd.
   PyObject* result(int rc, std::initializer_list<int> written) const {
     if (rc == NS_OK) {
       for (int i : written)
-        if (given(i)) {
-          const at::Tensor& t = THPVariable_Unpack(at[i]);
-          if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
-        }
+        if (given(i)) count_write(THPVariable_Unpack(at[i]));
       Py_RETURN_NONE;
     }
     return PyObject_CallFunction(g_check, "is", rc, sig.function);
@@ -405,6 +437,177 @@ PyObject* distill_grad(const Args& a) {
                   {4});
 }
 
+// The tensors of argument i, as the library takes them: of any floating type of its own, dense in memory.
+struct Tensors {
+  std::vector<at::Tensor> all;
+  std::vector<const void*> at;
+  std::vector<int64_t> numels;
+  std::vector<int> dtypes;
+
+  Tensors(const Args& a, int i) : all(a.tensors(i)) {
+    const size_t n = all.size();
+    if (n > INT_MAX) a.bad(i, "fewer tensors");
+    at.resize(n);
+    numels.resize(n);
+    dtypes.resize(n);
+    for (size_t j = 0; j < n; ++j) {
+      const at::Tensor& t = all[j];
+      const at::ScalarType type = t.scalar_type();
+      if (!a.here(t) || t.layout() != c10::kStrided || !t.is_non_overlapping_and_dense() ||
+          (type != at::kBFloat16 && type != at::kHalf && type != at::kFloat))
+        a.bad_item(i, j, "a GPU tensor of bfloat16, float16 or float32 without gaps in memory", t);
+      if (t.requires_grad() && c10::GradMode::is_enabled())
+        a.bad_item(i, j, "a tensor without gradients to record (detached or under no_grad)", t);
+      at[j] = t.data_ptr();
+      numels[j] = t.numel();
+      dtypes[j] = type == at::kFloat ? NS_DT_FP32 : type == at::kHalf ? NS_DT_FP16 : NS_DT_BF16;
+    }
+  }
+  int count() const { return static_cast<int>(all.size()); }
+};
+
+PyObject* grad_norm(const Args& a) {
+  const Tensors g(a, 0);
+  uint64_t ws_bytes;
+  void* ws = a.scratch(2, &ws_bytes);
+  return a.result(ns_grad_norm(g.at.data(), g.numels.data(), g.dtypes.data(), g.count(),
+                               static_cast<float*>(a.whole(1, at::kFloat, 1)), ws, ws_bytes, a.stream()),
+                  {1});
+}
+
+PyObject* grad_clip(const Args& a) {
+  const Tensors g(a, 0), out(a, 1);
+  if (g.count() != out.count()) a.bad(1, "as many tensors as grads");
+  for (int j = 0; j < g.count(); ++j) {
+    const at::Tensor &x = g.all[j], &y = out.all[j];
+    // the values of both lie in the same order
+    if (x.scalar_type() != y.scalar_type() || x.sizes() != y.sizes() ||
+        (x.strides() != y.strides() && !(x.is_contiguous() && y.is_contiguous())))
+      a.bad_item(1, j, "the type, shape and strides of grads' tensor", y);
+  }
+  const int rc = ns_grad_clip(g.at.data(), const_cast<void* const*>(out.at.data()), g.numels.data(), g.dtypes.data(),
+                              g.count(), static_cast<float*>(a.whole(2, at::kFloat, 1)), a.real(3, 0.0f),
+                              a.real(4, 1e-6f), a.stream());
+  if (rc == NS_OK)
+    for (const at::Tensor& t : out.all) Args::count_write(t);
+  return a.result(rc, {});
+}
+
+// Rows of a block's norms: all [tokens, dim] (None: not there), with their strides in the order they were added.
+struct Rows {
+  const Args& a;
+  int64_t tokens, dim;
+  int64_t strides[8] = {};
+  int n = 0;
+
+  Rows(const Args& args, int of) : a(args), tokens(args.gpu(of, 2).size(0)), dim(args.tensor(of).size(1)) {}
+  void* add(int i, at::ScalarType type) {
+    const int k = n++;
+    return a.given(i) ? a.matrix(i, type, tokens, dim, &strides[k]) : nullptr;
+  }
+};
+
+// The gate's form: [tokens, dim], or fp32 [tokens] or [tokens, 1].
+int gate_kind(const Rows& r, int i) {
+  if (!r.a.given(i)) return 0;
+  const at::Tensor& t = r.a.tensor(i);
+  return t.dim() == 2 && !(t.size(1) == 1 && t.scalar_type() == at::kFloat) ? 2 : 1;
+}
+void* add_gate(Rows& r, int i, int kind, at::ScalarType type) {
+  if (kind == 2) return r.add(i, type);
+  ++r.n;
+  return kind == 1 ? r.a.whole(i, at::kFloat, r.tokens) : nullptr;
+}
+
+// branch_weight and weight, of the block's type or fp32; neither has a use (nor the type a meaning) where no rows of
+// the block's type are given.
+struct BlockWeights {
+  const void *branch = nullptr, *next = nullptr;
+  int dtype = NS_DT_FP32;
+  BlockWeights(const Args& a, int i, at::ScalarType type, int64_t dim, bool used) {
+    if (!used) return;
+    const int first = a.given(i) ? i : i + 1;
+    const at::ScalarType t = a.given(first) ? a.tensor(first).scalar_type() : type;
+    if (t != type && t != at::kFloat) a.bad(first, std::string(c10::toString(type)) + " or Float");
+    dtype = t == at::kFloat ? NS_DT_FP32 : t == at::kHalf ? NS_DT_FP16 : NS_DT_BF16;
+    branch = a.whole(i, t, dim);
+    next = a.whole(i + 1, t, dim);
+  }
+};
+
+// The first of these arguments that is given, of which the block's type is.
+int first_given(const Args& a, std::initializer_list<int> of, int otherwise) {
+  for (int i : of)
+    if (a.given(i)) return i;
+  return otherwise;
+}
+
+PyObject* block_norm(const Args& a) {
+  Rows r(a, 1);
+  const int typed = first_given(a, {0, 3}, 1);
+  const at::ScalarType type = a.tensor(typed).scalar_type(), residual_type = a.tensor(1).scalar_type();
+  const void* branch = r.add(0, type);
+  const void* residual = r.add(1, residual_type);
+  void* residual_out = r.add(2, residual_type);
+  void* out = r.add(3, type);
+  const int kind = gate_kind(r, 6);
+  const void* gate = add_gate(r, 6, kind, type);
+  const BlockWeights w(a, 4, type, r.dim, typed != 1);
+  return a.result(ns_block_norm(branch, residual, residual_out, out, r.strides, a.dtype(typed), a.dtype(1), r.tokens, r.dim,
+                                w.branch, w.next, w.dtype, gate, kind, a.flag(7, true), a.real(8, 1.0f),
+                                a.real(9, 1.0f), a.real(10, 1e-6f), a.stream()),
+                  {2, 3});
+}
+
+PyObject* block_norm_grad(const Args& a) {
+  Rows r(a, 3);
+  const int typed = first_given(a, {2, 1}, 3);
+  const at::ScalarType type = a.tensor(typed).scalar_type(), residual_type = a.tensor(3).scalar_type();
+  const void* branch = r.add(2, type);
+  const void* residual_out = r.add(3, residual_type);
+  void* grad_branch = r.add(4, type);
+  void* grad_residual = r.add(5, residual_type);
+  const void* grad_residual_out = r.add(0, residual_type);
+  const void* grad_out = r.add(1, type);
+  const int kind = gate_kind(r, 8);
+  const void* gate = add_gate(r, 8, kind, type);
+  void* grad_gate = add_gate(r, 11, a.given(11) ? kind : 0, type);
+  if (a.given(11) && !kind) a.bad(11, "None without a gate");
+  const BlockWeights w(a, 6, type, r.dim, typed != 3);
+  uint64_t ws_bytes;
+  void* ws = a.scratch(12, &ws_bytes);
+  return a.result(
+      ns_block_norm_grad(grad_residual_out, grad_out, branch, residual_out, grad_branch, grad_residual, r.strides,
+                         a.dtype(typed), a.dtype(3), r.tokens, r.dim, w.branch, w.next, w.dtype, gate, kind,
+                         static_cast<float*>(a.whole(9, at::kFloat, r.dim)),
+                         static_cast<float*>(a.whole(10, at::kFloat, r.dim)), grad_gate, a.flag(13, true),
+                         a.real(14, 1.0f), a.real(15, 1.0f), a.real(16, 1e-6f), ws, ws_bytes, a.stream()),
+      {4, 5, 9, 10, 11});
+}
+
+PyObject* moe_few_tokens(const Args& a) {
+  const at::ScalarType type = a.tensor(0).scalar_type();
+  int64_t x_ld, y_ld;
+  const void* x = a.matrix(0, type, -1, -1, &x_ld);
+  const int64_t tokens = a.tensor(0).size(0), dim = a.tensor(0).size(1);
+  const at::Tensor &ids = a.gpu(1, 2), &up = a.gpu(3, 3), &down = a.gpu(4, 3);
+  if (ids.size(0) != tokens) a.bad(1, std::to_string(tokens) + " rows");
+  const int64_t k = ids.size(1), experts = up.size(0), ffn = down.size(2);
+  int id_bytes;
+  const void* expert_ids = a.indices(1, tokens * k, &id_bytes);
+  const float* weights = static_cast<float*>(a.whole(2, at::kFloat, tokens * k));
+  if (up.size(1) != 2 * ffn || up.size(2) != dim) a.bad(3, "[experts, 2 * ffn, dim]");
+  if (down.size(0) != experts || down.size(1) != dim) a.bad(4, "[experts, dim, ffn]");
+  const void* gate_up = a.whole(3, type, experts * 2 * ffn * dim);
+  const void* down_at = a.whole(4, type, experts * dim * ffn);
+  void* y = a.matrix(5, type, tokens, dim, &y_ld);
+  uint64_t ws_bytes;
+  void* ws = a.scratch(6, &ws_bytes);
+  return a.result(ns_moe_few_tokens(x, x_ld, a.dtype(0), tokens, as_int(k), dim, ffn, as_int(experts), expert_ids,
+                                    id_bytes, weights, gate_up, down_at, y, y_ld, ws, ws_bytes, a.stream()),
+                  {5});
+}
+
 Signature g_signatures[] = {
     {"ns_moe_sort", 7, 10,
      {"expert_ids", "experts", "row_of_slot", "slot_of_row", "counts", "offsets", "workspace", "align", "capacity", "stream"}},
@@ -422,6 +625,16 @@ Signature g_signatures[] = {
      {"logits", "teacher_values", "teacher_ids", "loss", "lse", "grad_logits", "weights", "teacher_lse", "temperature", "stream"}},
     {"ns_distill_grad", 5, 9,
      {"logits", "teacher_values", "teacher_ids", "lse", "grad_logits", "weights", "teacher_lse", "temperature", "stream"}},
+    {"ns_grad_norm", 3, 4, {"grads", "norm", "workspace", "stream"}},
+    {"ns_grad_clip", 4, 6, {"grads", "outs", "norm", "max_norm", "eps", "stream"}},
+    {"ns_block_norm", 4, 12,
+     {"branch", "residual", "residual_out", "out", "branch_weight", "weight", "gate", "post_norm", "residual_scale",
+      "branch_scale", "eps", "stream"}},
+    {"ns_block_norm_grad", 6, 18,
+     {"grad_residual_out", "grad_out", "branch", "residual_out", "grad_branch", "grad_residual", "branch_weight", "weight",
+      "gate", "grad_branch_weight", "grad_weight", "grad_gate", "workspace", "post_norm", "residual_scale", "branch_scale",
+      "eps", "stream"}},
+    {"ns_moe_few_tokens", 7, 8, {"x", "expert_ids", "weights", "gate_up", "down", "y", "workspace", "stream"}},
 };
 
 using Body = PyObject* (*)(const Args&);
@@ -485,6 +698,32 @@ PyMethodDef g_methods[] = {
               "teacher_lse=None, temperature=1.0, stream=None)\n--\n\n"
               "The gradient alone, from the lse that ns_distill_loss wrote; other weights are fine, but the gradient of a\n"
               "token that the loss left out (weight 0 or no entry) is NaN once it counts."),
+    NS_METHOD(9, grad_norm,
+              "ns_grad_norm(grads, norm, workspace, stream=None)\n--\n\n"
+              "norm (fp32, one value): the root of the sum of squares of all values of the tensors in the list grads,\n"
+              "which may differ in type. A tensor must be dense in memory, in any order of its dimensions."),
+    NS_METHOD(10, grad_clip,
+              "ns_grad_clip(grads, outs, norm, max_norm, eps=1e-6, stream=None)\n--\n\n"
+              "outs[i] = min(1, max_norm / (norm + eps)) * grads[i]; outs may be grads, untouched if that is 1."),
+    NS_METHOD(11, block_norm,
+              "ns_block_norm(branch, residual, residual_out, out, branch_weight=None, weight=None, gate=None, "
+              "post_norm=True, residual_scale=1.0, branch_scale=1.0, eps=1e-6, stream=None)\n--\n\n"
+              "residual_out = residual_scale * residual + branch_scale * gate * (norm of branch, or with post_norm false\n"
+              "branch itself, times branch_weight) and out = its norm times weight, all [tokens, dim]. The residual is of\n"
+              "branch's type or fp32; gate is [tokens, dim], or fp32 [tokens] or [tokens, 1]. branch, residual_out and out\n"
+              "may be None; residual_out may be residual, out may be branch or gate."),
+    NS_METHOD(12, block_norm_grad,
+              "ns_block_norm_grad(grad_residual_out, grad_out, branch, residual_out, grad_branch, grad_residual, "
+              "branch_weight=None, weight=None, gate=None, grad_branch_weight=None, grad_weight=None, grad_gate=None, "
+              "workspace=None, post_norm=True, residual_scale=1.0, branch_scale=1.0, eps=1e-6, stream=None)\n--\n\n"
+              "Gradient of ns_block_norm at the residual_out that it wrote. Either gradient may be None (zero), and so\n"
+              "may every output; the weights' gradients are fp32 [dim] and need the workspace. An output may take the\n"
+              "place of one input of its type and shape."),
+    NS_METHOD(13, moe_few_tokens,
+              "ns_moe_few_tokens(x, expert_ids, weights, gate_up, down, y, workspace, stream=None)\n--\n\n"
+              "A whole layer of experts for a few tokens: y [tokens, dim] = the sum over a token's expert_ids [tokens, k] of\n"
+              "its fp32 weight (None: 1) * down (silu(gate x) * (up x)), with gate_up [experts, 2 * ffn, dim] (gate rows\n"
+              "first) and down [experts, dim, ffn]. Negative ids go nowhere. At most 256 tokens."),
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_training", "Calls of the training-step operators on torch tensors.", -1,

@@ -232,7 +232,11 @@ int ns_profile_read(int reset, int64_t* launches, double* gpu_ms) {
 }
 
 int ns_profile_read_training(int reset, int64_t* launches, double* gpu_ms) {
-  return profile_read(kNsKinds, kKinds, reset, launches, gpu_ms);
+  return profile_read(kNsKinds, kTrainingKinds, reset, launches, gpu_ms);
+}
+
+int ns_profile_read_blocks(int reset, int64_t* launches, double* gpu_ms) {
+  return profile_read(kTrainingKinds, kKinds, reset, launches, gpu_ms);
 }
 
 }  // extern "C"
