@@ -1,5 +1,5 @@
 // A whole mixture-of-experts layer for a few tokens: each token's experts, their
-// gated products and the weighted sum, in two kernels.
+// gated products and the weighted sum, in two kernels and a short third.
 //
 //   h_s = silu(G_e x_t) * (U_e x_t)     for slot s = (t, j) with expert e
 //   y_t = sum over j of w_tj D_e h_s
@@ -26,12 +26,12 @@
 namespace nsk {
 namespace {
 
-constexpr int MF_WARPS = 8;                  // of a block
+constexpr int MF_WARPS = 16;                 // of a block, which has an SM to itself
 constexpr int MF_THREADS = 32 * MF_WARPS;
-constexpr int MF_BLOCKS = 2;                 // of an SM
+constexpr int MF_SUM_THREADS = 128;
 constexpr int MF_MAX_TOKENS = 256;
 constexpr int MF_ROWS = 32;                  // of a tile: two of the tensor instruction's
-constexpr int MF_NT = 4;                     // groups of 8 tokens that a pass over an expert's weights serves at most
+constexpr int MF_NT = 2;                     // groups of 8 slots that a pass over an expert's weights serves at most
 
 struct MoeFewParams {
   const void *x, *gate_up, *down;
@@ -43,9 +43,9 @@ struct MoeFewParams {
   const float* weights;
   void* hidden;        // [tokens * k][hidden_ld] of 4 bytes: h in fp32, or as two bf16 rows
   float* part;         // [tokens * k][part_ld]: D_e h
-  unsigned int* arrived;  // [dim / MF_ROWS]: passes whose part of these rows of y is there
   int team;            // warps that split k of a tile
   int entries;         // at most: passes over an expert
+  int held;            // words of the tokens' side that a lane holds in shared memory
   unsigned int* status;
 };
 
@@ -69,13 +69,44 @@ constexpr size_t routing_bytes(int entries, int experts, int slots) {
   return sizeof(Pass) * entries + sizeof(int) * experts + 2 * sizeof(short) * static_cast<size_t>(slots);
 }
 
-// Reads the ids, sorts the slots by expert and lists the passes; their number, and
-// the largest pass's slots. The order of the slots of a pass reaches no result:
+// Reads the ids, sorts the slots by expert and lists the passes; their number. The order of the slots of a pass reaches no result:
 // every column of a product is its own. So atomics may decide it, unless an
 // expert takes several passes, which have to be the same ones in every block.
-__device__ __forceinline__ int2 find_passes(const MoeFewParams& p, const Routing& r) {
+__device__ __forceinline__ int find_passes(const MoeFewParams& p, const Routing& r) {
   __shared__ int2 found;
   const int lane = threadIdx.x & 31, slots = p.tokens * p.k;
+  if (slots <= 32) {  // by one warp, without counts
+    if (threadIdx.x < 32) {
+      long long id = lane < slots ? load_index(p.ids, p.id_bytes, lane) : -1;
+      if (id >= p.experts) {
+        atomicOr(p.status, NS_DEV_BAD_INDEX);
+        id = -1;
+      }
+      const int e = id < 0 ? -1 : static_cast<int>(id);
+      const unsigned int same = __match_any_sync(0xffffffffu, e), before = (1u << lane) - 1;
+      const bool first = e >= 0 && !(same & before);
+      const unsigned int firsts = __ballot_sync(0xffffffffu, first);
+      int upto = first ? __popc(same) : 0;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += v;
+      }
+      const int start = __shfl_sync(0xffffffffu, upto - __popc(same), __ffs(same) - 1);  // of the expert's slots
+      const int rank = __popc(same & before);
+      if (e >= 0) r.sorted[start + rank] = static_cast<short>(lane);
+      // 32 slots make two passes of an expert at most, the second of which follows those before it
+      const unsigned int doubles = __ballot_sync(0xffffffffu, first && __popc(same) > 8 * MF_NT);
+      if (first) {
+        const int at = __popc(firsts & before) + __popc(doubles & before), n = __popc(same);
+        r.passes[at] = {e, start, min(n, 8 * MF_NT)};
+        if (n > 8 * MF_NT) r.passes[at + 1] = {e, start + 8 * MF_NT, n - 8 * MF_NT};
+      }
+      if (lane == 0) found.x = __popc(firsts) + __popc(doubles);
+    }
+    __syncthreads();
+    return found.x;
+  }
   for (int i = threadIdx.x; i < p.experts; i += MF_THREADS) r.counts[i] = 0;
   __syncthreads();
   for (int i = threadIdx.x; i < slots; i += MF_THREADS) {
@@ -125,7 +156,7 @@ __device__ __forceinline__ int2 find_passes(const MoeFewParams& p, const Routing
     }
   }
   __syncthreads();
-  return found;
+  return found.x;
 }
 
 // ------------------------------------------------------------------ products
@@ -185,42 +216,26 @@ struct Side {
   uint4 q[Q];  // PAIR: the upper parts, then the lower
   __device__ __forceinline__ uint32_t w(int i) const { return reinterpret_cast<const uint32_t*>(q)[i]; }
 
-  // A slot's row, null for none.
+  // A slot's row.
   static __device__ __forceinline__ const char* row(const MoeFewParams& p, int slot) {
-    if (slot < 0) return nullptr;
     if constexpr (HIDDEN)
       return static_cast<const char*>(p.hidden) + 4 * slot * p.hidden_ld;
     else
       return static_cast<const char*>(p.x) + sizeof(T) * (slot / p.k) * p.x_ld;
   }
-  // Word i of the values from k on.
-  static __device__ __forceinline__ const char* word(const MoeFewParams& p, const char* row, int i, int k) {
-    if constexpr (PAIR) return row + 2 * (k + i * p.hidden_ld);
-    if constexpr (HIDDEN) return row + 4 * (k + 4 * i);
-    return row + sizeof(T) * k;
-  }
+  // Its values from k on, zero from n on; `second`: bytes from the upper parts to the lower.
   template <bool VEC>
-  __device__ __forceinline__ void load(const MoeFewParams& p, const char* row, int k, int n) {
+  __device__ __forceinline__ void load(const char* row, int second, int k, int n) {
 #pragma unroll
-    for (int i = 0; i < Q; ++i) {
-      q[i] = make_uint4(0, 0, 0, 0);
-      if constexpr (HIDDEN || VEC) {
-        if (row && k < n) q[i] = load_words(word(p, row, i, k));
-      } else {
-        if (row) q[i] = load_values(reinterpret_cast<const T*>(row), k, n);
+    for (int i = 0; i < Q; ++i) q[i] = make_uint4(0, 0, 0, 0);
+    if constexpr (HIDDEN || VEC) {
+      if (k < n) {
+        constexpr int BYTES = PAIR ? 2 : HIDDEN ? 4 : sizeof(T);
+        q[0] = load_words(row + BYTES * k);
+        if constexpr (Q == 2) q[1] = load_words(row + BYTES * k + (PAIR ? second : 16));
       }
-    }
-  }
-  // The same on its way to shared memory, words 32 apart.
-  template <bool VEC>
-  static __device__ __forceinline__ void fetch(const MoeFewParams& p, const char* row, int k, int n, uint4* to) {
-    const bool there = row && k < n;
-#pragma unroll
-    for (int i = 0; i < Q; ++i) {
-      if constexpr (HIDDEN || VEC)
-        nsptx::cp_async16_shared(to + 32 * i, there ? word(p, row, i, k) : static_cast<const char*>(p.hidden), there ? 16 : 0);
-      else
-        to[32 * i] = there ? load_values(reinterpret_cast<const T*>(row), k, n) : make_uint4(0, 0, 0, 0);
+    } else {
+      q[0] = load_values(reinterpret_cast<const T*>(row), k, n);
     }
   }
 };
@@ -260,127 +275,132 @@ __device__ __forceinline__ void times(float (&c)[4], const uint4& r, const uint4
   }
 }
 
-// A warp's ring of shared memory holds the words of its next steps. Up to 16
-// slots bring their side of the products along; more are read when they are
-// used, from L1 as a rule.
-constexpr int MF_RING = 768;  // 16-byte words of a warp
-template <typename T, bool HIDDEN, int NT>
-struct Ring {
-  static constexpr bool SIDE = NT <= 2;
-  static constexpr int STAGE = 32 * (4 + (SIDE ? NT * Side<T, HIDDEN>::Q : 0));  // words of a step
-  static constexpr int AHEAD = MF_RING / STAGE - 1;                              // steps on their way, beside the one in use
-};
+// A warp's ring of shared memory: the words of the steps on their way, and of one
+// in use. The second product's tokens take more of the memory (64 experts by 16
+// slots each 95 us with two steps ahead, 109 with three and the tokens in L2).
+__host__ __device__ constexpr int ahead(bool hidden) { return hidden ? 2 : 3; }
+constexpr int MF_STAGE = 4 * 32;  // 16-byte words of a step
+__host__ __device__ constexpr int ring_words(bool hidden) { return (ahead(hidden) + 1) * MF_STAGE; }
 
 // A team of warps goes through the tiles of a block that fall to it, all passes in
 // a row: `Stream` copies the weights of a warp's next steps to its ring, into the
 // next tile and the next pass. (Held in registers they were waited for in the
-// wrong order: a warp has six counters for the loads that it waits for.)
-template <typename T, bool HIDDEN, bool VEC, int NT>
+// wrong order: a warp has six counters for the loads that it waits for.) The
+// tokens' side comes from L1, which the weights pass by. Rows past the last, and
+// columns of a pass without a slot, are computed from others and go nowhere.
+template <typename T, bool HIDDEN, bool VEC>
 struct Stream {
   using S = Side<T, HIDDEN>;
-  using R = Ring<T, HIDDEN, NT>;
-  static constexpr int V = 16 / sizeof(T);
+  static constexpr int V = 16 / sizeof(T), AHEAD = ahead(HIDDEN), RING = ring_words(HIDDEN);
   const MoeFewParams& p;
   const Routing& r;
   int tiles, end, stride;  // tiles of a pass; items (tiles of all passes) of the block; of a team
   int n, step, steps;      // values of a row, from a warp's step to its next, steps of a tile
+  int most_steps;          // of any of the team's warps
   int k0;                  // the lane's first value
   uint4* ring;
   int fill, take;
-  int item, pass, s;       // of the next copy
+  int item, k, s;          // of the next copy
   const T* at[4];          // the lane's rows there: r and r + 8 of each half of the tile
-  int values[4];           // of the rows that are there
-  const char* token[NT];   // the rows of the lane's columns there
 
   __device__ __forceinline__ Stream(const MoeFewParams& params, const Routing& routing, uint4* warp_ring, int first, int last,
                                     int team, int teams, int warp, int tiles_of_pass)
       : p(params), r(routing), tiles(tiles_of_pass), end(last), stride(teams), ring(warp_ring + (threadIdx.x & 31)), fill(0),
-        take(0), item(first + team), pass(-1), s(0) {
+        take(0), item(first + team) {
     n = static_cast<int>(HIDDEN ? p.ffn : p.dim);
     step = 4 * V * p.team;
+    most_steps = (n + step - 1) / step;
     steps = max(0, (n - warp * 4 * V + step - 1) / step);
     k0 = (warp * 4 + (threadIdx.x & 3)) * V;
+    if (steps == 0) item = end;
     rows();
 #pragma unroll
-    for (int i = 0; i < R::AHEAD; ++i) fetch();
-  }
-  // The rows of the lane's columns in a pass.
-  __device__ __forceinline__ void tokens_of(const Pass& of, const char* (&row)[NT]) const {
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      const int i = 8 * t + (threadIdx.x & 31) / 4;
-      row[t] = S::row(p, i < of.count ? r.sorted[of.first + i] : -1);
-    }
+    for (int i = 0; i < AHEAD; ++i) fetch();
   }
   __device__ __forceinline__ void rows() {
+    s = 0;
+    k = k0;
     if (item >= end) return;
     const int in = item / tiles, lane = (threadIdx.x & 31) / 4;
-    if (R::SIDE && in != pass) tokens_of(r.passes[in], token);
-    pass = in;
-    const long long e = r.passes[in].expert, j = item - in * tiles;
+    const long long e = r.passes[in].expert;
+    const int tile = item - in * tiles;
     if (HIDDEN) {  // 32 rows of D
       const T* base = static_cast<const T*>(p.down) + e * p.dim * p.ffn;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const long long d = j * MF_ROWS + 8 * i + lane;
-        values[i] = d < p.dim ? n : 0;
-        at[i] = d < p.dim ? base + d * p.ffn : base;
-      }
+      for (int i = 0; i < 4; ++i) at[i] = base + min(static_cast<long long>(tile * MF_ROWS + 8 * i + lane), p.dim - 1) * p.ffn;
     } else {       // 16 rows of G and the rows of U that go with them
       const T* base = static_cast<const T*>(p.gate_up) + 2 * e * p.ffn * p.dim;
 #pragma unroll
       for (int i = 0; i < 4; i += 2) {
-        const long long f = j * (MF_ROWS / 2) + 4 * i + lane;
-        values[i] = values[i + 1] = f < p.ffn ? n : 0;
-        at[i] = f < p.ffn ? base + f * p.dim : base;
+        at[i] = base + min(static_cast<long long>(tile * (MF_ROWS / 2) + 4 * i + lane), p.ffn - 1) * p.dim;
         at[i + 1] = at[i] + p.ffn * p.dim;
       }
     }
   }
   __device__ __forceinline__ void fetch() {
-    if (item < end && steps > 0) {
-      const int k = k0 + s * step;
+    if (item < end) {
+      uint4* const to = ring + fill;
+      if constexpr (VEC) {
+        const int bytes = k < n ? 16 : 0;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if constexpr (VEC) {
-          const bool there = k < values[i];
-          nsptx::cp_async16_upto(ring + fill + 32 * i, at[i] + (there ? k : 0), there ? 16 : 0);
-        } else {
-          ring[fill + 32 * i] = load_values(at[i], k, values[i]);
-        }
-      }
-      if constexpr (R::SIDE) {
+        for (int i = 0; i < 4; ++i) nsptx::cp_async16_upto(to + 32 * i, at[i] + k, bytes);
+      } else {
 #pragma unroll
-        for (int t = 0; t < NT; ++t) S::template fetch<VEC>(p, token[t], k, n, ring + fill + 32 * (4 + t * S::Q));
+        for (int i = 0; i < 4; ++i) to[32 * i] = load_values(at[i], k, n);
       }
+      k += step;
       if (++s == steps) {
-        s = 0;
         item += stride;
         rows();
       }
     }
     nsptx::cp_async_commit();
-    fill = fill == R::AHEAD * R::STAGE ? 0 : fill + R::STAGE;
+    fill = fill + MF_STAGE == RING ? 0 : fill + MF_STAGE;
   }
 
-  // The products of the next tile with 8 * NT slots, whose rows are `row` (where the ring does not hold them).
-  __device__ __forceinline__ void tile(const char* const (&row)[NT], float (&acc)[2][NT][4]) {
+  // The products of the next tile with 8 * NT slots, whose rows are `row` and whose words of all of the warp's steps
+  // are at `held`, if that is not null.
+  template <int NT>
+  __device__ __forceinline__ void hold(const char* const (&row)[NT], uint4* held) const {
     for (int i = 0; i < steps; ++i) {
-      nsptx::cp_async_wait<R::AHEAD - 1>();
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        S side;
+        side.template load<VEC>(row[t], static_cast<int>(2 * p.hidden_ld), k0 + i * step, n);
+#pragma unroll
+        for (int j = 0; j < S::Q; ++j) held[((i * NT + t) * S::Q + j) * 32] = side.q[j];
+      }
+    }
+  }
+  // Words that are not held are loaded a step ahead (`now`, at first those of step 0), while registers last.
+  template <int NT, bool HELD>
+  static constexpr bool EARLY = !HELD && NT * S::Q <= 4;
+  template <int NT>
+  __device__ __forceinline__ void load(const char* const (&row)[NT], S (&side)[NT], int i) const {
+#pragma unroll
+    for (int t = 0; t < NT; ++t) side[t].template load<VEC>(row[t], static_cast<int>(2 * p.hidden_ld), k0 + i * step, n);
+  }
+  template <int NT, bool HELD>
+  __device__ __forceinline__ void tile(const char* const (&row)[NT], const uint4* held, S (&now)[NT], float (&acc)[2][NT][4]) {
+    for (int i = 0; i < steps; ++i) {
+      S side[NT];
+      if constexpr (HELD) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int j = 0; j < S::Q; ++j) side[t].q[j] = held[((i * NT + t) * S::Q + j) * 32];
+      } else if constexpr (EARLY<NT, HELD>) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t) side[t] = now[t];
+        load<NT>(row, now, i + 1 < steps ? i + 1 : 0);
+      } else {
+        load<NT>(row, side, i);
+      }
+      nsptx::cp_async_wait<AHEAD - 1>();
       uint4 a[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) a[j] = ring[take + 32 * j];
-      S side[NT];
-#pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        if constexpr (R::SIDE) {
-#pragma unroll
-          for (int j = 0; j < S::Q; ++j) side[t].q[j] = ring[take + 32 * (4 + t * S::Q + j)];
-        } else {
-          side[t].template load<VEC>(p, row[t], k0 + i * step, n);
-        }
-      }
-      take = take == R::AHEAD * R::STAGE ? 0 : take + R::STAGE;
+      take = take + MF_STAGE == RING ? 0 : take + MF_STAGE;
       fetch();
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
@@ -390,98 +410,116 @@ struct Stream {
     }
   }
 };
-
 // A barrier of the team's warps, each of them together.
 __device__ __forceinline__ void team_sync(int team, int warps) {
   __syncwarp();
   asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "r"(32 * warps) : "memory");
 }
 
-// A block's share of all passes' tiles, each by a team of warps that split k:
-// use(tile, half, slot, a, b) gets the sums, a of row lane / 4 of a half of the
-// tile and b of the row 8 further, for a slot; done(tile) follows a tile's last.
-// Both in one warp of the team.
-template <typename T, bool HIDDEN, bool VEC, int NT, typename F, typename G>
-__device__ __forceinline__ void all_tiles(const MoeFewParams& p, const Routing& r, uint4* smem, int passes, int tiles, F&& use, G&& done) {
-  const long long items = static_cast<long long>(passes) * tiles;
-  const int first = static_cast<int>(items * blockIdx.x / gridDim.x), last = static_cast<int>(items * (blockIdx.x + 1) / gridDim.x);
-  const int lane = threadIdx.x & 31, warps = p.team, team = (threadIdx.x >> 5) / warps, warp = (threadIdx.x >> 5) & (warps - 1);
-  const int teams = MF_WARPS / warps;
-  Stream<T, HIDDEN, VEC, NT> stream(p, r, smem + (threadIdx.x >> 5) * MF_RING, first, last, team, teams, warp, tiles);
-  float* const sums = reinterpret_cast<float*>(smem + MF_WARPS * MF_RING) + team * warps * 8 * 32 + lane;
-  const char* row[NT] = {};
-  int held = -1;
-  for (int item = first + team; item < last; item += teams) {
-    const int pass = item / tiles, tile = item - pass * tiles;
-    const Pass& of = r.passes[pass];
-    if (!Ring<T, HIDDEN, NT>::SIDE && pass != held) stream.tokens_of(of, row);
-    held = pass;
+// What a team of warps, which split k of its tiles, has at hand.
+struct Team {
+  int warps, warp, id;   // of the team; this one's; the team's number
+  uint4* held;           // the lane's words
+  float* sums;           // [warps][8][32]
+};
+
+// A team's tiles of one pass, from `item` on: use(tile, row, slot, a, b) gets the
+// sums of rows `row` and `row` + 8 of a tile for a slot, row < 8 or 16 <= row < 24.
+template <int NT, bool HELD, typename S, typename F>
+__device__ __forceinline__ void tiles_of_pass(S& stream, const Team& team, int& item, int to, int pass, F&& use) {
+  const MoeFewParams& p = stream.p;
+  const Routing& r = stream.r;
+  const Pass of = r.passes[pass];
+  const int lane = threadIdx.x & 31;
+  const char* row[NT];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    const int i = 8 * t + lane / 4;
+    row[t] = S::S::row(p, r.sorted[of.first + (i < of.count ? i : 0)]);
+  }
+  typename S::S now[NT];
+  if constexpr (HELD) stream.template hold<NT>(row, team.held);
+  if constexpr (S::template EARLY<NT, HELD>) stream.template load<NT>(row, now, 0);
+  for (; item < to; item += stream.stride) {
+    const int tile = item - pass * stream.tiles;
     float acc[2][NT][4] = {};
-    stream.tile(row, acc);
-    if (warps > 1) {  // summed by the team's first warp, in a fixed order, 8 slots at a time
-#pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        team_sync(team, warps);  // the last ones are read
-        if (warp > 0) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) sums[(warp * 8 + i) * 32] = acc[i / 4][t][i % 4];
-        }
-        team_sync(team, warps);
-        if (warp > 0) continue;
-        for (int w = 1; w < warps; ++w)
-#pragma unroll
-          for (int i = 0; i < 8; ++i) acc[i / 4][t][i % 4] += sums[(w * 8 + i) * 32];
-      }
-      if (warp > 0) continue;
-    }
+    stream.template tile<NT, HELD>(row, team.held, now, acc);
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
+      // a lane's sums: of rows lane / 4 and 8 more of each half of the tile, columns 2 (lane % 4) and the next
+      auto give = [&](int half, int c, int at, float a, float b) {
+        const int j = 8 * t + 2 * (at & 3) + c;
+        if (j < of.count) use(tile, 16 * half + at / 4, static_cast<int>(r.sorted[of.first + j]), a, b);
+      };
+      if (team.warps == 1) {
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const int j = 8 * t + 2 * (lane & 3) + c;
-        if (j >= of.count) continue;
-        const int slot = r.sorted[of.first + j];
-        use(tile, 0, slot, acc[0][t][c], acc[0][t][c + 2]);
-        use(tile, 1, slot, acc[1][t][c], acc[1][t][c + 2]);
+        for (int q = 0; q < 4; ++q) give(q >> 1, q & 1, lane, acc[q >> 1][t][q & 1], acc[q >> 1][t][(q & 1) + 2]);
+        continue;
+      }
+      team_sync(team.id, team.warps);  // the last sums are read
+#pragma unroll
+      for (int i = 0; i < 8; ++i) team.sums[(team.warp * 8 + i) * 32 + lane] = acc[i / 4][t][i % 4];
+      team_sync(team.id, team.warps);
+      // in a fixed order of the warps
+      for (int q = team.warp; q < 4; q += team.warps) {
+        float a = 0.0f, b = 0.0f;
+        const float* from = team.sums + ((q >> 1) * 4 + (q & 1)) * 32 + lane;
+        for (int w = 0; w < team.warps; ++w, from += 8 * 32) {
+          a += from[0];
+          b += from[2 * 32];
+        }
+        give(q >> 1, q & 1, lane, a, b);
       }
     }
-    done(tile);
   }
 }
 
-// The same for passes of up to `most` slots.
-template <typename T, bool HIDDEN, bool VEC, typename F, typename G>
-__device__ __forceinline__ void all_tiles(const MoeFewParams& p, const Routing& r, uint4* smem, int2 found, int tiles, F&& use, G&& done) {
-  if (found.y <= 8)
-    all_tiles<T, HIDDEN, VEC, 1>(p, r, smem, found.x, tiles, use, done);
-  else if (found.y <= 16)
-    all_tiles<T, HIDDEN, VEC, 2>(p, r, smem, found.x, tiles, use, done);
-  else
-    all_tiles<T, HIDDEN, VEC, MF_NT>(p, r, smem, found.x, tiles, use, done);
+// A block's share of all passes' tiles.
+template <typename T, bool HIDDEN, bool VEC, typename F>
+__device__ __forceinline__ void all_tiles(const MoeFewParams& p, const Routing& r, uint4* smem, int passes, int tiles, F&& use) {
+  using S = Side<T, HIDDEN>;
+  const long long items = static_cast<long long>(passes) * tiles;
+  const int first = static_cast<int>(items * blockIdx.x / gridDim.x), last = static_cast<int>(items * (blockIdx.x + 1) / gridDim.x);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  uint4* const held = smem + MF_WARPS * ring_words(HIDDEN);
+  float* const sums = reinterpret_cast<float*>(held + MF_WARPS * p.held * 32);
+  const Team team = {p.team, warp & (p.team - 1), warp / p.team, held + warp * p.held * 32 + lane, sums + warp / p.team * p.team * 8 * 32};
+  Stream<T, HIDDEN, VEC> stream(p, r, smem + warp * ring_words(HIDDEN), first, last, team.id, MF_WARPS / p.team, team.warp, tiles);
+  for (int item = first + team.id; item < last;) {
+    const int pass = item / tiles, to = min(last, (pass + 1) * tiles), count = r.passes[pass].count;
+    const int words = S::Q * stream.most_steps;
+    if (count <= 8 && words <= p.held)
+      tiles_of_pass<1, true>(stream, team, item, to, pass, use);
+    else if (count <= 8)
+      tiles_of_pass<1, false>(stream, team, item, to, pass, use);
+    else if (2 * words <= p.held)
+      tiles_of_pass<2, true>(stream, team, item, to, pass, use);
+    else
+      tiles_of_pass<2, false>(stream, team, item, to, pass, use);
+  }
 }
 
-// Shared memory: the rings, the parts of split sums, the routing.
-constexpr int MF_SMEM_WORDS = MF_WARPS * MF_RING;
-__host__ __device__ constexpr int sums_words(int team) { return team > 1 ? MF_WARPS * 8 * 8 : 0; }
+// Shared memory: the rings, what is held of the tokens, the parts of split sums, the routing.
+__host__ __device__ constexpr int fixed_words(bool hidden) { return MF_WARPS * (ring_words(hidden) + 8 * 8); }
+constexpr int MF_HELD_WORDS = MF_WARPS * 32;
+constexpr size_t MF_SMEM = 226 * 1024;
+template <bool HIDDEN>
 __device__ __forceinline__ Routing routing_of(const MoeFewParams& p, uint4* smem) {
-  return Routing(p, smem + MF_SMEM_WORDS + sums_words(p.team));
+  return Routing(p, smem + fixed_words(HIDDEN) + p.held * MF_HELD_WORDS);
 }
 
 // h of all slots.
 template <typename T, bool VEC>
-__global__ void __launch_bounds__(MF_THREADS, MF_BLOCKS) ns_moe_few_hidden_kernel(const __grid_constant__ MoeFewParams p) {
+__global__ void __launch_bounds__(MF_THREADS, 1) ns_moe_few_hidden_kernel(const __grid_constant__ MoeFewParams p) {
   extern __shared__ uint4 few_smem[];
   nsptx::griddep_wait();
   nsptx::griddep_launch_dependents();
-  // the other kernel's counts, which no earlier kernel still uses
-  for (int i = blockIdx.x * MF_THREADS + threadIdx.x; i * MF_ROWS < p.dim; i += gridDim.x * MF_THREADS) p.arrived[i] = 0;
-  const Routing r = routing_of(p, few_smem);
-  const int2 found = find_passes(p, r);
-  const int row = (threadIdx.x & 31) / 4;
+  const Routing r = routing_of<false>(p, few_smem);
+  const int passes = find_passes(p, r);
   all_tiles<T, false, VEC>(
-      p, r, few_smem, found, static_cast<int>((p.ffn + MF_ROWS / 2 - 1) / (MF_ROWS / 2)),
-      [&](int tile, int half, int slot, float a, float b) {
-        const long long f = tile * (MF_ROWS / 2) + 8 * half + row;
+      p, r, few_smem, passes, static_cast<int>((p.ffn + MF_ROWS / 2 - 1) / (MF_ROWS / 2)),
+      [&](int tile, int row, int slot, float a, float b) {
+        const long long f = tile * (MF_ROWS / 2) + (row & 7) + row / 16 * 8;
         if (f >= p.hidden_ld) return;
         // zero up to the row's end: its last words are read whole
         const float h = f < p.ffn ? a / (1.0f + expf(-a)) * b : 0.0f;
@@ -494,79 +532,70 @@ __global__ void __launch_bounds__(MF_THREADS, MF_BLOCKS) ns_moe_few_hidden_kerne
         } else {
           static_cast<float*>(p.hidden)[slot * p.hidden_ld + f] = h;
         }
-      },
-      [](int) {});
-}
-
-// The rows of y of a tile: the sums over each token's slots, in the slots' order. A lane takes 4 rows of every
-// fourth token.
-template <typename T>
-__device__ __forceinline__ void sum_tile(const MoeFewParams& p, const Routing& r, int tile) {
-  const int lane = threadIdx.x & 31;
-  const long long d = tile * MF_ROWS + (lane & 7) * 4;
-  for (int t = lane / 8; t < p.tokens; t += 4) {
-    float y[4] = {};
-    for (int j0 = 0; j0 < p.k; j0 += 8) {
-      float4 v[8];
-      float w[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int slot = t * p.k + j0 + i;
-        const bool there = j0 + i < p.k && r.expert[slot] >= 0;
-        v[i] = there ? __ldcg(reinterpret_cast<const float4*>(p.part + slot * p.part_ld + d)) : make_float4(0, 0, 0, 0);
-        w[i] = there ? (p.weights ? p.weights[slot] : 1.0f) : 0.0f;
-      }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        y[0] = fmaf(w[i], v[i].x, y[0]);
-        y[1] = fmaf(w[i], v[i].y, y[1]);
-        y[2] = fmaf(w[i], v[i].z, y[2]);
-        y[3] = fmaf(w[i], v[i].w, y[3]);
-      }
-    }
-    T* const to = static_cast<T*>(p.y) + t * p.y_ld + d;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (d + i < p.dim) to[i] = from_float<T>(y[i]);
-  }
-}
-
-// D_e h of all slots, and, by the warp that comes last to a tile of y, its sums.
-template <typename T, bool VEC>
-__global__ void __launch_bounds__(MF_THREADS, MF_BLOCKS) ns_moe_few_sum_kernel(const __grid_constant__ MoeFewParams p) {
-  extern __shared__ uint4 few_smem[];
-  nsptx::griddep_wait();
-  nsptx::griddep_launch_dependents();
-  const Routing r = routing_of(p, few_smem);
-  const int2 found = find_passes(p, r);
-  const int passes = found.x, lane = threadIdx.x & 31, tiles = static_cast<int>((p.dim + MF_ROWS - 1) / MF_ROWS);
-  if (passes == 0) {  // no slot goes anywhere
-    for (int i = blockIdx.x * MF_WARPS + threadIdx.x / 32; i < tiles; i += gridDim.x * MF_WARPS) sum_tile<T>(p, r, i);
-    return;
-  }
-  all_tiles<T, true, VEC>(
-      p, r, few_smem, found, tiles,
-      [&](int tile, int half, int slot, float a, float b) {
-        // part_ld is a multiple of MF_ROWS
-        float* const to = p.part + slot * p.part_ld + tile * MF_ROWS + 16 * half + lane / 4;
-        to[0] = a;
-        to[8] = b;
-      },
-      [&](int tile) {
-        __threadfence();
-        __syncwarp();
-        unsigned int before = 0;
-        if (lane == 0) before = atomicAdd(&p.arrived[tile], 1u);
-        if (__shfl_sync(0xffffffffu, before, 0) != static_cast<unsigned int>(passes - 1)) return;
-        __threadfence();
-        sum_tile<T>(p, r, tile);
       });
 }
 
-// Warps that split a tile's k: as many as keep all of the card's warps busy, with 4 steps for each at least.
-int team_of(long long tiles, long long steps, int nsm) {
+// D_e h of all slots.
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(MF_THREADS, 1) ns_moe_few_down_kernel(const __grid_constant__ MoeFewParams p) {
+  extern __shared__ uint4 few_smem[];
+  nsptx::griddep_wait();
+  nsptx::griddep_launch_dependents();
+  const Routing r = routing_of<true>(p, few_smem);
+  const int passes = find_passes(p, r);
+  all_tiles<T, true, VEC>(p, r, few_smem, passes, static_cast<int>((p.dim + MF_ROWS - 1) / MF_ROWS),
+                          [&](int tile, int row, int slot, float a, float b) {
+                            // part_ld is a multiple of MF_ROWS
+                            float* const to = p.part + slot * p.part_ld + tile * MF_ROWS + row;
+                            to[0] = a;
+                            to[8] = b;
+                          });
+}
+
+// y: the sums over each token's slots, in the slots' order, 4 values a thread.
+// (Summed by the warp that brought a token's last part, the layer took one kernel
+// less and XXX more: a team waits for its warp's fence, count and loads.)
+template <typename T>
+__global__ void __launch_bounds__(MF_SUM_THREADS) ns_moe_few_sum_kernel(const __grid_constant__ MoeFewParams p) {
+  nsptx::griddep_wait();
+  nsptx::griddep_launch_dependents();
+  const int t = blockIdx.y;
+  const long long d = (static_cast<long long>(blockIdx.x) * MF_SUM_THREADS + threadIdx.x) * 4;
+  if (d >= p.dim) return;
+  float y[4] = {};
+  for (int j0 = 0; j0 < p.k; j0 += 8) {
+    float4 v[8];
+    float w[8];
+    bool there[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int slot = t * p.k + min(j0 + i, p.k - 1);
+      const long long e = load_index(p.ids, p.id_bytes, slot);
+      there[i] = j0 + i < p.k && e >= 0 && e < p.experts;
+      w[i] = p.weights ? p.weights[slot] : 1.0f;
+      v[i] = *reinterpret_cast<const float4*>(p.part + slot * p.part_ld + d);  // before it is known whether it is used
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (!there[i]) continue;
+      y[0] = fmaf(w[i], v[i].x, y[0]);
+      y[1] = fmaf(w[i], v[i].y, y[1]);
+      y[2] = fmaf(w[i], v[i].z, y[2]);
+      y[3] = fmaf(w[i], v[i].w, y[3]);
+    }
+  }
+  T* const to = static_cast<T*>(p.y) + t * p.y_ld + d;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (d + i < p.dim) to[i] = from_float<T>(y[i]);
+}
+
+// Warps that split a tile's k: as many as have some 4 steps each. A block's tiles are then few and small, so that all
+// blocks have as many, and it reads long pieces of rows. (A warp a tile: some warps have three tiles where others have
+// two.)
+int team_of(long long steps) {
   int team = 1;
-  while (team < MF_WARPS && tiles * 2 * team <= static_cast<long long>(nsm) * MF_BLOCKS * MF_WARPS && steps >= 8 * team) team *= 2;
+  while (team < MF_WARPS && steps >= 6 * team) team *= 2;
   return team;
 }
 
@@ -575,19 +604,32 @@ int launch_few(MoeFewParams p, int nsm, cudaStream_t st) {
   constexpr int VALUES = 64 / sizeof(T);  // of a step
   const int slots = p.tokens * p.k, named = std::min(p.experts, slots);
   p.entries = named + slots / (8 * MF_NT);
-  // every call sets the same limit
-  constexpr size_t MOST = sizeof(uint4) * (MF_SMEM_WORDS + sums_words(2)) + routing_bytes(1024 + MF_MAX_TOKENS * 32 / (8 * MF_NT), 1024, MF_MAX_TOKENS * 32);
-  auto launch = [&](void (*kernel)(MoeFewParams), long long tiles, long long n) {
-    p.team = team_of(tiles * named, (n + VALUES - 1) / VALUES, nsm);
+  const size_t routing = routing_bytes(p.entries, p.experts, slots);
+  static_assert(sizeof(uint4) * fixed_words(false) + routing_bytes(1024 + MF_MAX_TOKENS * 32 / (8 * MF_NT), 1024, MF_MAX_TOKENS * 32) <= MF_SMEM,
+                "shared memory of a block");
+  auto launch = [&](void (*kernel)(MoeFewParams), bool hidden, long long tiles, long long n, int words) {
+    const long long steps = (n + VALUES - 1) / VALUES;
+    p.team = team_of(steps);
+    const size_t fixed = sizeof(uint4) * fixed_words(hidden) + routing;
+    // of 8 or 16 slots; what is not held stays with L1
+    const long long room = (MF_SMEM - fixed) / (sizeof(uint4) * MF_HELD_WORDS);
+    const long long most = (steps + p.team - 1) / p.team * words;
+    p.held = static_cast<int>(p.tokens > 8 && 2 * most <= room ? 2 * most : most <= room ? most : 0);
+    const size_t smem = fixed + p.held * sizeof(uint4) * MF_HELD_WORDS;
     const long long teams = (tiles * p.entries * p.team + MF_WARPS - 1) / MF_WARPS;
-    const int blocks = static_cast<int>(std::min<long long>(nsm * MF_BLOCKS, teams));
-    const size_t smem = sizeof(uint4) * (MF_SMEM_WORDS + sums_words(p.team)) + routing_bytes(p.entries, p.experts, slots);
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(MOST));
+    const int blocks = static_cast<int>(std::min<long long>(nsm, teams));
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(MF_SMEM));
     if (e != cudaSuccess) return e;
     return nsorch::counted(nsorch::K_MOE, st, [&] { return launch_pdl(kernel, dim3(blocks), dim3(MF_THREADS), smem, st, p); });
   };
-  if (launch(ns_moe_few_hidden_kernel<T, VEC>, (p.ffn + MF_ROWS / 2 - 1) / (MF_ROWS / 2), p.dim) != cudaSuccess) return NS_ERR_CUDA;
-  return launch(ns_moe_few_sum_kernel<T, VEC>, (p.dim + MF_ROWS - 1) / MF_ROWS, p.ffn) == cudaSuccess ? NS_OK : NS_ERR_CUDA;
+  cudaError_t e = launch(ns_moe_few_hidden_kernel<T, VEC>, false, (p.ffn + MF_ROWS / 2 - 1) / (MF_ROWS / 2), p.dim, Side<T, false>::Q);
+  if (e == cudaSuccess) e = launch(ns_moe_few_down_kernel<T, VEC>, true, (p.dim + MF_ROWS - 1) / MF_ROWS, p.ffn, Side<T, true>::Q);
+  if (e != cudaSuccess) return NS_ERR_CUDA;
+  e = nsorch::counted(nsorch::K_MOE, st, [&] {
+    const unsigned int wide = static_cast<unsigned int>((p.dim + 4 * MF_SUM_THREADS - 1) / (4 * MF_SUM_THREADS));
+    return launch_pdl(ns_moe_few_sum_kernel<T>, dim3(wide, p.tokens), dim3(MF_SUM_THREADS), 0, st, p);
+  });
+  return e == cudaSuccess ? NS_OK : NS_ERR_CUDA;
 }
 
 template <typename T>
@@ -614,17 +656,16 @@ int check_few(int64_t tokens, int k, int64_t dim, int64_t ffn) {
   return NS_OK;
 }
 
-// The workspace's parts: hidden values, products, counts.
+// The workspace's parts: hidden values, products.
 struct FewParts {
   int64_t hidden_ld, part_ld;
-  uint64_t part, arrived, bytes;
+  uint64_t part, bytes;
   FewParts(int64_t tokens, int k, int64_t dim, int64_t ffn) {
     const uint64_t slots = static_cast<uint64_t>(tokens) * k;
     hidden_ld = (ffn + 7) / 8 * 8;
     part_ld = (dim + nsk::MF_ROWS - 1) / nsk::MF_ROWS * nsk::MF_ROWS;
     part = (4 * slots * hidden_ld + 255) / 256 * 256;
-    arrived = part + 4 * slots * part_ld;
-    bytes = arrived + 4 * (part_ld / nsk::MF_ROWS);
+    bytes = part + 4 * slots * part_ld;
   }
 };
 
@@ -675,7 +716,6 @@ int ns_moe_few_tokens(const void* x, int64_t x_stride, int dtype, int64_t tokens
   p.weights = weights;
   p.hidden = workspace;
   p.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + parts.part);
-  p.arrived = reinterpret_cast<unsigned int*>(static_cast<char*>(workspace) + parts.arrived);
   int dev, nsm;
   if ((rc = device_setup(&dev, &p.status, &nsm)) != NS_OK) return rc;
   cudaStream_t st = static_cast<cudaStream_t>(stream);

@@ -103,10 +103,6 @@ __device__ __forceinline__ void cp_async16(void* smem_dst, const void* src) {
 __device__ __forceinline__ void cp_async16_upto(void* smem_dst, const void* src, int bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(smem_dst)), "l"(src), "r"(bytes) : "memory");
 }
-// The same, kept in L1 for other warps that read it.
-__device__ __forceinline__ void cp_async16_shared(void* smem_dst, const void* src, int bytes) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(smem_dst)), "l"(src), "r"(bytes) : "memory");
-}
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void cp_async_wait() {

@@ -580,5 +580,5 @@ def test_launch_counts():
     nsg.ns_grad_clip([x], [x], torch.ones(1, device=DEV), 1.0)
     assert nsg.ns_profile_read_blocks(reset=True)[0] == {"grad_norm": 1, "block_norm": 1}
     run_few(x, torch.zeros(4, 1, dtype=torch.int64, device=DEV), None, torch.ones(1, 32, 64, device=DEV), torch.ones(1, 64, 16, device=DEV))
-    assert nsg.ns_profile_read_training(reset=True)[0]["moe"] == 2
+    assert nsg.ns_profile_read_training(reset=True)[0]["moe"] == 3
     ok()
