@@ -12,6 +12,11 @@
 //   s = beta g t,  z = s p,  db = r1 (z - y mean(z y))   (or z)
 //   dg = beta t u (summed over the row for a gate of the token)
 //   dw = sum over tokens of dn m,  dp = sum over tokens of s y.
+//
+// Every value is read and written once, so large calls are bound by memory. A
+// row stays in registers from its first sum to its last: a team of warps shares
+// it, 8 or 16 values a lane, and copies the rows that it takes next to shared
+// memory while it computes one.
 #include <algorithm>
 #include <climits>
 
@@ -24,6 +29,11 @@
 namespace nsk {
 namespace {
 
+constexpr int BN_WARPS = 16;        // of a block at most
+constexpr int BN_MAX_AHEAD = 3;     // rows on their way
+constexpr size_t BN_SMEM = 224 * 1024;
+// Blocks of an SM, by the registers and the copies of their rows.
+constexpr int bn_blocks(bool grad, int values) { return grad || values > 8 ? 1 : 2; }
 constexpr int BN_ANY_THREADS = 256;
 constexpr int BN_MAX_BLOCKS = 608;  // of a gradient launch, each with its own sums of dp and dw
 constexpr long long BN_MAX_DIM = 1 << 20;
@@ -43,7 +53,317 @@ struct BlockNormParams {
   int gate_kind, post, weight_fp32, norm;  // norm: whether n is wanted
   float alpha, beta, eps;
   float* partial;                  // gradient: [blocks][2][dim], dp and dw
+  int warps, teams;                // of a row, rows of a block
+  int stage, ahead;                // 16-byte words of a warp's part of a row, rows on their way
 };
+
+// ----------------------------------------------------------- rows in registers
+// The warps that share a row. Sums go through shared memory, where every other
+// one has its own place, so that one barrier is enough.
+struct RowTeam {
+  int warps, warp, id, lane, turn;
+  float* parts;  // [2][warps][3]
+  __device__ __forceinline__ RowTeam(const BlockNormParams& p, float* of_block)
+      : warps(p.warps), warp((threadIdx.x >> 5) % p.warps), id((threadIdx.x >> 5) / p.warps), lane(threadIdx.x & 31), turn(0),
+        parts(of_block + id * p.warps * 6) {}
+  template <int N>
+  __device__ __forceinline__ void sum(float (&v)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = warp_sum(v[i]);
+    if (warps == 1) return;
+    float* const to = parts + turn * warps * 3;
+    turn ^= 1;
+    if (lane == 0) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) to[warp * 3 + i] = v[i];
+    }
+    __syncwarp();
+    asm volatile("bar.sync %0, %1;" ::"r"(1 + id), "r"(32 * warps) : "memory");
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = lane < warps ? to[lane * 3 + i] : 0.0f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = warp_sum(v[i]);
+  }
+};
+
+// NV values of a lane: units of V, a unit's values side by side, units 32 * V *
+// warps apart.
+template <typename T, typename R, int NV>
+struct Lanes {
+  static constexpr int V = 16 / sizeof(T), U = NV / V, RW = sizeof(R) / sizeof(T);  // 16-byte words of a unit of R
+  const BlockNormParams& p;
+  const RowTeam& team;
+  uint4* ring;  // the warp's
+  int dim, fill, take;
+
+  __device__ __forceinline__ Lanes(const BlockNormParams& params, const RowTeam& t, uint4* smem)
+      : p(params), team(t), ring(smem + (threadIdx.x >> 5) * (params.ahead + 1) * params.stage),
+        dim(static_cast<int>(params.dim)), fill(0), take(0) {}
+  // First value of the lane's unit u, of its warp's.
+  __device__ __forceinline__ int of_warp(int u) const { return (u * team.warps + team.warp) * 32 * V; }
+  __device__ __forceinline__ int first(int u) const { return of_warp(u) + team.lane * V; }
+  __device__ __forceinline__ bool has(int u) const { return first(u) < dim; }
+  // A warp's part of a row on its way to place `at` of the stage; returns the next place.
+  template <typename E>
+  __device__ __forceinline__ int fetch(const void* base, long long ld, long long t, int at) const {
+    constexpr int W = sizeof(E) / sizeof(T), VE = 16 / sizeof(E);  // words of a unit, values of a word
+    if (base) {
+      const E* row = static_cast<const E*>(base) + t * ld;
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int j = 0; j < W; ++j) {
+          const int d = of_warp(u) + (j * 32 + team.lane) * VE;
+          if (d < dim) nsptx::cp_async16(ring + fill + at + (u * W + j) * 32 + team.lane, row + d);
+        }
+    }
+    return base ? at + U * W * 32 : at;
+  }
+  __device__ __forceinline__ void fetched() {
+    nsptx::cp_async_commit();
+    fill = fill == p.ahead * p.stage ? 0 : fill + p.stage;
+  }
+  // The row whose copies were issued first is there, for all lanes of the warp; and all have read the one before.
+  __device__ __forceinline__ void wait() const {
+    if (p.ahead == 3)
+      nsptx::cp_async_wait<2>();
+    else if (p.ahead == 2)
+      nsptx::cp_async_wait<1>();
+    else
+      nsptx::cp_async_wait<0>();
+    __syncwarp();
+  }
+  __device__ __forceinline__ void taken() { take = take == p.ahead * p.stage ? 0 : take + p.stage; }
+  template <typename E>
+  __device__ __forceinline__ int get_row(bool there, int at, float (&v)[NV]) const {
+    constexpr int W = sizeof(E) / sizeof(T), VE = 16 / sizeof(E);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int j = 0; j < W; ++j) {
+        Vec<E, VE> x = zero_vec<E, VE>();
+        if (there && has(u)) *reinterpret_cast<uint4*>(&x) = ring[take + at + u * W * 32 + team.lane * W + j];
+#pragma unroll
+        for (int i = 0; i < VE; ++i) v[u * V + j * VE + i] = get(x, i);
+      }
+    return there ? at + U * W * 32 : at;
+  }
+  template <typename E>
+  __device__ __forceinline__ void put_row(void* base, long long ld, long long t, const float (&v)[NV]) const {
+    constexpr int W = sizeof(E) / sizeof(T), VE = 16 / sizeof(E);
+    if (!base) return;
+    E* row = static_cast<E*>(base) + t * ld;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (!has(u)) continue;
+      if constexpr (W == 2) {  // 32 bytes at once
+        asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(row + first(u)), "f"(v[u * V]),
+                     "f"(v[u * V + 1]), "f"(v[u * V + 2]), "f"(v[u * V + 3]), "f"(v[u * V + 4]), "f"(v[u * V + 5]),
+                     "f"(v[u * V + 6]), "f"(v[u * V + 7])
+                     : "memory");
+      } else {
+        float f[VE];
+#pragma unroll
+        for (int i = 0; i < VE; ++i) f[i] = v[u * V + i];
+        store_vec<E, VE>(row + first(u), pack<E, VE>(f));
+      }
+    }
+  }
+  // Weights of the lane's columns, from L1 as a rule; 1 where there are none.
+  __device__ __forceinline__ void weights(const void* w, float (&v)[NV]) const {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (!w || !has(u)) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[u * V + i] = 1.0f;
+      } else if (sizeof(T) == 2 && p.weight_fp32) {
+#pragma unroll
+        for (int i = 0; i < V; i += 4) {
+          const float4 f = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(w) + first(u) + i));
+          v[u * V + i] = f.x, v[u * V + i + 1] = f.y, v[u * V + i + 2] = f.z, v[u * V + i + 3] = f.w;
+        }
+      } else {
+        Vec<T, V> x;
+        *reinterpret_cast<uint4*>(&x) = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(w) + first(u)));
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[u * V + i] = get(x, i);
+      }
+    }
+  }
+};
+
+template <typename T, typename R, int NV>
+__global__ void __launch_bounds__(32 * BN_WARPS, bn_blocks(false, NV)) ns_block_norm_kernel(const __grid_constant__ BlockNormParams p) {
+  extern __shared__ uint4 rows_smem[];
+  __shared__ float parts[BN_WARPS * 6];
+  nsptx::griddep_wait();
+  nsptx::griddep_launch_dependents();
+  RowTeam team(p, parts);
+  Lanes<T, R, NV> lanes(p, team, rows_smem);
+  const float inv_dim = 1.0f / p.dim;
+  const bool gated = p.gate_kind == VALUE_GATE;
+  const long long stride = static_cast<long long>(gridDim.x) * p.teams, t0 = static_cast<long long>(blockIdx.x) * p.teams + team.id;
+  auto fetch = [&](long long t) {
+    if (t < p.tokens) {
+      const int at = lanes.template fetch<T>(p.branch, p.branch_ld, t, 0);
+      lanes.template fetch<T>(gated ? p.gate : nullptr, p.gate_ld, t, lanes.template fetch<R>(p.x, p.x_ld, t, at));
+    }
+    lanes.fetched();
+  };
+  for (int i = 0; i < p.ahead; ++i) fetch(t0 + i * stride);
+  for (long long t = t0; t < p.tokens; t += stride) {
+    lanes.wait();
+    fetch(t + p.ahead * stride);
+    float b[NV], h[NV], w[NV];
+    const float beta = p.gate_kind == TOKEN_GATE ? p.beta * static_cast<const float*>(p.gate)[t] : p.beta;
+    const int at = lanes.template get_row<T>(p.branch, 0, b);
+    const int gate_at = lanes.template get_row<R>(true, at, h);
+    if (p.branch) {
+      lanes.weights(p.branch_weight, w);
+      float sum[1] = {0.0f};
+      if (p.post) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) sum[0] = fmaf(b[i], b[i], sum[0]);
+        team.sum(sum);
+      }
+      const float r1 = p.post ? rsqrtf(fmaf(sum[0], inv_dim, p.eps)) : 1.0f;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) b[i] = b[i] * r1 * w[i];
+      if (gated) {
+        lanes.template get_row<T>(true, gate_at, w);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) b[i] *= w[i];
+      }
+#pragma unroll
+      for (int i = 0; i < NV; ++i) h[i] = fmaf(beta, b[i], p.alpha * h[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) h[i] *= p.alpha;
+    }
+    lanes.taken();
+    lanes.template put_row<R>(p.h, p.h_ld, t, h);
+    if (!p.n) continue;
+    lanes.weights(p.weight, w);
+    float sum[1] = {0.0f};
+#pragma unroll
+    for (int i = 0; i < NV; ++i) sum[0] = fmaf(h[i], h[i], sum[0]);
+    team.sum(sum);
+    const float r2 = rsqrtf(fmaf(sum[0], inv_dim, p.eps));
+#pragma unroll
+    for (int i = 0; i < NV; ++i) h[i] = h[i] * r2 * w[i];
+    lanes.template put_row<T>(p.n, p.n_ld, t, h);
+  }
+}
+
+template <typename T, typename R, int NV>
+__global__ void __launch_bounds__(32 * BN_WARPS, bn_blocks(true, NV)) ns_block_norm_grad_kernel(const __grid_constant__ BlockNormParams p) {
+  extern __shared__ uint4 rows_smem[];
+  __shared__ float parts[BN_WARPS * 6];
+  nsptx::griddep_wait();
+  nsptx::griddep_launch_dependents();
+  RowTeam team(p, parts);
+  Lanes<T, R, NV> lanes(p, team, rows_smem);
+  const float inv_dim = 1.0f / p.dim;
+  const bool gated = p.gate_kind == VALUE_GATE;
+  const long long stride = static_cast<long long>(gridDim.x) * p.teams, t0 = static_cast<long long>(blockIdx.x) * p.teams + team.id;
+  auto fetch = [&](long long t) {
+    if (t < p.tokens) {
+      int at = lanes.template fetch<T>(p.dn, p.dn_ld, t, 0);
+      at = lanes.template fetch<R>(p.x, p.x_ld, t, at);
+      at = lanes.template fetch<R>(p.dh, p.dh_ld, t, at);
+      at = lanes.template fetch<T>(p.branch, p.branch_ld, t, at);
+      lanes.template fetch<T>(gated ? p.gate : nullptr, p.gate_ld, t, at);
+    }
+    lanes.fetched();
+  };
+  float dp[NV] = {}, dw[NV] = {};
+  for (int i = 0; i < p.ahead; ++i) fetch(t0 + i * stride);
+  for (long long t = t0; t < p.tokens; t += stride) {
+    lanes.wait();
+    fetch(t + p.ahead * stride);
+    float v[NV], h[NV], d[NV], b[NV], w[NV];
+    const float gt = p.gate_kind == TOKEN_GATE ? static_cast<const float*>(p.gate)[t] : 1.0f;
+    int at = lanes.template get_row<T>(p.dn, 0, v);
+    at = lanes.template get_row<R>(true, at, h);
+    at = lanes.template get_row<R>(p.dh, at, d);
+    at = lanes.template get_row<T>(p.branch, at, b);
+    lanes.weights(p.weight, w);
+    float sum[3] = {0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      sum[0] = fmaf(h[i], h[i], sum[0]);
+      sum[1] = fmaf(v[i] * w[i], h[i], sum[1]);
+      sum[2] = fmaf(b[i], b[i], sum[2]);
+    }
+    team.sum(sum);
+    const float r2 = p.dn ? rsqrtf(fmaf(sum[0], inv_dim, p.eps)) : 1.0f;
+    const float r1 = p.post ? rsqrtf(fmaf(sum[2], inv_dim, p.eps)) : 1.0f;
+    const float mean_vm = sum[1] * r2 * inv_dim;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const float m = h[i] * r2;
+      dw[i] = fmaf(v[i], m, dw[i]);
+      if (p.dn) d[i] = fmaf(r2, fmaf(-m, mean_vm, v[i] * w[i]), d[i]);  // t
+      h[i] = p.alpha * d[i];
+    }
+    lanes.template put_row<R>(p.dx, p.dx_ld, t, h);
+    if (p.branch) {
+      float g[NV];
+      lanes.weights(p.branch_weight, w);
+      if (gated) {
+        lanes.template get_row<T>(true, at, g);
+      } else {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) g[i] = gt;
+      }
+      float sums[2] = {0.0f, 0.0f};
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const float tb = p.beta * d[i], s = tb * g[i];
+        b[i] *= r1;                      // y
+        dp[i] = fmaf(s, b[i], dp[i]);
+        g[i] = tb * b[i] * w[i];         // of the gate
+        sums[1] += g[i];
+        d[i] = s * w[i];                 // z
+        sums[0] = fmaf(d[i], b[i], sums[0]);
+      }
+      if (gated) lanes.template put_row<T>(p.dgate, p.dgate_ld, t, g);
+      if (p.post || (p.dgate && !gated)) team.sum(sums);
+      if (p.dgate && !gated && team.warp == 0 && team.lane == 0) static_cast<float*>(p.dgate)[t] = sums[1];
+      const float mean_zy = sums[0] * inv_dim;
+      if (p.post) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) d[i] = r1 * fmaf(-b[i], mean_zy, d[i]);
+      }
+      lanes.template put_row<T>(p.dbranch, p.dbranch_ld, t, d);
+    }
+    lanes.taken();
+  }
+  if (!p.partial) return;
+  // the block's teams, in order; the rings are done with
+  nsptx::cp_async_wait<0>();
+  __syncthreads();
+  float* const joined = reinterpret_cast<float*>(rows_smem);  // [teams][2][dim]
+#pragma unroll
+  for (int u = 0; u < Lanes<T, R, NV>::U; ++u) {
+    constexpr int V = Lanes<T, R, NV>::V;
+    if (!lanes.has(u)) continue;
+    float* const to = joined + team.id * 2 * p.dim + lanes.first(u);
+#pragma unroll
+    for (int i = 0; i < V; i += 4) {
+      *reinterpret_cast<float4*>(to + i) = make_float4(dp[u * V + i], dp[u * V + i + 1], dp[u * V + i + 2], dp[u * V + i + 3]);
+      *reinterpret_cast<float4*>(to + p.dim + i) = make_float4(dw[u * V + i], dw[u * V + i + 1], dw[u * V + i + 2], dw[u * V + i + 3]);
+    }
+  }
+  __syncthreads();
+  for (int c = threadIdx.x; c < 2 * p.dim; c += blockDim.x) {
+    float sum = 0.0f;
+    for (int k = 0; k < p.teams; ++k) sum += joined[k * 2 * p.dim + c];
+    p.partial[static_cast<long long>(blockIdx.x) * 2 * p.dim + c] = sum;
+  }
+}
+
+// ------------------------------------------------------------- rows of any kind
 
 template <typename T>
 __device__ __forceinline__ float weight_of(const BlockNormParams& p, const void* w, long long d) {
@@ -202,8 +522,50 @@ __global__ void __launch_bounds__(1024) ns_block_norm_sum_kernel(const __grid_co
   if (out) out[c >= p.dim ? c - p.dim : c] = sum;
 }
 
+// NV values a lane; false if the copies of two rows do not fit an SM.
+template <typename T, typename R, int NV>
+bool launch_rows(bool grad, BlockNormParams p, int nsm, int* blocks, cudaStream_t st, cudaError_t* e) {
+  using L = Lanes<T, R, NV>;
+  constexpr int BLOCKS[2] = {bn_blocks(false, NV), bn_blocks(true, NV)};
+  p.warps = static_cast<int>((p.dim + 32 * NV - 1) / (32 * NV));
+  // few rows are spread over the SMs, many share a block
+  p.teams = static_cast<int>(std::clamp<long long>((p.tokens + nsm - 1) / nsm, 1, BN_WARPS / p.warps));
+  const int units = 32 * L::U, gate = p.gate_kind == VALUE_GATE, branch = p.branch != nullptr;
+  p.stage = grad ? units * ((p.dn != nullptr) + L::RW * (1 + (p.dh != nullptr)) + branch + gate) : units * (branch + L::RW + gate);
+  const size_t row = sizeof(uint4) * p.stage * p.warps * p.teams, rows = BN_SMEM / BLOCKS[grad] / row;
+  if (rows < 2) return false;
+  p.ahead = static_cast<int>(std::min<size_t>(BN_MAX_AHEAD, rows - 1));
+  const size_t joined = p.partial ? sizeof(float) * 2 * p.dim * p.teams : 0, smem = std::max(row * (p.ahead + 1), joined);
+  *blocks = static_cast<int>(std::min<long long>((p.tokens + p.teams - 1) / p.teams, std::min(nsm * BLOCKS[grad], BN_MAX_BLOCKS)));
+  void (*const kernel)(BlockNormParams) = grad ? ns_block_norm_grad_kernel<T, R, NV> : ns_block_norm_kernel<T, R, NV>;
+  *e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(BN_SMEM));
+  if (*e == cudaSuccess) *e = launch_pdl(kernel, dim3(*blocks), dim3(32 * p.warps * p.teams), smem, st, p);
+  return true;
+}
+
+// Whether a matrix's rows are made of aligned 16-byte words.
+bool words_ok(const void* base, long long ld, int bytes) {
+  return (reinterpret_cast<uintptr_t>(base) & 15) == 0 && (!base || ld * bytes % 16 == 0);
+}
+
 template <typename T, typename R>
 cudaError_t launch_block_norm(bool grad, const BlockNormParams& p, int nsm, int* blocks, cudaStream_t st) {
+  constexpr int X = sizeof(T), Y = sizeof(R);
+  const bool value = p.gate_kind == VALUE_GATE, many = p.tokens > 1;  // the stride of one row reaches nothing
+  auto ok = [&](const void* base, long long ld, int bytes) { return words_ok(base, many ? ld : 0, bytes); };
+  const bool words = p.dim % (16 / X) == 0 && p.dim <= 32 * BN_WARPS * 16 && ok(p.branch, p.branch_ld, X) && ok(p.x, p.x_ld, Y) &&
+                     ok(p.h, p.h_ld, Y) && ok(p.n, p.n_ld, X) && ok(p.dh, p.dh_ld, Y) && ok(p.dn, p.dn_ld, X) &&
+                     ok(p.dbranch, p.dbranch_ld, X) && ok(p.dx, p.dx_ld, Y) && ok(p.branch_weight, 0, 1) && ok(p.weight, 0, 1) &&
+                     (!value || (ok(p.gate, p.gate_ld, X) && ok(p.dgate, p.dgate_ld, X)));
+  // 32 bytes of an fp32 residual are stored at once
+  const bool wide = Y == X || ((reinterpret_cast<uintptr_t>(p.h) | reinterpret_cast<uintptr_t>(p.dx)) % 32 == 0 &&
+                               (!many || (p.h_ld % 8 == 0 && p.dx_ld % 8 == 0)));
+  if (words && wide) {
+    cudaError_t e;
+    const bool done = p.dim <= 32 * BN_WARPS * 8 ? launch_rows<T, R, 8>(grad, p, nsm, blocks, st, &e)
+                                                 : launch_rows<T, R, 16>(grad, p, nsm, blocks, st, &e);
+    if (done) return e;
+  }
   *blocks = static_cast<int>(std::min<long long>(p.tokens, std::min(nsm * 4, BN_MAX_BLOCKS)));
   if (grad) return launch_pdl(ns_block_norm_grad_any_kernel<T, R>, dim3(*blocks), dim3(BN_ANY_THREADS), 0, st, p);
   return launch_pdl(ns_block_norm_any_kernel<T, R>, dim3(*blocks), dim3(BN_ANY_THREADS), 0, st, p);
