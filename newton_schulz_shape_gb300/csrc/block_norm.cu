@@ -62,35 +62,58 @@ struct BlockNormParams {
 // one has its own place, so that one barrier is enough.
 struct RowTeam {
   int warps, warp, id, lane, turn;
-  float* parts;  // [2][warps][3]
+  float* parts;  // [2][warps][4]
   __device__ __forceinline__ RowTeam(const BlockNormParams& p, float* of_block)
       : warps(p.warps), warp((threadIdx.x >> 5) % p.warps), id((threadIdx.x >> 5) / p.warps), lane(threadIdx.x & 31), turn(0),
-        parts(of_block + id * p.warps * 6) {}
+        parts(of_block + id * p.warps * 8) {}
+  static __device__ __forceinline__ float from(float x, int distance) { return __shfl_xor_sync(0xffffffffu, x, distance); }
+  // N values, each summed over the team's lanes, in all of them. Half of the lanes go on with one half of the values:
+  // three take 6 exchanges in a warp and 6 among the warps, where one after the other they took 30.
   template <int N>
   __device__ __forceinline__ void sum(float (&v)[N]) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = warp_sum(v[i]);
-    if (warps == 1) return;
-    float* const to = parts + turn * warps * 3;
-    turn ^= 1;
-    if (lane == 0) {
-#pragma unroll
-      for (int i = 0; i < N; ++i) to[warp * 3 + i] = v[i];
+    static_assert(N <= 3, "places");
+    constexpr int S = N == 3 ? 4 : N;  // places of a warp; place i is summed in lane i * 32 / S
+    float x;
+    if constexpr (N == 1) {
+      x = v[0] + from(v[0], 16);
+      x += from(x, 8);
+    } else if constexpr (N == 2) {
+      const bool upper = lane & 16;
+      x = (upper ? v[1] : v[0]) + from(upper ? v[0] : v[1], 16);
+      x += from(x, 8);
+    } else {
+      const bool upper = lane & 16, odd = lane & 8;
+      const float a = (upper ? v[2] : v[0]) + from(upper ? v[0] : v[2], 16), b = (upper ? 0.0f : v[1]) + from(upper ? v[1] : 0.0f, 16);
+      x = (odd ? b : a) + from(odd ? a : b, 8);
     }
+#pragma unroll
+    for (int o = 4; o; o >>= 1) x += from(x, o);
+    if (warps == 1) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] = __shfl_sync(0xffffffffu, x, i * 32 / S);
+      return;
+    }
+    float* const to = parts + turn * warps * 4;
+    turn ^= 1;
+    if (lane % (32 / S) == 0) to[warp * S + lane / (32 / S)] = x;
     __syncwarp();
     asm volatile("bar.sync %0, %1;" ::"r"(1 + id), "r"(32 * warps) : "memory");
+    x = lane < warps * S ? to[lane] : 0.0f;
+    if (S == 4 && warps > 8) x += lane + 32 < warps * S ? to[lane + 32] : 0.0f;
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = lane < warps ? to[lane * 3 + i] : 0.0f;
+    for (int o = S; o < 32; o <<= 1) x += from(x, o);
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = warp_sum(v[i]);
+    for (int i = 0; i < N; ++i) v[i] = N == 1 ? x : __shfl_sync(0xffffffffu, x, i);
   }
 };
+
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 
 // NV values of a lane: units of V, a unit's values side by side, units 32 * V *
 // warps apart.
 template <typename T, typename R, int NV>
 struct Lanes {
-  static constexpr int V = 16 / sizeof(T), U = NV / V, RW = sizeof(R) / sizeof(T);  // 16-byte words of a unit of R
+  static constexpr int N = NV / 2, V = 16 / sizeof(T), U = NV / V, RW = sizeof(R) / sizeof(T);  // RW: words of a unit of R
   const BlockNormParams& p;
   const RowTeam& team;
   uint4* ring;  // the warp's
@@ -135,7 +158,7 @@ struct Lanes {
   }
   __device__ __forceinline__ void taken() { take = take == p.ahead * p.stage ? 0 : take + p.stage; }
   template <typename E>
-  __device__ __forceinline__ int get_row(bool there, int at, float (&v)[NV]) const {
+  __device__ __forceinline__ int get_row(bool there, int at, float2 (&v)[N]) const {
     constexpr int W = sizeof(E) / sizeof(T), VE = 16 / sizeof(E);
 #pragma unroll
     for (int u = 0; u < U; ++u)
@@ -144,12 +167,12 @@ struct Lanes {
         Vec<E, VE> x = zero_vec<E, VE>();
         if (there && has(u)) *reinterpret_cast<uint4*>(&x) = ring[take + at + u * W * 32 + team.lane * W + j];
 #pragma unroll
-        for (int i = 0; i < VE; ++i) v[u * V + j * VE + i] = get(x, i);
+        for (int i = 0; i < VE; i += 2) v[(u * V + j * VE + i) / 2] = make_float2(get(x, i), get(x, i + 1));
       }
     return there ? at + U * W * 32 : at;
   }
   template <typename E>
-  __device__ __forceinline__ void put_row(void* base, long long ld, long long t, const float (&v)[NV]) const {
+  __device__ __forceinline__ void put_row(void* base, long long ld, long long t, const float2 (&v)[N]) const {
     constexpr int W = sizeof(E) / sizeof(T), VE = 16 / sizeof(E);
     if (!base) return;
     E* row = static_cast<E*>(base) + t * ld;
@@ -157,36 +180,44 @@ struct Lanes {
     for (int u = 0; u < U; ++u) {
       if (!has(u)) continue;
       if constexpr (W == 2) {  // 32 bytes at once
-        asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(row + first(u)), "f"(v[u * V]),
-                     "f"(v[u * V + 1]), "f"(v[u * V + 2]), "f"(v[u * V + 3]), "f"(v[u * V + 4]), "f"(v[u * V + 5]),
-                     "f"(v[u * V + 6]), "f"(v[u * V + 7])
+        asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(row + first(u)), "f"(v[u * 4].x),
+                     "f"(v[u * 4].y), "f"(v[u * 4 + 1].x), "f"(v[u * 4 + 1].y), "f"(v[u * 4 + 2].x), "f"(v[u * 4 + 2].y),
+                     "f"(v[u * 4 + 3].x), "f"(v[u * 4 + 3].y)
                      : "memory");
       } else {
         float f[VE];
 #pragma unroll
-        for (int i = 0; i < VE; ++i) f[i] = v[u * V + i];
+        for (int i = 0; i < VE; i += 2) {
+          f[i] = v[(u * V + i) / 2].x;
+          f[i + 1] = v[(u * V + i) / 2].y;
+        }
         store_vec<E, VE>(row + first(u), pack<E, VE>(f));
       }
     }
   }
-  // Weights of the lane's columns, from L1 as a rule; 1 where there are none.
-  __device__ __forceinline__ void weights(const void* w, float (&v)[NV]) const {
+  // A token's own gate, 1 where there are none.
+  __device__ __forceinline__ float gate(long long t) const {
+    return p.gate_kind == TOKEN_GATE && t < p.tokens ? static_cast<const float*>(p.gate)[t] : 1.0f;
+  }
+  // Weights of the lane's columns; 1 where there are none.
+  __device__ __forceinline__ void weights(const void* w, float2 (&v)[N]) const {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       if (!w || !has(u)) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) v[u * V + i] = 1.0f;
+        for (int i = 0; i < V / 2; ++i) v[u * V / 2 + i] = both(1.0f);
       } else if (sizeof(T) == 2 && p.weight_fp32) {
 #pragma unroll
         for (int i = 0; i < V; i += 4) {
           const float4 f = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(w) + first(u) + i));
-          v[u * V + i] = f.x, v[u * V + i + 1] = f.y, v[u * V + i + 2] = f.z, v[u * V + i + 3] = f.w;
+          v[(u * V + i) / 2] = make_float2(f.x, f.y);
+          v[(u * V + i) / 2 + 1] = make_float2(f.z, f.w);
         }
       } else {
         Vec<T, V> x;
         *reinterpret_cast<uint4*>(&x) = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(w) + first(u)));
 #pragma unroll
-        for (int i = 0; i < V; ++i) v[u * V + i] = get(x, i);
+        for (int i = 0; i < V; i += 2) v[(u * V + i) / 2] = make_float2(get(x, i), get(x, i + 1));
       }
     }
   }
@@ -195,12 +226,15 @@ struct Lanes {
 template <typename T, typename R, int NV>
 __global__ void __launch_bounds__(32 * BN_WARPS, bn_blocks(false, NV)) ns_block_norm_kernel(const __grid_constant__ BlockNormParams p) {
   extern __shared__ uint4 rows_smem[];
-  __shared__ float parts[BN_WARPS * 6];
+  __shared__ float parts[BN_WARPS * 8];
   nsptx::griddep_wait();
   nsptx::griddep_launch_dependents();
+  constexpr int N = NV / 2;
+  constexpr bool KEEP = NV <= 8;  // the weights in registers
   RowTeam team(p, parts);
   Lanes<T, R, NV> lanes(p, team, rows_smem);
   const float inv_dim = 1.0f / p.dim;
+  const float2 alpha = both(p.alpha);
   const bool gated = p.gate_kind == VALUE_GATE;
   const long long stride = static_cast<long long>(gridDim.x) * p.teams, t0 = static_cast<long long>(blockIdx.x) * p.teams + team.id;
   auto fetch = [&](long long t) {
@@ -211,46 +245,57 @@ __global__ void __launch_bounds__(32 * BN_WARPS, bn_blocks(false, NV)) ns_block_
     lanes.fetched();
   };
   for (int i = 0; i < p.ahead; ++i) fetch(t0 + i * stride);
+  float2 pw[N], w[N];
+  if (KEEP) {
+    lanes.weights(p.branch_weight, pw);
+    lanes.weights(p.weight, w);
+  }
+  float gate = lanes.gate(t0);
   for (long long t = t0; t < p.tokens; t += stride) {
     lanes.wait();
     fetch(t + p.ahead * stride);
-    float b[NV], h[NV], w[NV];
-    const float beta = p.gate_kind == TOKEN_GATE ? p.beta * static_cast<const float*>(p.gate)[t] : p.beta;
+    float2 b[N], h[N];
+    const float2 beta = both(p.beta * gate);
+    gate = lanes.gate(t + stride);
     const int at = lanes.template get_row<T>(p.branch, 0, b);
     const int gate_at = lanes.template get_row<R>(true, at, h);
     if (p.branch) {
-      lanes.weights(p.branch_weight, w);
-      float sum[1] = {0.0f};
+      if (!KEEP) lanes.weights(p.branch_weight, pw);
+      float r1[1] = {1.0f};
       if (p.post) {
+        float2 s = both(0.0f);
 #pragma unroll
-        for (int i = 0; i < NV; ++i) sum[0] = fmaf(b[i], b[i], sum[0]);
-        team.sum(sum);
+        for (int i = 0; i < N; ++i) s = fma2(b[i], b[i], s);
+        r1[0] = s.x + s.y;
+        team.sum(r1);
+        r1[0] = rsqrtf(fmaf(r1[0], inv_dim, p.eps));
       }
-      const float r1 = p.post ? rsqrtf(fmaf(sum[0], inv_dim, p.eps)) : 1.0f;
 #pragma unroll
-      for (int i = 0; i < NV; ++i) b[i] = b[i] * r1 * w[i];
+      for (int i = 0; i < N; ++i) b[i] = mul2(mul2(b[i], both(r1[0])), pw[i]);
       if (gated) {
-        lanes.template get_row<T>(true, gate_at, w);
+        float2 g[N];
+        lanes.template get_row<T>(true, gate_at, g);
 #pragma unroll
-        for (int i = 0; i < NV; ++i) b[i] *= w[i];
+        for (int i = 0; i < N; ++i) b[i] = mul2(b[i], g[i]);
       }
 #pragma unroll
-      for (int i = 0; i < NV; ++i) h[i] = fmaf(beta, b[i], p.alpha * h[i]);
+      for (int i = 0; i < N; ++i) h[i] = fma2(beta, b[i], mul2(alpha, h[i]));
     } else {
 #pragma unroll
-      for (int i = 0; i < NV; ++i) h[i] *= p.alpha;
+      for (int i = 0; i < N; ++i) h[i] = mul2(alpha, h[i]);
     }
     lanes.taken();
     lanes.template put_row<R>(p.h, p.h_ld, t, h);
     if (!p.n) continue;
-    lanes.weights(p.weight, w);
-    float sum[1] = {0.0f};
+    if (!KEEP) lanes.weights(p.weight, w);
+    float2 s = both(0.0f);
 #pragma unroll
-    for (int i = 0; i < NV; ++i) sum[0] = fmaf(h[i], h[i], sum[0]);
-    team.sum(sum);
-    const float r2 = rsqrtf(fmaf(sum[0], inv_dim, p.eps));
+    for (int i = 0; i < N; ++i) s = fma2(h[i], h[i], s);
+    float r2[1] = {s.x + s.y};
+    team.sum(r2);
+    r2[0] = rsqrtf(fmaf(r2[0], inv_dim, p.eps));
 #pragma unroll
-    for (int i = 0; i < NV; ++i) h[i] = h[i] * r2 * w[i];
+    for (int i = 0; i < N; ++i) h[i] = mul2(mul2(h[i], both(r2[0])), w[i]);
     lanes.template put_row<T>(p.n, p.n_ld, t, h);
   }
 }
@@ -258,9 +303,11 @@ __global__ void __launch_bounds__(32 * BN_WARPS, bn_blocks(false, NV)) ns_block_
 template <typename T, typename R, int NV>
 __global__ void __launch_bounds__(32 * BN_WARPS, bn_blocks(true, NV)) ns_block_norm_grad_kernel(const __grid_constant__ BlockNormParams p) {
   extern __shared__ uint4 rows_smem[];
-  __shared__ float parts[BN_WARPS * 6];
+  __shared__ float parts[BN_WARPS * 8];
   nsptx::griddep_wait();
   nsptx::griddep_launch_dependents();
+  constexpr int N = NV / 2;
+  constexpr bool KEEP = NV <= 8;  // the weights in registers
   RowTeam team(p, parts);
   Lanes<T, R, NV> lanes(p, team, rows_smem);
   const float inv_dim = 1.0f / p.dim;
@@ -276,64 +323,80 @@ __global__ void __launch_bounds__(32 * BN_WARPS, bn_blocks(true, NV)) ns_block_n
     }
     lanes.fetched();
   };
-  float dp[NV] = {}, dw[NV] = {};
+  float2 dp[N], dw[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) dp[i] = dw[i] = both(0.0f);
   for (int i = 0; i < p.ahead; ++i) fetch(t0 + i * stride);
+  float2 pw[N], w[N];
+  if (KEEP) {
+    lanes.weights(p.branch_weight, pw);
+    lanes.weights(p.weight, w);
+  }
+  float gate = lanes.gate(t0);
   for (long long t = t0; t < p.tokens; t += stride) {
     lanes.wait();
     fetch(t + p.ahead * stride);
-    float v[NV], h[NV], d[NV], b[NV], w[NV];
-    const float gt = p.gate_kind == TOKEN_GATE ? static_cast<const float*>(p.gate)[t] : 1.0f;
+    float2 v[N], h[N], d[N], b[N];
+    const float gt = gate;
+    gate = lanes.gate(t + stride);
+    if (!KEEP) lanes.weights(p.weight, w);
     int at = lanes.template get_row<T>(p.dn, 0, v);
     at = lanes.template get_row<R>(true, at, h);
     at = lanes.template get_row<R>(p.dh, at, d);
     at = lanes.template get_row<T>(p.branch, at, b);
-    lanes.weights(p.weight, w);
-    float sum[3] = {0.0f, 0.0f, 0.0f};
+    float2 s0 = both(0.0f), s1 = s0, s2 = s0;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      sum[0] = fmaf(h[i], h[i], sum[0]);
-      sum[1] = fmaf(v[i] * w[i], h[i], sum[1]);
-      sum[2] = fmaf(b[i], b[i], sum[2]);
+    for (int i = 0; i < N; ++i) {
+      s0 = fma2(h[i], h[i], s0);
+      s1 = fma2(mul2(v[i], w[i]), h[i], s1);
+      s2 = fma2(b[i], b[i], s2);
     }
+    float sum[3] = {s0.x + s0.y, s1.x + s1.y, s2.x + s2.y};
     team.sum(sum);
-    const float r2 = p.dn ? rsqrtf(fmaf(sum[0], inv_dim, p.eps)) : 1.0f;
-    const float r1 = p.post ? rsqrtf(fmaf(sum[2], inv_dim, p.eps)) : 1.0f;
-    const float mean_vm = sum[1] * r2 * inv_dim;
+    if (p.dn) {
+      const float r = rsqrtf(fmaf(sum[0], inv_dim, p.eps)), mean = sum[1] * r * inv_dim;
+      const float2 r2 = both(r), minus = both(-mean);
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const float m = h[i] * r2;
-      dw[i] = fmaf(v[i], m, dw[i]);
-      if (p.dn) d[i] = fmaf(r2, fmaf(-m, mean_vm, v[i] * w[i]), d[i]);  // t
-      h[i] = p.alpha * d[i];
+      for (int i = 0; i < N; ++i) {
+        const float2 m = mul2(h[i], r2);
+        dw[i] = fma2(v[i], m, dw[i]);
+        d[i] = fma2(r2, fma2(m, minus, mul2(v[i], w[i])), d[i]);  // t
+      }
     }
-    lanes.template put_row<R>(p.dx, p.dx_ld, t, h);
+    if (p.dx) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) h[i] = mul2(d[i], both(p.alpha));
+      lanes.template put_row<R>(p.dx, p.dx_ld, t, h);
+    }
     if (p.branch) {
-      float g[NV];
-      lanes.weights(p.branch_weight, w);
+      const float r1 = p.post ? rsqrtf(fmaf(sum[2], inv_dim, p.eps)) : 1.0f;
+      if (!KEEP) lanes.weights(p.branch_weight, pw);
+      float2 g[N];
       if (gated) {
         lanes.template get_row<T>(true, at, g);
       } else {
 #pragma unroll
-        for (int i = 0; i < NV; ++i) g[i] = gt;
+        for (int i = 0; i < N; ++i) g[i] = both(gt);
       }
-      float sums[2] = {0.0f, 0.0f};
+      s0 = s1 = both(0.0f);
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const float tb = p.beta * d[i], s = tb * g[i];
-        b[i] *= r1;                      // y
-        dp[i] = fmaf(s, b[i], dp[i]);
-        g[i] = tb * b[i] * w[i];         // of the gate
-        sums[1] += g[i];
-        d[i] = s * w[i];                 // z
-        sums[0] = fmaf(d[i], b[i], sums[0]);
+      for (int i = 0; i < N; ++i) {
+        const float2 tb = mul2(d[i], both(p.beta)), s = mul2(tb, g[i]);
+        b[i] = mul2(b[i], both(r1));          // y
+        dp[i] = fma2(s, b[i], dp[i]);
+        g[i] = mul2(tb, mul2(b[i], pw[i]));   // of the gate
+        s1 = add2(s1, g[i]);
+        d[i] = mul2(s, pw[i]);                // z
+        s0 = fma2(d[i], b[i], s0);
       }
       if (gated) lanes.template put_row<T>(p.dgate, p.dgate_ld, t, g);
+      float sums[2] = {s0.x + s0.y, s1.x + s1.y};
       if (p.post || (p.dgate && !gated)) team.sum(sums);
       if (p.dgate && !gated && team.warp == 0 && team.lane == 0) static_cast<float*>(p.dgate)[t] = sums[1];
-      const float mean_zy = sums[0] * inv_dim;
       if (p.post) {
+        const float2 minus = both(-sums[0] * inv_dim);
 #pragma unroll
-        for (int i = 0; i < NV; ++i) d[i] = r1 * fmaf(-b[i], mean_zy, d[i]);
+        for (int i = 0; i < N; ++i) d[i] = mul2(fma2(b[i], minus, d[i]), both(r1));
       }
       lanes.template put_row<T>(p.dbranch, p.dbranch_ld, t, d);
     }
@@ -344,22 +407,23 @@ __global__ void __launch_bounds__(32 * BN_WARPS, bn_blocks(true, NV)) ns_block_n
   nsptx::cp_async_wait<0>();
   __syncthreads();
   float* const joined = reinterpret_cast<float*>(rows_smem);  // [teams][2][dim]
+  const int dim = static_cast<int>(p.dim);
 #pragma unroll
   for (int u = 0; u < Lanes<T, R, NV>::U; ++u) {
     constexpr int V = Lanes<T, R, NV>::V;
     if (!lanes.has(u)) continue;
-    float* const to = joined + team.id * 2 * p.dim + lanes.first(u);
+    float* const to = joined + team.id * 2 * dim + lanes.first(u);
 #pragma unroll
-    for (int i = 0; i < V; i += 4) {
-      *reinterpret_cast<float4*>(to + i) = make_float4(dp[u * V + i], dp[u * V + i + 1], dp[u * V + i + 2], dp[u * V + i + 3]);
-      *reinterpret_cast<float4*>(to + p.dim + i) = make_float4(dw[u * V + i], dw[u * V + i + 1], dw[u * V + i + 2], dw[u * V + i + 3]);
+    for (int i = 0; i < V / 2; ++i) {
+      *reinterpret_cast<float2*>(to + 2 * i) = dp[u * V / 2 + i];
+      *reinterpret_cast<float2*>(to + dim + 2 * i) = dw[u * V / 2 + i];
     }
   }
   __syncthreads();
-  for (int c = threadIdx.x; c < 2 * p.dim; c += blockDim.x) {
+  for (int c = threadIdx.x; c < 2 * dim; c += blockDim.x) {
     float sum = 0.0f;
-    for (int k = 0; k < p.teams; ++k) sum += joined[k * 2 * p.dim + c];
-    p.partial[static_cast<long long>(blockIdx.x) * 2 * p.dim + c] = sum;
+    for (int k = 0; k < p.teams; ++k) sum += joined[k * 2 * dim + c];
+    p.partial[static_cast<long long>(blockIdx.x) * 2 * dim + c] = sum;
   }
 }
 
