@@ -30,7 +30,7 @@ namespace nsk {
 namespace {
 
 constexpr int BN_WARPS = 16;        // of a block at most
-constexpr int BN_MAX_AHEAD = 3;     // rows on their way
+constexpr int BN_MAX_AHEAD = 2;     // rows on their way
 constexpr size_t BN_SMEM = 224 * 1024;
 // Blocks of an SM, by the registers and the copies of their rows.
 constexpr int bn_blocks(bool grad, int values) { return grad || values > 8 ? 1 : 2; }
@@ -53,6 +53,10 @@ struct BlockNormParams {
   int gate_kind, post, weight_fp32, norm;  // norm: whether n is wanted
   float alpha, beta, eps;
   float* partial;                  // gradient: [blocks][2][dim], dp and dw
+  // rows in registers: inputs and outputs by their place, with steps from row to row in bytes
+  const void* src[5];
+  void* dst[3];
+  int src_step[5], dst_step[3], place[5], wide[5];
   int warps, teams;                // of a row, rows of a block
   int stage, ahead;                // 16-byte words of a warp's part of a row, rows on their way
 };
@@ -109,38 +113,89 @@ struct RowTeam {
 
 __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 
+// Places of a warp's rows in shared memory, and their addresses in memory.
+enum Input { IN_DN = 0, IN_BRANCH = 0, IN_X = 1, IN_DH = 2, IN_GRAD_BRANCH = 3, IN_GATE = 4, INPUTS = 5 };
+enum Output { OUT_N = 0, OUT_H = 1, OUT_DBRANCH = 0, OUT_DX = 1, OUT_DGATE = 2, OUTPUTS = 3 };
+
 // NV values of a lane: units of V, a unit's values side by side, units 32 * V *
-// warps apart.
+// warps apart. Columns past the last are zero throughout.
 template <typename T, typename R, int NV>
 struct Lanes {
   static constexpr int N = NV / 2, V = 16 / sizeof(T), U = NV / V, RW = sizeof(R) / sizeof(T);  // RW: words of a unit of R
   const BlockNormParams& p;
   const RowTeam& team;
-  uint4* ring;  // the warp's
+  uint4* ring;         // the warp's
+  const uint4* zeros;  // for inputs that are not there
+  const float* weight; // the block's, [2][columns of a row]
   int dim, fill, take;
 
   __device__ __forceinline__ Lanes(const BlockNormParams& params, const RowTeam& t, uint4* smem)
-      : p(params), team(t), ring(smem + (threadIdx.x >> 5) * (params.ahead + 1) * params.stage),
-        dim(static_cast<int>(params.dim)), fill(0), take(0) {}
-  // First value of the lane's unit u, of its warp's.
+      : p(params), team(t), ring(smem + (threadIdx.x >> 5) * (params.ahead + 1) * params.stage), dim(static_cast<int>(params.dim)),
+        fill(0), take(0) {
+    uint4* const behind = smem + p.warps * p.teams * (p.ahead + 1) * p.stage;
+    zeros = behind;
+    weight = reinterpret_cast<float*>(behind + 32 * U * RW);
+  }
+  // Fills what the copies leave: zeros, the weights (by the block's first team). The block's call.
+  __device__ __forceinline__ void prepare() const {
+    uint4* const z = const_cast<uint4*>(zeros);
+    for (int i = threadIdx.x; i < 32 * U * RW; i += blockDim.x) z[i] = make_uint4(0, 0, 0, 0);
+    if (team.id == 0) {
+      put_weights(p.branch_weight, 0);
+      put_weights(p.weight, 1);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (of_warp(u) + 32 * V <= dim) continue;
+#pragma unroll
+      for (int j = 0; j < RW; ++j) {
+        const bool x = first(u) >= dim && j == 0, r = of_warp(u) + (j * 32 + team.lane) * (V / RW) >= dim;
+        for (int at = 0; at <= p.ahead * p.stage; at += p.stage)
+          for (int k = 0; k < INPUTS; ++k)
+            if (p.src[k] && (p.wide[k] ? r : x)) ring[at + p.place[k] + (u * (p.wide[k] ? RW : 1) + j) * 32 + team.lane] = make_uint4(0, 0, 0, 0);
+      }
+    }
+    __syncthreads();
+  }
+  __device__ __forceinline__ void put_weights(const void* w, int which) const {
+    float* const to = const_cast<float*>(weight) + which * team.warps * 32 * NV;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      float f[V];
+#pragma unroll
+      for (int i = 0; i < V; ++i) f[i] = first(u) < dim ? 1.0f : 0.0f;
+      if (w && first(u) < dim) {
+        if (sizeof(T) == 2 && p.weight_fp32) {
+#pragma unroll
+          for (int i = 0; i < V; i += 4)
+            *reinterpret_cast<float4*>(f + i) = *reinterpret_cast<const float4*>(static_cast<const float*>(w) + first(u) + i);
+        } else {
+          const Vec<T, V> x = load_vec<T, V>(static_cast<const T*>(w) + first(u));
+#pragma unroll
+          for (int i = 0; i < V; ++i) f[i] = get(x, i);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < V; i += 4) *reinterpret_cast<float4*>(to + first(u) + i) = make_float4(f[i], f[i + 1], f[i + 2], f[i + 3]);
+    }
+  }
+  // First value of the warp's unit u, of the lane's.
   __device__ __forceinline__ int of_warp(int u) const { return (u * team.warps + team.warp) * 32 * V; }
   __device__ __forceinline__ int first(int u) const { return of_warp(u) + team.lane * V; }
-  __device__ __forceinline__ bool has(int u) const { return first(u) < dim; }
-  // A warp's part of a row on its way to place `at` of the stage; returns the next place.
+  // The warp's part of a row of input k on its way.
   template <typename E>
-  __device__ __forceinline__ int fetch(const void* base, long long ld, long long t, int at) const {
+  __device__ __forceinline__ void fetch(int k, int t) const {
     constexpr int W = sizeof(E) / sizeof(T), VE = 16 / sizeof(E);  // words of a unit, values of a word
-    if (base) {
-      const E* row = static_cast<const E*>(base) + t * ld;
+    if (!p.src[k]) return;
+    const char* const row = static_cast<const char*>(p.src[k]) + static_cast<long long>(t) * p.src_step[k];
+    uint4* const to = ring + fill + p.place[k] + team.lane;
 #pragma unroll
-      for (int u = 0; u < U; ++u)
+    for (int u = 0; u < U; ++u)
 #pragma unroll
-        for (int j = 0; j < W; ++j) {
-          const int d = of_warp(u) + (j * 32 + team.lane) * VE;
-          if (d < dim) nsptx::cp_async16(ring + fill + at + (u * W + j) * 32 + team.lane, row + d);
-        }
-    }
-    return base ? at + U * W * 32 : at;
+      for (int j = 0; j < W; ++j) {
+        const int d = of_warp(u) + (j * 32 + team.lane) * VE;
+        if (d < dim) nsptx::cp_async16(to + (u * W + j) * 32, row + d * static_cast<int>(sizeof(E)));
+      }
   }
   __device__ __forceinline__ void fetched() {
     nsptx::cp_async_commit();
@@ -148,9 +203,7 @@ struct Lanes {
   }
   // The row whose copies were issued first is there, for all lanes of the warp; and all have read the one before.
   __device__ __forceinline__ void wait() const {
-    if (p.ahead == 3)
-      nsptx::cp_async_wait<2>();
-    else if (p.ahead == 2)
+    if (p.ahead >= 2)
       nsptx::cp_async_wait<1>();
     else
       nsptx::cp_async_wait<0>();
@@ -158,32 +211,33 @@ struct Lanes {
   }
   __device__ __forceinline__ void taken() { take = take == p.ahead * p.stage ? 0 : take + p.stage; }
   template <typename E>
-  __device__ __forceinline__ int get_row(bool there, int at, float2 (&v)[N]) const {
+  __device__ __forceinline__ void get_row(int k, float2 (&v)[N]) const {
     constexpr int W = sizeof(E) / sizeof(T), VE = 16 / sizeof(E);
+    const uint4* const from = (p.src[k] ? ring + take + p.place[k] : zeros) + team.lane * W;
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
       for (int j = 0; j < W; ++j) {
-        Vec<E, VE> x = zero_vec<E, VE>();
-        if (there && has(u)) *reinterpret_cast<uint4*>(&x) = ring[take + at + u * W * 32 + team.lane * W + j];
+        Vec<E, VE> x;
+        *reinterpret_cast<uint4*>(&x) = from[u * W * 32 + j];
 #pragma unroll
         for (int i = 0; i < VE; i += 2) v[(u * V + j * VE + i) / 2] = make_float2(get(x, i), get(x, i + 1));
       }
-    return there ? at + U * W * 32 : at;
   }
   template <typename E>
-  __device__ __forceinline__ void put_row(void* base, long long ld, long long t, const float2 (&v)[N]) const {
+  __device__ __forceinline__ void put_row(int k, int t, const float2 (&v)[N]) const {
     constexpr int W = sizeof(E) / sizeof(T), VE = 16 / sizeof(E);
-    if (!base) return;
-    E* row = static_cast<E*>(base) + t * ld;
+    if (!p.dst[k]) return;
+    char* const to = static_cast<char*>(p.dst[k]) + static_cast<long long>(t) * p.dst_step[k];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      if (!has(u)) continue;
+      E* const row = reinterpret_cast<E*>(to + first(u) * static_cast<int>(sizeof(E)));
       if constexpr (W == 2) {  // 32 bytes at once
-        asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(row + first(u)), "f"(v[u * 4].x),
-                     "f"(v[u * 4].y), "f"(v[u * 4 + 1].x), "f"(v[u * 4 + 1].y), "f"(v[u * 4 + 2].x), "f"(v[u * 4 + 2].y),
-                     "f"(v[u * 4 + 3].x), "f"(v[u * 4 + 3].y)
-                     : "memory");
+        if (first(u) < dim)
+          asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(row), "f"(v[u * 4].x), "f"(v[u * 4].y),
+                       "f"(v[u * 4 + 1].x), "f"(v[u * 4 + 1].y), "f"(v[u * 4 + 2].x), "f"(v[u * 4 + 2].y), "f"(v[u * 4 + 3].x),
+                       "f"(v[u * 4 + 3].y)
+                       : "memory");
       } else {
         float f[VE];
 #pragma unroll
@@ -191,35 +245,25 @@ struct Lanes {
           f[i] = v[(u * V + i) / 2].x;
           f[i + 1] = v[(u * V + i) / 2].y;
         }
-        store_vec<E, VE>(row + first(u), pack<E, VE>(f));
+        if (first(u) < dim) store_vec<E, VE>(row, pack<E, VE>(f));
       }
     }
   }
   // A token's own gate, 1 where there are none.
-  __device__ __forceinline__ float gate(long long t) const {
+  __device__ __forceinline__ float gate(int t) const {
     return p.gate_kind == TOKEN_GATE && t < p.tokens ? static_cast<const float*>(p.gate)[t] : 1.0f;
   }
-  // Weights of the lane's columns; 1 where there are none.
-  __device__ __forceinline__ void weights(const void* w, float2 (&v)[N]) const {
+  // Weights of the lane's columns: of the branch (0), of the norm after (1).
+  __device__ __forceinline__ void weights(int which, float2 (&v)[N]) const {
+    const float* const from = weight + which * team.warps * 32 * NV;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (!w || !has(u)) {
+    for (int u = 0; u < U; ++u)
 #pragma unroll
-        for (int i = 0; i < V / 2; ++i) v[u * V / 2 + i] = both(1.0f);
-      } else if (sizeof(T) == 2 && p.weight_fp32) {
-#pragma unroll
-        for (int i = 0; i < V; i += 4) {
-          const float4 f = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(w) + first(u) + i));
-          v[(u * V + i) / 2] = make_float2(f.x, f.y);
-          v[(u * V + i) / 2 + 1] = make_float2(f.z, f.w);
-        }
-      } else {
-        Vec<T, V> x;
-        *reinterpret_cast<uint4*>(&x) = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(w) + first(u)));
-#pragma unroll
-        for (int i = 0; i < V; i += 2) v[(u * V + i) / 2] = make_float2(get(x, i), get(x, i + 1));
+      for (int i = 0; i < V; i += 4) {
+        const float4 f = *reinterpret_cast<const float4*>(from + first(u) + i);
+        v[(u * V + i) / 2] = make_float2(f.x, f.y);
+        v[(u * V + i) / 2 + 1] = make_float2(f.z, f.w);
       }
-    }
   }
 };
 
@@ -230,37 +274,34 @@ __global__ void __launch_bounds__(32 * BN_WARPS, bn_blocks(false, NV)) ns_block_
   nsptx::griddep_wait();
   nsptx::griddep_launch_dependents();
   constexpr int N = NV / 2;
-  constexpr bool KEEP = NV <= 8;  // the weights in registers
   RowTeam team(p, parts);
   Lanes<T, R, NV> lanes(p, team, rows_smem);
   const float inv_dim = 1.0f / p.dim;
   const float2 alpha = both(p.alpha);
   const bool gated = p.gate_kind == VALUE_GATE;
-  const long long stride = static_cast<long long>(gridDim.x) * p.teams, t0 = static_cast<long long>(blockIdx.x) * p.teams + team.id;
-  auto fetch = [&](long long t) {
-    if (t < p.tokens) {
-      const int at = lanes.template fetch<T>(p.branch, p.branch_ld, t, 0);
-      lanes.template fetch<T>(gated ? p.gate : nullptr, p.gate_ld, t, lanes.template fetch<R>(p.x, p.x_ld, t, at));
+  const int tokens = static_cast<int>(p.tokens), stride = gridDim.x * p.teams, t0 = blockIdx.x * p.teams + team.id;
+  auto fetch = [&](int t) {
+    if (t < tokens) {
+      lanes.template fetch<T>(IN_BRANCH, t);
+      lanes.template fetch<R>(IN_X, t);
+      lanes.template fetch<T>(IN_GATE, t);
     }
     lanes.fetched();
   };
   for (int i = 0; i < p.ahead; ++i) fetch(t0 + i * stride);
-  float2 pw[N], w[N];
-  if (KEEP) {
-    lanes.weights(p.branch_weight, pw);
-    lanes.weights(p.weight, w);
-  }
   float gate = lanes.gate(t0);
-  for (long long t = t0; t < p.tokens; t += stride) {
+  lanes.prepare();
+  for (int t = t0; t < tokens; t += stride) {
     lanes.wait();
     fetch(t + p.ahead * stride);
     float2 b[N], h[N];
     const float2 beta = both(p.beta * gate);
     gate = lanes.gate(t + stride);
-    const int at = lanes.template get_row<T>(p.branch, 0, b);
-    const int gate_at = lanes.template get_row<R>(true, at, h);
+    float2 w[N];
+    lanes.template get_row<T>(IN_BRANCH, b);
+    lanes.template get_row<R>(IN_X, h);
     if (p.branch) {
-      if (!KEEP) lanes.weights(p.branch_weight, pw);
+      lanes.weights(0, w);
       float r1[1] = {1.0f};
       if (p.post) {
         float2 s = both(0.0f);
@@ -271,10 +312,10 @@ __global__ void __launch_bounds__(32 * BN_WARPS, bn_blocks(false, NV)) ns_block_
         r1[0] = rsqrtf(fmaf(r1[0], inv_dim, p.eps));
       }
 #pragma unroll
-      for (int i = 0; i < N; ++i) b[i] = mul2(mul2(b[i], both(r1[0])), pw[i]);
+      for (int i = 0; i < N; ++i) b[i] = mul2(mul2(b[i], both(r1[0])), w[i]);
       if (gated) {
         float2 g[N];
-        lanes.template get_row<T>(true, gate_at, g);
+        lanes.template get_row<T>(IN_GATE, g);
 #pragma unroll
         for (int i = 0; i < N; ++i) b[i] = mul2(b[i], g[i]);
       }
@@ -285,9 +326,9 @@ __global__ void __launch_bounds__(32 * BN_WARPS, bn_blocks(false, NV)) ns_block_
       for (int i = 0; i < N; ++i) h[i] = mul2(alpha, h[i]);
     }
     lanes.taken();
-    lanes.template put_row<R>(p.h, p.h_ld, t, h);
+    lanes.template put_row<R>(OUT_H, t, h);
     if (!p.n) continue;
-    if (!KEEP) lanes.weights(p.weight, w);
+    lanes.weights(1, w);
     float2 s = both(0.0f);
 #pragma unroll
     for (int i = 0; i < N; ++i) s = fma2(h[i], h[i], s);
@@ -296,7 +337,7 @@ __global__ void __launch_bounds__(32 * BN_WARPS, bn_blocks(false, NV)) ns_block_
     r2[0] = rsqrtf(fmaf(r2[0], inv_dim, p.eps));
 #pragma unroll
     for (int i = 0; i < N; ++i) h[i] = mul2(mul2(h[i], both(r2[0])), w[i]);
-    lanes.template put_row<T>(p.n, p.n_ld, t, h);
+    lanes.template put_row<T>(OUT_N, t, h);
   }
 }
 
@@ -307,19 +348,18 @@ __global__ void __launch_bounds__(32 * BN_WARPS, bn_blocks(true, NV)) ns_block_n
   nsptx::griddep_wait();
   nsptx::griddep_launch_dependents();
   constexpr int N = NV / 2;
-  constexpr bool KEEP = NV <= 8;  // the weights in registers
   RowTeam team(p, parts);
   Lanes<T, R, NV> lanes(p, team, rows_smem);
   const float inv_dim = 1.0f / p.dim;
   const bool gated = p.gate_kind == VALUE_GATE;
-  const long long stride = static_cast<long long>(gridDim.x) * p.teams, t0 = static_cast<long long>(blockIdx.x) * p.teams + team.id;
-  auto fetch = [&](long long t) {
-    if (t < p.tokens) {
-      int at = lanes.template fetch<T>(p.dn, p.dn_ld, t, 0);
-      at = lanes.template fetch<R>(p.x, p.x_ld, t, at);
-      at = lanes.template fetch<R>(p.dh, p.dh_ld, t, at);
-      at = lanes.template fetch<T>(p.branch, p.branch_ld, t, at);
-      lanes.template fetch<T>(gated ? p.gate : nullptr, p.gate_ld, t, at);
+  const int tokens = static_cast<int>(p.tokens), stride = gridDim.x * p.teams, t0 = blockIdx.x * p.teams + team.id;
+  auto fetch = [&](int t) {
+    if (t < tokens) {
+      lanes.template fetch<T>(IN_DN, t);
+      lanes.template fetch<R>(IN_X, t);
+      lanes.template fetch<R>(IN_DH, t);
+      lanes.template fetch<T>(IN_GRAD_BRANCH, t);
+      lanes.template fetch<T>(IN_GATE, t);
     }
     lanes.fetched();
   };
@@ -327,23 +367,19 @@ __global__ void __launch_bounds__(32 * BN_WARPS, bn_blocks(true, NV)) ns_block_n
 #pragma unroll
   for (int i = 0; i < N; ++i) dp[i] = dw[i] = both(0.0f);
   for (int i = 0; i < p.ahead; ++i) fetch(t0 + i * stride);
-  float2 pw[N], w[N];
-  if (KEEP) {
-    lanes.weights(p.branch_weight, pw);
-    lanes.weights(p.weight, w);
-  }
   float gate = lanes.gate(t0);
-  for (long long t = t0; t < p.tokens; t += stride) {
+  lanes.prepare();
+  for (int t = t0; t < tokens; t += stride) {
     lanes.wait();
     fetch(t + p.ahead * stride);
-    float2 v[N], h[N], d[N], b[N];
+    float2 v[N], h[N], d[N], b[N], w[N];
     const float gt = gate;
     gate = lanes.gate(t + stride);
-    if (!KEEP) lanes.weights(p.weight, w);
-    int at = lanes.template get_row<T>(p.dn, 0, v);
-    at = lanes.template get_row<R>(true, at, h);
-    at = lanes.template get_row<R>(p.dh, at, d);
-    at = lanes.template get_row<T>(p.branch, at, b);
+    lanes.weights(1, w);
+    lanes.template get_row<T>(IN_DN, v);
+    lanes.template get_row<R>(IN_X, h);
+    lanes.template get_row<R>(IN_DH, d);
+    lanes.template get_row<T>(IN_GRAD_BRANCH, b);
     float2 s0 = both(0.0f), s1 = s0, s2 = s0;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
@@ -366,14 +402,14 @@ __global__ void __launch_bounds__(32 * BN_WARPS, bn_blocks(true, NV)) ns_block_n
     if (p.dx) {
 #pragma unroll
       for (int i = 0; i < N; ++i) h[i] = mul2(d[i], both(p.alpha));
-      lanes.template put_row<R>(p.dx, p.dx_ld, t, h);
+      lanes.template put_row<R>(OUT_DX, t, h);
     }
     if (p.branch) {
       const float r1 = p.post ? rsqrtf(fmaf(sum[2], inv_dim, p.eps)) : 1.0f;
-      if (!KEEP) lanes.weights(p.branch_weight, pw);
+      lanes.weights(0, w);
       float2 g[N];
       if (gated) {
-        lanes.template get_row<T>(true, at, g);
+        lanes.template get_row<T>(IN_GATE, g);
       } else {
 #pragma unroll
         for (int i = 0; i < N; ++i) g[i] = both(gt);
@@ -384,12 +420,12 @@ __global__ void __launch_bounds__(32 * BN_WARPS, bn_blocks(true, NV)) ns_block_n
         const float2 tb = mul2(d[i], both(p.beta)), s = mul2(tb, g[i]);
         b[i] = mul2(b[i], both(r1));          // y
         dp[i] = fma2(s, b[i], dp[i]);
-        g[i] = mul2(tb, mul2(b[i], pw[i]));   // of the gate
+        g[i] = mul2(tb, mul2(b[i], w[i]));    // of the gate
         s1 = add2(s1, g[i]);
-        d[i] = mul2(s, pw[i]);                // z
+        d[i] = mul2(s, w[i]);                 // z
         s0 = fma2(d[i], b[i], s0);
       }
-      if (gated) lanes.template put_row<T>(p.dgate, p.dgate_ld, t, g);
+      if (gated) lanes.template put_row<T>(OUT_DGATE, t, g);
       float sums[2] = {s0.x + s0.y, s1.x + s1.y};
       if (p.post || (p.dgate && !gated)) team.sum(sums);
       if (p.dgate && !gated && team.warp == 0 && team.lane == 0) static_cast<float*>(p.dgate)[t] = sums[1];
@@ -398,7 +434,7 @@ __global__ void __launch_bounds__(32 * BN_WARPS, bn_blocks(true, NV)) ns_block_n
 #pragma unroll
         for (int i = 0; i < N; ++i) d[i] = mul2(fma2(b[i], minus, d[i]), both(r1));
       }
-      lanes.template put_row<T>(p.dbranch, p.dbranch_ld, t, d);
+      lanes.template put_row<T>(OUT_DBRANCH, t, d);
     }
     lanes.taken();
   }
@@ -411,7 +447,7 @@ __global__ void __launch_bounds__(32 * BN_WARPS, bn_blocks(true, NV)) ns_block_n
 #pragma unroll
   for (int u = 0; u < Lanes<T, R, NV>::U; ++u) {
     constexpr int V = Lanes<T, R, NV>::V;
-    if (!lanes.has(u)) continue;
+    if (lanes.first(u) >= dim) continue;
     float* const to = joined + team.id * 2 * dim + lanes.first(u);
 #pragma unroll
     for (int i = 0; i < V / 2; ++i) {
@@ -586,7 +622,7 @@ __global__ void __launch_bounds__(1024) ns_block_norm_sum_kernel(const __grid_co
   if (out) out[c >= p.dim ? c - p.dim : c] = sum;
 }
 
-// NV values a lane; false if the copies of two rows do not fit an SM.
+// NV values a lane; false if the copies of two rows do not fit an SM, or steps an int.
 template <typename T, typename R, int NV>
 bool launch_rows(bool grad, BlockNormParams p, int nsm, int* blocks, cudaStream_t st, cudaError_t* e) {
   using L = Lanes<T, R, NV>;
@@ -594,12 +630,45 @@ bool launch_rows(bool grad, BlockNormParams p, int nsm, int* blocks, cudaStream_
   p.warps = static_cast<int>((p.dim + 32 * NV - 1) / (32 * NV));
   // few rows are spread over the SMs, many share a block
   p.teams = static_cast<int>(std::clamp<long long>((p.tokens + nsm - 1) / nsm, 1, BN_WARPS / p.warps));
-  const int units = 32 * L::U, gate = p.gate_kind == VALUE_GATE, branch = p.branch != nullptr;
-  p.stage = grad ? units * ((p.dn != nullptr) + L::RW * (1 + (p.dh != nullptr)) + branch + gate) : units * (branch + L::RW + gate);
-  const size_t row = sizeof(uint4) * p.stage * p.warps * p.teams, rows = BN_SMEM / BLOCKS[grad] / row;
+  struct {
+    const void* at;
+    long long ld;
+    bool wide;
+  } const in[2][INPUTS] = {{{p.branch, p.branch_ld, false}, {p.x, p.x_ld, true}, {}, {}, {p.gate, p.gate_ld, false}},
+                           {{p.dn, p.dn_ld, false}, {p.x, p.x_ld, true}, {p.dh, p.dh_ld, true}, {p.branch, p.branch_ld, false}, {p.gate, p.gate_ld, false}}};
+  struct {
+    void* at;
+    long long ld;
+    bool wide;
+  } const out[2][OUTPUTS] = {{{p.n, p.n_ld, false}, {p.h, p.h_ld, true}, {}},
+                             {{p.dbranch, p.dbranch_ld, false}, {p.dx, p.dx_ld, true}, {p.dgate, p.dgate_ld, false}}};
+  const bool value = p.gate_kind == VALUE_GATE;
+  auto step = [&](long long ld, bool wide, int* bytes) {
+    const long long b = p.tokens > 1 ? ld * static_cast<long long>(wide ? sizeof(R) : sizeof(T)) : 0;
+    *bytes = static_cast<int>(b);
+    return b <= INT_MAX / 4;
+  };
+  for (int k = 0; k < INPUTS; ++k) {
+    const auto& i = in[grad][k];
+    p.src[k] = k == IN_GATE && !value ? nullptr : i.at;
+    p.wide[k] = i.wide && L::RW == 2;
+    p.place[k] = p.stage;
+    if (p.src[k]) p.stage += 32 * L::U * (i.wide ? L::RW : 1);
+    if (p.src[k] && !step(i.ld, i.wide, &p.src_step[k])) return false;
+  }
+  for (int k = 0; k < OUTPUTS; ++k) {
+    const auto& o = out[grad][k];
+    p.dst[k] = k == OUT_DGATE && !value ? nullptr : o.at;
+    if (p.dst[k] && !step(o.ld, o.wide, &p.dst_step[k])) return false;
+  }
+  if (p.tokens > INT_MAX / 4) return false;
+  // a block's rows, zeros, weights
+  const size_t row = sizeof(uint4) * p.stage * p.warps * p.teams;
+  const size_t more = sizeof(uint4) * 32 * L::U * L::RW + sizeof(float) * 2 * 32 * NV * p.warps;
+  const size_t rows = (BN_SMEM / BLOCKS[grad] - more) / row;
   if (rows < 2) return false;
   p.ahead = static_cast<int>(std::min<size_t>(BN_MAX_AHEAD, rows - 1));
-  const size_t joined = p.partial ? sizeof(float) * 2 * p.dim * p.teams : 0, smem = std::max(row * (p.ahead + 1), joined);
+  const size_t joined = p.partial ? sizeof(float) * 2 * p.dim * p.teams : 0, smem = std::max(row * (p.ahead + 1) + more, joined);
   *blocks = static_cast<int>(std::min<long long>((p.tokens + p.teams - 1) / p.teams, std::min(nsm * BLOCKS[grad], BN_MAX_BLOCKS)));
   void (*const kernel)(BlockNormParams) = grad ? ns_block_norm_grad_kernel<T, R, NV> : ns_block_norm_kernel<T, R, NV>;
   *e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(BN_SMEM));
