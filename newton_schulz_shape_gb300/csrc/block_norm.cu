@@ -15,8 +15,10 @@
 //
 // Every value is read and written once, so large calls are bound by memory. A
 // row stays in registers from its first sum to its last: a team of warps shares
-// it, 8 or 16 values a lane, and copies the rows that it takes next to shared
-// memory while it computes one.
+// it, 8 or 16 values a lane, and copies the row that it takes next to shared
+// memory while it computes one. (With two or three rows on their way the reads
+// and the writes disturb each other: 16384 rows of 4096 bf16 with an fp32
+// residual 134 us, with one 121.)
 #include <algorithm>
 #include <climits>
 
@@ -30,7 +32,6 @@ namespace nsk {
 namespace {
 
 constexpr int BN_WARPS = 16;        // of a block at most
-constexpr int BN_MAX_AHEAD = 2;     // rows on their way
 constexpr size_t BN_SMEM = 224 * 1024;
 // Blocks of an SM, by the registers and the copies of their rows.
 constexpr int bn_blocks(bool grad, int values) { return grad || values > 8 ? 1 : 2; }
@@ -58,8 +59,14 @@ struct BlockNormParams {
   void* dst[3];
   int src_step[5], dst_step[3], place[5], wide[5];
   int warps, teams;                // of a row, rows of a block
-  int stage, ahead;                // 16-byte words of a warp's part of a row, rows on their way
+  int stage;                       // 16-byte words of a warp's part of a row
 };
+
+template <typename T>
+__device__ __forceinline__ float weight_of(const BlockNormParams& p, const void* w, long long d) {
+  if (!w) return 1.0f;
+  return p.weight_fp32 ? static_cast<const float*>(w)[d] : to_float(static_cast<const T*>(w)[d]);
+}
 
 // ----------------------------------------------------------- rows in registers
 // The warps that share a row. Sums go through shared memory, where every other
@@ -130,9 +137,9 @@ struct Lanes {
   int dim, fill, take;
 
   __device__ __forceinline__ Lanes(const BlockNormParams& params, const RowTeam& t, uint4* smem)
-      : p(params), team(t), ring(smem + (threadIdx.x >> 5) * (params.ahead + 1) * params.stage), dim(static_cast<int>(params.dim)),
+      : p(params), team(t), ring(smem + (threadIdx.x >> 5) * 2 * params.stage), dim(static_cast<int>(params.dim)),
         fill(0), take(0) {
-    uint4* const behind = smem + p.warps * p.teams * (p.ahead + 1) * p.stage;
+    uint4* const behind = smem + p.warps * p.teams * 2 * p.stage;
     zeros = behind;
     weight = reinterpret_cast<float*>(behind + 32 * U * RW);
   }
@@ -150,7 +157,7 @@ struct Lanes {
 #pragma unroll
       for (int j = 0; j < RW; ++j) {
         const bool x = first(u) >= dim && j == 0, r = of_warp(u) + (j * 32 + team.lane) * (V / RW) >= dim;
-        for (int at = 0; at <= p.ahead * p.stage; at += p.stage)
+        for (int at = 0; at <= p.stage; at += p.stage)
           for (int k = 0; k < INPUTS; ++k)
             if (p.src[k] && (p.wide[k] ? r : x)) ring[at + p.place[k] + u * (p.wide[k] ? RW : 1) * 32 + (p.wide[k] ? place<RW>(j * 32 + team.lane) : team.lane)] = make_uint4(0, 0, 0, 0);
       }
@@ -208,17 +215,14 @@ struct Lanes {
   }
   __device__ __forceinline__ void fetched() {
     nsptx::cp_async_commit();
-    fill = fill == p.ahead * p.stage ? 0 : fill + p.stage;
+    fill = p.stage - fill;
   }
-  // The row whose copies were issued first is there, for all lanes of the warp; and all have read the one before.
-  __device__ __forceinline__ void wait() const {
-    if (p.ahead == 2)
-      nsptx::cp_async_wait<1>();
-    else
-      nsptx::cp_async_wait<0>();
+  // The row on its way is there, for all lanes of the warp; and all have read the one before.
+  __device__ __forceinline__ void wait(int) const {
+    nsptx::cp_async_wait<0>();
     __syncwarp();
   }
-  __device__ __forceinline__ void taken() { take = take == p.ahead * p.stage ? 0 : take + p.stage; }
+  __device__ __forceinline__ void taken() { take = p.stage - take; }
   template <typename E>
   __device__ __forceinline__ void get_row(int k, float2 (&v)[N]) const {
     constexpr int W = sizeof(E) / sizeof(T), VE = 16 / sizeof(E);
@@ -258,6 +262,18 @@ struct Lanes {
       }
     }
   }
+  // A lane's sums of the weights' gradients to their columns of [2][dim].
+  __device__ __forceinline__ void join(float* to, const float2 (&dp)[N], const float2 (&dw)[N]) const {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (first(u) >= dim) continue;
+#pragma unroll
+      for (int i = 0; i < V / 2; ++i) {
+        *reinterpret_cast<float2*>(to + first(u) + 2 * i) = dp[u * V / 2 + i];
+        *reinterpret_cast<float2*>(to + dim + first(u) + 2 * i) = dw[u * V / 2 + i];
+      }
+    }
+  }
   // A token's own gate, 1 where there are none.
   __device__ __forceinline__ float gate(int t) const {
     return p.gate_kind == TOKEN_GATE && t < p.tokens ? static_cast<const float*>(p.gate)[t] : 1.0f;
@@ -276,7 +292,69 @@ struct Lanes {
   }
 };
 
-template <typename T, typename R, int NV>
+// The same for rows of any width, stride and alignment, value by value from
+// memory: value i of a lane is column i * 32 * warps + its place in the team.
+template <typename T, typename R, int NV, bool GRAD>
+struct Singles {
+  static constexpr int N = NV / 2;
+  const BlockNormParams& p;
+  const RowTeam& team;
+  const float* weight;  // the block's, [2][columns of a row]
+  int dim, at, step, row;
+
+  __device__ __forceinline__ Singles(const BlockNormParams& params, const RowTeam& t, uint4* smem)
+      : p(params), team(t), weight(reinterpret_cast<float*>(smem)), dim(static_cast<int>(params.dim)), at(t.warp * 32 + t.lane),
+        step(32 * t.warps), row(0) {}
+  __device__ __forceinline__ void prepare() const {
+    float* const to = const_cast<float*>(weight);
+    for (int i = threadIdx.x; i < step * NV; i += blockDim.x) {
+      to[i] = i < dim ? weight_of<T>(p, p.branch_weight, i) : 0.0f;
+      to[step * NV + i] = i < dim ? weight_of<T>(p, p.weight, i) : 0.0f;
+    }
+    __syncthreads();
+  }
+  template <typename E>
+  __device__ __forceinline__ void fetch(int, int) const {}
+  __device__ __forceinline__ void fetched() const {}
+  __device__ __forceinline__ void wait(int t) { row = t; }
+  __device__ __forceinline__ void taken() const {}
+  template <typename E>
+  __device__ __forceinline__ void get_row(int k, float2 (&v)[N]) const {
+    const E* const from = reinterpret_cast<const E*>(static_cast<const char*>(p.src[k]) + static_cast<long long>(row) * p.src_step[k]);
+    float f[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) f[i] = p.src[k] && at + i * step < dim ? to_float(from[at + i * step]) : 0.0f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = make_float2(f[2 * i], f[2 * i + 1]);
+  }
+  template <typename E>
+  __device__ __forceinline__ void put_row(int k, int t, const float2 (&v)[N]) const {
+    if (!p.dst[k]) return;
+    E* const to = reinterpret_cast<E*>(static_cast<char*>(p.dst[k]) + static_cast<long long>(t) * p.dst_step[k]);
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if (at + i * step < dim) to[at + i * step] = from_float<E>(i % 2 ? v[i / 2].y : v[i / 2].x);
+  }
+  __device__ __forceinline__ float gate(int t) const {
+    return p.gate_kind == TOKEN_GATE && t < p.tokens ? static_cast<const float*>(p.gate)[t] : 1.0f;
+  }
+  __device__ __forceinline__ void weights(int which, float2 (&v)[N]) const {
+    const float* const from = weight + which * step * NV + at;
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = make_float2(from[2 * i * step], from[(2 * i + 1) * step]);
+  }
+  // A lane's sums of the weights' gradients to their columns of [2][dim].
+  __device__ __forceinline__ void join(float* to, const float2 (&dp)[N], const float2 (&dw)[N]) const {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      if (at + i * step >= dim) continue;
+      to[at + i * step] = i % 2 ? dp[i / 2].y : dp[i / 2].x;
+      to[dim + at + i * step] = i % 2 ? dw[i / 2].y : dw[i / 2].x;
+    }
+  }
+};
+
+template <typename T, typename R, int NV, bool WORDS>
 __global__ void __launch_bounds__(32 * BN_WARPS, bn_blocks(false, NV)) ns_block_norm_kernel(const __grid_constant__ BlockNormParams p) {
   extern __shared__ uint4 rows_smem[];
   __shared__ float parts[BN_WARPS * 8];
@@ -284,7 +362,7 @@ __global__ void __launch_bounds__(32 * BN_WARPS, bn_blocks(false, NV)) ns_block_
   nsptx::griddep_launch_dependents();
   constexpr int N = NV / 2;
   RowTeam team(p, parts);
-  Lanes<T, R, NV, false> lanes(p, team, rows_smem);
+  typename std::conditional<WORDS, Lanes<T, R, NV, false>, Singles<T, R, NV, false>>::type lanes(p, team, rows_smem);
   const float inv_dim = 1.0f / p.dim;
   const float2 alpha = both(p.alpha);
   const bool gated = p.gate_kind == VALUE_GATE;
@@ -297,12 +375,12 @@ __global__ void __launch_bounds__(32 * BN_WARPS, bn_blocks(false, NV)) ns_block_
     }
     lanes.fetched();
   };
-  for (int i = 0; i < p.ahead; ++i) fetch(t0 + i * stride);
+  fetch(t0);
   float gate = lanes.gate(t0);
   lanes.prepare();
   for (int t = t0; t < tokens; t += stride) {
-    lanes.wait();
-    fetch(t + p.ahead * stride);
+    lanes.wait(t);
+    fetch(t + stride);
     float2 b[N], h[N];
     const float2 beta = both(p.beta * gate);
     gate = lanes.gate(t + stride);
@@ -350,7 +428,7 @@ __global__ void __launch_bounds__(32 * BN_WARPS, bn_blocks(false, NV)) ns_block_
   }
 }
 
-template <typename T, typename R, int NV>
+template <typename T, typename R, int NV, bool WORDS>
 __global__ void __launch_bounds__(32 * BN_WARPS, bn_blocks(true, NV)) ns_block_norm_grad_kernel(const __grid_constant__ BlockNormParams p) {
   extern __shared__ uint4 rows_smem[];
   __shared__ float parts[BN_WARPS * 8];
@@ -358,7 +436,7 @@ __global__ void __launch_bounds__(32 * BN_WARPS, bn_blocks(true, NV)) ns_block_n
   nsptx::griddep_launch_dependents();
   constexpr int N = NV / 2;
   RowTeam team(p, parts);
-  Lanes<T, R, NV, true> lanes(p, team, rows_smem);
+  typename std::conditional<WORDS, Lanes<T, R, NV, true>, Singles<T, R, NV, true>>::type lanes(p, team, rows_smem);
   const float inv_dim = 1.0f / p.dim;
   const bool gated = p.gate_kind == VALUE_GATE;
   const int tokens = static_cast<int>(p.tokens), stride = gridDim.x * p.teams, t0 = blockIdx.x * p.teams + team.id;
@@ -375,12 +453,12 @@ __global__ void __launch_bounds__(32 * BN_WARPS, bn_blocks(true, NV)) ns_block_n
   float2 dp[N], dw[N];
 #pragma unroll
   for (int i = 0; i < N; ++i) dp[i] = dw[i] = both(0.0f);
-  for (int i = 0; i < p.ahead; ++i) fetch(t0 + i * stride);
+  fetch(t0);
   float gate = lanes.gate(t0);
   lanes.prepare();
   for (int t = t0; t < tokens; t += stride) {
-    lanes.wait();
-    fetch(t + p.ahead * stride);
+    lanes.wait(t);
+    fetch(t + stride);
     float2 v[N], h[N], d[N], b[N], w[N];
     const float gt = gate;
     gate = lanes.gate(t + stride);
@@ -453,17 +531,7 @@ __global__ void __launch_bounds__(32 * BN_WARPS, bn_blocks(true, NV)) ns_block_n
   __syncthreads();
   float* const joined = reinterpret_cast<float*>(rows_smem);  // [teams][2][dim]
   const int dim = static_cast<int>(p.dim);
-#pragma unroll
-  for (int u = 0; u < Lanes<T, R, NV, true>::U; ++u) {
-    constexpr int V = Lanes<T, R, NV, true>::V;
-    if (lanes.first(u) >= dim) continue;
-    float* const to = joined + team.id * 2 * dim + lanes.first(u);
-#pragma unroll
-    for (int i = 0; i < V / 2; ++i) {
-      *reinterpret_cast<float2*>(to + 2 * i) = dp[u * V / 2 + i];
-      *reinterpret_cast<float2*>(to + dim + 2 * i) = dw[u * V / 2 + i];
-    }
-  }
+  lanes.join(joined + team.id * 2 * dim, dp, dw);
   __syncthreads();
   for (int c = threadIdx.x; c < 2 * dim; c += blockDim.x) {
     float sum = 0.0f;
@@ -473,12 +541,6 @@ __global__ void __launch_bounds__(32 * BN_WARPS, bn_blocks(true, NV)) ns_block_n
 }
 
 // ------------------------------------------------------------- rows of any kind
-
-template <typename T>
-__device__ __forceinline__ float weight_of(const BlockNormParams& p, const void* w, long long d) {
-  if (!w) return 1.0f;
-  return p.weight_fp32 ? static_cast<const float*>(w)[d] : to_float(static_cast<const T*>(w)[d]);
-}
 
 // Sums of a and b over the block, in all of its threads.
 __device__ __forceinline__ float2 block_sum(float2 v, float2* parts) {
@@ -632,7 +694,7 @@ __global__ void __launch_bounds__(1024) ns_block_norm_sum_kernel(const __grid_co
 }
 
 // NV values a lane; false if the copies of two rows do not fit an SM, or steps an int.
-template <typename T, typename R, int NV>
+template <typename T, typename R, int NV, bool WORDS>
 bool launch_rows(bool grad, BlockNormParams p, int nsm, int* blocks, cudaStream_t st, cudaError_t* e) {
   using L = Lanes<T, R, NV, true>;
   constexpr int BLOCKS[2] = {bn_blocks(false, NV), bn_blocks(true, NV)};
@@ -662,7 +724,7 @@ bool launch_rows(bool grad, BlockNormParams p, int nsm, int* blocks, cudaStream_
     p.src[k] = k == IN_GATE && !value ? nullptr : i.at;
     p.wide[k] = i.wide && L::RW == 2;
     p.place[k] = p.stage;
-    if (p.src[k]) p.stage += 32 * L::U * (i.wide ? L::RW : 1);
+    if (WORDS && p.src[k]) p.stage += 32 * L::U * (i.wide ? L::RW : 1);
     if (p.src[k] && !step(i.ld, i.wide, &p.src_step[k])) return false;
   }
   for (int k = 0; k < OUTPUTS; ++k) {
@@ -673,13 +735,11 @@ bool launch_rows(bool grad, BlockNormParams p, int nsm, int* blocks, cudaStream_
   if (p.tokens > INT_MAX / 4) return false;
   // a block's rows, zeros, weights
   const size_t row = sizeof(uint4) * p.stage * p.warps * p.teams;
-  const size_t more = sizeof(uint4) * 32 * L::U * L::RW + sizeof(float) * 2 * 32 * NV * p.warps;
-  const size_t rows = (BN_SMEM / BLOCKS[grad] - more) / row;
-  if (rows < 2) return false;
-  p.ahead = static_cast<int>(std::min<size_t>(BN_MAX_AHEAD, rows - 1));
-  const size_t joined = p.partial ? sizeof(float) * 2 * p.dim * p.teams : 0, smem = std::max(row * (p.ahead + 1) + more, joined);
+  const size_t more = (WORDS ? sizeof(uint4) * 32 * L::U * L::RW : 0) + sizeof(float) * 2 * 32 * NV * p.warps;
+  if (2 * row + more > BN_SMEM / BLOCKS[grad]) return false;
+  const size_t joined = p.partial ? sizeof(float) * 2 * p.dim * p.teams : 0, smem = std::max(2 * row + more, joined);
   *blocks = static_cast<int>(std::min<long long>((p.tokens + p.teams - 1) / p.teams, std::min(nsm * BLOCKS[grad], BN_MAX_BLOCKS)));
-  void (*const kernel)(BlockNormParams) = grad ? ns_block_norm_grad_kernel<T, R, NV> : ns_block_norm_kernel<T, R, NV>;
+  void (*const kernel)(BlockNormParams) = grad ? ns_block_norm_grad_kernel<T, R, NV, WORDS> : ns_block_norm_kernel<T, R, NV, WORDS>;
   *e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(BN_SMEM));
   if (*e == cudaSuccess) *e = launch_pdl(kernel, dim3(*blocks), dim3(32 * p.warps * p.teams), smem, st, p);
   return true;
@@ -695,18 +755,19 @@ cudaError_t launch_block_norm(bool grad, const BlockNormParams& p, int nsm, int*
   constexpr int X = sizeof(T), Y = sizeof(R);
   const bool value = p.gate_kind == VALUE_GATE, many = p.tokens > 1;  // the stride of one row reaches nothing
   auto ok = [&](const void* base, long long ld, int bytes) { return words_ok(base, many ? ld : 0, bytes); };
-  const bool words = p.dim % (16 / X) == 0 && p.dim <= 32 * BN_WARPS * 16 && ok(p.branch, p.branch_ld, X) && ok(p.x, p.x_ld, Y) &&
+  const bool words = p.dim % (16 / X) == 0 && ok(p.branch, p.branch_ld, X) && ok(p.x, p.x_ld, Y) &&
                      ok(p.h, p.h_ld, Y) && ok(p.n, p.n_ld, X) && ok(p.dh, p.dh_ld, Y) && ok(p.dn, p.dn_ld, X) &&
                      ok(p.dbranch, p.dbranch_ld, X) && ok(p.dx, p.dx_ld, Y) && ok(p.branch_weight, 0, 1) && ok(p.weight, 0, 1) &&
                      (!value || (ok(p.gate, p.gate_ld, X) && ok(p.dgate, p.dgate_ld, X)));
   // 32 bytes of an fp32 residual are stored at once
   const bool wide = Y == X || ((reinterpret_cast<uintptr_t>(p.h) | reinterpret_cast<uintptr_t>(p.dx)) % 32 == 0 &&
                                (!many || (p.h_ld % 8 == 0 && p.dx_ld % 8 == 0)));
-  if (words && wide) {
+  if (p.dim <= 32 * BN_WARPS * 16) {
+    const bool few = p.dim <= 32 * BN_WARPS * 8;
     cudaError_t e;
-    const bool done = p.dim <= 32 * BN_WARPS * 8 ? launch_rows<T, R, 8>(grad, p, nsm, blocks, st, &e)
-                                                 : launch_rows<T, R, 16>(grad, p, nsm, blocks, st, &e);
-    if (done) return e;
+    if (words && wide && (few ? launch_rows<T, R, 8, true>(grad, p, nsm, blocks, st, &e) : launch_rows<T, R, 16, true>(grad, p, nsm, blocks, st, &e)))
+      return e;
+    if (few ? launch_rows<T, R, 8, false>(grad, p, nsm, blocks, st, &e) : launch_rows<T, R, 16, false>(grad, p, nsm, blocks, st, &e)) return e;
   }
   *blocks = static_cast<int>(std::min<long long>(p.tokens, std::min(nsm * 4, BN_MAX_BLOCKS)));
   if (grad) return launch_pdl(ns_block_norm_grad_any_kernel<T, R>, dim3(*blocks), dim3(BN_ANY_THREADS), 0, st, p);

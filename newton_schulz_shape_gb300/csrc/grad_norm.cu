@@ -25,8 +25,11 @@ namespace nsk {
 namespace {
 
 constexpr int GN_THREADS = 256;
-constexpr int GN_BLOCKS = 8;                     // of an SM
-constexpr int GN_WORDS = 4;                      // 16-byte words of a chunk that a lane takes
+constexpr int GN_WORDS = 8;                      // 16-byte words of a chunk that a lane takes
+// Blocks of an SM. Reading alone wants much on its way (2.0 GB normed at 7.1 TB/s with 4 blocks of 8 words a lane, 6.2
+// with 8 of 4), reading beside writing little: clipped at 6.6 TB/s with 3 blocks of 4 words at a time, 4.7 with 8 of 4
+// and 3.4 with 6 of 8.
+constexpr int GN_BLOCKS = 4, GN_CLIP_BLOCKS = 3, GN_CLIP_WORDS = 4;
 constexpr int CHUNK_WORDS = GN_THREADS * GN_WORDS;
 constexpr int GN_TENSORS = 512;                  // of a launch
 constexpr int GN_MAX_BLOCKS = 2048;              // partial sums of a launch
@@ -109,7 +112,7 @@ __device__ __noinline__ double wide_sum(const Chunk<T> c) {
   return sum;
 }
 
-// A lane's share of a chunk's sum of squares: at most 48 values, in fp32 (two
+// A lane's share of a chunk's sum of squares: at most 80 values, in fp32 (two
 // values at a time). A sum that is not finite, or so small that squares may have
 // vanished though values are there, is formed again in 64 bits.
 template <typename T>
@@ -139,7 +142,7 @@ __device__ __forceinline__ double chunk_sum(const T* p, long long n, int k) {
   if (i < c.heads) ends = to_float(c.head[i]);
   if (i < c.tails) s[1].x = fmaf(to_float(c.tail[i]), to_float(c.tail[i]), s[1].x);
   const float sum = fmaf(ends, ends, (s[0].x + s[0].y) + (s[1].x + s[1].y));
-  // 2^-100 over 48 squares: what fp32's smallest values took away is below 2^-24 of it
+  // 2^-100 over 80 squares: what fp32's smallest values took away is below 2^-24 of it
   if (sum > 0x1p-100f && sum < INFINITY) return sum;
   const uint32_t sign = sizeof(T) == 4 ? 0x80000000u : 0x80008000u;
   if (!(any & ~sign) && c.heads + c.tails == 0) return 0.0;
@@ -194,19 +197,22 @@ __device__ __forceinline__ void clip_chunk(const T* p, T* out, long long n, int 
   const Chunk<T> c(p, n, k);
   T* const to = out + (c.at - p);
   if ((reinterpret_cast<uintptr_t>(to) & 15) == 0) {
-    Vec<T, V> x[GN_WORDS];
 #pragma unroll
-    for (int w = 0; w < GN_WORDS; ++w) {
-      const int i = w * GN_THREADS + threadIdx.x;
-      if (i < c.words) x[w] = load_vec<T, V>(c.at + i * V);
-    }
+    for (int w0 = 0; w0 < GN_WORDS; w0 += GN_CLIP_WORDS) {
+      Vec<T, V> x[GN_CLIP_WORDS];
 #pragma unroll
-    for (int w = 0; w < GN_WORDS; ++w) {
-      const int i = w * GN_THREADS + threadIdx.x;
-      float f[V];
+      for (int w = 0; w < GN_CLIP_WORDS; ++w) {
+        const int i = (w0 + w) * GN_THREADS + threadIdx.x;
+        if (i < c.words) x[w] = load_vec<T, V>(c.at + i * V);
+      }
 #pragma unroll
-      for (int j = 0; j < V; ++j) f[j] = get(x[w], j) * scale;
-      if (i < c.words) store_vec<T, V>(to + i * V, pack<T, V>(f));
+      for (int w = 0; w < GN_CLIP_WORDS; ++w) {
+        const int i = (w0 + w) * GN_THREADS + threadIdx.x;
+        float f[V];
+#pragma unroll
+        for (int j = 0; j < V; ++j) f[j] = get(x[w], j) * scale;
+        if (i < c.words) store_vec<T, V>(to + i * V, pack<T, V>(f));
+      }
     }
   } else {  // the two start at different places of a word
     for (int i = threadIdx.x; i < c.words * V; i += GN_THREADS) to[i] = from_float<T>(to_float(c.at[i]) * scale);
@@ -217,7 +223,7 @@ __device__ __forceinline__ void clip_chunk(const T* p, T* out, long long n, int 
 }
 
 // From the last chunk back: the norm read it last, so that L2 still holds some.
-__global__ void __launch_bounds__(GN_THREADS, GN_BLOCKS) ns_grad_clip_kernel(const __grid_constant__ GradClipParams p) {
+__global__ void __launch_bounds__(GN_THREADS, GN_CLIP_BLOCKS) ns_grad_clip_kernel(const __grid_constant__ GradClipParams p) {
   nsptx::griddep_wait();
   nsptx::griddep_launch_dependents();
   const double norm = static_cast<double>(*p.norm) + p.eps;  // NaN stays visible
@@ -351,7 +357,7 @@ int ns_grad_clip(const void* const* grads, void* const* outs, const int64_t* num
     if (p.in.tensors == 0) break;
     if (!ready && (rc = device_setup(&dev, &status, &nsm)) != NS_OK) return rc;
     ready = true;
-    const int blocks = std::min(p.in.chunks, std::min(nsm * nsk::GN_BLOCKS, nsk::GN_MAX_BLOCKS));
+    const int blocks = std::min(p.in.chunks, nsm * nsk::GN_CLIP_BLOCKS);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const cudaError_t e = counted(K_GRAD, st, [&] {
       return nsk::launch_pdl(nsk::ns_grad_clip_kernel, dim3(blocks), dim3(nsk::GN_THREADS), 0, st, p);

@@ -5,8 +5,9 @@ Tolerances, element by element and stated before the first run. u = 2^-24 is
 fp32's rounding, U the output type's (half its eps), tiny its smallest positive
 value; every store adds U |value| + tiny.
 
-* the norm: a lane's sum of at most 48 squares in fp32, the rest in 64 bits:
-  (48 + 2) u of the sum, half of it after the root, + 1 u for the store: 32 u;
+* the norm: a lane's sum of at most 80 squares in fp32, in four chains of at most
+  20 that are then added, the rest in 64 bits: (20 + 4) u of the sum, half of it
+  after the root, + 1 u for the store: within 32 u;
 * clipping: the scale is computed in 64 bits from the fp32 norm that the test
   passes and rounded to fp32 (1 u), the product 1 u;
 * a mean of D squares and its reciprocal square root: (D + 16) u relative, and
