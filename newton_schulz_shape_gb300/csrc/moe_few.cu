@@ -278,9 +278,11 @@ __device__ __forceinline__ void times(float (&c)[4], const uint4& r, const uint4
 // A warp's ring of shared memory: the words of the steps on their way, and of one
 // in use. The second product's tokens take more of the memory (64 experts by 16
 // slots each 95 us with two steps ahead, 109 with three and the tokens in L2).
-__host__ __device__ constexpr int ahead(bool hidden) { return hidden ? 2 : 3; }
-constexpr int MF_STAGE = 4 * 32;  // 16-byte words of a step
-__host__ __device__ constexpr int ring_words(bool hidden) { return (ahead(hidden) + 1) * MF_STAGE; }
+__host__ __device__ constexpr int ahead(bool hidden, bool vec) { return hidden || !vec ? 2 : 3; }
+// 16-byte words of a step: four rows of 16 bytes a lane. Rows that are not made of aligned 16-byte words are copied in
+// aligned 4-byte words, five of which cover the values of a 16-bit type.
+__host__ __device__ constexpr int stage_words(bool vec) { return vec ? 4 * 32 : 5 * 32; }
+__host__ __device__ constexpr int ring_words(bool hidden, bool vec) { return (ahead(hidden, vec) + 1) * stage_words(vec); }
 
 // A team of warps goes through the tiles of a block that fall to it, all passes in
 // a row: `Stream` copies the weights of a warp's next steps to its ring, into the
@@ -291,7 +293,10 @@ __host__ __device__ constexpr int ring_words(bool hidden) { return (ahead(hidden
 template <typename T, bool HIDDEN, bool VEC>
 struct Stream {
   using S = Side<T, HIDDEN>;
-  static constexpr int V = 16 / sizeof(T), AHEAD = ahead(HIDDEN), RING = ring_words(HIDDEN);
+  static constexpr int V = 16 / sizeof(T), AHEAD = ahead(HIDDEN, VEC), STAGE = stage_words(VEC), RING = ring_words(HIDDEN, VEC);
+  // 4-byte words of a row, where there are no 16-byte ones
+  static constexpr int PLANES = sizeof(T) == 4 ? 4 : 5;
+  static_assert(32 * 4 * PLANES <= 4 * stage_words(false), "a stage");
   const MoeFewParams& p;
   const Routing& r;
   int tiles, end, stride;  // tiles of a pass; items (tiles of all passes) of the block; of a team
@@ -305,7 +310,7 @@ struct Stream {
 
   __device__ __forceinline__ Stream(const MoeFewParams& params, const Routing& routing, uint4* warp_ring, int first, int last,
                                     int team, int teams, int warp, int tiles_of_pass)
-      : p(params), r(routing), tiles(tiles_of_pass), end(last), stride(teams), ring(warp_ring + (threadIdx.x & 31)), fill(0),
+      : p(params), r(routing), tiles(tiles_of_pass), end(last), stride(teams), ring(warp_ring), fill(0),
         take(0), item(first + team) {
     n = static_cast<int>(HIDDEN ? p.ffn : p.dim);
     step = 4 * V * p.team;
@@ -317,36 +322,33 @@ struct Stream {
 #pragma unroll
     for (int i = 0; i < AHEAD; ++i) fetch();
   }
+  static __device__ __forceinline__ const T* base(const MoeFewParams& p) { return static_cast<const T*>(HIDDEN ? p.down : p.gate_up); }
+  // The matrix row of the lane's row i (r and r + 8 of each half) of an item's tile: 32 rows of D; or 16 rows of G, each
+  // followed by the row of U that goes with it.
+  __device__ __forceinline__ long long row_of(int of, int i) const {
+    const int in = of / tiles, lane = (threadIdx.x & 31) / 4, tile = of - in * tiles;
+    const long long e = r.passes[in].expert;
+    if (HIDDEN) return e * p.dim + min(static_cast<long long>(tile * MF_ROWS + 8 * i + lane), p.dim - 1);
+    return e * 2 * p.ffn + (i & 1) * p.ffn + min(static_cast<long long>(tile * (MF_ROWS / 2) + 8 * (i / 2) + lane), p.ffn - 1);
+  }
   __device__ __forceinline__ void rows() {
     s = 0;
     k = k0;
     if (item >= end) return;
-    const int in = item / tiles, lane = (threadIdx.x & 31) / 4;
-    const long long e = r.passes[in].expert;
-    const int tile = item - in * tiles;
-    if (HIDDEN) {  // 32 rows of D
-      const T* base = static_cast<const T*>(p.down) + e * p.dim * p.ffn;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) at[i] = base + min(static_cast<long long>(tile * MF_ROWS + 8 * i + lane), p.dim - 1) * p.ffn;
-    } else {       // 16 rows of G and the rows of U that go with them
-      const T* base = static_cast<const T*>(p.gate_up) + 2 * e * p.ffn * p.dim;
-#pragma unroll
-      for (int i = 0; i < 4; i += 2) {
-        at[i] = base + min(static_cast<long long>(tile * (MF_ROWS / 2) + 4 * i + lane), p.ffn - 1) * p.dim;
-        at[i + 1] = at[i] + p.ffn * p.dim;
-      }
-    }
+    for (int i = 0; i < 4; ++i) at[i] = base(p) + row_of(item, i) * n;
   }
   __device__ __forceinline__ void fetch() {
     if (item < end) {
-      uint4* const to = ring + fill;
+      const int lane = threadIdx.x & 31;
       if constexpr (VEC) {
         const int bytes = k < n ? 16 : 0;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) nsptx::cp_async16_upto(to + 32 * i, at[i] + k, bytes);
+        for (int i = 0; i < 4; ++i) nsptx::cp_async16_upto(ring + fill + 32 * i + lane, at[i] + k, bytes);
       } else {
+        const T* const last = base(p) + (HIDDEN ? p.experts * p.dim : p.experts * 2 * p.ffn) * n;  // past the matrices
 #pragma unroll
-        for (int i = 0; i < 4; ++i) to[32 * i] = load_values(at[i], k, n);
+        for (int i = 0; i < 4; ++i) fetch_words(reinterpret_cast<uint32_t*>(ring + fill) + i * PLANES * 32 + lane, at[i], last);
       }
       k += step;
       if (++s == steps) {
@@ -355,7 +357,42 @@ struct Stream {
       }
     }
     nsptx::cp_async_commit();
-    fill = fill + MF_STAGE == RING ? 0 : fill + MF_STAGE;
+    fill = fill + STAGE == RING ? 0 : fill + STAGE;
+  }
+  // The aligned 4-byte words, 32 apart, that cover what is left of 16 bytes from k on. One that begins before the
+  // matrices or ends behind them is put together from its values.
+  __device__ __forceinline__ void fetch_words(uint32_t* to, const T* row, const T* last) const {
+    const uintptr_t from = reinterpret_cast<uintptr_t>(row + k), word = from & ~uintptr_t{3};
+    const int bytes = static_cast<int>(from - word) + min(n - k, V) * static_cast<int>(sizeof(T));
+#pragma unroll
+    for (int w = 0; w < PLANES; ++w) {
+      if (4 * w >= bytes || k >= n) break;
+      const uintptr_t q = word + 4 * w;
+      if (sizeof(T) == 4 || (q >= reinterpret_cast<uintptr_t>(base(p)) && q + 4 <= reinterpret_cast<uintptr_t>(last))) {
+        nsptx::cp_async4(to + 32 * w, reinterpret_cast<const void*>(q));
+      } else {
+        uint32_t v = 0;
+        if (q >= reinterpret_cast<uintptr_t>(base(p))) v = *reinterpret_cast<const unsigned short*>(q);
+        if (q + 4 <= reinterpret_cast<uintptr_t>(last)) v |= static_cast<uint32_t>(*reinterpret_cast<const unsigned short*>(q + 2)) << 16;
+        to[32 * w] = v;
+      }
+    }
+  }
+  // 16 bytes of a row from those words, `odd`: from the middle of the first on; `left` values, zeros behind.
+  static __device__ __forceinline__ uint4 from_words(const uint32_t* words, bool odd, int left) {
+    uint32_t w[PLANES], v[4];
+#pragma unroll
+    for (int i = 0; i < PLANES; ++i) w[i] = words[32 * i];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[i] = sizeof(T) == 2 && odd ? __funnelshift_r(w[i], w[PLANES - 1 < i + 1 ? i : i + 1], 16) : w[i];
+      constexpr int PER = 4 / sizeof(T);
+      if (left <= PER * i)
+        v[i] = 0;
+      else if (PER == 2 && left == 2 * i + 1)
+        v[i] &= 0xffffu;
+    }
+    return make_uint4(v[0], v[1], v[2], v[3]);
   }
 
   // The products of the next tile with 8 * NT slots, whose rows are `row` and whose words of all of the warp's steps
@@ -381,7 +418,13 @@ struct Stream {
     for (int t = 0; t < NT; ++t) side[t].template load<VEC>(row[t], static_cast<int>(2 * p.hidden_ld), k0 + i * step, n);
   }
   template <int NT, bool HELD>
-  __device__ __forceinline__ void tile(const char* const (&row)[NT], const uint4* held, S (&now)[NT], float (&acc)[2][NT][4]) {
+  __device__ __forceinline__ void tile(int of, const char* const (&row)[NT], const uint4* held, S (&now)[NT], float (&acc)[2][NT][4]) {
+    const int lane = threadIdx.x & 31;
+    bool odd[4] = {};
+    if constexpr (!VEC && sizeof(T) == 2) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) odd[i] = reinterpret_cast<uintptr_t>(base(p) + row_of(of, i) * n) & 2;
+    }
     for (int i = 0; i < steps; ++i) {
       S side[NT];
       if constexpr (HELD) {
@@ -399,8 +442,13 @@ struct Stream {
       nsptx::cp_async_wait<AHEAD - 1>();
       uint4 a[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) a[j] = ring[take + 32 * j];
-      take = take + MF_STAGE == RING ? 0 : take + MF_STAGE;
+      for (int j = 0; j < 4; ++j) {
+        if constexpr (VEC)
+          a[j] = ring[take + 32 * j + lane];
+        else
+          a[j] = from_words(reinterpret_cast<const uint32_t*>(ring + take) + j * PLANES * 32 + lane, odd[j], n - k0 - i * step);
+      }
+      take = take + STAGE == RING ? 0 : take + STAGE;
       fetch();
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
@@ -443,7 +491,7 @@ __device__ __forceinline__ void tiles_of_pass(S& stream, const Team& team, int& 
   for (; item < to; item += stream.stride) {
     const int tile = item - pass * stream.tiles;
     float acc[2][NT][4] = {};
-    stream.template tile<NT, HELD>(row, team.held, now, acc);
+    stream.template tile<NT, HELD>(item, row, team.held, now, acc);
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
       // a lane's sums: of rows lane / 4 and 8 more of each half of the tile, columns 2 (lane % 4) and the next
@@ -481,10 +529,10 @@ __device__ __forceinline__ void all_tiles(const MoeFewParams& p, const Routing& 
   const long long items = static_cast<long long>(passes) * tiles;
   const int first = static_cast<int>(items * blockIdx.x / gridDim.x), last = static_cast<int>(items * (blockIdx.x + 1) / gridDim.x);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  uint4* const held = smem + MF_WARPS * ring_words(HIDDEN);
+  uint4* const held = smem + MF_WARPS * ring_words(HIDDEN, VEC);
   float* const sums = reinterpret_cast<float*>(held + MF_WARPS * p.held * 32);
   const Team team = {p.team, warp & (p.team - 1), warp / p.team, held + warp * p.held * 32 + lane, sums + warp / p.team * p.team * 8 * 32};
-  Stream<T, HIDDEN, VEC> stream(p, r, smem + warp * ring_words(HIDDEN), first, last, team.id, MF_WARPS / p.team, team.warp, tiles);
+  Stream<T, HIDDEN, VEC> stream(p, r, smem + warp * ring_words(HIDDEN, VEC), first, last, team.id, MF_WARPS / p.team, team.warp, tiles);
   for (int item = first + team.id; item < last;) {
     const int pass = item / tiles, to = min(last, (pass + 1) * tiles), count = r.passes[pass].count;
     const int words = S::Q * stream.most_steps;
@@ -500,12 +548,12 @@ __device__ __forceinline__ void all_tiles(const MoeFewParams& p, const Routing& 
 }
 
 // Shared memory: the rings, what is held of the tokens, the parts of split sums, the routing.
-__host__ __device__ constexpr int fixed_words(bool hidden) { return MF_WARPS * (ring_words(hidden) + 8 * 8); }
+__host__ __device__ constexpr int fixed_words(bool hidden, bool vec) { return MF_WARPS * (ring_words(hidden, vec) + 8 * 8); }
 constexpr int MF_HELD_WORDS = MF_WARPS * 32;
 constexpr size_t MF_SMEM = 226 * 1024;
-template <bool HIDDEN>
+template <bool HIDDEN, bool VEC>
 __device__ __forceinline__ Routing routing_of(const MoeFewParams& p, uint4* smem) {
-  return Routing(p, smem + fixed_words(HIDDEN) + p.held * MF_HELD_WORDS);
+  return Routing(p, smem + fixed_words(HIDDEN, VEC) + p.held * MF_HELD_WORDS);
 }
 
 // h of all slots.
@@ -514,7 +562,7 @@ __global__ void __launch_bounds__(MF_THREADS, 1) ns_moe_few_hidden_kernel(const 
   extern __shared__ uint4 few_smem[];
   nsptx::griddep_wait();
   nsptx::griddep_launch_dependents();
-  const Routing r = routing_of<false>(p, few_smem);
+  const Routing r = routing_of<false, VEC>(p, few_smem);
   const int passes = find_passes(p, r);
   all_tiles<T, false, VEC>(
       p, r, few_smem, passes, static_cast<int>((p.ffn + MF_ROWS / 2 - 1) / (MF_ROWS / 2)),
@@ -541,7 +589,7 @@ __global__ void __launch_bounds__(MF_THREADS, 1) ns_moe_few_down_kernel(const __
   extern __shared__ uint4 few_smem[];
   nsptx::griddep_wait();
   nsptx::griddep_launch_dependents();
-  const Routing r = routing_of<true>(p, few_smem);
+  const Routing r = routing_of<true, VEC>(p, few_smem);
   const int passes = find_passes(p, r);
   all_tiles<T, true, VEC>(p, r, few_smem, passes, static_cast<int>((p.dim + MF_ROWS - 1) / MF_ROWS),
                           [&](int tile, int row, int slot, float a, float b) {
@@ -592,10 +640,10 @@ __global__ void __launch_bounds__(MF_SUM_THREADS) ns_moe_few_sum_kernel(const __
 
 // Warps that split a tile's k: as many as have some 4 steps each. A block's tiles are then few and small, so that all
 // blocks have as many, and it reads long pieces of rows. (A warp a tile: some warps have three tiles where others have
-// two.)
-int team_of(long long steps) {
+// two.) Where there are too few tiles for the card's warps, a step or two each.
+int team_of(long long tiles, long long steps, int nsm) {
   int team = 1;
-  while (team < MF_WARPS && steps >= 6 * team) team *= 2;
+  while (team < MF_WARPS && (steps >= 6 * team || (steps >= 2 * team && 2 * team * tiles <= nsm * MF_WARPS))) team *= 2;
   return team;
 }
 
@@ -605,12 +653,12 @@ int launch_few(MoeFewParams p, int nsm, cudaStream_t st) {
   const int slots = p.tokens * p.k, named = std::min(p.experts, slots);
   p.entries = named + slots / (8 * MF_NT);
   const size_t routing = routing_bytes(p.entries, p.experts, slots);
-  static_assert(sizeof(uint4) * fixed_words(false) + routing_bytes(1024 + MF_MAX_TOKENS * 32 / (8 * MF_NT), 1024, MF_MAX_TOKENS * 32) <= MF_SMEM,
+  static_assert(sizeof(uint4) * fixed_words(false, VEC) + routing_bytes(1024 + MF_MAX_TOKENS * 32 / (8 * MF_NT), 1024, MF_MAX_TOKENS * 32) <= MF_SMEM,
                 "shared memory of a block");
   auto launch = [&](void (*kernel)(MoeFewParams), bool hidden, long long tiles, long long n, int words) {
     const long long steps = (n + VALUES - 1) / VALUES;
-    p.team = team_of(steps);
-    const size_t fixed = sizeof(uint4) * fixed_words(hidden) + routing;
+    p.team = team_of(tiles * named, steps, nsm);
+    const size_t fixed = sizeof(uint4) * fixed_words(hidden, VEC) + routing;
     // of 8 or 16 slots; what is not held stays with L1
     const long long room = (MF_SMEM - fixed) / (sizeof(uint4) * MF_HELD_WORDS);
     const long long most = (steps + p.team - 1) / p.team * words;
