@@ -252,6 +252,11 @@ __device__ __forceinline__ void times(float (&c)[4], const uint4& r, const uint4
       if constexpr (S::PAIR) mma_16<T>(c, a[0][i], a[1][i], a[0][i + 1], a[1][i + 1], side.w(4 + i), side.w(5 + i));
     }
   } else {
+    // The instruction cuts what it adds at the sum's last place, always towards zero: in fp32, where that shows (1e-6 over
+    // long rows), a few products make a sum of their own, the small ones first, and are added to the rest as usual.
+    constexpr bool APART = sizeof(T) == 4;
+    float few[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    float(&sum)[4] = APART ? few : c;
 #pragma unroll
     for (int i = 0; i < 16 / static_cast<int>(sizeof(T)); i += 2) {
       uint32_t hi[2], lo[2], w[2][2], rest[2][2];  // [k][row]
@@ -268,9 +273,13 @@ __device__ __forceinline__ void times(float (&c)[4], const uint4& r, const uint4
           }
         }
       }
-      mma_tf32_8(c, w[0][0], w[0][1], w[1][0], w[1][1], hi[0], hi[1]);
-      mma_tf32_8(c, w[0][0], w[0][1], w[1][0], w[1][1], lo[0], lo[1]);
-      if constexpr (sizeof(T) == 4) mma_tf32_8(c, rest[0][0], rest[0][1], rest[1][0], rest[1][1], hi[0], hi[1]);
+      mma_tf32_8(sum, w[0][0], w[0][1], w[1][0], w[1][1], lo[0], lo[1]);
+      if constexpr (sizeof(T) == 4) mma_tf32_8(sum, rest[0][0], rest[0][1], rest[1][0], rest[1][1], hi[0], hi[1]);
+      mma_tf32_8(sum, w[0][0], w[0][1], w[1][0], w[1][1], hi[0], hi[1]);
+    }
+    if constexpr (APART) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) c[i] += few[i];
     }
   }
 }
