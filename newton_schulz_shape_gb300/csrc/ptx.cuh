@@ -99,9 +99,16 @@ __device__ __forceinline__ bool mbar_wait_drain(uint64_t* bar, uint32_t parity, 
 __device__ __forceinline__ void cp_async16(void* smem_dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(smem_dst)), "l"(src) : "memory");
 }
-// The first `bytes` of them (0 to 16), zeros behind; of 0 nothing is read.
-__device__ __forceinline__ void cp_async16_upto(void* smem_dst, const void* src, int bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(smem_dst)), "l"(src), "r"(bytes) : "memory");
+// A policy for data that is read once: the first that L2 gives up.
+__device__ __forceinline__ uint64_t evict_first_policy() {
+  uint64_t p;
+  asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+  return p;
+}
+// The first `bytes` of 16 (0 to 16), zeros behind; of 0 nothing is read.
+__device__ __forceinline__ void cp_async16_upto(void* smem_dst, const void* src, int bytes, uint64_t policy) {
+  asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, %3;"
+               ::"r"(smem_u32(smem_dst)), "l"(src), "r"(bytes), "l"(policy) : "memory");
 }
 // 4 bytes, kept in L1 for the neighbours that read beside them.
 __device__ __forceinline__ void cp_async4(void* smem_dst, const void* src) {
