@@ -126,7 +126,7 @@ enum Output { OUT_N = 0, OUT_H = 1, OUT_DBRANCH = 0, OUT_DX = 1, OUT_DGATE = 2, 
 
 // NV values of a lane: units of V, a unit's values side by side, units 32 * V *
 // warps apart. Columns past the last are zero throughout.
-template <typename T, typename R, int NV, bool GRAD>
+template <typename T, typename R, int NV, bool GRAD, bool FULL>
 struct Lanes {
   static constexpr int N = NV / 2, V = 16 / sizeof(T), U = NV / V, RW = sizeof(R) / sizeof(T);  // RW: words of a unit of R
   const BlockNormParams& p;
@@ -188,6 +188,9 @@ struct Lanes {
       for (int i = 0; i < V; i += 4) *reinterpret_cast<float4*>(to + quad(u, i)) = make_float4(f[i], f[i + 1], f[i + 2], f[i + 3]);
     }
   }
+  // Which inputs and outputs there are.
+  __device__ __forceinline__ bool in(int k) const { return FULL ? k < IN_GATE : p.src[k] != nullptr; }
+  __device__ __forceinline__ bool out(int k) const { return FULL ? k < OUT_DGATE : p.dst[k] != nullptr; }
   // Place of word w of a unit of W words a lane. The gradient reads two words side by side without conflicts (16384 rows
   // of 2048 bf16 with an fp32 residual 101 us against 106); forward, where memory alone is the limit, the plain order is
   // the faster one (65 against 69).
@@ -202,7 +205,7 @@ struct Lanes {
   template <typename E>
   __device__ __forceinline__ void fetch(int k, int t) const {
     constexpr int W = sizeof(E) / sizeof(T), VE = 16 / sizeof(E);  // words of a unit, values of a word
-    if (!p.src[k]) return;
+    if (!in(k)) return;
     const char* const row = static_cast<const char*>(p.src[k]) + static_cast<long long>(t) * p.src_step[k];
     uint4* const to = ring + fill + p.place[k];
 #pragma unroll
@@ -226,7 +229,7 @@ struct Lanes {
   template <typename E>
   __device__ __forceinline__ void get_row(int k, float2 (&v)[N]) const {
     constexpr int W = sizeof(E) / sizeof(T), VE = 16 / sizeof(E);
-    const uint4* const from = p.src[k] ? ring + take + p.place[k] : zeros;
+    const uint4* const from = in(k) ? ring + take + p.place[k] : zeros;
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
@@ -240,7 +243,7 @@ struct Lanes {
   template <typename E>
   __device__ __forceinline__ void put_row(int k, int t, const float2 (&v)[N]) const {
     constexpr int W = sizeof(E) / sizeof(T), VE = 16 / sizeof(E);
-    if (!p.dst[k]) return;
+    if (!out(k)) return;
     char* const to = static_cast<char*>(p.dst[k]) + static_cast<long long>(t) * p.dst_step[k];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -274,9 +277,12 @@ struct Lanes {
       }
     }
   }
-  // A token's own gate, 1 where there are none.
-  __device__ __forceinline__ float gate(int t) const {
-    return p.gate_kind == TOKEN_GATE && t < p.tokens ? static_cast<const float*>(p.gate)[t] : 1.0f;
+  // A token's own gate, on its way with the row; 1 where there are none.
+  __device__ __forceinline__ void fetch_gate(int t) const {
+    if (p.gate_kind == TOKEN_GATE && team.lane == 0) nsptx::cp_async4(ring + fill + p.stage - 1, static_cast<const float*>(p.gate) + t);
+  }
+  __device__ __forceinline__ float gate() const {
+    return p.gate_kind == TOKEN_GATE ? *reinterpret_cast<const float*>(ring + take + p.stage - 1) : 1.0f;
   }
   // Weights of the lane's columns: of the branch (0), of the norm after (1).
   __device__ __forceinline__ void weights(int which, float2 (&v)[N]) const {
@@ -335,9 +341,8 @@ struct Singles {
     for (int i = 0; i < NV; ++i)
       if (at + i * step < dim) to[at + i * step] = from_float<E>(i % 2 ? v[i / 2].y : v[i / 2].x);
   }
-  __device__ __forceinline__ float gate(int t) const {
-    return p.gate_kind == TOKEN_GATE && t < p.tokens ? static_cast<const float*>(p.gate)[t] : 1.0f;
-  }
+  __device__ __forceinline__ void fetch_gate(int) const {}
+  __device__ __forceinline__ float gate() const { return p.gate_kind == TOKEN_GATE ? static_cast<const float*>(p.gate)[row] : 1.0f; }
   __device__ __forceinline__ void weights(int which, float2 (&v)[N]) const {
     const float* const from = weight + which * step * NV + at;
 #pragma unroll
@@ -362,7 +367,7 @@ __global__ void __launch_bounds__(32 * BN_WARPS, bn_blocks(false, NV)) ns_block_
   nsptx::griddep_launch_dependents();
   constexpr int N = NV / 2;
   RowTeam team(p, parts);
-  typename std::conditional<WORDS, Lanes<T, R, NV, false>, Singles<T, R, NV, false>>::type lanes(p, team, rows_smem);
+  typename std::conditional<WORDS, Lanes<T, R, NV, false, false>, Singles<T, R, NV, false>>::type lanes(p, team, rows_smem);
   const float inv_dim = 1.0f / p.dim;
   const float2 alpha = both(p.alpha);
   const bool gated = p.gate_kind == VALUE_GATE;
@@ -372,18 +377,17 @@ __global__ void __launch_bounds__(32 * BN_WARPS, bn_blocks(false, NV)) ns_block_
       lanes.template fetch<T>(IN_BRANCH, t);
       lanes.template fetch<R>(IN_X, t);
       lanes.template fetch<T>(IN_GATE, t);
+      lanes.fetch_gate(t);
     }
     lanes.fetched();
   };
   fetch(t0);
-  float gate = lanes.gate(t0);
   lanes.prepare();
   for (int t = t0; t < tokens; t += stride) {
     lanes.wait(t);
     fetch(t + stride);
     float2 b[N], h[N];
-    const float2 beta = both(p.beta * gate);
-    gate = lanes.gate(t + stride);
+    const float2 beta = both(p.beta * lanes.gate());
     float2 w[N];
     lanes.template get_row<T>(IN_BRANCH, b);
     lanes.template get_row<R>(IN_X, h);
@@ -428,7 +432,7 @@ __global__ void __launch_bounds__(32 * BN_WARPS, bn_blocks(false, NV)) ns_block_
   }
 }
 
-template <typename T, typename R, int NV, bool WORDS>
+template <typename T, typename R, int NV, bool WORDS, bool FULL>
 __global__ void __launch_bounds__(32 * BN_WARPS, bn_blocks(true, NV)) ns_block_norm_grad_kernel(const __grid_constant__ BlockNormParams p) {
   extern __shared__ uint4 rows_smem[];
   __shared__ float parts[BN_WARPS * 8];
@@ -436,9 +440,9 @@ __global__ void __launch_bounds__(32 * BN_WARPS, bn_blocks(true, NV)) ns_block_n
   nsptx::griddep_launch_dependents();
   constexpr int N = NV / 2;
   RowTeam team(p, parts);
-  typename std::conditional<WORDS, Lanes<T, R, NV, true>, Singles<T, R, NV, true>>::type lanes(p, team, rows_smem);
+  typename std::conditional<WORDS, Lanes<T, R, NV, true, FULL>, Singles<T, R, NV, true>>::type lanes(p, team, rows_smem);
   const float inv_dim = 1.0f / p.dim;
-  const bool gated = p.gate_kind == VALUE_GATE;
+  const bool gated = !FULL && p.gate_kind == VALUE_GATE, has_dn = FULL || p.dn, has_dx = FULL || p.dx, has_branch = FULL || p.branch, post = FULL || p.post;
   const int tokens = static_cast<int>(p.tokens), stride = gridDim.x * p.teams, t0 = blockIdx.x * p.teams + team.id;
   auto fetch = [&](int t) {
     if (t < tokens) {
@@ -447,6 +451,7 @@ __global__ void __launch_bounds__(32 * BN_WARPS, bn_blocks(true, NV)) ns_block_n
       lanes.template fetch<R>(IN_DH, t);
       lanes.template fetch<T>(IN_GRAD_BRANCH, t);
       lanes.template fetch<T>(IN_GATE, t);
+      lanes.fetch_gate(t);
     }
     lanes.fetched();
   };
@@ -454,14 +459,12 @@ __global__ void __launch_bounds__(32 * BN_WARPS, bn_blocks(true, NV)) ns_block_n
 #pragma unroll
   for (int i = 0; i < N; ++i) dp[i] = dw[i] = both(0.0f);
   fetch(t0);
-  float gate = lanes.gate(t0);
   lanes.prepare();
   for (int t = t0; t < tokens; t += stride) {
     lanes.wait(t);
     fetch(t + stride);
     float2 v[N], h[N], d[N], b[N], w[N];
-    const float gt = gate;
-    gate = lanes.gate(t + stride);
+    const float gt = lanes.gate();
     lanes.weights(1, w);
     lanes.template get_row<T>(IN_DN, v);
     lanes.template get_row<R>(IN_X, h);
@@ -476,7 +479,7 @@ __global__ void __launch_bounds__(32 * BN_WARPS, bn_blocks(true, NV)) ns_block_n
     }
     float sum[3] = {s0.x + s0.y, s1.x + s1.y, s2.x + s2.y};
     team.sum(sum);
-    if (p.dn) {
+    if (has_dn) {
       const float r = rsqrtf(fmaf(sum[0], inv_dim, p.eps)), mean = sum[1] * r * inv_dim;
       const float2 r2 = both(r), minus = both(-mean);
 #pragma unroll
@@ -486,13 +489,13 @@ __global__ void __launch_bounds__(32 * BN_WARPS, bn_blocks(true, NV)) ns_block_n
         d[i] = fma2(r2, fma2(m, minus, mul2(v[i], w[i])), d[i]);  // t
       }
     }
-    if (p.dx) {
+    if (has_dx) {
 #pragma unroll
       for (int i = 0; i < N; ++i) h[i] = mul2(d[i], both(p.alpha));
       lanes.template put_row<R>(OUT_DX, t, h);
     }
-    if (p.branch) {
-      const float r1 = p.post ? rsqrtf(fmaf(sum[2], inv_dim, p.eps)) : 1.0f;
+    if (has_branch) {
+      const float r1 = post ? rsqrtf(fmaf(sum[2], inv_dim, p.eps)) : 1.0f;
       lanes.weights(0, w);
       float2 g[N];
       if (gated) {
@@ -514,9 +517,9 @@ __global__ void __launch_bounds__(32 * BN_WARPS, bn_blocks(true, NV)) ns_block_n
       }
       if (gated) lanes.template put_row<T>(OUT_DGATE, t, g);
       float sums[2] = {s0.x + s0.y, s1.x + s1.y};
-      if (p.post || (p.dgate && !gated)) team.sum(sums);
+      if (post || (p.dgate && !gated)) team.sum(sums);
       if (p.dgate && !gated && team.warp == 0 && team.lane == 0) static_cast<float*>(p.dgate)[t] = sums[1];
-      if (p.post) {
+      if (post) {
         const float2 minus = both(-sums[0] * inv_dim);
 #pragma unroll
         for (int i = 0; i < N; ++i) d[i] = mul2(fma2(b[i], minus, d[i]), both(r1));
@@ -696,7 +699,7 @@ __global__ void __launch_bounds__(1024) ns_block_norm_sum_kernel(const __grid_co
 // NV values a lane; false if the copies of two rows do not fit an SM, or steps an int.
 template <typename T, typename R, int NV, bool WORDS>
 bool launch_rows(bool grad, BlockNormParams p, int nsm, int* blocks, cudaStream_t st, cudaError_t* e) {
-  using L = Lanes<T, R, NV, true>;
+  using L = Lanes<T, R, NV, true, false>;
   constexpr int BLOCKS[2] = {bn_blocks(false, NV), bn_blocks(true, NV)};
   p.warps = static_cast<int>((p.dim + 32 * NV - 1) / (32 * NV));
   // few rows are spread over the SMs, many share a block
@@ -733,13 +736,20 @@ bool launch_rows(bool grad, BlockNormParams p, int nsm, int* blocks, cudaStream_
     if (p.dst[k] && !step(o.ld, o.wide, &p.dst_step[k])) return false;
   }
   if (p.tokens > INT_MAX / 4) return false;
+  if (WORDS && p.gate_kind == TOKEN_GATE) ++p.stage;
   // a block's rows, zeros, weights
   const size_t row = sizeof(uint4) * p.stage * p.warps * p.teams;
   const size_t more = (WORDS ? sizeof(uint4) * 32 * L::U * L::RW : 0) + sizeof(float) * 2 * 32 * NV * p.warps;
   if (2 * row + more > BN_SMEM / BLOCKS[grad]) return false;
   const size_t joined = p.partial ? sizeof(float) * 2 * p.dim * p.teams : 0, smem = std::max(2 * row + more, joined);
   *blocks = static_cast<int>(std::min<long long>((p.tokens + p.teams - 1) / p.teams, std::min(nsm * BLOCKS[grad], BN_MAX_BLOCKS)));
-  void (*const kernel)(BlockNormParams) = grad ? ns_block_norm_grad_kernel<T, R, NV, WORDS> : ns_block_norm_kernel<T, R, NV, WORDS>;
+  void (*kernel)(BlockNormParams) = ns_block_norm_kernel<T, R, NV, WORDS>;
+  if (grad) kernel = ns_block_norm_grad_kernel<T, R, NV, WORDS, false>;
+  if constexpr (WORDS) {
+    // the usual gradient, without a choice for each row
+    if (grad && p.post && p.src[IN_DN] && p.src[IN_DH] && p.src[IN_GRAD_BRANCH] && !p.src[IN_GATE] && p.dst[OUT_DBRANCH] && p.dst[OUT_DX])
+      kernel = ns_block_norm_grad_kernel<T, R, NV, WORDS, true>;
+  }
   *e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(BN_SMEM));
   if (*e == cudaSuccess) *e = launch_pdl(kernel, dim3(*blocks), dim3(32 * p.warps * p.teams), smem, st, p);
   return true;
