@@ -531,8 +531,10 @@ int ns_moe_few_tokens_workspace_bytes(int64_t tokens, int k, int64_t dim, int64_
  * int32 or int64; a negative one goes nowhere, one >= experts is refused and goes
  * nowhere; a token may name an expert more than once. weights fp32
  * [tokens][k], NULL = 1; the weight of a slot that goes nowhere is not used,
- * whatever it holds, and the weights of experts that no token names are not
- * read. y may be x itself. tokens <= 256, 1 <= k <= 32, 1 <= experts <= 1024,
+ * whatever it holds, and the matrices of experts that no token names are not
+ * read. Products are of fp32's precision and summed in fp32 (fp32 factors as two
+ * tf32 values each); an infinite matrix value or hidden value may give NaN where
+ * infinity is due, in the tokens that meet it. y may be x itself. tokens <= 256, 1 <= k <= 32, 1 <= experts <= 1024,
  * dim and ffn < 2^20, ffn >= 1; for more tokens: ns_moe_sort, ns_moe_dispatch
  * and ns_moe_combine. */
 int ns_moe_few_tokens(const void* x, int64_t x_stride, int dtype, int64_t tokens, int k, int64_t dim, int64_t ffn,

@@ -740,9 +740,10 @@ bool launch_rows(bool grad, BlockNormParams p, int nsm, int* blocks, cudaStream_
   // a block's rows, zeros, weights
   const size_t row = sizeof(uint4) * p.stage * p.warps * p.teams;
   const size_t more = (WORDS ? sizeof(uint4) * 32 * L::U * L::RW : 0) + sizeof(float) * 2 * 32 * NV * p.warps;
-  if (2 * row + more > BN_SMEM / BLOCKS[grad]) return false;
+  const int per_sm = 2 * row + more <= BN_SMEM / BLOCKS[grad] ? BLOCKS[grad] : 1;
+  if (2 * row + more > BN_SMEM / per_sm) return false;
   const size_t joined = p.partial ? sizeof(float) * 2 * p.dim * p.teams : 0, smem = std::max(2 * row + more, joined);
-  *blocks = static_cast<int>(std::min<long long>((p.tokens + p.teams - 1) / p.teams, std::min(nsm * BLOCKS[grad], BN_MAX_BLOCKS)));
+  *blocks = static_cast<int>(std::min<long long>((p.tokens + p.teams - 1) / p.teams, std::min(nsm * per_sm, BN_MAX_BLOCKS)));
   void (*kernel)(BlockNormParams) = ns_block_norm_kernel<T, R, NV, WORDS>;
   if (grad) kernel = ns_block_norm_grad_kernel<T, R, NV, WORDS, false>;
   if constexpr (WORDS) {

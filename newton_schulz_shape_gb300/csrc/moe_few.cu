@@ -309,45 +309,50 @@ struct Stream {
   static_assert(32 * 4 * PLANES <= 4 * stage_words(false), "a stage");
   const MoeFewParams& p;
   const Routing& r;
-  int tiles, end, stride;  // tiles of a pass; items (tiles of all passes) of the block; of a team
+  int tiles, rows, end, stride;  // tiles of a pass, rows of a matrix; items (tiles of all passes) of the block; of a team
   int n, step, steps;      // values of a row, from a warp's step to its next, steps of a tile
   int most_steps;          // of any of the team's warps
   int k0;                  // the lane's first value
   uint4* ring;
   int fill, take;
-  int item, k, s;          // of the next copy
+  int item, pass, tile, k, s;  // of the next copy
   const T* at[4];          // the lane's rows there: r and r + 8 of each half of the tile
   uint64_t policy;
 
   __device__ __forceinline__ Stream(const MoeFewParams& params, const Routing& routing, uint4* warp_ring, int first, int last,
                                     int team, int teams, int warp, int tiles_of_pass)
       : p(params), r(routing), tiles(tiles_of_pass), end(last), stride(teams), ring(warp_ring), fill(0),
-        take(0), item(first + team), policy(nsptx::evict_first_policy()) {
+        take(0), item(first + team), pass(item / tiles), tile(item - pass * tiles), policy(nsptx::evict_first_policy()) {
     n = static_cast<int>(HIDDEN ? p.ffn : p.dim);
+    rows = static_cast<int>(HIDDEN ? p.dim : p.ffn);
     step = 4 * V * p.team;
     most_steps = (n + step - 1) / step;
     steps = max(0, (n - warp * 4 * V + step - 1) / step);
     k0 = (warp * 4 + (threadIdx.x & 3)) * V;
     if (steps == 0) item = end;
-    rows();
+    find_rows();
 #pragma unroll
     for (int i = 0; i < AHEAD; ++i) fetch();
   }
   static __device__ __forceinline__ const T* base(const MoeFewParams& p) { return static_cast<const T*>(HIDDEN ? p.down : p.gate_up); }
-  // The matrix row of the lane's row i (r and r + 8 of each half) of an item's tile: 32 rows of D; or 16 rows of G, each
+  // The lane's row i (r and r + 8 of each half) of a tile in a pass's matrix: 32 rows of D; or 16 rows of G, each
   // followed by the row of U that goes with it.
-  __device__ __forceinline__ long long row_of(int of, int i) const {
-    const int in = of / tiles, lane = (threadIdx.x & 31) / 4, tile = of - in * tiles;
-    const long long e = r.passes[in].expert;
-    if (HIDDEN) return e * p.dim + min(static_cast<long long>(tile * MF_ROWS + 8 * i + lane), p.dim - 1);
-    return e * 2 * p.ffn + (i & 1) * p.ffn + min(static_cast<long long>(tile * (MF_ROWS / 2) + 8 * (i / 2) + lane), p.ffn - 1);
+  __device__ __forceinline__ const T* row_of(int in, int of, int i) const {
+    const int lane = (threadIdx.x & 31) / 4;
+    const T* const matrix = base(p) + static_cast<long long>(r.passes[in].expert * (HIDDEN ? 1 : 2)) * rows * n;
+    const int row = HIDDEN ? of * MF_ROWS + 8 * i + lane : of * (MF_ROWS / 2) + 8 * (i / 2) + lane;
+    return matrix + static_cast<long long>(min(row, rows - 1) + (HIDDEN ? 0 : (i & 1) * rows)) * n;
   }
-  __device__ __forceinline__ void rows() {
+  __device__ __forceinline__ void find_rows() {
     s = 0;
     k = k0;
     if (item >= end) return;
+    while (tile >= tiles) {
+      tile -= tiles;
+      ++pass;
+    }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) at[i] = base(p) + row_of(item, i) * n;
+    for (int i = 0; i < 4; ++i) at[i] = row_of(pass, tile, i);
   }
   __device__ __forceinline__ void fetch() {
     if (item < end) {
@@ -364,7 +369,8 @@ struct Stream {
       k += step;
       if (++s == steps) {
         item += stride;
-        rows();
+        tile += stride;
+        find_rows();
       }
     }
     nsptx::cp_async_commit();
@@ -429,12 +435,12 @@ struct Stream {
     for (int t = 0; t < NT; ++t) side[t].template load<VEC>(row[t], static_cast<int>(2 * p.hidden_ld), k0 + i * step, n);
   }
   template <int NT, bool HELD>
-  __device__ __forceinline__ void tile(int of, const char* const (&row)[NT], const uint4* held, S (&now)[NT], float (&acc)[2][NT][4]) {
+  __device__ __forceinline__ void products(int in, int of, const char* const (&row)[NT], const uint4* held, S (&now)[NT], float (&acc)[2][NT][4]) {
     const int lane = threadIdx.x & 31;
     bool odd[4] = {};
     if constexpr (!VEC && sizeof(T) == 2) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) odd[i] = reinterpret_cast<uintptr_t>(base(p) + row_of(of, i) * n) & 2;
+      for (int i = 0; i < 4; ++i) odd[i] = reinterpret_cast<uintptr_t>(row_of(in, of, i)) & 2;
     }
     for (int i = 0; i < steps; ++i) {
       S side[NT];
@@ -502,7 +508,7 @@ __device__ __forceinline__ void tiles_of_pass(S& stream, const Team& team, int& 
   for (; item < to; item += stream.stride) {
     const int tile = item - pass * stream.tiles;
     float acc[2][NT][4] = {};
-    stream.template tile<NT, HELD>(item, row, team.held, now, acc);
+    stream.template products<NT, HELD>(pass, tile, row, team.held, now, acc);
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
       // a lane's sums: of rows lane / 4 and 8 more of each half of the tile, columns 2 (lane % 4) and the next
@@ -544,8 +550,8 @@ __device__ __forceinline__ void all_tiles(const MoeFewParams& p, const Routing& 
   float* const sums = reinterpret_cast<float*>(held + MF_WARPS * p.held * 32);
   const Team team = {p.team, warp & (p.team - 1), warp / p.team, held + warp * p.held * 32 + lane, sums + warp / p.team * p.team * 8 * 32};
   Stream<T, HIDDEN, VEC> stream(p, r, smem + warp * ring_words(HIDDEN, VEC), first, last, team.id, MF_WARPS / p.team, team.warp, tiles);
-  for (int item = first + team.id; item < last;) {
-    const int pass = item / tiles, to = min(last, (pass + 1) * tiles), count = r.passes[pass].count;
+  for (int item = first + team.id, pass = item / tiles; item < last; ++pass) {
+    const int to = min(last, (pass + 1) * tiles), count = r.passes[pass].count;
     const int words = S::Q * stream.most_steps;
     if (count <= 8 && words <= p.held)
       tiles_of_pass<1, true>(stream, team, item, to, pass, use);
