@@ -51,7 +51,7 @@ struct BlockNormParams {
   const void *branch_weight, *weight;
   long long branch_ld, x_ld, h_ld, n_ld, dh_ld, dn_ld, dbranch_ld, dx_ld, gate_ld, dgate_ld;
   long long tokens, dim;
-  int gate_kind, post, weight_fp32, norm;  // norm: whether n is wanted
+  int gate_kind, post, weight_fp32;
   float alpha, beta, eps;
   float* partial;                  // gradient: [blocks][2][dim], dp and dw
   // rows in registers: inputs and outputs by their place, with steps from row to row in bytes

@@ -5,15 +5,23 @@
 //   y_t = sum over j of w_tj D_e h_s
 // with silu(a) = a / (1 + exp(-a)).
 //
-// The weights of the experts that are named, 3 dim ffn values each, are read
-// once and are nearly all of the bytes, so the layer is bound by memory: n
-// tokens of an expert make 2 n operations of each value. The products run on
-// m16n8k16 tensor instructions on registers (16 rows of weights, 8 tokens),
-// which keep pace up to some 30 tokens an expert, because the weights then go
-// from global memory to their instruction without a stop in shared memory: the
-// order of k within a product is free, so a lane takes 16 consecutive bytes of a
-// row and the tokens' values in the same order. Blocks find the tokens of their
-// experts among all slots themselves, which spares a kernel.
+// The matrices of the experts that are named, 3 dim ffn values each, are read
+// once and are nearly all of the bytes, so the layer is bound by memory: n tokens
+// of an expert make 2 n operations of each value. Up to 16 of an expert's slots
+// share a pass over its matrices, whose tiles (32 rows) all blocks deal among
+// them; the 16 warps of a block split k of a tile. Each lane copies the 16-byte
+// words of its rows ahead to its own places of shared memory and hands them to
+// m16n8k16 tensor instructions as they are: the order of k within a product is
+// free, so its words and the tokens' are taken in the same order, and nothing is
+// exchanged between lanes. (The 5th-generation instruction takes 128 rows, whose
+// tiles are too few for the card: 8 experts of 1408 rows make 176.)
+// Blocks find the tokens of their experts among all slots themselves, which
+// spares a kernel.
+//
+// 64 experts of 1408 x 2048 bf16 by one slot each take 198 us (5.6 TB/s with the
+// three launches; 0.83 of the measured copy), by 8 each 208 and by 16 each 235;
+// one token of 8 experts 36 us (3.8 TB/s: three kernels of 3 us each with nothing
+// to do, and 4.6 tiles a block).
 #include <algorithm>
 #include <climits>
 
@@ -69,9 +77,10 @@ constexpr size_t routing_bytes(int entries, int experts, int slots) {
   return sizeof(Pass) * entries + sizeof(int) * experts + 2 * sizeof(short) * static_cast<size_t>(slots);
 }
 
-// Reads the ids, sorts the slots by expert and lists the passes; their number. The order of the slots of a pass reaches no result:
-// every column of a product is its own. So atomics may decide it, unless an
-// expert takes several passes, which have to be the same ones in every block.
+// Reads the ids, sorts the slots by expert and lists the passes; their number.
+// The order of the slots of a pass reaches no result: every column of a product
+// is its own. So atomics may decide it, unless an expert takes several passes,
+// which have to be the same ones in every block.
 __device__ __forceinline__ int find_passes(const MoeFewParams& p, const Routing& r) {
   __shared__ int2 found;
   const int lane = threadIdx.x & 31, slots = p.tokens * p.k;
@@ -309,14 +318,15 @@ struct Stream {
   static_assert(32 * 4 * PLANES <= 4 * stage_words(false), "a stage");
   const MoeFewParams& p;
   const Routing& r;
-  int tiles, rows, end, stride;  // tiles of a pass, rows of a matrix; items (tiles of all passes) of the block; of a team
-  int n, step, steps;      // values of a row, from a warp's step to its next, steps of a tile
-  int most_steps;          // of any of the team's warps
-  int k0;                  // the lane's first value
+  int tiles, rows;             // tiles of a pass, rows of a matrix
+  int end, stride;             // items (tiles of all passes): the block's last, from a team's to its next
+  int n, step, steps;          // values of a row, from a warp's step to its next, steps of a tile
+  int most_steps;              // of any of the team's warps
+  int k0;                      // the lane's first value
   uint4* ring;
   int fill, take;
   int item, pass, tile, k, s;  // of the next copy
-  const T* at[4];          // the lane's rows there: r and r + 8 of each half of the tile
+  const T* at[4];              // the lane's rows there: r and r + 8 of each half of the tile
   uint64_t policy;
 
   __device__ __forceinline__ Stream(const MoeFewParams& params, const Routing& routing, uint4* warp_ring, int first, int last,
@@ -412,8 +422,7 @@ struct Stream {
     return make_uint4(v[0], v[1], v[2], v[3]);
   }
 
-  // The products of the next tile with 8 * NT slots, whose rows are `row` and whose words of all of the warp's steps
-  // are at `held`, if that is not null.
+  // Puts the lane's words of 8 * NT slots, whose rows are `row`, for all of the warp's steps at `held`.
   template <int NT>
   __device__ __forceinline__ void hold(const char* const (&row)[NT], uint4* held) const {
     for (int i = 0; i < steps; ++i) {
@@ -434,6 +443,7 @@ struct Stream {
 #pragma unroll
     for (int t = 0; t < NT; ++t) side[t].template load<VEC>(row[t], static_cast<int>(2 * p.hidden_ld), k0 + i * step, n);
   }
+  // The products of the next tile, `of` of pass `in`, with those slots.
   template <int NT, bool HELD>
   __device__ __forceinline__ void products(int in, int of, const char* const (&row)[NT], const uint4* held, S (&now)[NT], float (&acc)[2][NT][4]) {
     const int lane = threadIdx.x & 31;
@@ -475,6 +485,7 @@ struct Stream {
     }
   }
 };
+
 // A barrier of the team's warps, each of them together.
 __device__ __forceinline__ void team_sync(int team, int warps) {
   __syncwarp();
@@ -525,7 +536,8 @@ __device__ __forceinline__ void tiles_of_pass(S& stream, const Team& team, int& 
 #pragma unroll
       for (int i = 0; i < 8; ++i) team.sums[(team.warp * 8 + i) * 32 + lane] = acc[i / 4][t][i % 4];
       team_sync(team.id, team.warps);
-      // in a fixed order of the warps
+      // By four warps, in a fixed order of all, while the others go on with the next tile. (By two of them in wider words
+      // 64 experts by 8 slots each take 228 us, by all 225, so 208.)
       for (int q = team.warp; q < 4; q += team.warps) {
         float a = 0.0f, b = 0.0f;
         const float* from = team.sums + ((q >> 1) * 4 + (q & 1)) * 32 + lane;
@@ -619,7 +631,8 @@ __global__ void __launch_bounds__(MF_THREADS, 1) ns_moe_few_down_kernel(const __
 
 // y: the sums over each token's slots, in the slots' order, 4 values a thread.
 // (Summed by the warp that brought a token's last part, the layer took one kernel
-// less and XXX more: a team waits for its warp's fence, count and loads.)
+// less and 64 experts by one slot each 237 us instead of 202: a team waits for its
+// warp's fence, count and loads.)
 template <typename T>
 __global__ void __launch_bounds__(MF_SUM_THREADS) ns_moe_few_sum_kernel(const __grid_constant__ MoeFewParams p) {
   nsptx::griddep_wait();
