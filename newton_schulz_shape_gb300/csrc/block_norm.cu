@@ -489,6 +489,10 @@ __global__ void __launch_bounds__(32 * BN_WARPS, bn_blocks(true, NV)) ns_block_n
         d[i] = fma2(r2, fma2(m, minus, mul2(v[i], w[i])), d[i]);  // t
       }
     }
+    float2 g[N];
+    // value by value a row's inputs are in memory only, where an output may take their place
+    if constexpr (!WORDS)
+      if (gated) lanes.template get_row<T>(IN_GATE, g);
     if (has_dx) {
 #pragma unroll
       for (int i = 0; i < N; ++i) h[i] = mul2(d[i], both(p.alpha));
@@ -497,12 +501,11 @@ __global__ void __launch_bounds__(32 * BN_WARPS, bn_blocks(true, NV)) ns_block_n
     if (has_branch) {
       const float r1 = post ? rsqrtf(fmaf(sum[2], inv_dim, p.eps)) : 1.0f;
       lanes.weights(0, w);
-      float2 g[N];
-      if (gated) {
-        lanes.template get_row<T>(IN_GATE, g);
-      } else {
+      if (!gated) {
 #pragma unroll
         for (int i = 0; i < N; ++i) g[i] = both(gt);
+      } else if constexpr (WORDS) {
+        lanes.template get_row<T>(IN_GATE, g);
       }
       s0 = s1 = both(0.0f);
 #pragma unroll

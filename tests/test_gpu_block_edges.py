@@ -123,6 +123,33 @@ def test_rows_at_the_limits_of_a_team(D, x, r, gate):
         bo.test_block_norm_gradient(T, D, True, gate, True, 0, 0, x, r, False)
 
 
+# Rows in words, value by value in registers, and longer than those.
+@pytest.mark.parametrize("D", [64, 33, 4097, 8200])
+@pytest.mark.parametrize("gate", ["none", "token", "value"])
+def test_every_output_of_the_gradient_in_place_of_every_input(D, gate):
+    g = gen(D)
+    T = 9
+    dh, dn, b, h = (randn(g, T, D) for _ in range(4))
+    gt = dict(none=None, token=randn(g, T), value=randn(g, T, D))[gate]
+    p, w = randn(g, D), randn(g, D)
+    ins = dict(dh=dh, dn=dn, b=b, h=h, **({"gt": gt} if gate == "value" else {}))
+    names = ["db", "dx"] + (["dg"] if gate == "value" else [])
+
+    def run(ins, outs):
+        nsg.ns_block_norm_grad(ins["dh"], ins["dn"], ins["b"], ins["h"], outs["db"], outs["dx"], p, w, ins.get("gt", gt),
+                               grad_gate=outs.get("dg"), residual_scale=0.75, branch_scale=1.5)
+        return outs
+
+    want = run(ins, {n: torch.empty(T, D, device=DEV) for n in names})
+    for n in names:
+        for at in ins:
+            now = {k: v.clone() for k, v in ins.items()}
+            got = run(now, {m: now[at] if m == n else torch.empty(T, D, device=DEV) for m in names})
+            assert all(torch.equal(got[m], want[m]) for m in names), (n, at)
+            assert all(torch.equal(now[k], ins[k]) for k in ins if k != at)
+    ok()
+
+
 def test_rows_past_32_bits():
     T, D = (2 ** 32 + 2 ** 20) // 8192 + 3, 8192
     x = torch.zeros(T, D, dtype=bf16, device=DEV)
