@@ -37,6 +37,9 @@ constexpr size_t BN_SMEM = 224 * 1024;
 constexpr int bn_blocks(bool grad, int values) { return grad || values > 8 ? 1 : 2; }
 constexpr int BN_ANY_THREADS = 256;
 constexpr int BN_MAX_BLOCKS = 608;  // of a gradient launch, each with its own sums of dp and dw
+// Of a block that joins partial sums: few enough to stand beside the gradient's blocks and wait there (200 rows of 8192
+// bf16 backward 15.8 us, with 32 warps 17.0).
+constexpr int BN_SUM_WARPS = 8;
 constexpr long long BN_MAX_DIM = 1 << 20;
 
 enum Gate { NO_GATE, TOKEN_GATE, VALUE_GATE };
@@ -678,9 +681,9 @@ struct BlockNormSumParams {
 };
 
 // The weights' gradients: sums of the blocks' partial sums, in a fixed order: 32
-// columns a block, whose 32 warps split the partial sums.
-__global__ void __launch_bounds__(1024) ns_block_norm_sum_kernel(const __grid_constant__ BlockNormSumParams p) {
-  __shared__ float part[32][33];
+// columns a block, whose warps split the partial sums.
+__global__ void __launch_bounds__(32 * BN_SUM_WARPS) ns_block_norm_sum_kernel(const __grid_constant__ BlockNormSumParams p) {
+  __shared__ float part[BN_SUM_WARPS][32];
   nsptx::griddep_wait();
   nsptx::griddep_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -688,15 +691,14 @@ __global__ void __launch_bounds__(1024) ns_block_norm_sum_kernel(const __grid_co
   float sum = 0.0f;
   if (col < 2 * p.dim) {
 #pragma unroll 8
-    for (int b = warp; b < p.blocks; b += 32) sum += p.partial[b * 2 * p.dim + col];
+    for (int b = warp; b < p.blocks; b += BN_SUM_WARPS) sum += p.partial[b * 2 * p.dim + col];
   }
   part[warp][lane] = sum;
   __syncthreads();
-  sum = warp_sum(part[lane][warp]);  // warp w: column w's parts
-  const long long c = static_cast<long long>(blockIdx.x) * 32 + warp;
-  if (lane || c >= 2 * p.dim) return;
-  float* out = p.out[c >= p.dim];
-  if (out) out[c >= p.dim ? c - p.dim : c] = sum;
+  if (warp || col >= 2 * p.dim) return;
+  for (int w = 1; w < BN_SUM_WARPS; ++w) sum += part[w][lane];
+  float* out = p.out[col >= p.dim];
+  if (out) out[col >= p.dim ? col - p.dim : col] = sum;
 }
 
 // NV values a lane; false if the copies of two rows do not fit an SM, or steps an int.
@@ -965,7 +967,7 @@ int ns_block_norm_grad(const void* grad_residual_out, const void* grad_out, cons
   if ((rc = device_setup(&dev, &status, &nsm)) != NS_OK) return rc;
   nsk::BlockNormSumParams sp = {static_cast<const float*>(workspace), {grad_branch_weight, grad_weight}, dim, blocks};
   const cudaError_t e = counted(K_BLOCK_NORM, st, [&] {
-    return nsk::launch_pdl(nsk::ns_block_norm_sum_kernel, dim3(static_cast<unsigned>((2 * dim + 31) / 32)), dim3(1024), 0, st, sp);
+    return nsk::launch_pdl(nsk::ns_block_norm_sum_kernel, dim3(static_cast<unsigned>((2 * dim + 31) / 32)), dim3(32 * nsk::BN_SUM_WARPS), 0, st, sp);
   });
   return e == cudaSuccess ? NS_OK : NS_ERR_CUDA;
 }
