@@ -441,13 +441,16 @@ struct Tensors {
     at.resize(n);
     numels.resize(n);
     dtypes.resize(n);
-    const int device = c10::cuda::current_device();
+    int device = -1;  // the call's, once there is a GPU
     const bool recording = c10::GradMode::is_enabled();
     for (Py_ssize_t j = 0; j < n; ++j) {
       PyObject* const item = PySequence_Fast_GET_ITEM(items.get(), j);
       if (!THPVariable_CheckExact(item) && !THPVariable_Check(item)) a.bad_item(i, j, "a tensor", Py_TYPE(item)->tp_name);
-      const at::Tensor& t = THPVariable_Unpack(item);
+    }
+    for (Py_ssize_t j = 0; j < n; ++j) {
+      const at::Tensor& t = tensor(j);
       const at::ScalarType type = t.scalar_type();
+      if (device < 0 && t.is_cuda()) device = c10::cuda::current_device();
       if (!t.is_cuda() || t.get_device() != device || t.layout() != c10::kStrided || !t.is_non_overlapping_and_dense() ||
           (type != at::kBFloat16 && type != at::kHalf && type != at::kFloat))
         a.bad_item(i, j, "a GPU tensor of bfloat16, float16 or float32 without gaps in memory", t);
