@@ -18,10 +18,10 @@
 // Blocks find the tokens of their experts among all slots themselves, which
 // spares a kernel.
 //
-// 64 experts of 1408 x 2048 bf16 by one slot each take 198 us (5.6 TB/s with the
-// three launches; 0.83 of the measured copy), by 8 each 208 and by 16 each 235;
-// one token of 8 experts 36 us (3.8 TB/s: three kernels of 3 us each with nothing
-// to do, and 4.6 tiles a block).
+// 64 experts of 1408 x 2048 bf16 by one slot each take 197-201 us (5.6 TB/s with
+// the three launches; 0.83 of the measured copy), by 8 each 207-211 and by 16 each
+// 236; one token of 8 experts 36 us (3.8 TB/s: three kernels of 3 us each with
+// nothing to do, and 4.6 tiles a block).
 #include <algorithm>
 #include <climits>
 
@@ -293,14 +293,19 @@ __device__ __forceinline__ void times(float (&c)[4], const uint4& r, const uint4
   }
 }
 
-// A warp's ring of shared memory: the words of the steps on their way, and of one
-// in use. The second product's tokens take more of the memory (64 experts by 16
-// slots each 95 us with two steps ahead, 109 with three and the tokens in L2).
-__host__ __device__ constexpr int ahead(bool hidden, bool vec) { return hidden || !vec ? 2 : 3; }
+// Steps of a warp whose words are on their way, and places for them in the warp's
+// ring of shared memory. A lane copies into its own words there, once the products
+// that took the step before from them are issued. Where those take long (`wide`:
+// tf32, several a value) one step more has its place and is copied before them (17
+// tokens by 4 of 60 experts of 2112 x 960 fp32 168 us, without 186; for bf16 the
+// memory is better spent on sums: 64 tokens by 6 of 64 experts of 1408 x 2048
+// 217-222 us, was 235). h is then twice its size, and takes the memory of one.
+__host__ __device__ constexpr int ahead(bool hidden, bool vec, bool wide) { return wide && (hidden || !vec) ? 2 : 3; }
 // 16-byte words of a step: four rows of 16 bytes a lane. Rows that are not made of aligned 16-byte words are copied in
 // aligned 4-byte words, five of which cover the values of a 16-bit type.
 __host__ __device__ constexpr int stage_words(bool vec) { return vec ? 4 * 32 : 5 * 32; }
-__host__ __device__ constexpr int ring_words(bool hidden, bool vec) { return (ahead(hidden, vec) + 1) * stage_words(vec); }
+template <typename S, bool HIDDEN, bool VEC>
+constexpr int RING_WORDS = (ahead(HIDDEN, VEC, S::WIDE) + S::WIDE) * stage_words(VEC);
 
 // A team of warps goes through the tiles of a block that fall to it, all passes in
 // a row: `Stream` copies the weights of a warp's next steps to its ring, into the
@@ -312,7 +317,7 @@ __host__ __device__ constexpr int ring_words(bool hidden, bool vec) { return (ah
 template <typename T, bool HIDDEN, bool VEC>
 struct Stream {
   using S = Side<T, HIDDEN>;
-  static constexpr int V = 16 / sizeof(T), AHEAD = ahead(HIDDEN, VEC), STAGE = stage_words(VEC), RING = ring_words(HIDDEN, VEC);
+  static constexpr int V = 16 / sizeof(T), AHEAD = ahead(HIDDEN, VEC, S::WIDE), STAGE = stage_words(VEC), RING = RING_WORDS<S, HIDDEN, VEC>;
   // 4-byte words of a row, where there are no 16-byte ones
   static constexpr int PLANES = sizeof(T) == 4 ? 4 : 5;
   static_assert(32 * 4 * PLANES <= 4 * stage_words(false), "a stage");
@@ -476,12 +481,13 @@ struct Stream {
           a[j] = from_words(reinterpret_cast<const uint32_t*>(ring + take) + j * PLANES * 32 + lane, odd[j], n - k0 - i * step);
       }
       take = take + STAGE == RING ? 0 : take + STAGE;
-      fetch();
+      if constexpr (S::WIDE) fetch();
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
         times(acc[0][t], a[0], a[1], side[t]);
         times(acc[1][t], a[2], a[3], side[t]);
       }
+      if constexpr (!S::WIDE) fetch();
     }
   }
 };
@@ -496,7 +502,7 @@ __device__ __forceinline__ void team_sync(int team, int warps) {
 struct Team {
   int warps, warp, id;   // of the team; this one's; the team's number
   uint4* held;           // the lane's words
-  float* sums;           // [warps][8][32]
+  float* sums;           // [MF_NT][warps][8][32]
 };
 
 // A team's tiles of one pass, from `item` on: use(tile, row, slot, a, b) gets the
@@ -520,33 +526,36 @@ __device__ __forceinline__ void tiles_of_pass(S& stream, const Team& team, int& 
     const int tile = item - pass * stream.tiles;
     float acc[2][NT][4] = {};
     stream.template products<NT, HELD>(pass, tile, row, team.held, now, acc);
+    // a lane's sums: of rows lane / 4 and 8 more of each half of the tile, columns 2 (lane % 4) and the next
+    auto give = [&](int t, int half, int c, int at, float a, float b) {
+      const int j = 8 * t + 2 * (at & 3) + c;
+      if (j < of.count) use(tile, 16 * half + at / 4, static_cast<int>(r.sorted[of.first + j]), a, b);
+    };
+    if (team.warps == 1) {
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      // a lane's sums: of rows lane / 4 and 8 more of each half of the tile, columns 2 (lane % 4) and the next
-      auto give = [&](int half, int c, int at, float a, float b) {
-        const int j = 8 * t + 2 * (at & 3) + c;
-        if (j < of.count) use(tile, 16 * half + at / 4, static_cast<int>(r.sorted[of.first + j]), a, b);
-      };
-      if (team.warps == 1) {
+      for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int q = 0; q < 4; ++q) give(q >> 1, q & 1, lane, acc[q >> 1][t][q & 1], acc[q >> 1][t][(q & 1) + 2]);
-        continue;
+        for (int q = 0; q < 4; ++q) give(t, q >> 1, q & 1, lane, acc[q >> 1][t][q & 1], acc[q >> 1][t][(q & 1) + 2]);
+      continue;
+    }
+    team_sync(team.id, team.warps);  // the last sums are read
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) team.sums[((t * team.warps + team.warp) * 8 + i) * 32 + lane] = acc[i / 4][t][i % 4];
+    team_sync(team.id, team.warps);
+    // Of all slots at once (64 experts by 12 slots each 222 us, 8 by 8 of them 236).
+    // By four warps for 8 slots, in a fixed order of all, while the others go on with the next tile. (By two of them in
+    // wider words 64 experts by 8 slots each take 228 us, by all 225, so 208.)
+    for (int q = team.warp; q < 4 * NT; q += team.warps) {
+      const int t = q >> 2, half = (q >> 1) & 1, c = q & 1;
+      float a = 0.0f, b = 0.0f;
+      const float* from = team.sums + (t * team.warps * 8 + half * 4 + c) * 32 + lane;
+      for (int w = 0; w < team.warps; ++w, from += 8 * 32) {
+        a += from[0];
+        b += from[2 * 32];
       }
-      team_sync(team.id, team.warps);  // the last sums are read
-#pragma unroll
-      for (int i = 0; i < 8; ++i) team.sums[(team.warp * 8 + i) * 32 + lane] = acc[i / 4][t][i % 4];
-      team_sync(team.id, team.warps);
-      // By four warps, in a fixed order of all, while the others go on with the next tile. (By two of them in wider words
-      // 64 experts by 8 slots each take 228 us, by all 225, so 208.)
-      for (int q = team.warp; q < 4; q += team.warps) {
-        float a = 0.0f, b = 0.0f;
-        const float* from = team.sums + ((q >> 1) * 4 + (q & 1)) * 32 + lane;
-        for (int w = 0; w < team.warps; ++w, from += 8 * 32) {
-          a += from[0];
-          b += from[2 * 32];
-        }
-        give(q >> 1, q & 1, lane, a, b);
-      }
+      give(t, half, c, lane, a, b);
     }
   }
 }
@@ -558,10 +567,11 @@ __device__ __forceinline__ void all_tiles(const MoeFewParams& p, const Routing& 
   const long long items = static_cast<long long>(passes) * tiles;
   const int first = static_cast<int>(items * blockIdx.x / gridDim.x), last = static_cast<int>(items * (blockIdx.x + 1) / gridDim.x);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  uint4* const held = smem + MF_WARPS * ring_words(HIDDEN, VEC);
+  constexpr int RING = RING_WORDS<S, HIDDEN, VEC>;
+  uint4* const held = smem + MF_WARPS * RING;
   float* const sums = reinterpret_cast<float*>(held + MF_WARPS * p.held * 32);
-  const Team team = {p.team, warp & (p.team - 1), warp / p.team, held + warp * p.held * 32 + lane, sums + warp / p.team * p.team * 8 * 32};
-  Stream<T, HIDDEN, VEC> stream(p, r, smem + warp * ring_words(HIDDEN, VEC), first, last, team.id, MF_WARPS / p.team, team.warp, tiles);
+  const Team team = {p.team, warp & (p.team - 1), warp / p.team, held + warp * p.held * 32 + lane, sums + warp / p.team * p.team * MF_NT * 8 * 32};
+  Stream<T, HIDDEN, VEC> stream(p, r, smem + warp * RING, first, last, team.id, MF_WARPS / p.team, team.warp, tiles);
   for (int item = first + team.id, pass = item / tiles; item < last; ++pass) {
     const int to = min(last, (pass + 1) * tiles), count = r.passes[pass].count;
     const int words = S::Q * stream.most_steps;
@@ -577,12 +587,13 @@ __device__ __forceinline__ void all_tiles(const MoeFewParams& p, const Routing& 
 }
 
 // Shared memory: the rings, what is held of the tokens, the parts of split sums, the routing.
-__host__ __device__ constexpr int fixed_words(bool hidden, bool vec) { return MF_WARPS * (ring_words(hidden, vec) + 8 * 8); }
+template <typename T, bool HIDDEN, bool VEC>
+constexpr int FIXED_WORDS = MF_WARPS * (RING_WORDS<Side<T, HIDDEN>, HIDDEN, VEC> + 8 * 8 * MF_NT);
 constexpr int MF_HELD_WORDS = MF_WARPS * 32;
 constexpr size_t MF_SMEM = 226 * 1024;
-template <bool HIDDEN, bool VEC>
+template <typename T, bool HIDDEN, bool VEC>
 __device__ __forceinline__ Routing routing_of(const MoeFewParams& p, uint4* smem) {
-  return Routing(p, smem + fixed_words(HIDDEN, VEC) + p.held * MF_HELD_WORDS);
+  return Routing(p, smem + FIXED_WORDS<T, HIDDEN, VEC> + p.held * MF_HELD_WORDS);
 }
 
 // h of all slots.
@@ -591,7 +602,7 @@ __global__ void __launch_bounds__(MF_THREADS, 1) ns_moe_few_hidden_kernel(const 
   extern __shared__ uint4 few_smem[];
   nsptx::griddep_wait();
   nsptx::griddep_launch_dependents();
-  const Routing r = routing_of<false, VEC>(p, few_smem);
+  const Routing r = routing_of<T, false, VEC>(p, few_smem);
   const int passes = find_passes(p, r);
   all_tiles<T, false, VEC>(
       p, r, few_smem, passes, static_cast<int>((p.ffn + MF_ROWS / 2 - 1) / (MF_ROWS / 2)),
@@ -618,7 +629,7 @@ __global__ void __launch_bounds__(MF_THREADS, 1) ns_moe_few_down_kernel(const __
   extern __shared__ uint4 few_smem[];
   nsptx::griddep_wait();
   nsptx::griddep_launch_dependents();
-  const Routing r = routing_of<true, VEC>(p, few_smem);
+  const Routing r = routing_of<T, true, VEC>(p, few_smem);
   const int passes = find_passes(p, r);
   all_tiles<T, true, VEC>(p, r, few_smem, passes, static_cast<int>((p.dim + MF_ROWS - 1) / MF_ROWS),
                           [&](int tile, int row, int slot, float a, float b) {
@@ -683,12 +694,12 @@ int launch_few(MoeFewParams p, int nsm, cudaStream_t st) {
   const int slots = p.tokens * p.k, named = std::min(p.experts, slots);
   p.entries = named + slots / (8 * MF_NT);
   const size_t routing = routing_bytes(p.entries, p.experts, slots);
-  static_assert(sizeof(uint4) * fixed_words(false, VEC) + routing_bytes(1024 + MF_MAX_TOKENS * 32 / (8 * MF_NT), 1024, MF_MAX_TOKENS * 32) <= MF_SMEM,
+  static_assert(sizeof(uint4) * std::max(FIXED_WORDS<T, false, VEC>, FIXED_WORDS<T, true, VEC>) + routing_bytes(1024 + MF_MAX_TOKENS * 32 / (8 * MF_NT), 1024, MF_MAX_TOKENS * 32) <= MF_SMEM,
                 "shared memory of a block");
-  auto launch = [&](void (*kernel)(MoeFewParams), bool hidden, long long tiles, long long n, int words) {
+  auto launch = [&](void (*kernel)(MoeFewParams), int fixed_words, long long tiles, long long n, int words) {
     const long long steps = (n + VALUES - 1) / VALUES;
     p.team = team_of(tiles * named, steps, nsm);
-    const size_t fixed = sizeof(uint4) * fixed_words(hidden, VEC) + routing;
+    const size_t fixed = sizeof(uint4) * fixed_words + routing;
     // of 8 or 16 slots; what is not held stays with L1
     const long long room = (MF_SMEM - fixed) / (sizeof(uint4) * MF_HELD_WORDS);
     const long long most = (steps + p.team - 1) / p.team * words;
@@ -700,8 +711,8 @@ int launch_few(MoeFewParams p, int nsm, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     return nsorch::counted(nsorch::K_MOE, st, [&] { return launch_pdl(kernel, dim3(blocks), dim3(MF_THREADS), smem, st, p); });
   };
-  cudaError_t e = launch(ns_moe_few_hidden_kernel<T, VEC>, false, (p.ffn + MF_ROWS / 2 - 1) / (MF_ROWS / 2), p.dim, Side<T, false>::Q);
-  if (e == cudaSuccess) e = launch(ns_moe_few_down_kernel<T, VEC>, true, (p.dim + MF_ROWS - 1) / MF_ROWS, p.ffn, Side<T, true>::Q);
+  cudaError_t e = launch(ns_moe_few_hidden_kernel<T, VEC>, FIXED_WORDS<T, false, VEC>, (p.ffn + MF_ROWS / 2 - 1) / (MF_ROWS / 2), p.dim, Side<T, false>::Q);
+  if (e == cudaSuccess) e = launch(ns_moe_few_down_kernel<T, VEC>, FIXED_WORDS<T, true, VEC>, (p.dim + MF_ROWS - 1) / MF_ROWS, p.ffn, Side<T, true>::Q);
   if (e != cudaSuccess) return NS_ERR_CUDA;
   e = nsorch::counted(nsorch::K_MOE, st, [&] {
     const unsigned int wide = static_cast<unsigned int>((p.dim + 4 * MF_SUM_THREADS - 1) / (4 * MF_SUM_THREADS));
