@@ -299,7 +299,7 @@ __device__ __forceinline__ void times(float (&c)[4], const uint4& r, const uint4
 // tf32, several a value) one step more has its place and is copied before them (17
 // tokens by 4 of 60 experts of 2112 x 960 fp32 168 us, without 186; for bf16 the
 // memory is better spent on sums: 64 tokens by 6 of 64 experts of 1408 x 2048
-// 217-222 us, was 235). h is then twice its size, and takes the memory of one.
+// 212-226 us, was 233-240). h is then twice its size, and takes the memory of one.
 __host__ __device__ constexpr int ahead(bool hidden, bool vec, bool wide) { return wide && (hidden || !vec) ? 2 : 3; }
 // 16-byte words of a step: four rows of 16 bytes a lane. Rows that are not made of aligned 16-byte words are copied in
 // aligned 4-byte words, five of which cover the values of a 16-bit type.
