@@ -189,9 +189,9 @@ struct Args {
     if (!p && PyErr_Occurred()) throw Refused();
     return p;
   }
-  // The items of a list or tuple, a new reference.
+  // The items of a list or tuple as a tuple, a new reference: a list may change while another thread runs.
   PyObject* items(int i) const {
-    PyObject* found = PySequence_Fast(at[i], sig.names[i]);
+    PyObject* found = PySequence_Tuple(at[i]);
     if (found) return found;
     PyErr_Clear();
     bad(i, "a list of tensors");
@@ -427,8 +427,8 @@ PyObject* distill_grad(const Args& a) {
 }
 
 // The tensors of argument i, as the library takes them: of any floating type of its own, dense in memory. There may be
-// hundreds, each of which costs more host time than its values cost the GPU: what they share is looked up once, and the
-// list keeps them (270 small tensors normed and clipped into others in 30 us, was 75; host time both).
+// hundreds, each of which costs more host time than its values cost the GPU: what they share is looked up once, and a
+// tuple keeps them (270 small tensors normed and clipped into others in 30 us, was 75; host time both).
 struct Tensors {
   std::unique_ptr<PyObject, decltype(&Py_DecRef)> items;
   std::vector<const void*> at;
@@ -436,7 +436,7 @@ struct Tensors {
   std::vector<int> dtypes;
 
   Tensors(const Args& a, int i) : items(a.items(i), &Py_DecRef) {
-    const Py_ssize_t n = PySequence_Fast_GET_SIZE(items.get());
+    const Py_ssize_t n = PyTuple_GET_SIZE(items.get());
     if (n > INT_MAX) a.bad(i, "fewer tensors");
     at.resize(n);
     numels.resize(n);
@@ -444,7 +444,7 @@ struct Tensors {
     int device = -1;  // the call's, once there is a GPU
     const bool recording = c10::GradMode::is_enabled();
     for (Py_ssize_t j = 0; j < n; ++j) {
-      PyObject* const item = PySequence_Fast_GET_ITEM(items.get(), j);
+      PyObject* const item = PyTuple_GET_ITEM(items.get(), j);
       if (!THPVariable_CheckExact(item) && !THPVariable_Check(item)) a.bad_item(i, j, "a tensor", Py_TYPE(item)->tp_name);
     }
     for (Py_ssize_t j = 0; j < n; ++j) {
@@ -462,7 +462,7 @@ struct Tensors {
     }
   }
   int count() const { return static_cast<int>(at.size()); }
-  const at::Tensor& tensor(int j) const { return THPVariable_Unpack(PySequence_Fast_GET_ITEM(items.get(), j)); }
+  const at::Tensor& tensor(int j) const { return THPVariable_Unpack(PyTuple_GET_ITEM(items.get(), j)); }
 };
 
 PyObject* grad_norm(const Args& a) {

@@ -272,3 +272,24 @@ def test_gradients_that_a_captured_step_clips():
             c = ob.clip_scale(norm.item(), 1.0)
             near(b, c * f64(a), 2 * u * np.abs(c * f64(a)), a.dtype)
     ok()
+
+
+def test_a_list_that_changes_during_the_call():
+    # python code that runs between the look at the tensors and the launch empties the list
+    grads = [torch.ones(1000, device=DEV) for _ in range(50)]
+    norm = torch.full((1,), 4.0, device=DEV)
+
+    class Number:
+        def __float__(self):
+            grads.clear()
+            return 1.0
+
+    kept = list(grads)
+    nsg.ns_grad_clip(grads, grads, norm, Number(), eps=0.0)
+    assert not grads
+    assert all(t._version == 1 for t in kept)       # as the write counts
+    assert all((t == 0.25).all() for t in kept)
+    for given in (tuple(kept), iter(kept)):
+        nsg.ns_grad_norm(given, norm, scratch(nsg.ns_grad_norm_workspace_bytes(50)))
+        assert abs(norm.item() - (50 * 1000 / 16) ** 0.5) <= 32 * u * norm.item()
+    ok()
