@@ -63,6 +63,7 @@ struct BlockNormParams {
   int src_step[5], dst_step[3], place[5], wide[5];
   int warps, teams;                // of a row, rows of a block
   int stage;                       // 16-byte words of a warp's part of a row
+  int places;                      // rows of a warp in shared memory: the one in use, and the next where there is room
 };
 
 template <typename T>
@@ -301,63 +302,104 @@ struct Lanes {
   }
 };
 
-// The same for rows of any width, stride and alignment, value by value from
-// memory: value i of a lane is column i * 32 * warps + its place in the team.
+// The same for rows of any width, stride and alignment: a warp has 32 * NV columns
+// side by side, copies the aligned 16-byte words that cover them and takes them
+// from shared memory value by value. (Value by value from memory 4098 rows of 4095
+// bf16 took 331 us backward.)
 template <typename T, typename R, int NV, bool GRAD>
 struct Singles {
   static constexpr int N = NV / 2;
   const BlockNormParams& p;
   const RowTeam& team;
+  uint4* ring;          // the warp's
   const float* weight;  // the block's, [2][columns of a row]
-  int dim, at, step, row;
+  int first, count;     // columns of the warp
+  int fill, take, row;
 
   __device__ __forceinline__ Singles(const BlockNormParams& params, const RowTeam& t, uint4* smem)
-      : p(params), team(t), weight(reinterpret_cast<float*>(smem)), dim(static_cast<int>(params.dim)), at(t.warp * 32 + t.lane),
-        step(32 * t.warps), row(0) {}
+      : p(params), team(t), ring(smem + (threadIdx.x >> 5) * p.places * p.stage),
+        weight(reinterpret_cast<float*>(smem + p.warps * p.teams * p.places * p.stage)), first(t.warp * 32 * NV),
+        count(min(static_cast<int>(p.dim) - first, 32 * NV)), fill(0), take(0), row(0) {}
+  // Words of a warp's columns of E, wherever they start.
+  template <typename E>
+  static constexpr int WORDS_OF = 2 * NV * sizeof(E) + 1;
   __device__ __forceinline__ void prepare() const {
     float* const to = const_cast<float*>(weight);
-    for (int i = threadIdx.x; i < step * NV; i += blockDim.x) {
-      to[i] = i < dim ? weight_of<T>(p, p.branch_weight, i) : 0.0f;
-      to[step * NV + i] = i < dim ? weight_of<T>(p, p.weight, i) : 0.0f;
+    const int columns = 32 * NV * team.warps;
+    for (int i = threadIdx.x; i < columns; i += blockDim.x) {
+      to[i] = i < p.dim ? weight_of<T>(p, p.branch_weight, i) : 0.0f;
+      to[columns + i] = i < p.dim ? weight_of<T>(p, p.weight, i) : 0.0f;
     }
     __syncthreads();
   }
   template <typename E>
-  __device__ __forceinline__ void fetch(int, int) const {}
-  __device__ __forceinline__ void fetched() const {}
-  __device__ __forceinline__ void wait(int t) { row = t; }
-  __device__ __forceinline__ void taken() const {}
+  __device__ __forceinline__ const char* columns_of(int k, int t) const {
+    return static_cast<const char*>(p.src[k]) + static_cast<long long>(t) * p.src_step[k] + first * static_cast<int>(sizeof(E));
+  }
+  // The words begin in the row or, from the second row on, in the one before or between the two. What is before the
+  // first row is not the matrix's: its word there is put together from its values.
+  template <typename E>
+  __device__ __forceinline__ void fetch(int k, int t) const {
+    if (!p.src[k]) return;
+    const char* const from = columns_of<E>(k, t);
+    const int skip = static_cast<int>(reinterpret_cast<uintptr_t>(from) & 15), bytes = skip + count * static_cast<int>(sizeof(E));
+    uint4* const to = ring + fill + p.place[k];
+    for (int w = team.lane; 16 * w < bytes; w += 32) {
+      const char* const q = from - skip + 16 * w;
+      if (q >= static_cast<const char*>(p.src[k])) {
+        nsptx::cp_async16_upto(to + w, q, min(16, bytes - 16 * w));
+      } else {
+        for (int i = 0; i < count && skip + i * static_cast<int>(sizeof(E)) < 16; ++i)
+          *reinterpret_cast<E*>(reinterpret_cast<char*>(to) + skip + i * sizeof(E)) = reinterpret_cast<const E*>(from)[i];
+      }
+    }
+  }
+  __device__ __forceinline__ void fetched() {
+    nsptx::cp_async_commit();
+    fill = p.places == 2 ? p.stage - fill : 0;
+  }
+  __device__ __forceinline__ void wait(int t) {
+    nsptx::cp_async_wait<0>();
+    __syncwarp();
+    row = t;
+  }
+  __device__ __forceinline__ void taken() { take = p.places == 2 ? p.stage - take : 0; }
   template <typename E>
   __device__ __forceinline__ void get_row(int k, float2 (&v)[N]) const {
-    const E* const from = reinterpret_cast<const E*>(static_cast<const char*>(p.src[k]) + static_cast<long long>(row) * p.src_step[k]);
+    const int skip = static_cast<int>(reinterpret_cast<uintptr_t>(columns_of<E>(k, row)) & 15);
+    const E* const from = reinterpret_cast<const E*>(reinterpret_cast<const char*>(ring + take + p.place[k]) + skip);
     float f[NV];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) f[i] = p.src[k] && at + i * step < dim ? to_float(from[at + i * step]) : 0.0f;
+    for (int i = 0; i < NV; ++i) f[i] = p.src[k] && i * 32 + team.lane < count ? to_float(from[i * 32 + team.lane]) : 0.0f;
 #pragma unroll
     for (int i = 0; i < N; ++i) v[i] = make_float2(f[2 * i], f[2 * i + 1]);
   }
   template <typename E>
   __device__ __forceinline__ void put_row(int k, int t, const float2 (&v)[N]) const {
     if (!p.dst[k]) return;
-    E* const to = reinterpret_cast<E*>(static_cast<char*>(p.dst[k]) + static_cast<long long>(t) * p.dst_step[k]);
+    E* const to = reinterpret_cast<E*>(static_cast<char*>(p.dst[k]) + static_cast<long long>(t) * p.dst_step[k]) + first;
 #pragma unroll
     for (int i = 0; i < NV; ++i)
-      if (at + i * step < dim) to[at + i * step] = from_float<E>(i % 2 ? v[i / 2].y : v[i / 2].x);
+      if (i * 32 + team.lane < count) to[i * 32 + team.lane] = from_float<E>(i % 2 ? v[i / 2].y : v[i / 2].x);
   }
-  __device__ __forceinline__ void fetch_gate(int) const {}
-  __device__ __forceinline__ float gate() const { return p.gate_kind == TOKEN_GATE ? static_cast<const float*>(p.gate)[row] : 1.0f; }
+  __device__ __forceinline__ void fetch_gate(int t) const {
+    if (p.gate_kind == TOKEN_GATE && team.lane == 0) nsptx::cp_async4(ring + fill + p.stage - 1, static_cast<const float*>(p.gate) + t);
+  }
+  __device__ __forceinline__ float gate() const {
+    return p.gate_kind == TOKEN_GATE ? *reinterpret_cast<const float*>(ring + take + p.stage - 1) : 1.0f;
+  }
   __device__ __forceinline__ void weights(int which, float2 (&v)[N]) const {
-    const float* const from = weight + which * step * NV + at;
+    const float* const from = weight + which * team.warps * 32 * NV + first + team.lane;
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = make_float2(from[2 * i * step], from[(2 * i + 1) * step]);
+    for (int i = 0; i < N; ++i) v[i] = make_float2(from[2 * i * 32], from[(2 * i + 1) * 32]);
   }
   // A lane's sums of the weights' gradients to their columns of [2][dim].
   __device__ __forceinline__ void join(float* to, const float2 (&dp)[N], const float2 (&dw)[N]) const {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      if (at + i * step >= dim) continue;
-      to[at + i * step] = i % 2 ? dp[i / 2].y : dp[i / 2].x;
-      to[dim + at + i * step] = i % 2 ? dw[i / 2].y : dw[i / 2].x;
+      if (i * 32 + team.lane >= count) continue;
+      to[first + i * 32 + team.lane] = i % 2 ? dp[i / 2].y : dp[i / 2].x;
+      to[p.dim + first + i * 32 + team.lane] = i % 2 ? dw[i / 2].y : dw[i / 2].x;
     }
   }
 };
@@ -388,7 +430,7 @@ __global__ void __launch_bounds__(32 * BN_WARPS, bn_blocks(false, NV)) ns_block_
   lanes.prepare();
   for (int t = t0; t < tokens; t += stride) {
     lanes.wait(t);
-    fetch(t + stride);
+    if (WORDS || p.places == 2) fetch(t + stride);
     float2 b[N], h[N];
     const float2 beta = both(p.beta * lanes.gate());
     float2 w[N];
@@ -420,6 +462,10 @@ __global__ void __launch_bounds__(32 * BN_WARPS, bn_blocks(false, NV)) ns_block_
       for (int i = 0; i < N; ++i) h[i] = mul2(alpha, h[i]);
     }
     lanes.taken();
+    if (!WORDS && p.places == 1) {
+      __syncwarp();
+      fetch(t + stride);
+    }
     lanes.template put_row<R>(OUT_H, t, h);
     if (!p.n) continue;
     lanes.weights(1, w);
@@ -465,7 +511,7 @@ __global__ void __launch_bounds__(32 * BN_WARPS, bn_blocks(true, NV)) ns_block_n
   lanes.prepare();
   for (int t = t0; t < tokens; t += stride) {
     lanes.wait(t);
-    fetch(t + stride);
+    if (WORDS || p.places == 2) fetch(t + stride);
     float2 v[N], h[N], d[N], b[N], w[N];
     const float gt = lanes.gate();
     lanes.weights(1, w);
@@ -492,10 +538,6 @@ __global__ void __launch_bounds__(32 * BN_WARPS, bn_blocks(true, NV)) ns_block_n
         d[i] = fma2(r2, fma2(m, minus, mul2(v[i], w[i])), d[i]);  // t
       }
     }
-    float2 g[N];
-    // value by value a row's inputs are in memory only, where an output may take their place
-    if constexpr (!WORDS)
-      if (gated) lanes.template get_row<T>(IN_GATE, g);
     if (has_dx) {
 #pragma unroll
       for (int i = 0; i < N; ++i) h[i] = mul2(d[i], both(p.alpha));
@@ -504,11 +546,12 @@ __global__ void __launch_bounds__(32 * BN_WARPS, bn_blocks(true, NV)) ns_block_n
     if (has_branch) {
       const float r1 = post ? rsqrtf(fmaf(sum[2], inv_dim, p.eps)) : 1.0f;
       lanes.weights(0, w);
-      if (!gated) {
+      float2 g[N];
+      if (gated) {
+        lanes.template get_row<T>(IN_GATE, g);
+      } else {
 #pragma unroll
         for (int i = 0; i < N; ++i) g[i] = both(gt);
-      } else if constexpr (WORDS) {
-        lanes.template get_row<T>(IN_GATE, g);
       }
       s0 = s1 = both(0.0f);
 #pragma unroll
@@ -533,6 +576,10 @@ __global__ void __launch_bounds__(32 * BN_WARPS, bn_blocks(true, NV)) ns_block_n
       lanes.template put_row<T>(OUT_DBRANCH, t, d);
     }
     lanes.taken();
+    if (!WORDS && p.places == 1) {
+      __syncwarp();
+      fetch(t + stride);
+    }
   }
   if (!p.partial) return;
   // the block's teams, in order; the rings are done with
@@ -705,6 +752,7 @@ __global__ void __launch_bounds__(32 * BN_SUM_WARPS) ns_block_norm_sum_kernel(co
 template <typename T, typename R, int NV, bool WORDS>
 bool launch_rows(bool grad, BlockNormParams p, int nsm, int* blocks, cudaStream_t st, cudaError_t* e) {
   using L = Lanes<T, R, NV, true, false>;
+  using S = Singles<T, R, NV, true>;
   constexpr int BLOCKS[2] = {bn_blocks(false, NV), bn_blocks(true, NV)};
   p.warps = static_cast<int>((p.dim + 32 * NV - 1) / (32 * NV));
   // few rows are spread over the SMs, many share a block
@@ -732,7 +780,7 @@ bool launch_rows(bool grad, BlockNormParams p, int nsm, int* blocks, cudaStream_
     p.src[k] = k == IN_GATE && !value ? nullptr : i.at;
     p.wide[k] = i.wide && L::RW == 2;
     p.place[k] = p.stage;
-    if (WORDS && p.src[k]) p.stage += 32 * L::U * (i.wide ? L::RW : 1);
+    if (p.src[k]) p.stage += WORDS ? 32 * L::U * (i.wide ? L::RW : 1) : i.wide ? S::template WORDS_OF<R> : S::template WORDS_OF<T>;
     if (p.src[k] && !step(i.ld, i.wide, &p.src_step[k])) return false;
   }
   for (int k = 0; k < OUTPUTS; ++k) {
@@ -741,13 +789,14 @@ bool launch_rows(bool grad, BlockNormParams p, int nsm, int* blocks, cudaStream_
     if (p.dst[k] && !step(o.ld, o.wide, &p.dst_step[k])) return false;
   }
   if (p.tokens > INT_MAX / 4) return false;
-  if (WORDS && p.gate_kind == TOKEN_GATE) ++p.stage;
+  if (p.gate_kind == TOKEN_GATE) ++p.stage;
   // a block's rows, zeros, weights
   const size_t row = sizeof(uint4) * p.stage * p.warps * p.teams;
   const size_t more = (WORDS ? sizeof(uint4) * 32 * L::U * L::RW : 0) + sizeof(float) * 2 * 32 * NV * p.warps;
   const int per_sm = 2 * row + more <= BN_SMEM / BLOCKS[grad] ? BLOCKS[grad] : 1;
-  if (2 * row + more > BN_SMEM / per_sm) return false;
-  const size_t joined = p.partial ? sizeof(float) * 2 * p.dim * p.teams : 0, smem = std::max(2 * row + more, joined);
+  p.places = WORDS || 2 * row + more <= BN_SMEM / per_sm ? 2 : 1;
+  if (p.places * row + more > BN_SMEM / per_sm) return false;
+  const size_t joined = p.partial ? sizeof(float) * 2 * p.dim * p.teams : 0, smem = std::max(p.places * row + more, joined);
   *blocks = static_cast<int>(std::min<long long>((p.tokens + p.teams - 1) / p.teams, std::min(nsm * per_sm, BN_MAX_BLOCKS)));
   void (*kernel)(BlockNormParams) = ns_block_norm_kernel<T, R, NV, WORDS>;
   if (grad) kernel = ns_block_norm_grad_kernel<T, R, NV, WORDS, false>;

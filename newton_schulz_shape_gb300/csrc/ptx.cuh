@@ -110,6 +110,9 @@ __device__ __forceinline__ void cp_async16_upto(void* smem_dst, const void* src,
   asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, %3;"
                ::"r"(smem_u32(smem_dst)), "l"(src), "r"(bytes), "l"(policy) : "memory");
 }
+__device__ __forceinline__ void cp_async16_upto(void* smem_dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(smem_dst)), "l"(src), "r"(bytes) : "memory");
+}
 // 4 bytes, kept in L1 for the neighbours that read beside them.
 __device__ __forceinline__ void cp_async4(void* smem_dst, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(smem_dst)), "l"(src) : "memory");
