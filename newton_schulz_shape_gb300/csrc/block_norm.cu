@@ -304,8 +304,9 @@ struct Lanes {
 
 // The same for rows of any width, stride and alignment: a warp has 32 * NV columns
 // side by side, copies the aligned 16-byte words that cover them and takes them
-// from shared memory value by value. (Value by value from memory 4098 rows of 4095
-// bf16 took 331 us backward.)
+// from shared memory value by value. (Value by value from memory 8196 rows of 2047
+// bf16 took 313 us backward and 59 forward, so 91 and 46; 5003 rows of 1001 fp16
+// without a branch, which L2 holds, took 8.0 us, so 9.2.) Bound by instructions.
 template <typename T, typename R, int NV, bool GRAD>
 struct Singles {
   static constexpr int N = NV / 2;
@@ -344,8 +345,11 @@ struct Singles {
     const char* const from = columns_of<E>(k, t);
     const int skip = static_cast<int>(reinterpret_cast<uintptr_t>(from) & 15), bytes = skip + count * static_cast<int>(sizeof(E));
     uint4* const to = ring + fill + p.place[k];
-    for (int w = team.lane; 16 * w < bytes; w += 32) {
+#pragma unroll
+    for (int w0 = 0; w0 < WORDS_OF<E>; w0 += 32) {
+      const int w = w0 + team.lane;
       const char* const q = from - skip + 16 * w;
+      if (16 * w >= bytes) break;
       if (q >= static_cast<const char*>(p.src[k])) {
         nsptx::cp_async16_upto(to + w, q, min(16, bytes - 16 * w));
       } else {
