@@ -532,10 +532,10 @@ int ns_moe_few_tokens_workspace_bytes(int64_t tokens, int k, int64_t dim, int64_
  * nowhere; a token may name an expert more than once. weights fp32
  * [tokens][k], NULL = 1; the weight of a slot that goes nowhere is not used,
  * whatever it holds, and the matrices of experts that no token names are not
- * read. Products are of fp32's precision and summed in fp32 (fp32 factors as two
- * tf32 values each); an infinite factor (an fp32 x, a matrix value, a hidden
- * value) may give NaN where infinity is due, in the tokens that meet it. y may be
- * x itself. tokens <= 256, 1 <= k <= 32, 1 <= experts <= 1024, dim and ffn <
+ * read. Products of bf16 and fp16 factors are exact; the hidden value and the
+ * factors of fp32 layers take part as two tf32 values each (2^-22 off); sums are
+ * in fp32. An infinite factor (an fp32 x, a matrix value, a hidden value) may give
+ * NaN where infinity is due, in the tokens that meet it. y may be x itself. tokens <= 256, 1 <= k <= 32, 1 <= experts <= 1024, dim and ffn <
  * 2^20, ffn >= 1; for more tokens: ns_moe_sort, ns_moe_dispatch
  * and ns_moe_combine. */
 int ns_moe_few_tokens(const void* x, int64_t x_stride, int dtype, int64_t tokens, int k, int64_t dim, int64_t ffn,

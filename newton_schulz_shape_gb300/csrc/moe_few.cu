@@ -18,9 +18,9 @@
 // Blocks find the tokens of their experts among all slots themselves, which
 // spares a kernel.
 //
-// 64 experts of 1408 x 2048 bf16 by one slot each take 197-201 us (5.6 TB/s with
-// the three launches; 0.83 of the measured copy), by 8 each 207-211 and by 16 each
-// 236; one token of 8 experts 36 us (3.8 TB/s: three kernels of 3 us each with
+// 64 experts of 1408 x 2048 bf16 by one slot each take 196-201 us (5.6 TB/s with
+// the three launches; 0.83 of the measured copy), by 8 each 207-212 and by 16 each
+// 237; one token of 8 experts 36-38 us (3.7 TB/s: three kernels of 3 us each with
 // nothing to do, and 4.6 tiles a block).
 #include <algorithm>
 #include <climits>
@@ -49,7 +49,7 @@ struct MoeFewParams {
   long long x_ld, y_ld, dim, ffn;
   long long hidden_ld, part_ld;  // values of a slot's rows below
   const float* weights;
-  void* hidden;        // [tokens * k][hidden_ld] of 4 bytes: h in fp32, or as two bf16 rows
+  float* hidden;       // [tokens * k][hidden_ld]: h
   float* part;         // [tokens * k][part_ld]: D_e h
   int team;            // warps that split k of a tile
   int entries;         // at most: passes over an expert
@@ -195,6 +195,11 @@ __device__ __forceinline__ void split(float x, uint32_t* hi, uint32_t* lo) {
   const float h = __uint_as_float(*hi);
   *lo = __float_as_uint(x == h ? 0.0f : x - h);
 }
+// Two values of a 16-bit type, which tf32 holds.
+__device__ __forceinline__ float2 wide2(__nv_bfloat16, uint32_t w) {
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+__device__ __forceinline__ float2 wide2(__half, uint32_t w) { return __half22float2(*reinterpret_cast<const __half2*>(&w)); }
 
 // 16 bytes of consecutive values of a row from k on, value by value, zero from n on.
 template <typename T>
@@ -213,35 +218,39 @@ __device__ __forceinline__ uint4 load_words(const void* p) {
   return v;
 }
 
-// The tokens' side of a product, 16 bytes' worth of k: of x, or (HIDDEN) of h.
-// bf16 and fp16 products of x are exact; an fp32 factor is split in two. h has
-// more bits and a larger range than 16-bit types: it meets bf16 weights as two
-// bf16 values (2^-18 off), and fp16 weights, which tf32 holds, as two tf32 values.
+// The tokens' side of a product, 16 bytes' worth of the weights' k: of x, or
+// (HIDDEN) of h. bf16 and fp16 products of x are exact. h, in fp32, has more bits
+// and a larger range than 16-bit types: it is split in two tf32 values, which
+// meet the weights as tf32, and so are both factors of fp32 layers (without the
+// product of their lower parts, 2^-24). D_e h is then 1.9e-7 of its size off, as
+// with products in fp32 (1.5e-7). With bf16 weights and h as two bf16 values it was
+// 2.5e-6 and 64 tokens through 64 experts took 220 us, now 232; with three bf16
+// values 1e-7 and 249.
 template <typename T, bool HIDDEN>
 struct Side {
-  static constexpr bool PAIR = HIDDEN && std::is_same<T, __nv_bfloat16>::value;
-  static constexpr bool WIDE = sizeof(T) == 4 || (HIDDEN && !PAIR);
+  static constexpr bool WIDE = sizeof(T) == 4 || HIDDEN;      // products of tf32
+  static constexpr bool BOTH = sizeof(T) == 4;                // both factors are split
   static constexpr int Q = HIDDEN && sizeof(T) == 2 ? 2 : 1;  // 16-byte words
-  uint4 q[Q];  // PAIR: the upper parts, then the lower
+  uint4 q[Q];
   __device__ __forceinline__ uint32_t w(int i) const { return reinterpret_cast<const uint32_t*>(q)[i]; }
 
   // A slot's row.
   static __device__ __forceinline__ const char* row(const MoeFewParams& p, int slot) {
     if constexpr (HIDDEN)
-      return static_cast<const char*>(p.hidden) + 4 * slot * p.hidden_ld;
+      return reinterpret_cast<const char*>(p.hidden + slot * p.hidden_ld);
     else
       return static_cast<const char*>(p.x) + sizeof(T) * (slot / p.k) * p.x_ld;
   }
-  // Its values from k on, zero from n on; `second`: bytes from the upper parts to the lower.
+  // Its values from k on, zero from n on.
   template <bool VEC>
-  __device__ __forceinline__ void load(const char* row, int second, int k, int n) {
+  __device__ __forceinline__ void load(const char* row, int k, int n) {
 #pragma unroll
     for (int i = 0; i < Q; ++i) q[i] = make_uint4(0, 0, 0, 0);
     if constexpr (HIDDEN || VEC) {
       if (k < n) {
-        constexpr int BYTES = PAIR ? 2 : HIDDEN ? 4 : sizeof(T);
-        q[0] = load_words(row + BYTES * k);
-        if constexpr (Q == 2) q[1] = load_words(row + BYTES * k + (PAIR ? second : 16));
+        constexpr int BYTES = HIDDEN ? 4 : sizeof(T);
+#pragma unroll
+        for (int i = 0; i < Q; ++i) q[i] = load_words(row + BYTES * k + 16 * i);
       }
     } else {
       q[0] = load_values(reinterpret_cast<const T*>(row), k, n);
@@ -249,23 +258,19 @@ struct Side {
   }
 };
 
-// The weights' side, rows r and r + 8 of a tile, times that.
+// The weights' side, rows r and r + 8 of a tile, times that. The instruction cuts
+// what it adds at the sum's last place, always towards zero, which shows over long
+// rows (1e-6 of the result): a step's products make a sum of their own, the small
+// ones first, and that is added to the rest as usual.
 template <typename T, bool HIDDEN>
 __device__ __forceinline__ void times(float (&c)[4], const uint4& r, const uint4& r8, const Side<T, HIDDEN>& side) {
   using S = Side<T, HIDDEN>;
   const uint32_t a[2][4] = {{r.x, r.y, r.z, r.w}, {r8.x, r8.y, r8.z, r8.w}};
+  float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
   if constexpr (!S::WIDE) {
 #pragma unroll
-    for (int i = 0; i < 4; i += 2) {
-      mma_16<T>(c, a[0][i], a[1][i], a[0][i + 1], a[1][i + 1], side.w(i), side.w(i + 1));
-      if constexpr (S::PAIR) mma_16<T>(c, a[0][i], a[1][i], a[0][i + 1], a[1][i + 1], side.w(4 + i), side.w(5 + i));
-    }
+    for (int i = 0; i < 4; i += 2) mma_16<T>(sum, a[0][i], a[1][i], a[0][i + 1], a[1][i + 1], side.w(i), side.w(i + 1));
   } else {
-    // The instruction cuts what it adds at the sum's last place, always towards zero: in fp32, where that shows (1e-6 over
-    // long rows), a few products make a sum of their own, the small ones first, and are added to the rest as usual.
-    constexpr bool APART = sizeof(T) == 4;
-    float few[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    float(&sum)[4] = APART ? few : c;
 #pragma unroll
     for (int i = 0; i < 16 / static_cast<int>(sizeof(T)); i += 2) {
       uint32_t hi[2], lo[2], w[2][2], rest[2][2];  // [k][row]
@@ -277,7 +282,7 @@ __device__ __forceinline__ void times(float (&c)[4], const uint4& r, const uint4
           if constexpr (sizeof(T) == 4) {
             split(__uint_as_float(a[q][i + j]), &w[j][q], &rest[j][q]);
           } else {
-            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&a[q][i / 2]));
+            const float2 f = wide2(T(), a[q][i / 2]);
             w[j][q] = __float_as_uint(j ? f.y : f.x);
           }
         }
@@ -286,26 +291,23 @@ __device__ __forceinline__ void times(float (&c)[4], const uint4& r, const uint4
       if constexpr (sizeof(T) == 4) mma_tf32_8(sum, rest[0][0], rest[0][1], rest[1][0], rest[1][1], hi[0], hi[1]);
       mma_tf32_8(sum, w[0][0], w[0][1], w[1][0], w[1][1], hi[0], hi[1]);
     }
-    if constexpr (APART) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) c[i] += few[i];
-    }
   }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) c[i] += sum[i];
 }
 
 // Steps of a warp whose words are on their way, and places for them in the warp's
 // ring of shared memory. A lane copies into its own words there, once the products
-// that took the step before from them are issued. Where those take long (`wide`:
-// tf32, several a value) one step more has its place and is copied before them (17
-// tokens by 4 of 60 experts of 2112 x 960 fp32 168 us, without 186; for bf16 the
-// memory is better spent on sums: 64 tokens by 6 of 64 experts of 1408 x 2048
-// 212-226 us, was 233-240). h is then twice its size, and takes the memory of one.
-__host__ __device__ constexpr int ahead(bool hidden, bool vec, bool wide) { return wide && (hidden || !vec) ? 2 : 3; }
+// that took the step before from them are issued. Where those take long (`both`
+// factors are split) one step more has its place and is copied before them (17
+// tokens by 4 of 60 experts of 2112 x 960 fp32 168 us, without 186; 64 tokens by 6
+// of 64 experts of 1408 x 2048 bf16 236 us with it, 232 without).
+__host__ __device__ constexpr int ahead(bool hidden, bool vec, bool both) { return both && (hidden || !vec) ? 2 : 3; }
 // 16-byte words of a step: four rows of 16 bytes a lane. Rows that are not made of aligned 16-byte words are copied in
 // aligned 4-byte words, five of which cover the values of a 16-bit type.
 __host__ __device__ constexpr int stage_words(bool vec) { return vec ? 4 * 32 : 5 * 32; }
 template <typename S, bool HIDDEN, bool VEC>
-constexpr int RING_WORDS = (ahead(HIDDEN, VEC, S::WIDE) + S::WIDE) * stage_words(VEC);
+constexpr int RING_WORDS = (ahead(HIDDEN, VEC, S::BOTH) + S::BOTH) * stage_words(VEC);
 
 // A team of warps goes through the tiles of a block that fall to it, all passes in
 // a row: `Stream` copies the weights of a warp's next steps to its ring, into the
@@ -317,7 +319,7 @@ constexpr int RING_WORDS = (ahead(HIDDEN, VEC, S::WIDE) + S::WIDE) * stage_words
 template <typename T, bool HIDDEN, bool VEC>
 struct Stream {
   using S = Side<T, HIDDEN>;
-  static constexpr int V = 16 / sizeof(T), AHEAD = ahead(HIDDEN, VEC, S::WIDE), STAGE = stage_words(VEC), RING = RING_WORDS<S, HIDDEN, VEC>;
+  static constexpr int V = 16 / sizeof(T), AHEAD = ahead(HIDDEN, VEC, S::BOTH), STAGE = stage_words(VEC), RING = RING_WORDS<S, HIDDEN, VEC>;
   // 4-byte words of a row, where there are no 16-byte ones
   static constexpr int PLANES = sizeof(T) == 4 ? 4 : 5;
   static_assert(32 * 4 * PLANES <= 4 * stage_words(false), "a stage");
@@ -434,7 +436,7 @@ struct Stream {
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
         S side;
-        side.template load<VEC>(row[t], static_cast<int>(2 * p.hidden_ld), k0 + i * step, n);
+        side.template load<VEC>(row[t], k0 + i * step, n);
 #pragma unroll
         for (int j = 0; j < S::Q; ++j) held[((i * NT + t) * S::Q + j) * 32] = side.q[j];
       }
@@ -446,7 +448,7 @@ struct Stream {
   template <int NT>
   __device__ __forceinline__ void load(const char* const (&row)[NT], S (&side)[NT], int i) const {
 #pragma unroll
-    for (int t = 0; t < NT; ++t) side[t].template load<VEC>(row[t], static_cast<int>(2 * p.hidden_ld), k0 + i * step, n);
+    for (int t = 0; t < NT; ++t) side[t].template load<VEC>(row[t], k0 + i * step, n);
   }
   // The products of the next tile, `of` of pass `in`, with those slots.
   template <int NT, bool HELD>
@@ -481,13 +483,13 @@ struct Stream {
           a[j] = from_words(reinterpret_cast<const uint32_t*>(ring + take) + j * PLANES * 32 + lane, odd[j], n - k0 - i * step);
       }
       take = take + STAGE == RING ? 0 : take + STAGE;
-      if constexpr (S::WIDE) fetch();
+      if constexpr (S::BOTH) fetch();
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
         times(acc[0][t], a[0], a[1], side[t]);
         times(acc[1][t], a[2], a[3], side[t]);
       }
-      if constexpr (!S::WIDE) fetch();
+      if constexpr (!S::BOTH) fetch();
     }
   }
 };
@@ -610,16 +612,7 @@ __global__ void __launch_bounds__(MF_THREADS, 1) ns_moe_few_hidden_kernel(const 
         const long long f = tile * (MF_ROWS / 2) + (row & 7) + row / 16 * 8;
         if (f >= p.hidden_ld) return;
         // zero up to the row's end: its last words are read whole
-        const float h = f < p.ffn ? a / (1.0f + expf(-a)) * b : 0.0f;
-        if constexpr (std::is_same<T, __nv_bfloat16>::value) {
-          __nv_bfloat16* const to = static_cast<__nv_bfloat16*>(p.hidden) + slot * 2 * p.hidden_ld + f;
-          const __nv_bfloat16 hi = from_float<__nv_bfloat16>(h);
-          const float rounded = to_float(hi);
-          to[0] = hi;
-          to[p.hidden_ld] = from_float<__nv_bfloat16>(rounded - rounded == 0.0f ? h - rounded : 0.0f);
-        } else {
-          static_cast<float*>(p.hidden)[slot * p.hidden_ld + f] = h;
-        }
+        p.hidden[slot * p.hidden_ld + f] = f < p.ffn ? a / (1.0f + expf(-a)) * b : 0.0f;
       });
 }
 
@@ -803,7 +796,7 @@ int ns_moe_few_tokens(const void* x, int64_t x_stride, int dtype, int64_t tokens
   p.hidden_ld = parts.hidden_ld;
   p.part_ld = parts.part_ld;
   p.weights = weights;
-  p.hidden = workspace;
+  p.hidden = static_cast<float*>(workspace);
   p.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + parts.part);
   int dev, nsm;
   if ((rc = device_setup(&dev, &p.status, &nsm)) != NS_OK) return rc;
