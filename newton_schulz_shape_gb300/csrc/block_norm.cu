@@ -712,7 +712,7 @@ __global__ void __launch_bounds__(BN_ANY_THREADS) ns_block_norm_grad_any_kernel(
     for (long long d = threadIdx.x; d < p.dim; d += BN_ANY_THREADS) {
       const float tv = t_at(d), m = to_float(h[d]) * r2, dnv = dn ? to_float(dn[d]) : 0.0f;
       const float bv = b ? to_float(b[d]) : 0.0f, g = gv ? to_float(gv[d]) : gt;
-      if (dp) dw[d] = fmaf(dnv, m, dw[d]);
+      if (dp && dn) dw[d] = fmaf(dnv, m, dw[d]);
       if (p.dx) static_cast<R*>(p.dx)[t * p.dx_ld + d] = from_float<R>(p.alpha * tv);
       if (!b) continue;
       const float tb = p.beta * tv, s = tb * g, y = bv * r1, pw = weight_of<T>(p, p.branch_weight, d);
