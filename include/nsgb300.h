@@ -472,8 +472,9 @@ int ns_grad_norm(const void* const* grads, const int64_t* numels, const int* dty
 /* outs[i] = c * grads[i], c = min(1, max_norm / (*norm + eps)), rounded once.
  * *norm is on the device: what ns_grad_norm wrote, or the norm over several
  * calls or ranks. outs[i] may be grads[i] itself, and is not touched then if
- * c = 1. An infinite norm gives c = 0 (infinite values become NaN), a norm that
- * is NaN makes every value NaN. max_norm >= 0, eps >= 0 and finite. */
+ * c = 1. An infinite norm gives c = 0 (infinite values become NaN), unless
+ * max_norm is infinite as well (c = 1); a norm that is NaN makes every value NaN.
+ * max_norm >= 0, eps >= 0 and finite. */
 int ns_grad_clip(const void* const* grads, void* const* outs, const int64_t* numels, const int* dtypes, int count,
                  const float* norm, float max_norm, float eps, void* stream);
 

@@ -195,8 +195,14 @@ __global__ void __launch_bounds__(GN_TOTAL_THREADS) ns_grad_total_kernel(const _
   if (threadIdx.x == 0) *p.norm = static_cast<float>(sqrt(sum));
 }
 
-template <typename T>
-__device__ __forceinline__ void clip_chunk(const T* p, T* out, long long n, int k, float scale) {
+// A value times the scale, in fp32's or the scale's bits, whichever are more.
+template <typename F>
+__device__ __forceinline__ float scaled(float x, F scale) {
+  return static_cast<float>(x * scale);
+}
+
+template <typename T, typename F>
+__device__ __forceinline__ void clip_chunk(const T* p, T* out, long long n, int k, F scale) {
   constexpr int V = 16 / sizeof(T);
   const Chunk<T> c(p, n, k);
   T* const to = out + (c.at - p);
@@ -214,34 +220,47 @@ __device__ __forceinline__ void clip_chunk(const T* p, T* out, long long n, int 
         const int i = (w0 + w) * GN_THREADS + threadIdx.x;
         float f[V];
 #pragma unroll
-        for (int j = 0; j < V; ++j) f[j] = get(x[w], j) * scale;
+        for (int j = 0; j < V; ++j) f[j] = scaled(get(x[w], j), scale);
         if (i < c.words) store_vec<T, V>(to + i * V, pack<T, V>(f));
       }
     }
   } else {  // the two start at different places of a word
-    for (int i = threadIdx.x; i < c.words * V; i += GN_THREADS) to[i] = from_float<T>(to_float(c.at[i]) * scale);
+    for (int i = threadIdx.x; i < c.words * V; i += GN_THREADS) to[i] = from_float<T>(scaled(to_float(c.at[i]), scale));
   }
   const int i = threadIdx.x;
-  if (i < c.heads) out[i] = from_float<T>(to_float(c.head[i]) * scale);
-  if (i < c.tails) out[c.tail - p + i] = from_float<T>(to_float(c.tail[i]) * scale);
+  if (i < c.heads) out[i] = from_float<T>(scaled(to_float(c.head[i]), scale));
+  if (i < c.tails) out[c.tail - p + i] = from_float<T>(scaled(to_float(c.tail[i]), scale));
 }
 
-// From the last chunk back: the norm read it last, so that L2 still holds some.
+// Chunk k of tensor t.
+template <typename F>
+__device__ __forceinline__ void clip_tensor(const GradClipParams& p, int t, int k, F scale) {
+  const int type = static_cast<int>(p.in.size[t] & 3);
+  const long long n = p.in.size[t] >> 2;
+  if (type == NS_DT_BF16)
+    clip_chunk(static_cast<const __nv_bfloat16*>(p.in.src[t]), static_cast<__nv_bfloat16*>(p.out[t]), n, k, scale);
+  else if (type == NS_DT_FP16)
+    clip_chunk(static_cast<const __half*>(p.in.src[t]), static_cast<__half*>(p.out[t]), n, k, scale);
+  else
+    clip_chunk(static_cast<const float*>(p.in.src[t]), static_cast<float*>(p.out[t]), n, k, scale);
+}
+__device__ __noinline__ void clip_tensor_wide(const GradClipParams& p, int t, int k, double scale) { clip_tensor(p, t, k, scale); }
+
+// From the last chunk back: the norm read it last, so that L2 still holds some. A
+// scale below fp32's normal range would lose bits there (a norm of 3e38 clipped to
+// 1e-4: 2e-3 of every value) and is multiplied in 64 bits.
 __global__ void __launch_bounds__(GN_THREADS, GN_CLIP_BLOCKS) ns_grad_clip_kernel(const __grid_constant__ GradClipParams p) {
   nsptx::griddep_wait();
   nsptx::griddep_launch_dependents();
-  const double norm = static_cast<double>(*p.norm) + p.eps;  // NaN stays visible
-  const float scale = norm <= p.max_norm ? 1.0f : static_cast<float>(p.max_norm / norm);
+  const double norm = static_cast<double>(*p.norm) + p.eps, wide = norm <= p.max_norm ? 1.0 : p.max_norm / norm;  // NaN stays visible
+  const float scale = static_cast<float>(wide);
   for (int i = p.in.chunks - 1 - blockIdx.x; i >= 0; i -= gridDim.x) {
-    const int t = tensor_of(p.in, i), k = i - p.in.first[t], type = static_cast<int>(p.in.size[t] & 3);
-    const long long n = p.in.size[t] >> 2;
+    const int t = tensor_of(p.in, i), k = i - p.in.first[t];
     if (scale == 1.0f && p.in.src[t] == p.out[t]) continue;
-    if (type == NS_DT_BF16)
-      clip_chunk(static_cast<const __nv_bfloat16*>(p.in.src[t]), static_cast<__nv_bfloat16*>(p.out[t]), n, k, scale);
-    else if (type == NS_DT_FP16)
-      clip_chunk(static_cast<const __half*>(p.in.src[t]), static_cast<__half*>(p.out[t]), n, k, scale);
+    if (wide > 0.0 && wide < 0x1p-126)
+      clip_tensor_wide(p, t, k, wide);
     else
-      clip_chunk(static_cast<const float*>(p.in.src[t]), static_cast<float*>(p.out[t]), n, k, scale);
+      clip_tensor(p, t, k, scale);
   }
 }
 
