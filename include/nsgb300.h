@@ -456,8 +456,9 @@ int ns_distill_grad(const void* logits, int64_t logits_stride, int dtype, int64_
  * addresses, numbers of values and types (NS_DT_*, which may differ from tensor
  * to tensor): host arrays that are read before the call returns. A tensor's
  * values are contiguous in memory, at any address that they can have; it may
- * be empty. At most 2^20 tensors, 2^43 bytes together. Tensors of one call must
- * not overlap. */
+ * be empty. At most 2^20 tensors, 2^43 bytes together. A tensor that ns_grad_clip
+ * writes must not overlap the call's others (several blocks would write it at
+ * once); the calls on torch tensors refuse one that begins where another does. */
 
 /* Bytes of device workspace of ns_grad_norm. Host only. */
 int ns_grad_norm_workspace_bytes(int count, uint64_t* bytes);

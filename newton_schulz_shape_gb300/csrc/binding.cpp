@@ -18,6 +18,7 @@
 
 #include <algorithm>
 #include <climits>
+#include <cstdint>
 #include <exception>
 #include <initializer_list>
 #include <memory>
@@ -474,6 +475,53 @@ PyObject* grad_norm(const Args& a) {
                   {1});
 }
 
+// An output that begins where another output does, or an input that it does not take the place of: such tensors would be
+// written by several blocks at once. -1 where there is none. Tensors one behind the other, as in a flat buffer, are seen
+// to be apart without a table.
+int named_twice(const Tensors& in, const Tensors& out) {
+  const auto begin = [](const Tensors& t, int j) { return reinterpret_cast<uintptr_t>(t.at[j]); };
+  const auto end = [&](const Tensors& t, int j) { return begin(t, j) + t.numels[j] * (t.dtypes[j] == NS_DT_FP32 ? 4 : 2); };
+  const auto in_order = [&](const Tensors& t) {
+    uintptr_t last = 0;
+    for (int j = 0; j < t.count(); ++j) {
+      if (t.numels[j] == 0) continue;
+      if (begin(t, j) < last) return false;
+      last = end(t, j);
+    }
+    return true;
+  };
+  const int n = out.count();
+  if (in_order(out)) {
+    if (&in == &out) return -1;
+    uintptr_t low = UINTPTR_MAX, high = 0;
+    for (int j = 0; j < n; ++j)
+      if (out.numels[j]) low = std::min(low, begin(out, j)), high = std::max(high, end(out, j));
+    bool apart = true;
+    for (int j = 0; j < n; ++j) apart &= !in.numels[j] || begin(in, j) == begin(out, j) || end(in, j) <= low || begin(in, j) >= high;
+    if (apart) return -1;
+  }
+  int bits = 4;
+  while ((1 << bits) < 2 * n) ++bits;
+  std::vector<int> table(size_t{1} << bits, -1);
+  const auto place = [&](const void* p) {  // of p's output, or a free one
+    size_t k = (reinterpret_cast<uintptr_t>(p) * 0x9E3779B97F4A7C15u) >> (64 - bits);
+    while (table[k] >= 0 && out.at[table[k]] != p) k = (k + 1) & (table.size() - 1);
+    return k;
+  };
+  for (int j = 0; j < n; ++j) {
+    if (out.numels[j] == 0) continue;
+    const size_t k = place(out.at[j]);
+    if (table[k] >= 0) return j;
+    table[k] = j;
+  }
+  for (int j = 0; &in != &out && j < n; ++j) {
+    if (in.numels[j] == 0) continue;
+    const int k = table[place(in.at[j])];
+    if (k >= 0 && k != j) return k;
+  }
+  return -1;
+}
+
 PyObject* grad_clip(const Args& a) {
   const Tensors g(a, 0);
   std::optional<Tensors> other;  // than grads themselves
@@ -487,6 +535,8 @@ PyObject* grad_clip(const Args& a) {
         (x.strides() != y.strides() && !(x.is_contiguous() && y.is_contiguous())))
       a.bad_item(1, j, "the type, shape and strides of grads' tensor", y);
   }
+  if (const int twice = named_twice(g, out); twice >= 0)
+    a.bad_item(1, twice, "a tensor that the call names in no other place", out.tensor(twice));
   const int rc = ns_grad_clip(g.at.data(), const_cast<void* const*>(out.at.data()), g.numels.data(), g.dtypes.data(),
                               g.count(), static_cast<float*>(a.whole(2, at::kFloat, 1)), a.real(3, 0.0f),
                               a.real(4, 1e-6f), a.stream());
@@ -706,7 +756,8 @@ PyMethodDef g_methods[] = {
               "which may differ in type. A tensor must be dense in memory, in any order of its dimensions."),
     NS_METHOD(10, grad_clip,
               "ns_grad_clip(grads, outs, norm, max_norm, eps=1e-6, stream=None)\n--\n\n"
-              "outs[i] = min(1, max_norm / (norm + eps)) * grads[i]; outs may be grads, untouched if that is 1."),
+              "outs[i] = min(1, max_norm / (norm + eps)) * grads[i]; outs may be grads, untouched if that is 1. A tensor of outs\n"
+              "must not overlap the call's others: one that begins where another does is refused."),
     NS_METHOD(11, block_norm,
               "ns_block_norm(branch, residual, residual_out, out, branch_weight=None, weight=None, gate=None, "
               "post_norm=True, residual_scale=1.0, branch_scale=1.0, eps=1e-6, stream=None)\n--\n\n"
