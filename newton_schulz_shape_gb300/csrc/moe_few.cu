@@ -229,7 +229,8 @@ __device__ __forceinline__ uint4 load_words(const void* p) {
 template <typename T, bool HIDDEN>
 struct Side {
   static constexpr bool WIDE = sizeof(T) == 4 || HIDDEN;      // products of tf32
-  static constexpr bool BOTH = sizeof(T) == 4;                // both factors are split
+  // the weights have to be converted, or split as well
+  static constexpr bool LONG = sizeof(T) == 4 || (HIDDEN && std::is_same<T, __half>::value);
   static constexpr int Q = HIDDEN && sizeof(T) == 2 ? 2 : 1;  // 16-byte words
   uint4 q[Q];
   __device__ __forceinline__ uint32_t w(int i) const { return reinterpret_cast<const uint32_t*>(q)[i]; }
@@ -298,16 +299,17 @@ __device__ __forceinline__ void times(float (&c)[4], const uint4& r, const uint4
 
 // Steps of a warp whose words are on their way, and places for them in the warp's
 // ring of shared memory. A lane copies into its own words there, once the products
-// that took the step before from them are issued. Where those take long (`both`
-// factors are split) one step more has its place and is copied before them (17
-// tokens by 4 of 60 experts of 2112 x 960 fp32 168 us, without 186; 64 tokens by 6
-// of 64 experts of 1408 x 2048 bf16 236 us with it, 232 without).
-__host__ __device__ constexpr int ahead(bool hidden, bool vec, bool both) { return both && (hidden || !vec) ? 2 : 3; }
+// that took the step before from them are issued. Where those take long, one step
+// more has its place and is copied before them (17 tokens by 4 of 60 experts of
+// 2112 x 960 fp32 168 us, without 186; 64 tokens by 6 of 64 experts of 1408 x 2048
+// fp16 233 us, without 239, and bf16 236, without 232). h is then twice its size or
+// the ring wider, and takes the memory of one.
+__host__ __device__ constexpr int ahead(bool hidden, bool vec, bool slow) { return slow && (hidden || !vec) ? 2 : 3; }
 // 16-byte words of a step: four rows of 16 bytes a lane. Rows that are not made of aligned 16-byte words are copied in
 // aligned 4-byte words, five of which cover the values of a 16-bit type.
 __host__ __device__ constexpr int stage_words(bool vec) { return vec ? 4 * 32 : 5 * 32; }
 template <typename S, bool HIDDEN, bool VEC>
-constexpr int RING_WORDS = (ahead(HIDDEN, VEC, S::BOTH) + S::BOTH) * stage_words(VEC);
+constexpr int RING_WORDS = (ahead(HIDDEN, VEC, S::LONG) + S::LONG) * stage_words(VEC);
 
 // A team of warps goes through the tiles of a block that fall to it, all passes in
 // a row: `Stream` copies the weights of a warp's next steps to its ring, into the
@@ -319,7 +321,7 @@ constexpr int RING_WORDS = (ahead(HIDDEN, VEC, S::BOTH) + S::BOTH) * stage_words
 template <typename T, bool HIDDEN, bool VEC>
 struct Stream {
   using S = Side<T, HIDDEN>;
-  static constexpr int V = 16 / sizeof(T), AHEAD = ahead(HIDDEN, VEC, S::BOTH), STAGE = stage_words(VEC), RING = RING_WORDS<S, HIDDEN, VEC>;
+  static constexpr int V = 16 / sizeof(T), AHEAD = ahead(HIDDEN, VEC, S::LONG), STAGE = stage_words(VEC), RING = RING_WORDS<S, HIDDEN, VEC>;
   // 4-byte words of a row, where there are no 16-byte ones
   static constexpr int PLANES = sizeof(T) == 4 ? 4 : 5;
   static_assert(32 * 4 * PLANES <= 4 * stage_words(false), "a stage");
@@ -483,13 +485,13 @@ struct Stream {
           a[j] = from_words(reinterpret_cast<const uint32_t*>(ring + take) + j * PLANES * 32 + lane, odd[j], n - k0 - i * step);
       }
       take = take + STAGE == RING ? 0 : take + STAGE;
-      if constexpr (S::BOTH) fetch();
+      if constexpr (S::LONG) fetch();
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
         times(acc[0][t], a[0], a[1], side[t]);
         times(acc[1][t], a[2], a[3], side[t]);
       }
-      if constexpr (!S::BOTH) fetch();
+      if constexpr (!S::LONG) fetch();
     }
   }
 };
