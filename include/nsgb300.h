@@ -493,8 +493,10 @@ int ns_grad_clip(const void* const* grads, void* const* outs, const int64_t* num
  * out NULL: not wanted; n is computed from h before h is rounded. strides[5]:
  * row strides of branch, residual, residual_out, out and gate. residual_out may
  * be residual and out may be branch or gate, with the same stride. dim at most
- * 2^20, tokens * dim at most 2^40. Sums of squares are in fp32: a root mean
- * square above 1e17 has no norm there. */
+ * 2^20, tokens * dim at most 2^40. Sums of squares are in fp32: a row whose sum is
+ * above 3.4e38 (a root mean square of 1e17 at 32768 columns) has no norm there, nor
+ * with eps = 0 one whose root mean square is below 1e-18. Rows beyond 8192 columns
+ * are read several times. */
 int ns_block_norm(const void* branch, const void* residual, void* residual_out, void* out, const int64_t* strides,
                   int dtype, int residual_dtype, int64_t tokens, int64_t dim, const void* branch_weight,
                   const void* weight, int weight_dtype, const void* gate, int gate_kind, int post_norm,
@@ -513,7 +515,9 @@ int ns_block_norm_grad_workspace_bytes(int64_t dim, uint64_t* bytes);
  * grad_residual, grad_residual_out, grad_out, gate and grad_gate. Outputs may be
  * inputs of the same type and shape with the same stride (grad_residual may be
  * grad_residual_out, grad_branch may be grad_out or branch, grad_gate may be
- * gate), each input at most once. */
+ * gate), each input at most once. The sum of grad_out * weight * residual_out over a
+ * row is in fp32 as well. Without tokens the weights' gradients are zero; with dim 0
+ * nothing is written. */
 int ns_block_norm_grad(const void* grad_residual_out, const void* grad_out, const void* branch, const void* residual_out,
                        void* grad_branch, void* grad_residual, const int64_t* strides, int dtype, int residual_dtype,
                        int64_t tokens, int64_t dim, const void* branch_weight, const void* weight, int weight_dtype,
@@ -534,12 +538,13 @@ int ns_moe_few_tokens_workspace_bytes(int64_t tokens, int k, int64_t dim, int64_
  * nowhere; a token may name an expert more than once. weights fp32
  * [tokens][k], NULL = 1; the weight of a slot that goes nowhere is not used,
  * whatever it holds, and the matrices of experts that no token names are not
- * read. Products of bf16 and fp16 factors are exact; the hidden value and the
- * factors of fp32 layers take part as two tf32 values each (2^-22 off); sums are
- * in fp32. An infinite factor (an fp32 x, a matrix value, a hidden value) may give
- * NaN where infinity is due, in the tokens that meet it. y may be x itself. tokens <= 256, 1 <= k <= 32, 1 <= experts <= 1024, dim and ffn <
- * 2^20, ffn >= 1; for more tokens: ns_moe_sort, ns_moe_dispatch
- * and ns_moe_combine. */
+ * read. Those of the others are read once for every 16 slots that name them.
+ * Products of bf16 and fp16 factors are exact; the hidden value and the factors of
+ * fp32 layers take part as two tf32 values each (2^-22 off); sums are in fp32. An
+ * infinite factor (an fp32 x, a matrix value, a hidden value) may give NaN where
+ * infinity is due, in the tokens that meet it. y may be x itself. tokens <= 256,
+ * 1 <= k <= 32, 1 <= experts <= 1024, dim and ffn < 2^20, ffn >= 1; for more
+ * tokens: ns_moe_sort, ns_moe_dispatch and ns_moe_combine. */
 int ns_moe_few_tokens(const void* x, int64_t x_stride, int dtype, int64_t tokens, int k, int64_t dim, int64_t ffn,
                       int experts, const void* expert_ids, int id_bytes, const float* weights, const void* gate_up,
                       const void* down, void* y, int64_t y_stride, void* workspace, uint64_t workspace_bytes,

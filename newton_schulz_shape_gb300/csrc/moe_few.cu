@@ -5,22 +5,25 @@
 //   y_t = sum over j of w_tj D_e h_s
 // with silu(a) = a / (1 + exp(-a)).
 //
-// The matrices of the experts that are named, 3 dim ffn values each, are read
-// once and are nearly all of the bytes, so the layer is bound by memory: n tokens
-// of an expert make 2 n operations of each value. Up to 16 of an expert's slots
-// share a pass over its matrices, whose tiles (32 rows) all blocks deal among
-// them; the 16 warps of a block split k of a tile. Each lane copies the 16-byte
-// words of its rows ahead to its own places of shared memory and hands them to
-// m16n8k16 tensor instructions as they are: the order of k within a product is
-// free, so its words and the tokens' are taken in the same order, and nothing is
-// exchanged between lanes. (The 5th-generation instruction takes 128 rows, whose
-// tiles are too few for the card: 8 experts of 1408 rows make 176.)
+// The matrices of the experts that are named, 3 dim ffn values each, are nearly
+// all of the bytes, so the layer is bound by memory: n tokens of an expert make
+// 2 n operations of each value. Up to 16 of an expert's slots share a pass over its
+// matrices, which are read once for each pass (128 tokens by 8 of 64 experts make
+// 1.5 readings and 352 us, 64 by 2 of 8 as many and 58 us); a pass's tiles (32 rows)
+// all blocks deal among them, and the 16 warps of a block split k of a tile. Each
+// lane copies the 16-byte words of its rows ahead to its own places of shared
+// memory and hands them to tensor instructions as they are (x by G and U, 16-bit
+// types) or widened to tf32: the order of k within a product is free, so its words
+// and the tokens' are taken in the same order, and nothing is exchanged between
+// lanes. (The 5th-generation instruction takes 128 rows, whose tiles are too few
+// for the card where few experts are named: 8 of 1408 rows make 176. It was not
+// tried for many.)
 // Blocks find the tokens of their experts among all slots themselves, which
 // spares a kernel.
 //
-// 64 experts of 1408 x 2048 bf16 by one slot each take 196-201 us (5.6 TB/s with
-// the three launches; 0.83 of the measured copy), by 8 each 207-212 and by 16 each
-// 237; one token of 8 experts 36-38 us (3.7 TB/s: three kernels of 3 us each with
+// 64 experts of 1408 x 2048 bf16 by one slot each take 194-201 us (5.6 TB/s with
+// the three launches; 0.83 of the measured copy), by 8 each 208-212 and by 16 each
+// 237; one token of 8 experts 36-37 us (3.7 TB/s: three kernels of 3 us each with
 // nothing to do, and 4.6 tiles a block).
 #include <algorithm>
 #include <climits>
@@ -548,7 +551,7 @@ __device__ __forceinline__ void tiles_of_pass(S& stream, const Team& team, int& 
 #pragma unroll
       for (int i = 0; i < 8; ++i) team.sums[((t * team.warps + team.warp) * 8 + i) * 32 + lane] = acc[i / 4][t][i % 4];
     team_sync(team.id, team.warps);
-    // Of all slots at once (64 experts by 12 slots each 222 us, 8 by 8 of them 236).
+    // Of all slots at once (64 experts by 12 slots each took 222 us then, 8 by 8 of them 236).
     // By four warps for 8 slots, in a fixed order of all, while the others go on with the next tile. (By two of them in
     // wider words 64 experts by 8 slots each take 228 us, by all 225, so 208.)
     for (int q = team.warp; q < 4 * NT; q += team.warps) {
